@@ -59,7 +59,8 @@ typedef enum {
   I8_ERR_UNSUPPORTED = 3,     /* K % 16 != 0, K > 131072, size out of range */
   I8_ERR_WORKSPACE = 4,       /* workspace missing or smaller than required */
   I8_ERR_CUDA = 5,            /* a CUDA runtime or launch error */
-  I8_ERR_DEVICE_TIMEOUT = 6   /* a kernel's pipeline wait ran out of time */
+  I8_ERR_DEVICE_TIMEOUT = 6,  /* a kernel's pipeline wait ran out of time */
+  I8_ERR_DEVICE_DATA = 7      /* a kernel met lengths, slots or block ids out of range */
 } i8_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -255,6 +256,114 @@ i8_status i8_gelu_quant_act_pertoken(const void* x_bf16, int64_t M, int64_t K,
                                      int64_t ldq, float* s_a, void* y_bf16,
                                      int64_t ldy, i8_stream_t stream);
 
+/* ------------------------------------------------------------------ serving
+ * What a decoder built on the linear layer runs besides it at every step: the
+ * norm in front of a layer, the step's block tables, and attention over a
+ * paged cache of keys and values held in 8 bits.  (No counterpart on the
+ * pages; the conventions are those of the calls above.)  Sizes that only the
+ * device knows (lengths, slots, block ids) are checked by the kernels: what is
+ * out of range is left out, no access goes out of bounds, and the next
+ * i8_sync_check() returns I8_ERR_DEVICE_DATA. */
+
+/* The residual's addition, the root-mean-square norm with a gain, and the
+ * per-token quantizer of its output, in one pass.  Per row:
+ *   h = x + residual                        (x alone where residual is NULL)
+ *   y = h * weight / sqrt(mean(h^2) + eps)  (weight NULL: ones)
+ *   s_a = max|y| / L, q = round_half_even(y / s_a), L = 127 (int8, fp16-held
+ *   codes) or 448 (E4M3); a row of zeros gets scale 0 and codes 0.
+ * h and y are fp32 inside; the only other rounding is h's to bf16 where it is
+ * stored.  In detail t = h * weight (fp32), s_t = max|t| / L, q =
+ * round_half_even(t / s_t) (IEEE fp32 steps) and s_a = s_t / sqrt(...): the
+ * codes do not depend on the order of the sum.
+ *   x, residual [M,K] bf16 (row strides ldx, ldr, % 8 == 0), weight [K] bf16,
+ *   q [M,K] codes and s_a [M] as in i8_layernorm_quant_act_pertoken,
+ *   h [M,K] bf16 or NULL (row stride ldh, % 8 == 0); h may be residual or x
+ *   (in place, with the same stride).  K % 16 == 0, K <= 32768.             */
+i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x_bf16, int64_t M, int64_t K,
+                                            int64_t ldx, const void* residual_bf16,
+                                            int64_t ldr, const void* weight_bf16, float eps,
+                                            int fmt, void* q, int64_t ldq, float* s_a,
+                                            void* h_bf16, int64_t ldh, i8_stream_t stream);
+
+/* One step's block tables, offsets, slots and positions from the requests'
+ * lengths.  Request r holds context_lens[r] tokens in the first
+ * ceil(context / block_size) columns of its row of block_tables and brings
+ * new_lens[r] tokens; the blocks it lacks are taken from free_blocks in
+ * request order, from entry *taken on (NULL: 0), and written into its row.
+ *   block_tables [requests, width] int32, row stride ld_table; only the fresh
+ *                columns are written
+ *   cu_new [requests + 1]  exclusive sums of new_lens
+ *   seq_lens [requests]    context + new
+ *   slots [max_tokens]     int64, block * block_size + offset of the step's
+ *                          tokens in request order; -1 past their number and
+ *                          for tokens without a block
+ *   positions [max_tokens] position of each token in its request; 0 past them
+ *   counts [3]             tokens; entries of free_blocks in use after the
+ *                          step; tokens that got no block because the free
+ *                          list or the table's width ran out
+ * Negative lengths count as 0.  requests <= 16384, block_size <= 1024; the
+ * tables, free list and outputs do not overlap (taken and counts neither).  */
+i8_status i8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens,
+                                int64_t requests, int32_t* block_tables, int64_t width,
+                                int64_t ld_table, const int32_t* free_blocks, int64_t n_free,
+                                const int32_t* taken, int64_t block_size, int64_t max_tokens,
+                                int32_t* cu_new, int32_t* seq_lens, int64_t* slots,
+                                int32_t* positions, int32_t* counts, i8_stream_t stream);
+
+/* A paged cache of keys and values in 8 bits, one scale for each block of
+ * tokens and head: value = code * scale. */
+typedef struct {
+  void* k;            /* codes [blocks, kv_heads, block_size, head_dim], 16-byte aligned */
+  void* v;            /* the same of the values */
+  float* k_scale;     /* [blocks, kv_heads] */
+  float* v_scale;
+  int64_t blocks;
+  int32_t block_size; /* tokens a block: % 16 == 0, <= 1024 */
+  int32_t kv_heads;
+  int32_t head_dim;   /* 64, 128 or 256 */
+  int32_t fmt;        /* I8_CODES_INT8 or I8_CODES_E4M3 */
+} i8_kv_cache;
+
+/* Appends the step's keys and values to the cache.
+ *   k, v [tokens, kv_heads, head_dim] bf16: element strides between tokens
+ *   and between heads (% 8 == 0), head_dim contiguous
+ *   slots [tokens] int64 as i8_build_block_tables writes them; negative: the
+ *   token is skipped.  A block's tokens come in order, with none of another
+ *   block between them.
+ * A block's new tokens start at some offset; the tokens before it are older
+ * ones.  Per block and head, with L = 127 or 448:
+ *   s = max(older tokens' scale, max|new| / L);
+ *   where s grew, the older codes become round_half_even(code * (s_old / s));
+ *   the new ones are round_half_even(x / s).
+ * A block that is begun at offset 0 starts over with max|new| / L.          */
+i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_head,
+                             const void* v_bf16, int64_t ldv_token, int64_t ldv_head,
+                             const int64_t* slots, int64_t tokens, const i8_kv_cache* cache,
+                             i8_stream_t stream);
+
+/* Causal attention of the step's tokens over the cache (which holds them
+ * already): out = softmax(scale * q K^T) V per query head, query head h
+ * reading kv head h / (q_heads / kv_heads).  The new tokens of request r are
+ * rows cu_new[r] .. cu_new[r + 1] of q, the last ones of its seq_lens[r]
+ * tokens; each sees the positions up to its own.  A row that sees nothing
+ * (a request whose seq_len is less than its count of new tokens) gives 0, and
+ * -inf in lse.
+ *   q, out [tokens, q_heads, head_dim] bf16, element strides between tokens
+ *   and heads (% 8 == 0); lse [tokens, q_heads] fp32 or NULL: the natural log
+ *   of the sum of exponentials
+ *   max_new: no request brings more new tokens than this
+ *   ws / ws_bytes: at least i8_paged_attention_workspace_bytes()
+ * Rows of q that belong to no request are not written.                      */
+size_t i8_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          int64_t max_new);
+i8_status i8_paged_attention(const void* q_bf16, int64_t ldq_token, int64_t ldq_head,
+                             int64_t tokens, int64_t q_heads, const i8_kv_cache* cache,
+                             const int32_t* block_tables, int64_t width, int64_t ld_table,
+                             const int32_t* seq_lens, const int32_t* cu_new, int64_t requests,
+                             int64_t max_new, float scale, void* out_bf16, int64_t ldo_token,
+                             int64_t ldo_head, float* lse, void* ws, size_t ws_bytes,
+                             i8_stream_t stream);
+
 /* i8_gemm_dequant_bias_bf16 for callers that cannot allocate device memory
  * at call time -- for example a plugin running inside another runtime that
  * offers no workspace hook, an application whose device memory is all owned
@@ -444,8 +553,9 @@ i8_status i8_plan_query(int64_t M, int64_t N, int64_t K, i8_route route, int sms
 i8_status i8_selftest_timeout(int limit_ms, i8_stream_t stream);
 
 /* Waits for `stream`, then reads and clears the current device's status
- * word: I8_ERR_DEVICE_TIMEOUT if any kernel of this library timed out since
- * the last check, I8_ERR_CUDA on a CUDA error, else I8_OK. */
+ * words: I8_ERR_DEVICE_TIMEOUT if any kernel of this library timed out since
+ * the last check, I8_ERR_DEVICE_DATA if one met data out of range,
+ * I8_ERR_CUDA on a CUDA error, else I8_OK. */
 i8_status i8_sync_check(i8_stream_t stream);
 
 #ifdef __cplusplus

@@ -22,7 +22,7 @@ _lib = None
 
 STATUS = {
     0: "I8_OK", 1: "I8_ERR_INVALID_ARG", 2: "I8_ERR_ALIGNMENT", 3: "I8_ERR_UNSUPPORTED",
-    4: "I8_ERR_WORKSPACE", 5: "I8_ERR_CUDA", 6: "I8_ERR_DEVICE_TIMEOUT",
+    4: "I8_ERR_WORKSPACE", 5: "I8_ERR_CUDA", 6: "I8_ERR_DEVICE_TIMEOUT", 7: "I8_ERR_DEVICE_DATA",
 }
 OPTIONS = {"chunk_k": 1, "force_splits": 2, "max_ctas": 3, "tile_n": 4, "quant_vpl": 5, "cta_pair": 6,
            "skinny_max_m": 7, "pdl": 8, "quant_rows": 9, "stream_k": 10, "nvtx": 11,
@@ -43,6 +43,14 @@ class PlanInfo(ctypes.Structure):
                 ("n_fastest", ctypes.c_int32), ("ws_bytes", ctypes.c_int64),
                 ("model_us", ctypes.c_double), ("sk_waves", ctypes.c_int32),
                 ("sk_pairs", ctypes.c_int32)]
+
+
+class KVCacheInfo(ctypes.Structure):
+    """i8_kv_cache of include/i8.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("blocks", ctypes.c_int64),
+                ("block_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
 class I8Error(RuntimeError):
@@ -102,6 +110,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                  vp, i64, vp, vp, i64, vp], st),
             "i8_gelu_quant_act_pertoken": ([vp, i64, i64, i64, ctypes.c_int, vp, i64, vp, vp, i64,
                                             vp], st),
+            "i8_add_rmsnorm_quant_act_pertoken": ([vp, i64, i64, i64, vp, i64, vp, ctypes.c_float,
+                                                   ctypes.c_int, vp, i64, vp, vp, i64, vp], st),
+            "i8_build_block_tables": ([vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp,
+                                       vp, vp, vp, vp], st),
+            "i8_kv_cache_append": ([vp, i64, i64, vp, i64, i64, vp, i64,
+                                    ctypes.POINTER(KVCacheInfo), vp], st),
+            "i8_paged_attention_workspace_bytes": ([i64, i64, i64, i64], sz),
+            "i8_paged_attention": ([vp, i64, i64, i64, i64, ctypes.POINTER(KVCacheInfo), vp, i64,
+                                    i64, vp, vp, i64, i64, ctypes.c_float, vp, i64, i64, vp, vp,
+                                    sz, vp], st),
             "i8_sync_check": ([vp], st),
             "i8_selftest_timeout": ([ctypes.c_int, vp], st),
             "i8_plan_query": ([i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,

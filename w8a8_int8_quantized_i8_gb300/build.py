@@ -2,9 +2,10 @@
 and beside it libi8probe.so, a measurement helper for the benchmark (the
 legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path).
 
-One translation unit each, one ``-gencode`` target (sm_103a), no cmake; the
-two compile in parallel.  The outputs are git-ignored and rebuilt whenever a
-source is newer than them.
+libi8.so is two translation units (the linear layer, the serving operators),
+the probe one; one ``-gencode`` target (sm_103a), no cmake; all three compile
+in parallel.  The outputs are git-ignored and rebuilt whenever a source is
+newer than them.
 """
 from __future__ import annotations
 
@@ -17,7 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libi8.so")
-MAIN = os.path.join(CSRC, "i8_api.cu")
+UNITS = [os.path.join(CSRC, "i8_api.cu"), os.path.join(CSRC, "serving_api.cu")]
 PROBE_LIB = os.path.join(PKG, "libi8probe.so")
 PROBE_SRC = os.path.join(CSRC, "engine_probe.cu")
 
@@ -27,7 +28,7 @@ NVCC_FLAGS = [
     # IEEE fp32 behaviour (nvcc's defaults, stated so no flag set can drop
     # them): no flush to zero, correctly rounded division and square root
     "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -41,7 +42,7 @@ def nvcc() -> str:
 
 def _sources():
     return ([s for s in glob.glob(os.path.join(CSRC, "*.cu")) if s != PROBE_SRC]
-            + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "i8.h")])
+            + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "i8.h")])
 
 
 def _stale(lib, sources) -> bool:
@@ -57,19 +58,35 @@ def stale() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libi8.so and libi8probe.so if missing or older than their sources."""
+    targets = []
+    if force or _stale(LIB, _sources()):
+        targets.append((LIB, UNITS))
+    if force or _stale(PROBE_LIB, [PROBE_SRC]):
+        targets.append((PROBE_LIB, [PROBE_SRC]))
+
+    def start(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        return subprocess.Popen(cmd)
+
     jobs = []
-    for lib, src, sources in ((LIB, MAIN, _sources()), (PROBE_LIB, PROBE_SRC, [PROBE_SRC])):
-        if force or _stale(lib, sources):
-            tmp = lib + f".tmp{os.getpid()}"
-            cmd = [nvcc(), *NVCC_FLAGS, "-o", tmp, src]
-            if verbose:
-                print(" ".join(cmd))
-            jobs.append((subprocess.Popen(cmd), tmp, lib))
-    failed = [lib for proc, _, lib in jobs if proc.wait() != 0]
+    for lib, units in targets:
+        objects = [f"{lib}.{os.path.basename(u)}.tmp{os.getpid()}.o" for u in units]
+        jobs.append((lib, objects, [start([nvcc(), *NVCC_FLAGS, "-c", "-o", o, u])
+                                    for o, u in zip(objects, units)]))
+    failed = []
+    for lib, objects, procs in jobs:
+        ok = all([p.wait() == 0 for p in procs])
+        tmp = f"{lib}.tmp{os.getpid()}"
+        if ok and start([nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objects]).wait() == 0:
+            os.replace(tmp, lib)
+        else:
+            failed.append(os.path.basename(lib))
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     if failed:
-        raise RuntimeError(f"nvcc failed building {', '.join(os.path.basename(f) for f in failed)}")
-    for _, tmp, lib in jobs:
-        os.replace(tmp, lib)
+        raise RuntimeError(f"nvcc failed building {', '.join(failed)}")
     return LIB
 
 

@@ -1,0 +1,193 @@
+// block_tables.cuh -- block tables, slot map, positions and offsets of one
+// serving step, from the requests' lengths, on the device.
+//
+// Request r holds context[r] tokens in ceil(context[r] / B) blocks and brings
+// news[r] new ones.  With exclusive sums over the requests,
+//   cu_new[r]    = sum of news before r
+//   first[r]     = taken + sum of fresh blocks before r,
+//   fresh[r]     = ceil((context + news) / B) - ceil(context / B),
+// the request's fresh block c (counted from its first) is
+// free_blocks[first[r] + c], and the new token at position p gets the slot
+// table[r][p / B] * B + p % B.
+//
+// The work is a few bytes a token: a launch's latency bounds it.  So it is one
+// launch without a grid-wide wait: every CTA scans all requests by itself (two
+// loads a request, from L2) into shared memory, then writes its share of the
+// tokens and of the tables.  A fresh block is taken from the free list, not
+// from the table that another CTA may still be writing.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace i8 {
+
+constexpr int kTableThreads = 512;
+constexpr int kTableMaxRequests = 16384;  // two words a request in shared memory: 128 KB
+constexpr int kTableTokensPerThread = 4;
+
+struct TableArgs {
+  const int32_t* context;
+  const int32_t* news;
+  int32_t* table;
+  const int32_t* free_blocks;
+  const int32_t* taken;
+  int32_t* cu_new;
+  int32_t* seq_lens;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* counts;
+  int64_t ld_table;
+  int64_t n_free;
+  int64_t max_tokens;
+  int32_t requests;
+  int32_t width;
+  int32_t block;
+};
+
+__device__ __forceinline__ int32_t saturate_i32(int64_t v) {
+  return static_cast<int32_t>(v > INT32_MAX ? INT32_MAX : v);
+}
+
+// Exclusive sums of (a, b) over the CTA; the totals come back in ta, tb.
+__device__ __forceinline__ void scan_pair(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb,
+                                          int64_t (*sm)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t a0 = a, b0 = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, a, o);
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, b, o);
+    if (lane >= o) {
+      a += x;
+      b += y;
+    }
+  }
+  __syncthreads();  // the previous round's sums have been read
+  if (lane == 31) {
+    sm[warp][0] = a;
+    sm[warp][1] = b;
+  }
+  __syncthreads();
+  int64_t pa = 0, pb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int w = 0; w < kTableThreads / 32; ++w) {
+    if (w < warp) {
+      pa += sm[w][0];
+      pb += sm[w][1];
+    }
+    ta += sm[w][0];
+    tb += sm[w][1];
+  }
+  a += pa - a0;
+  b += pb - b0;
+}
+
+__global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const TableArgs p) {
+  extern __shared__ int32_t sm_dyn[];
+  __shared__ int64_t sm_scan[kTableThreads / 32][2];
+  __shared__ int sm_lost;
+  int32_t* cu = sm_dyn;                    // [requests + 1]
+  int32_t* first = sm_dyn + p.requests + 1;  // [requests]: free-list index of column 0, were it fresh
+  const int tid = threadIdx.x;
+  if (tid == 0) sm_lost = 0;
+
+  pdl_wait();
+  const int64_t taken = p.taken ? max(0, *p.taken) : 0;
+  int64_t base_t = 0, base_b = taken;
+  for (int r0 = 0; r0 < p.requests; r0 += kTableThreads) {
+    const int r = r0 + tid;
+    int64_t ctx = 0, nw = 0;
+    if (r < p.requests) {
+      ctx = max(0, p.context[r]);
+      nw = max(0, p.news[r]);
+    }
+    const int64_t held = min((ctx + p.block - 1) / p.block, static_cast<int64_t>(p.width));
+    const int64_t need = min((ctx + nw + p.block - 1) / p.block, static_cast<int64_t>(p.width));
+    int64_t t = nw, b = need - held, tt, tb;
+    scan_pair(t, b, tt, tb, sm_scan);
+    if (r < p.requests) {
+      cu[r] = saturate_i32(base_t + t);
+      // clamped to the free list's end: beyond it every index is out of blocks
+      first[r] = static_cast<int32_t>(min(base_b + b, p.n_free) - held);
+      if (blockIdx.x == 0) {
+        p.cu_new[r] = saturate_i32(base_t + t);
+        p.seq_lens[r] = saturate_i32(ctx + nw);
+        const int64_t have = held + min(need - held, max(static_cast<int64_t>(0), p.n_free - base_b - b));
+        const int64_t lost = ctx + nw - max(ctx, min(ctx + nw, have * p.block));
+        if (lost > 0) atomicAdd(&sm_lost, saturate_i32(lost));
+      }
+    }
+    base_t += tt;
+    base_b += tb;
+  }
+  if (tid == 0) cu[p.requests] = saturate_i32(base_t);
+  __syncthreads();
+  pdl_trigger();
+  if (blockIdx.x == 0 && tid == 0) {
+    p.cu_new[p.requests] = saturate_i32(base_t);
+    p.counts[0] = saturate_i32(base_t);
+    p.counts[1] = saturate_i32(min(base_b, max(taken, p.n_free)));
+    p.counts[2] = sm_lost;
+  }
+
+  // the tables' fresh columns: a warp a request
+  const int lane = tid & 31;
+  const int warps = static_cast<int>(gridDim.x) * (kTableThreads / 32);
+  for (int r = blockIdx.x * (kTableThreads / 32) + (tid >> 5); r < p.requests; r += warps) {
+    const int64_t ctx = max(0, p.context[r]), nw = max(0, p.news[r]);
+    const int held = static_cast<int>(min((ctx + p.block - 1) / p.block, static_cast<int64_t>(p.width)));
+    const int need = static_cast<int>(min((ctx + nw + p.block - 1) / p.block, static_cast<int64_t>(p.width)));
+    for (int c = held + lane; c < need; c += 32) {
+      const int64_t at = static_cast<int64_t>(first[r]) + c;
+      p.table[r * p.ld_table + c] = at < p.n_free ? p.free_blocks[at] : -1;
+    }
+  }
+
+  // the tokens: a few consecutive ones a thread, one search for the first
+  const int total = cu[p.requests];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTableThreads * kTableTokensPerThread;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kTableThreads + tid) * kTableTokensPerThread;
+       t0 < p.max_tokens; t0 += stride) {
+    int r = 0;
+    if (t0 < total) {
+      int lo = 0, hi = p.requests;  // the last request with cu[r] <= t0 and tokens of its own
+      for (int step = 0; step < 32 && hi - lo > 1; ++step) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t0) lo = mid;
+        else hi = mid;
+      }
+      r = lo;
+    }
+#pragma unroll
+    for (int j = 0; j < kTableTokensPerThread; ++j) {
+      const int64_t t = t0 + j;
+      if (t >= p.max_tokens) break;
+      int64_t slot = -1;
+      int pos = 0;
+      if (t < total) {
+        for (int skip = 0; skip < p.requests && cu[r + 1] <= t; ++skip) ++r;  // empty requests
+        const int64_t ctx = max(0, p.context[r]);
+        const int64_t at = ctx + t - cu[r];
+        pos = saturate_i32(at);
+        const int64_t c = at / p.block;
+        if (c < p.width) {
+          const int64_t held = (ctx + p.block - 1) / p.block;
+          int64_t blk;
+          if (c < held) {
+            blk = p.table[r * p.ld_table + c];
+          } else {
+            const int64_t f = first[r] + c;
+            blk = f < p.n_free ? p.free_blocks[f] : -1;
+          }
+          if (blk >= 0) slot = blk * p.block + at % p.block;
+        }
+      }
+      p.slots[t] = slot;
+      p.positions[t] = pos;
+    }
+  }
+}
+
+}  // namespace i8

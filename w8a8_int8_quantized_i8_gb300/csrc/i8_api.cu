@@ -1,9 +1,9 @@
 // i8_api.cu -- the C ABI of libi8 (declared in include/i8.h): argument
 // validation, the shape -> kernel-configuration table, TMA descriptors and
-// the launches.  The whole library is this one translation unit.
+// the launches of the linear layer.  The serving operators' half of the ABI
+// is serving_api.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
 #include <cstdlib>
@@ -17,12 +17,15 @@
 #include "gemm.cuh"
 #include "gemm_direct.cuh"
 #include "gemm_pair.cuh"
+#include "host.h"
 #include "producer.cuh"
 #include "skinny.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
 namespace i8 {
+
+Options g_opt;  // process-wide tuning knobs (host.h)
 
 // ----------------------------------------------------------------- widen
 // int8 codes -> fp16 codes (exact); 16 codes per thread per step.
@@ -60,36 +63,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// Process-wide tuning knobs (i8_set_option).
-struct Options {
-  int chunk_k = 1024;      // K per exact fp32 chunk (multiple of 64, <= 1024)
-  int force_splits = 0;    // 0 = table
-  int max_ctas = 0;        // 0 = all SMs
-  int force_bn = 0;        // 0 = table, else 128 or 256
-  int quant_vpl = 6;       // max 16-byte vectors per lane in the quantizer
-  int cta_pair = 0;        // 0 = table, 1 = never, 2 = whenever the shape allows
-  int skinny_max_m = 16;   // token counts up to this use the weight-streaming kernel (0 = off)
-  int pdl = 1;             // launch with programmatic stream serialization
-  int quant_rows = 0;      // quantizer rows per CTA (0 = by shape)
-  int stream_k = 1;        // CTA-pair stream-K: 0 never, 1 by the table, 2 whenever pairs idle
-  int nvtx = 0;            // NVTX range around every ABI call
-  int pair_stage_k = 0;    // K per fp16 stage of the int8-code pair kernel: 0 (table) / 64 / 128
-  int raster = 0;          // tile order: 0 table, 1 M blocks fastest, 2 N blocks fastest
-};
-Options g_opt;
-
-// NVTX range for the lifetime of one ABI call (when I8_OPT_NVTX is on).
-struct NvtxScope {
-  bool on;
-  explicit NvtxScope(const char* name) : on(g_opt.nvtx != 0) {
-    if (on) nvtxRangePushA(name);
-  }
-  ~NvtxScope() {
-    if (on) nvtxRangePop();
-  }
-};
-#define I8_NVTX() NvtxScope i8_nvtx_scope_(__func__)
-
 struct DeviceInfo {
   bool init = false;
   int sms = 0;
@@ -105,8 +78,6 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
-
-i8_status cuda_status(cudaError_t e) { return e == cudaSuccess ? I8_OK : I8_ERR_CUDA; }
 
 i8_status device_info(DeviceInfo** out, int* dev_out) {
   int dev = 0;
@@ -136,29 +107,6 @@ i8_status device_info(DeviceInfo** out, int* dev_out) {
   if (dev_out) *dev_out = dev;
   return I8_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Launch with programmatic stream serialization (unless switched off): the
-// kernel may be scheduled while the previous kernel of the stream drains.
-// Every kernel launched this way calls pdl_wait() before it touches global
-// memory, so the stream order of memory effects is unchanged.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = g_opt.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // ----------------------------------------------------------------- quant
 template <int V>
@@ -1185,6 +1133,7 @@ const char* i8_status_string(i8_status s) {
     case I8_ERR_WORKSPACE: return "I8_ERR_WORKSPACE";
     case I8_ERR_CUDA: return "I8_ERR_CUDA";
     case I8_ERR_DEVICE_TIMEOUT: return "I8_ERR_DEVICE_TIMEOUT";
+    case I8_ERR_DEVICE_DATA: return "I8_ERR_DEVICE_DATA";
   }
   return "I8_ERR_UNKNOWN";
 }
@@ -1572,10 +1521,13 @@ i8_status i8_sync_check(i8_stream_t stream) {
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return I8_ERR_CUDA;
-    if (word & (1u << I8_ERR_DEVICE_TIMEOUT)) return I8_ERR_DEVICE_TIMEOUT;
-    return I8_ERR_CUDA;
   }
-  return I8_OK;
+  unsigned int serving = 0;
+  if (take_serving_status(&serving) != cudaSuccess) return I8_ERR_CUDA;
+  word |= serving;
+  if (word & (1u << I8_ERR_DEVICE_TIMEOUT)) return I8_ERR_DEVICE_TIMEOUT;
+  if (word & (1u << I8_ERR_DEVICE_DATA)) return I8_ERR_DEVICE_DATA;
+  return word == 0 ? I8_OK : I8_ERR_CUDA;
 }
 
 }  // extern "C"

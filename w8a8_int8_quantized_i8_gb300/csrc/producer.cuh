@@ -35,16 +35,6 @@ namespace i8 {
 
 enum ProducerOp : int { kOpLayerNorm = 0, kOpGelu = 1 };
 
-// The two bf16 halves of a word as fp32 (exact widening).
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// Two fp32 values -> two bf16 (round to nearest even), lo in the low half.
-__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-
 // GELU in erf form, x * Phi(x) with Phi the standard normal CDF.  With
 // t = erfc(|x| / sqrt 2): Phi(x) = 1 - t / 2 for x >= 0 and t / 2 for x < 0.
 // One erfc per element, the same call on every lane (no divergent branch),

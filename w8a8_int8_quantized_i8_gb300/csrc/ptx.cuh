@@ -10,9 +10,9 @@
 namespace i8 {
 
 // Per-device status word: bit (1 << c) is set when a kernel records status
-// code c (an i8_status value); i8_sync_check() reads and clears it.  The
-// library is built as a single translation unit, so this is its definition.
-__device__ unsigned int g_status = 0;
+// code c (an i8_status value); i8_sync_check() reads and clears it.  Each of
+// the library's translation units has a word of its own.
+static __device__ unsigned int g_status = 0;
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 

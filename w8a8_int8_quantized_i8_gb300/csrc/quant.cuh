@@ -25,6 +25,8 @@
 //     |t| <= 127.x, ties to even); the low byte of that sum's bit pattern is
 //     the two's-complement int8 code.
 #pragma once
+#include <cuda_bf16.h>
+
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -66,6 +68,16 @@ __device__ __forceinline__ unsigned long long f2_sub(unsigned long long a, unsig
   unsigned long long d;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// The two bf16 halves of a word as fp32 (exact widening).
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two fp32 values -> two bf16 (round to nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
 }
 
 // Low bytes of four fp32 bit patterns -> one word (first pattern in byte 0).

@@ -1,0 +1,163 @@
+// rmsnorm.cuh -- the residual's addition, the root-mean-square norm with a
+// gain, and the per-token quantizer of its output, in one pass over a row.
+//
+// For a row of x, a residual r and a gain w, all bf16:
+//   h = x + r                      (stored as the new residual, bf16)
+//   y = h * rstd * w,  rstd = 1 / sqrt(mean(h^2) + eps)
+//   scale = max|y| / L,  code = rne(y / scale),  L = 127 (int8) or 448 (E4M3)
+// rstd is one number for the row, so it cancels in y / scale.  With t = h * w:
+//   code = rne(t / s_t),  s_t = max|t| / L,  scale = s_t * rstd.
+// The sum of squares and max|t| therefore come out of the same reduction, one
+// barrier a row, and the codes do not depend on the order in which the squares
+// are summed.  h and t are fp32 (h is rounded to bf16 only where it is stored;
+// the norm uses the unrounded sum), and the row is never rounded to bf16
+// between the norm and the quantizer: one rounding, to the 8-bit code.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace i8 {
+
+// 8 fp32 -> 8 int8 codes, rne(fl(t / s)): t * fl(1/s) is within 2^-15 of
+// fl(t / s), so only a value within 2^-14 of a tie needs the IEEE division
+// (quant.cuh has the bound; it does not depend on t being a bf16 value).
+__device__ __forceinline__ uint2 quant_f32x8(const float (&t)[8], float s, float r, bool fast) {
+  uint32_t b[8];
+  float dmax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = __fmul_rn(t[i], r);
+    const float y = __fadd_rn(q, kRoundMagic);
+    dmax = fmaxf(dmax, fabsf(__fsub_rn(q, __fsub_rn(y, kRoundMagic))));
+    b[i] = __float_as_uint(y);
+  }
+  if (!fast || !(dmax <= kNearTie)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = quant_exact(t[i], s);
+  }
+  return make_uint2(low_bytes4(b[0], b[1], b[2], b[3]), low_bytes4(b[4], b[5], b[6], b[7]));
+}
+
+// 8 fp32 -> 8 E4M3 codes of fl(t / s).  q = t * fl(1/s) is within 3 units in
+// the last place of fl(t / s).  E4M3 keeps 3 of the 23 mantissa bits, so both
+// round alike unless the 20 dropped bits of q lie within 4 of one half; below
+// 2^-6 (E4M3's subnormals, another spacing) the division decides as well.
+__device__ __forceinline__ uint2 quant_f32x8_e4m3(const float (&t)[8], float s, float r,
+                                                  bool fast) {
+  float q[8];
+  bool sure = fast;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = __fmul_rn(t[i], r);
+    const uint32_t u = __float_as_uint(q[i]);
+    const bool tie = ((u & 0xFFFFFu) - (0x80000u - 4u)) <= 8u;
+    sure = sure && !tie && (fabsf(q[i]) >= 0x1p-6f || t[i] == 0.0f);
+  }
+  if (!sure) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(t[i], s);
+  }
+  return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16),
+                    e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
+}
+
+// One row per CTA of G warps, V 16-byte vectors a lane in registers.
+template <int V, int FMT>
+__global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(
+    const uint16_t* __restrict__ x, int K, int64_t ldx, const uint16_t* __restrict__ res,
+    int64_t ldr, const uint16_t* __restrict__ weight, float eps, int8_t* __restrict__ q,
+    int64_t ldq, float* __restrict__ scale, uint16_t* __restrict__ h_out, int64_t ldh, int G) {
+  __shared__ float red_s[16];
+  __shared__ uint32_t red_m[16];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x;
+  const int slice0 = warp * (32 * 8 * V);
+  const uint16_t* xr = x + row * ldx;
+  const uint16_t* rr = res ? res + row * ldr : nullptr;
+
+  pdl_wait();
+  uint4 v[V], u[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = slice0 + (i * 32 + lane) * 8;
+    v[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
+    // the residual may be updated in place (h_out == res), so its loads are
+    // ordinary ones; each thread reads the elements that it writes
+    if (e < K) {
+      v[i] = *reinterpret_cast<const uint4*>(xr + e);
+      if (rr) u[i] = *reinterpret_cast<const uint4*>(rr + e);
+    }
+  }
+  pdl_trigger();
+
+  float t[V][8];
+  float ss = 0.0f;
+  uint32_t amax = 0;  // bit patterns of |t| order like the values; a NaN wins
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = slice0 + (i * 32 + lane) * 8;
+    const uint32_t a[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    const uint32_t b[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    uint4 g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);  // ones
+    if (weight && e < K) g = __ldg(reinterpret_cast<const uint4*>(weight + e));
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float h0 = __fadd_rn(bf16_lo(a[j]), bf16_lo(b[j]));
+      const float h1 = __fadd_rn(bf16_hi(a[j]), bf16_hi(b[j]));
+      ss = fmaf(h0, h0, ss);
+      ss = fmaf(h1, h1, ss);
+      t[i][2 * j] = __fmul_rn(h0, bf16_lo(w[j]));
+      t[i][2 * j + 1] = __fmul_rn(h1, bf16_hi(w[j]));
+      amax = max(amax, max(__float_as_uint(fabsf(t[i][2 * j])), __float_as_uint(fabsf(t[i][2 * j + 1]))));
+      o[j] = pack_bf16x2_rn(h0, h1);
+    }
+    if (h_out && e < K)
+      *reinterpret_cast<uint4*>(h_out + row * ldh + e) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+  if (G > 1) {
+    if (lane == 0) {
+      red_s[warp] = ss;
+      red_m[warp] = amax;
+    }
+    __syncthreads();
+    ss = 0.0f;
+    amax = 0;
+    for (int j = 0; j < G; ++j) {
+      ss += red_s[j];
+      amax = max(amax, red_m[j]);
+    }
+  }
+  const float s = __fdiv_rn(__uint_as_float(amax), FMT == kQuantE4M3 ? 448.0f : 127.0f);
+  if (threadIdx.x == 0) {
+    const float mean = __fdiv_rn(ss, static_cast<float>(K));
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
+    scale[row] = amax == 0 ? 0.0f : __fmul_rn(s, rstd);
+  }
+  int8_t* qr = q + row * ldq * (FMT == kQuantF16 ? 2 : 1);
+  const bool fast = s >= 0x1p-126f;
+  const float r = __frcp_rn(s);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = slice0 + (i * 32 + lane) * 8;
+    if (e < K) {
+      uint2 c = make_uint2(0u, 0u);
+      if (amax != 0) {
+        if constexpr (FMT == kQuantE4M3) c = quant_f32x8_e4m3(t[i], s, r, fast);
+        else c = quant_f32x8(t[i], s, r, fast);
+      }
+      store_codes8<FMT>(qr, e, c);
+    }
+  }
+}
+
+}  // namespace i8

@@ -1,0 +1,298 @@
+// serving_api.cu -- the C ABI of the serving operators (declared in
+// include/i8.h): the norm with the residual's addition and an 8-bit output,
+// block tables, the 8-bit paged cache's append and the attention over it.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/i8.h"
+#include "block_tables.cuh"
+#include "host.h"
+#include "kv_append.cuh"
+#include "kv_attention.cuh"
+#include "ptx.cuh"
+#include "rmsnorm.cuh"
+
+namespace i8 {
+
+cudaError_t take_serving_status(unsigned int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_status, sizeof(*word));
+  if (e == cudaSuccess && *word != 0) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  }
+  return e;
+}
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+i8_status device_sms(int* sms) {
+  static int cached[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return I8_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cached[dev] == 0 &&
+      cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return I8_ERR_CUDA;
+  *sms = cached[dev];
+  return I8_OK;
+}
+
+// Shared memory beyond 48 KB, allowed once per kernel and device.
+template <auto KERN>
+i8_status allow_smem(size_t bytes) {
+  static bool done[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return I8_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  if (done[dev]) return I8_OK;
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes)) != cudaSuccess)
+    return I8_ERR_CUDA;
+  done[dev] = true;
+  return I8_OK;
+}
+
+// ----------------------------------------------------------------- norm
+struct NormArgs {
+  const uint16_t *x, *res, *weight;
+  uint16_t* h;
+  int8_t* q;
+  float* scale;
+  int64_t rows, ldx, ldr, ldq, ldh;
+  int K, G;
+  float eps;
+};
+
+template <int V>
+cudaError_t launch_norm_v(const NormArgs& a, int fmt, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.rows)), block(32 * a.G);
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, grid, block, 0, st, a.x, a.K, a.ldx, a.res, a.ldr, a.weight, a.eps, a.q,
+                      a.ldq, a.scale, a.h, a.ldh, a.G);
+  };
+  if (fmt == kQuantE4M3) return go(add_rmsnorm_quant_kernel<V, kQuantE4M3>);
+  if (fmt == kQuantF16) return go(add_rmsnorm_quant_kernel<V, kQuantF16>);
+  return go(add_rmsnorm_quant_kernel<V, kQuantInt8>);
+}
+
+// ----------------------------------------------------------------- cache checks
+i8_status check_cache(const i8_kv_cache* c) {
+  if (!c || c->blocks < 0 || c->block_size <= 0 || c->kv_heads <= 0 || c->head_dim <= 0)
+    return I8_ERR_INVALID_ARG;
+  if (c->fmt != I8_CODES_INT8 && c->fmt != I8_CODES_E4M3) return I8_ERR_INVALID_ARG;
+  if (c->blocks > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return I8_ERR_INVALID_ARG;
+  if (c->block_size % 16 != 0 || c->block_size > 1024 || c->blocks > INT32_MAX ||
+      c->kv_heads > 32767)
+    return I8_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return I8_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+    return I8_ERR_ALIGNMENT;
+  return I8_OK;
+}
+
+// ----------------------------------------------------------------- attention
+template <int D, bool E4M3, int NT>
+i8_status launch_attention(const AttnArgs& a, cudaStream_t st) {
+  const size_t smem = sizeof(float) * kAttnWarps * 8 * NT * D;
+  if (i8_status e = allow_smem<kv_attention_kernel<D, E4M3, NT>>(smem)) return e;
+  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
+  const int64_t tiles = (rows + 8 * NT - 1) / (8 * NT);
+  if (tiles * a.requests > INT32_MAX) return I8_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(tiles * a.requests), static_cast<unsigned>(a.kv_heads));
+  return cuda_status(launch_pdl(kv_attention_kernel<D, E4M3, NT>, grid, dim3(kAttnThreads), smem, st, a));
+}
+
+template <int D, bool E4M3>
+i8_status launch_attention_nt(const AttnArgs& a, cudaStream_t st) {
+  // a second column tile shares the decoded codes of the first, but at 256
+  // head dimensions its accumulators do not fit the registers
+  if (D == 256 || static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads) <= 8)
+    return launch_attention<D, E4M3, 1>(a, st);
+  return launch_attention<D, E4M3, D == 256 ? 1 : 2>(a, st);
+}
+
+}  // namespace
+}  // namespace i8
+
+using namespace i8;
+
+extern "C" {
+
+i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x, int64_t M, int64_t K, int64_t ldx,
+                                            const void* residual, int64_t ldr, const void* weight,
+                                            float eps, int fmt, void* q, int64_t ldq, float* s_a,
+                                            void* h, int64_t ldh, i8_stream_t stream) {
+  I8_NVTX();
+  if (M < 0 || K <= 0 || ldx < K || ldq < K || (residual && ldr < K) || (h && ldh < K))
+    return I8_ERR_INVALID_ARG;
+  if (fmt != kQuantInt8 && fmt != kQuantE4M3 && fmt != kQuantF16) return I8_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f && eps <= 3.0e38f)) return I8_ERR_INVALID_ARG;
+  if (M > 0 && (!x || !q || !s_a)) return I8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > 32768 || M > INT32_MAX) return I8_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(s_a) || ldx % 8 != 0 ||
+      ldq % (fmt == kQuantF16 ? 8 : 16) != 0 || !aligned16(residual) ||
+      (residual && ldr % 8 != 0) || !aligned16(weight) || !aligned16(h) || (h && ldh % 8 != 0))
+    return I8_ERR_ALIGNMENT;
+  if (M == 0) return I8_OK;
+  const int vecs = static_cast<int>(K / 8);
+  int G = 1;
+  while (G < 16 && (vecs + 32 * G - 1) / (32 * G) > 6) G *= 2;
+  const int need = (vecs + 32 * G - 1) / (32 * G);
+  const NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
+                   static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(h),
+                   static_cast<int8_t*>(q), s_a, M, ldx, ldr, ldq, ldh, static_cast<int>(K), G, eps};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (need <= 1) e = launch_norm_v<1>(a, fmt, st);
+  else if (need <= 2) e = launch_norm_v<2>(a, fmt, st);
+  else if (need <= 4) e = launch_norm_v<4>(a, fmt, st);
+  else if (need <= 6) e = launch_norm_v<6>(a, fmt, st);
+  else e = launch_norm_v<8>(a, fmt, st);
+  return cuda_status(e);
+}
+
+i8_status i8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens,
+                                int64_t requests, int32_t* block_tables, int64_t width,
+                                int64_t ld_table, const int32_t* free_blocks, int64_t n_free,
+                                const int32_t* taken, int64_t block_size, int64_t max_tokens,
+                                int32_t* cu_new, int32_t* seq_lens, int64_t* slots,
+                                int32_t* positions, int32_t* counts, i8_stream_t stream) {
+  I8_NVTX();
+  if (requests < 0 || width < 0 || ld_table < width || n_free < 0 || block_size <= 0 ||
+      max_tokens < 0)
+    return I8_ERR_INVALID_ARG;
+  if (!cu_new || !counts || (max_tokens > 0 && (!slots || !positions)) || (n_free > 0 && !free_blocks) ||
+      (requests > 0 && (!context_lens || !new_lens || !seq_lens || (width > 0 && !block_tables))))
+    return I8_ERR_INVALID_ARG;
+  if (requests > kTableMaxRequests || block_size > 1024 || width > INT32_MAX ||
+      n_free > INT32_MAX - width || max_tokens > INT32_MAX || width * block_size > INT32_MAX)
+    return I8_ERR_UNSUPPORTED;
+  if (!aligned4(context_lens) || !aligned4(new_lens) || !aligned4(block_tables) ||
+      !aligned4(free_blocks) || !aligned4(taken) || !aligned4(cu_new) || !aligned4(seq_lens) ||
+      !aligned8(slots) || !aligned4(positions) || !aligned4(counts))
+    return I8_ERR_ALIGNMENT;
+  TableArgs a{context_lens, new_lens, block_tables, free_blocks, taken, cu_new, seq_lens, slots,
+              positions, counts, ld_table, n_free, max_tokens, static_cast<int32_t>(requests),
+              static_cast<int32_t>(width), static_cast<int32_t>(block_size)};
+  int sms;
+  if (i8_status e = device_sms(&sms)) return e;
+  const size_t smem = sizeof(int32_t) * (2 * static_cast<size_t>(requests) + 1);
+  if (i8_status e = allow_smem<block_tables_kernel>(sizeof(int32_t) * (2 * kTableMaxRequests + 1)))
+    return e;
+  const int64_t per = kTableThreads * kTableTokensPerThread;
+  const int64_t grid = std::max<int64_t>(
+      1, std::min<int64_t>(sms, std::max((max_tokens + per - 1) / per, requests / (kTableThreads / 32))));
+  return cuda_status(launch_pdl(block_tables_kernel, dim3(static_cast<unsigned>(grid)),
+                                dim3(kTableThreads), smem, reinterpret_cast<cudaStream_t>(stream), a));
+}
+
+i8_status i8_kv_cache_append(const void* k, int64_t ldk_token, int64_t ldk_head, const void* v,
+                             int64_t ldv_token, int64_t ldv_head, const int64_t* slots,
+                             int64_t tokens, const i8_kv_cache* cache, i8_stream_t stream) {
+  I8_NVTX();
+  if (i8_status e = check_cache(cache)) return e;
+  if (tokens < 0 || (tokens > 0 && (!k || !v || !slots))) return I8_ERR_INVALID_ARG;
+  if (ldk_token < 0 || ldk_head < 0 || ldv_token < 0 || ldv_head < 0) return I8_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX) return I8_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || ldk_token % 8 != 0 ||
+      ldk_head % 8 != 0 || ldv_token % 8 != 0 || ldv_head % 8 != 0)
+    return I8_ERR_ALIGNMENT;
+  if (tokens == 0 || cache->blocks == 0) return I8_OK;
+  int sms;
+  if (i8_status e = device_sms(&sms)) return e;
+  AppendArgs a;
+  a.k = {static_cast<const uint16_t*>(k), ldk_token, ldk_head, static_cast<uint8_t*>(cache->k),
+         cache->k_scale};
+  a.v = {static_cast<const uint16_t*>(v), ldv_token, ldv_head, static_cast<uint8_t*>(cache->v),
+         cache->v_scale};
+  a.slots = slots;
+  a.tokens = tokens;
+  a.blocks = cache->blocks;
+  a.heads = cache->kv_heads;
+  a.block = cache->block_size;
+  a.dim = cache->head_dim;
+  const int64_t units = tokens * 2 * cache->kv_heads;
+  a.window = static_cast<int32_t>(std::min<int64_t>(
+      kAppendMaxWindow, std::max<int64_t>(kAppendThreads / 32, units / (static_cast<int64_t>(sms) * 16))));
+  const dim3 grid(static_cast<unsigned>((tokens + a.window - 1) / a.window),
+                  static_cast<unsigned>(2 * cache->kv_heads));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(cache->fmt == I8_CODES_E4M3
+                         ? launch_pdl(kv_append_kernel<true>, grid, dim3(kAppendThreads), 0, st, a)
+                         : launch_pdl(kv_append_kernel<false>, grid, dim3(kAppendThreads), 0, st, a));
+}
+
+size_t i8_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          int64_t max_new) {
+  (void)q_heads, (void)kv_heads, (void)head_dim, (void)max_new;
+  return 0;
+}
+
+i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head, int64_t tokens,
+                             int64_t q_heads, const i8_kv_cache* cache,
+                             const int32_t* block_tables, int64_t width, int64_t ld_table,
+                             const int32_t* seq_lens, const int32_t* cu_new, int64_t requests,
+                             int64_t max_new, float scale, void* out, int64_t ldo_token,
+                             int64_t ldo_head, float* lse, void* ws, size_t ws_bytes,
+                             i8_stream_t stream) {
+  I8_NVTX();
+  (void)ws, (void)ws_bytes;
+  if (i8_status e = check_cache(cache)) return e;
+  if (tokens < 0 || requests < 0 || width < 0 || ld_table < width || max_new < 0 || q_heads <= 0 ||
+      q_heads % cache->kv_heads != 0)
+    return I8_ERR_INVALID_ARG;
+  if (ldq_token < 0 || ldq_head < 0 || ldo_token < 0 || ldo_head < 0) return I8_ERR_INVALID_ARG;
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return I8_ERR_INVALID_ARG;
+  if (tokens > 0 && requests > 0 &&
+      (!q || !out || !seq_lens || !cu_new || (width > 0 && !block_tables)))
+    return I8_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX || requests > INT32_MAX || q_heads > 65535 ||
+      width * cache->block_size > INT32_MAX - 1024)
+    return I8_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || ldq_token % 8 != 0 || ldq_head % 8 != 0 ||
+      ldo_token % 8 != 0 || ldo_head % 8 != 0 || !aligned4(block_tables) || !aligned4(seq_lens) ||
+      !aligned4(cu_new) || !aligned4(lse))
+    return I8_ERR_ALIGNMENT;
+  if (tokens == 0 || requests == 0 || max_new == 0) return I8_OK;
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq_token = ldq_token;
+  a.ldq_head = ldq_head;
+  a.k = static_cast<const uint8_t*>(cache->k);
+  a.v = static_cast<const uint8_t*>(cache->v);
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.table = block_tables;
+  a.ld_table = ld_table;
+  a.seq_lens = seq_lens;
+  a.cu_new = cu_new;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo_token = ldo_token;
+  a.ldo_head = ldo_head;
+  a.lse = lse;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.tokens = tokens;
+  a.blocks = cache->blocks;
+  a.requests = static_cast<int32_t>(requests);
+  a.width = static_cast<int32_t>(width);
+  a.block = cache->block_size;
+  a.q_heads = static_cast<int32_t>(q_heads);
+  a.kv_heads = cache->kv_heads;
+  a.max_new = static_cast<int32_t>(std::min(max_new, tokens));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->fmt == I8_CODES_E4M3;
+  switch (cache->head_dim) {
+    case 64: return e4m3 ? launch_attention_nt<64, true>(a, st) : launch_attention_nt<64, false>(a, st);
+    case 128: return e4m3 ? launch_attention_nt<128, true>(a, st) : launch_attention_nt<128, false>(a, st);
+    default: return e4m3 ? launch_attention_nt<256, true>(a, st) : launch_attention_nt<256, false>(a, st);
+  }
+}
+
+}  // extern "C"
