@@ -352,10 +352,12 @@ i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_
  *   and heads (% 8 == 0); lse [tokens, q_heads] fp32 or NULL: the natural log
  *   of the sum of exponentials
  *   max_new: no request brings more new tokens than this
- *   ws / ws_bytes: at least i8_paged_attention_workspace_bytes()
+ *   ws / ws_bytes: 16-byte aligned, at least
+ *   i8_paged_attention_workspace_bytes(); calls that may overlap in time do
+ *   not share one
  * Rows of q that belong to no request are not written.                      */
 size_t i8_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                                          int64_t max_new);
+                                          int fmt, int64_t max_new);
 i8_status i8_paged_attention(const void* q_bf16, int64_t ldq_token, int64_t ldq_head,
                              int64_t tokens, int64_t q_heads, const i8_kv_cache* cache,
                              const int32_t* block_tables, int64_t width, int64_t ld_table,

@@ -116,7 +116,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                        vp, vp, vp, vp], st),
             "i8_kv_cache_append": ([vp, i64, i64, vp, i64, i64, vp, i64,
                                     ctypes.POINTER(KVCacheInfo), vp], st),
-            "i8_paged_attention_workspace_bytes": ([i64, i64, i64, i64], sz),
+            "i8_paged_attention_workspace_bytes": ([i64, i64, i64, ctypes.c_int, i64], sz),
             "i8_paged_attention": ([vp, i64, i64, i64, i64, ctypes.POINTER(KVCacheInfo), vp, i64,
                                     i64, vp, vp, i64, i64, ctypes.c_float, vp, i64, i64, vp, vp,
                                     sz, vp], st),

@@ -41,9 +41,21 @@
 
 namespace i8 {
 
+// How the work is split.  An item is a request's row tile (8 * NT rows) of one
+// kv head; its tokens come in units of 128.  The units of all items, request
+// after request, are one line that the resident CTAs cut into equal shares, so
+// ragged lengths balance and one long context fills the GPU.  Nobody but the
+// device knows the lengths: every CTA adds up the requests' units by itself
+// (two loads a request).  A CTA that covers an item whole writes its rows; the
+// pieces of an item that is cut go to the workspace (two slots a CTA: an item
+// begun before its share, an item that goes on after it), and a second, small
+// kernel joins them in the order of the tokens, so results do not depend on
+// timing.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnTile = 32;  // tokens a warp takes at a time (two halves of 16)
+constexpr int kAttnUnit = kAttnTile * kAttnWarps;
+constexpr int kJoinGroups = 4;  // groups of kAttnThreads that share an item's pieces in the join
 
 struct AttnArgs {
   const uint16_t* q;          // [tokens, q_heads, D] bf16
@@ -64,6 +76,8 @@ struct AttnArgs {
   int64_t blocks;
   int32_t requests, width, block;
   int32_t q_heads, kv_heads, max_new;
+  float* pieces;              // workspace: [2 * workers][8 * NT * (D + 2)]
+  int4* cut;                  // [2 * workers]: the item begun, but not ended, by a worker
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -114,6 +128,97 @@ struct AttnState {
   float l[NT][2];          // this lane's share of the sum of 2^(10 + S - m)
   float s_ref;             // largest block scale of V so far
 };
+
+// Adds the calls' values up over the CTA: returns the exclusive sum before
+// this thread, and the total.
+__device__ __forceinline__ int64_t attn_scan(int64_t v, int64_t& total, int64_t* sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  total = 0;
+  int64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) before += sm[w];
+    total += sm[w];
+  }
+  return before + x - v;
+}
+
+// What a CTA needs to know of a request.
+struct AttnRequest {
+  int q0, fresh, len;
+  int tiles;       // row tiles
+  int per_item;    // units of an item
+  int64_t units;
+};
+
+template <int ROWS>
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
+  AttnRequest a;
+  a.q0 = p.cu_new[r];
+  const int64_t fresh = static_cast<int64_t>(p.cu_new[r + 1]) - a.q0;
+  a.len = max(0, p.seq_lens[r]);
+  const bool bad = a.q0 < 0 || a.q0 + fresh > p.tokens || fresh > p.max_new;
+  a.fresh = bad || fresh < 0 ? 0 : static_cast<int>(fresh);
+  if (bad || a.len > static_cast<int64_t>(p.width) * p.block) {
+    atomicOr(&g_status, 1u << 7);
+    a.len = min(a.len, p.width * p.block);
+  }
+  a.tiles = static_cast<int>((static_cast<int64_t>(a.fresh) * (p.q_heads / p.kv_heads) + ROWS - 1) / ROWS);
+  a.per_item = max(1, (a.len + kAttnUnit - 1) / kAttnUnit);  // one even where there is nothing to see
+  a.units = static_cast<int64_t>(a.per_item) * a.tiles * p.kv_heads;
+  return a;
+}
+
+// D / 16 contiguous head dimensions of one row, times inv, to bf16.
+template <int D>
+__device__ __forceinline__ void attn_store_row(uint16_t* out, const float (&o)[D / 16], float inv) {
+  uint32_t w[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+    w[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  if constexpr (D == 64) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 4)
+      *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
+
+// In the epilogues thread t of kAttnThreads owns, of each column tile n, row
+// 8n + 2c + ((t >> 5) & 1) and the head dimensions of m-tiles (t >> 6) * D / 32
+// on (D / 16 of them, contiguous), with (g, c) those of its lane.
+template <int D>
+__device__ __forceinline__ int attn_own_dim(int t) {
+  constexpr int VB = D / 8 < 16 ? D / 8 : 16;
+  const int byte = (t >> 6) * (D / 16);
+  return (byte / VB) * 128 + ((t & 31) >> 2) * VB + byte % VB;
+}
+__device__ __forceinline__ int attn_own_row(int t) { return 2 * (t & 3) + ((t >> 5) & 1); }
+
+template <int D>
+__device__ __forceinline__ void attn_write(const AttnArgs& p, int q0, int r, int head, int t,
+                                           const float (&o)[D / 16], float m, float l) {
+  const int group = p.q_heads / p.kv_heads;
+  const int i = r / group, hq = head * group + r - i * group;
+  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;  // a row that sees nothing gives 0
+  const int d = attn_own_dim<D>(t);
+  const int64_t token = static_cast<int64_t>(q0) + i;
+  attn_store_row<D>(p.out + token * p.ldo_token + hq * p.ldo_head + d, o, inv);
+  if (p.lse && d == 0)
+    p.lse[token * p.q_heads + hq] =
+        l > 0.0f ? (m + (log2f(l) - 10.0f)) * 0.69314718055994531f : -INFINITY;
+}
 
 // A row tile of a request's rows against tokens [begin, end) of one kv head,
 // in steps of kAttnTile * kAttnWarps; the warp takes every kAttnWarps-th tile.
@@ -292,154 +397,265 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
   }
 }
 
-// Head dimension of O^T row `half` (0: row g, 1: row g + 8) of m-tile j.
-// m-tile 2w + i takes bytes 2i, 2i + 1 of word w of the lane's V chunk.
-template <int D>
-__device__ __forceinline__ int attn_out_dim(int j, int half, int g) {
-  constexpr int VB = D / 8 < 16 ? D / 8 : 16;
-  const int byte = 2 * j + half;               // among the lane's D / 8 bytes
-  return (byte / VB) * 128 + g * VB + byte % VB;
-}
-
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnArgs p) {
   constexpr int ROWS = 8 * NT;
-  extern __shared__ float sm_o[];   // [warps][ROWS][D]
+  constexpr int FRAG = D / 16 * NT * 4;  // accumulators a lane
+  constexpr int PIECE = ROWS * (D + 2);
+  extern __shared__ float sm_o[];        // [warps][FRAG][32]
   __shared__ float sm_m[kAttnWarps][ROWS], sm_l[kAttnWarps][ROWS];
+  __shared__ int64_t sm_scan[kAttnWarps];
+  __shared__ int64_t sm_base;
+  __shared__ int sm_req;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int row_tiles = (p.max_new * (p.q_heads / p.kv_heads) + ROWS - 1) / ROWS;
-  const int req = blockIdx.x / row_tiles, head = blockIdx.y;
   const int group = p.q_heads / p.kv_heads;
 
   pdl_wait();
-  const int64_t q0 = p.cu_new[req];
-  int fresh = p.cu_new[req + 1] - p.cu_new[req];
-  const int len = p.seq_lens[req];
-  if (q0 < 0 || q0 + fresh > p.tokens || fresh > p.max_new) {
-    if (threadIdx.x == 0) atomicOr(&g_status, 1u << 7);
+  // ---- this CTA's share of the units
+  const int chunk = (p.requests + kAttnThreads - 1) / kAttnThreads;
+  const int r_lo = min(p.requests, static_cast<int>(threadIdx.x) * chunk);
+  const int r_hi = min(p.requests, r_lo + chunk);
+  int64_t mine = 0, total;
+  for (int r = r_lo; r < r_hi; ++r) mine += attn_request<ROWS>(p, r).units;
+  int64_t before = attn_scan(mine, total, sm_scan);
+  const int64_t workers = min(total, static_cast<int64_t>(gridDim.x));
+  if (blockIdx.x >= workers) {
+    if (threadIdx.x == 0) p.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const int rows = fresh * group;
-  const int row0 = (blockIdx.x % row_tiles) * ROWS;
-  if (row0 >= rows) return;
-  const int pos0 = len - fresh;  // position of the request's first new token
-
-  // q fragments (column n of a tile is row g) and what the lane's two columns
-  // of S^T need: their factor and the first position that they do not see
-  uint32_t qf[NT][D / 16][2];
-  float rowfac[NT][2];
-  int limit[NT][2];
-  int most = 0, least = 0x7FFFFFFF;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = row0 + 8 * n + g;
-    const bool real = r < rows;
-    const int i = real ? r / group : 0;
-    const uint16_t* qp = p.q + (q0 + i) * p.ldq_token + (head * group + (real ? r - i * group : 0)) * p.ldq_head;
-    uint2 w[D / 16];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      // step j = 4 * chunk + word: head dimensions chunk * 64 + c * 16 + 4 * word ..
-      const int d = (j >> 2) * 64 + c * 16 + (j & 3) * 4;
-      w[j] = real ? __ldg(reinterpret_cast<const uint2*>(qp + d)) : make_uint2(0u, 0u);
-      const uint32_t a = (w[j].x & 0x7FFF7FFFu), b = (w[j].y & 0x7FFF7FFFu);
-      amax = max(amax, max(max(a & 0xFFFFu, a >> 16), max(b & 0xFFFFu, b >> 16)));
+  int64_t u = blockIdx.x * total / workers;
+  const int64_t u_end = (blockIdx.x + 1) * total / workers;
+  if (before <= u && u < before + mine) {
+    int r = r_lo;
+    for (; r < r_hi - 1; ++r) {
+      const int64_t n = attn_request<ROWS>(p, r).units;
+      if (u < before + n) break;
+      before += n;
     }
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    // 2^e with e = 14 - exponent(amax): amax * 2^e in [2^14, 2^15).  For rows
-    // of zeros or below 2^-100 the largest factor kept in range is 2^114.
-    const int e = 14 - max(static_cast<int>(amax >> 7) - 127, -100);
-    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      qf[n][j][0] = pack_f16x2(__uint_as_float(w[j].x << 16) * up, __uint_as_float(w[j].x & 0xFFFF0000u) * up);
-      qf[n][j][1] = pack_f16x2(__uint_as_float(w[j].y << 16) * up, __uint_as_float(w[j].y & 0xFFFF0000u) * up);
-    }
-    // row g's exponent and limit go to the lanes whose columns 2c, 2c + 1 it is
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (E4M3 ? 256.0f : 1.0f) * p.scale_log2;
-    const int lim = real ? min(max(pos0 + i + 1, 0), len) : 0;
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      rowfac[n][i2] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i2) * 4);
-      limit[n][i2] = __shfl_sync(0xFFFFFFFFu, lim, (2 * c + i2) * 4);
-    }
-    most = max(most, lim);
-    least = min(least, real ? lim : 0x7FFFFFFF);
+    sm_req = r;
+    sm_base = before;
   }
-  most = __reduce_max_sync(0xFFFFFFFFu, most);
-  if (most > p.width * p.block) {  // more tokens than the table has columns for
-    if (threadIdx.x == 0) atomicOr(&g_status, 1u << 7);
-    most = p.width * p.block;
-  }
-  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  __syncthreads();
+  int req = sm_req;
+  int64_t base = sm_base;  // the request's first unit
+  AttnRequest rq = attn_request<ROWS>(p, req);
+  if (threadIdx.x == 0) p.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-  AttnState<D, NT> st;
+  // every round ends an item or the share, so there are at most u_end - u
+  for (; u < u_end;) {
+    for (; u >= base + rq.units && req + 1 < p.requests;) {
+      base += rq.units;
+      rq = attn_request<ROWS>(p, ++req);
+    }
+    const int64_t item = (u - base) / rq.per_item;
+    const int64_t item_u = base + item * rq.per_item;  // the item's first unit
+    const int first = static_cast<int>(u - item_u);
+    const int last = static_cast<int>(min(static_cast<int64_t>(rq.per_item), u_end - item_u));
+    const int head = static_cast<int>(item / rq.tiles);
+    const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * rq.tiles) * ROWS;
+    const int rows = rq.fresh * group;
+    const int pos0 = rq.len - rq.fresh;  // position of the request's first new token
+
+    // q fragments (column n of a tile is row g) and what the lane's two columns
+    // of S^T need: their factor and the first position that they do not see
+    uint32_t qf[NT][D / 16][2];
+    float rowfac[NT][2];
+    int limit[NT][2];
+    int most = 0, least = 0x7FFFFFFF;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    st.m[n][0] = st.m[n][1] = -INFINITY;
-    st.l[n][0] = st.l[n][1] = 0.0f;
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool real = r < rows;
+      const int i = real ? r / group : 0;
+      const uint16_t* qp = p.q + (static_cast<int64_t>(rq.q0) + i) * p.ldq_token +
+                           (head * group + (real ? r - i * group : 0)) * p.ldq_head;
+      uint2 w[D / 16];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        // step j = 4 * chunk + word: head dimensions chunk * 64 + c * 16 + 4 * word ..
+        const int d = (j >> 2) * 64 + c * 16 + (j & 3) * 4;
+        w[j] = real ? __ldg(reinterpret_cast<const uint2*>(qp + d)) : make_uint2(0u, 0u);
+        const uint32_t a = (w[j].x & 0x7FFF7FFFu), b = (w[j].y & 0x7FFF7FFFu);
+        amax = max(amax, max(max(a & 0xFFFFu, a >> 16), max(b & 0xFFFFu, b >> 16)));
+      }
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      // 2^e with e = 14 - exponent(amax): amax * 2^e in [2^14, 2^15).  For rows
+      // of zeros or below 2^-100 the largest factor kept in range is 2^114.
+      const int e = 14 - max(static_cast<int>(amax >> 7) - 127, -100);
+      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        qf[n][j][0] = pack_f16x2(__uint_as_float(w[j].x << 16) * up, __uint_as_float(w[j].x & 0xFFFF0000u) * up);
+        qf[n][j][1] = pack_f16x2(__uint_as_float(w[j].y << 16) * up, __uint_as_float(w[j].y & 0xFFFF0000u) * up);
+      }
+      // row g's exponent and limit go to the lanes whose columns 2c, 2c + 1 it is
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (E4M3 ? 256.0f : 1.0f) * p.scale_log2;
+      const int lim = real ? min(max(pos0 + i + 1, 0), rq.len) : 0;
+#pragma unroll
+      for (int i2 = 0; i2 < 2; ++i2) {
+        rowfac[n][i2] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i2) * 4);
+        limit[n][i2] = __shfl_sync(0xFFFFFFFFu, lim, (2 * c + i2) * 4);
+      }
+      most = max(most, lim);
+      least = min(least, real ? lim : 0x7FFFFFFF);
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+
+    AttnState<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      st.m[n][0] = st.m[n][1] = -INFINITY;
+      st.l[n][0] = st.l[n][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[j][n][i] = 0.0f;
+    }
+    st.s_ref = 0.0f;
+    attend_tiles<D, E4M3, NT>(p, p.table + req * p.ld_table, head, qf, rowfac, limit, least,
+                              first * kAttnUnit, min(most, last * kAttnUnit), warp, lane, st);
+
+    // ---- the four warps' parts meet
+    __syncthreads();  // the previous item's have been read
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = st.l[n][i];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        if (g == 0) {
+          sm_m[warp][8 * n + 2 * c + i] = st.m[n][i];
+          sm_l[warp][8 * n + 2 * c + i] = l;
+        }
+      }
+    const float unit = st.s_ref * (E4M3 ? 256.0f : 1.0f);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.o[j][n][i] = 0.0f;
-  }
-  st.s_ref = 0.0f;
-  attend_tiles<D, E4M3, NT>(p, p.table + req * p.ld_table, head, qf, rowfac, limit, least, 0, most,
-                            warp, lane, st);
-
-  // ---- the four warps' parts meet
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < 4; ++i)
+          sm_o[(warp * FRAG + (j * NT + n) * 4 + i) * 32 + lane] = st.o[j][n][i] * unit;
+    __syncthreads();
+    const bool whole = first == 0 && last == rq.per_item;
+    // a piece of an item begun earlier goes to the first slot, of one that
+    // goes on to the second
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0);
+    float* piece = p.pieces + slot * PIECE;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float l = st.l[n][i];
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-      const int col = 8 * n + 2 * c + i;
-      if (g == 0) {
-        sm_m[warp][col] = st.m[n][i];
-        sm_l[warp][col] = l;
+    for (int n = 0; n < NT; ++n) {
+      const int row = 8 * n + attn_own_row(threadIdx.x);
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w][row]);
+      float l = 0.0f, o[D / 16];
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) o[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float f = sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f;
+        l = fmaf(f, sm_l[w][row], l);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int j = static_cast<int>(threadIdx.x >> 6) * (D / 32) + (k >> 1);
+          const int i = 2 * (k & 1) + ((threadIdx.x >> 5) & 1);
+          o[k] = fmaf(f, sm_o[(w * FRAG + (j * NT + n) * 4 + i) * 32 + lane], o[k]);
+        }
+      }
+      if (whole) {
+        if (row0 + row < rows) attn_write<D>(p, rq.q0, row0 + row, head, threadIdx.x, o, m, l);
+      } else {
+        float* to = piece + (n * kAttnThreads + threadIdx.x) * (D / 16);
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 4)
+          *reinterpret_cast<float4*>(to + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        if (attn_own_dim<D>(threadIdx.x) == 0) {
+          piece[ROWS * D + 2 * row] = m;
+          piece[ROWS * D + 2 * row + 1] = l;
+        }
       }
     }
-  const float unit = st.s_ref * (E4M3 ? 256.0f : 1.0f);
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sm_o[(warp * ROWS + 8 * n + 2 * c + (i & 1)) * D + attn_out_dim<D>(j, i >> 1, g)] =
-            st.o[j][n][i] * unit;
-  __syncthreads();
-  pdl_trigger();
-  for (int e = threadIdx.x * 2; e < ROWS * D; e += kAttnThreads * 2) {
-    const int row = e / D, d = e - row * D;
-    const int r = row0 + row;
-    if (r >= rows) break;
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w][row]);
-    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      const float f = sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f;
-      const float2 o = *reinterpret_cast<const float2*>(sm_o + (w * ROWS + row) * D + d);
-      l = fmaf(f, sm_l[w][row], l);
-      o0 = fmaf(f, o.x, o0);
-      o1 = fmaf(f, o.y, o1);
+    if (!whole && first == 0 && threadIdx.x == 0) {
+      // the worker that holds the item's last unit
+      const int64_t w_end = ((item_u + rq.per_item) * workers - 1) / total;
+      p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), head, row0, rows);
+      p.cut[2 * blockIdx.x + 1] = make_int4(rq.q0, 0, 0, 0);
     }
-    const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;  // a row that sees nothing gives 0
-    const int i = r / group, hq = head * group + r - i * group;
-    const __nv_bfloat162 y = __floats2bfloat162_rn(o0 * inv, o1 * inv);
-    *reinterpret_cast<__nv_bfloat162*>(p.out + (q0 + i) * p.ldo_token + hq * p.ldo_head + d) = y;
-    if (p.lse && d == 0)
-      p.lse[(q0 + i) * p.q_heads + hq] =
-          l > 0.0f ? (m + (log2f(l) - 10.0f)) * 0.69314718055994531f : -INFINITY;
+    u = item_u + last;
   }
+  pdl_trigger();
+}
+
+// Joins the pieces of the items that workers began and did not end: CTA (w, n)
+// the column tile n of worker w's.  Its groups of kAttnThreads take every
+// kJoinGroups-th piece; the groups' sums meet in a fixed order.
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads* kJoinGroups) kv_attention_join_kernel(const AttnArgs p) {
+  constexpr int ROWS = 8 * NT;
+  constexpr int PIECE = ROWS * (D + 2);
+  __shared__ float sm_m[kJoinGroups][8], sm_l[kJoinGroups][8];
+  __shared__ float sm_o[kJoinGroups - 1][D / 16][kAttnThreads];
+  const int w0 = blockIdx.x, n = blockIdx.y;
+  const int t = threadIdx.x % kAttnThreads, grp = threadIdx.x / kAttnThreads;
+  pdl_wait();
+  const int4 cut = p.cut[2 * w0];
+  pdl_trigger();
+  if (cut.x < 0) return;
+  const int q0 = p.cut[2 * w0 + 1].x;
+  const int pieces = cut.x - w0 + 1;
+  const int row = attn_own_row(t);
+  float m = -INFINITY, l = 0.0f, o[D / 16];
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) o[k] = 0.0f;
+#pragma unroll 2
+  for (int i = grp; i < pieces; i += kJoinGroups) {
+    const float* piece = p.pieces + (i == 0 ? 2 * static_cast<int64_t>(w0) + 1 : 2 * (static_cast<int64_t>(w0) + i)) * PIECE;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece + ROWS * D) + 8 * n + row);
+    float4 v[D / 64];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      v[k] = __ldcg(reinterpret_cast<const float4*>(piece + (n * kAttnThreads + t) * (D / 16)) + k);
+    const float top = fmaxf(m, ml.x);
+    const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
+    const float add = ml.x > -INFINITY ? ex2(ml.x - top) : 0.0f;
+    m = top;
+    l = l * keep + ml.y * add;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      o[4 * k] = o[4 * k] * keep + v[k].x * add;
+      o[4 * k + 1] = o[4 * k + 1] * keep + v[k].y * add;
+      o[4 * k + 2] = o[4 * k + 2] * keep + v[k].z * add;
+      o[4 * k + 3] = o[4 * k + 3] * keep + v[k].w * add;
+    }
+  }
+  if (attn_own_dim<D>(t) == 0) {
+    sm_m[grp][row] = m;
+    sm_l[grp][row] = l;
+  }
+  if (grp > 0) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) sm_o[grp - 1][k][t] = o[k];
+  }
+  __syncthreads();
+  if (grp > 0) return;
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJoinGroups; ++i) top = fmaxf(top, sm_m[i][row]);
+#pragma unroll
+  for (int i = 0; i < kJoinGroups; ++i) {
+    const float f = sm_m[i][row] > -INFINITY ? ex2(sm_m[i][row] - top) : 0.0f;
+    sum = fmaf(f, sm_l[i][row], sum);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) o[k] = i == 0 ? o[k] * f : fmaf(f, sm_o[i > 0 ? i - 1 : 0][k][t], o[k]);
+  }
+  const int r = cut.z + 8 * n + row;
+  if (r < cut.w) attn_write<D>(p, q0, r, cut.y, t, o, top, sum);
 }
 
 }  // namespace i8

@@ -98,24 +98,86 @@ i8_status check_cache(const i8_kv_cache* c) {
 }
 
 // ----------------------------------------------------------------- attention
+// Column tiles of 8 rows a CTA takes at once.  A second one shares the decoded
+// codes of the first, but at 256 head dimensions its accumulators do not fit
+// the registers.
+int attention_nt(int64_t rows, int64_t head_dim) { return head_dim == 256 || rows <= 8 ? 1 : 2; }
+
 template <int D, bool E4M3, int NT>
-i8_status launch_attention(const AttnArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(float) * kAttnWarps * 8 * NT * D;
-  if (i8_status e = allow_smem<kv_attention_kernel<D, E4M3, NT>>(smem)) return e;
-  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
-  const int64_t tiles = (rows + 8 * NT - 1) / (8 * NT);
-  if (tiles * a.requests > INT32_MAX) return I8_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(tiles * a.requests), static_cast<unsigned>(a.kv_heads));
-  return cuda_status(launch_pdl(kv_attention_kernel<D, E4M3, NT>, grid, dim3(kAttnThreads), smem, st, a));
+size_t attention_smem() {
+  return sizeof(float) * kAttnWarps * (D / 16) * NT * 4 * 32;
 }
 
+// CTAs of a kernel that are resident at once.
+template <int D, bool E4M3, int NT>
+i8_status attention_workers(int* workers) {
+  static int cached[kMaxDevices] = {};
+  static std::mutex mu;
+  constexpr auto kern = kv_attention_kernel<D, E4M3, NT>;
+  const size_t smem = attention_smem<D, E4M3, NT>();
+  if (i8_status e = allow_smem<kern>(smem)) return e;
+  int sms, dev = 0, per_sm = 0;
+  if (i8_status e = device_sms(&sms)) return e;
+  if (cudaGetDevice(&dev) != cudaSuccess) return I8_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cached[dev] == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAttnThreads, smem) != cudaSuccess ||
+        per_sm < 1)
+      return I8_ERR_CUDA;
+    cached[dev] = sms * per_sm;
+  }
+  *workers = cached[dev];
+  return I8_OK;
+}
+
+template <int D, int NT>
+size_t attention_ws(int workers) {
+  return static_cast<size_t>(workers) * 2 * (sizeof(int4) + sizeof(float) * 8 * NT * (D + 2));
+}
+
+template <int D, bool E4M3, int NT>
+i8_status launch_attention(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need, cudaStream_t st) {
+  int workers;
+  if (i8_status e = attention_workers<D, E4M3, NT>(&workers)) return e;
+  const size_t bytes = attention_ws<D, NT>(workers);
+  if (need) {
+    *need = bytes;
+    return I8_OK;
+  }
+  if (!ws || ws_bytes < bytes) return I8_ERR_WORKSPACE;
+  if (!aligned16(ws)) return I8_ERR_ALIGNMENT;
+  a.cut = static_cast<int4*>(ws);
+  a.pieces = reinterpret_cast<float*>(a.cut + 2 * static_cast<size_t>(workers));
+  const dim3 grid(static_cast<unsigned>(workers));
+  if (cudaError_t e = launch_pdl(kv_attention_kernel<D, E4M3, NT>, grid, dim3(kAttnThreads),
+                                 attention_smem<D, E4M3, NT>(), st, a))
+    return cuda_status(e);
+  return cuda_status(launch_pdl(kv_attention_join_kernel<D, NT>, dim3(grid.x, NT),
+                                dim3(kAttnThreads * kJoinGroups), 0, st, a));
+}
+
+// Runs the attention, or with `need` only says how much workspace it wants.
 template <int D, bool E4M3>
-i8_status launch_attention_nt(const AttnArgs& a, cudaStream_t st) {
-  // a second column tile shares the decoded codes of the first, but at 256
-  // head dimensions its accumulators do not fit the registers
-  if (D == 256 || static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads) <= 8)
-    return launch_attention<D, E4M3, 1>(a, st);
-  return launch_attention<D, E4M3, D == 256 ? 1 : 2>(a, st);
+i8_status attention_nt_dispatch(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
+  if (attention_nt(rows, D) == 1) return launch_attention<D, E4M3, 1>(a, ws, ws_bytes, need, st);
+  return launch_attention<D, E4M3, D == 256 ? 1 : 2>(a, ws, ws_bytes, need, st);
+}
+
+i8_status attention_dispatch(AttnArgs& a, int head_dim, bool e4m3, void* ws, size_t ws_bytes,
+                             size_t* need, cudaStream_t st) {
+  switch (head_dim) {
+    case 64:
+      return e4m3 ? attention_nt_dispatch<64, true>(a, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<64, false>(a, ws, ws_bytes, need, st);
+    case 128:
+      return e4m3 ? attention_nt_dispatch<128, true>(a, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<128, false>(a, ws, ws_bytes, need, st);
+    case 256:
+      return e4m3 ? attention_nt_dispatch<256, true>(a, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<256, false>(a, ws, ws_bytes, need, st);
+  }
+  return I8_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -230,9 +292,20 @@ i8_status i8_kv_cache_append(const void* k, int64_t ldk_token, int64_t ldk_head,
 }
 
 size_t i8_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                                          int64_t max_new) {
-  (void)q_heads, (void)kv_heads, (void)head_dim, (void)max_new;
-  return 0;
+                                          int fmt, int64_t max_new) {
+  I8_NVTX();
+  if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || q_heads > 65535 || max_new < 0 ||
+      max_new > INT32_MAX || (fmt != I8_CODES_INT8 && fmt != I8_CODES_E4M3))
+    return 0;
+  AttnArgs a{};
+  a.q_heads = static_cast<int32_t>(q_heads);
+  a.kv_heads = static_cast<int32_t>(kv_heads);
+  a.max_new = static_cast<int32_t>(max_new);
+  size_t need = 0;
+  if (attention_dispatch(a, static_cast<int>(head_dim), fmt == I8_CODES_E4M3, nullptr, 0, &need,
+                         nullptr) != I8_OK)
+    return 0;
+  return need;
 }
 
 i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head, int64_t tokens,
@@ -243,7 +316,6 @@ i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head,
                              int64_t ldo_head, float* lse, void* ws, size_t ws_bytes,
                              i8_stream_t stream) {
   I8_NVTX();
-  (void)ws, (void)ws_bytes;
   if (i8_status e = check_cache(cache)) return e;
   if (tokens < 0 || requests < 0 || width < 0 || ld_table < width || max_new < 0 || q_heads <= 0 ||
       q_heads % cache->kv_heads != 0)
@@ -286,13 +358,8 @@ i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head,
   a.q_heads = static_cast<int32_t>(q_heads);
   a.kv_heads = cache->kv_heads;
   a.max_new = static_cast<int32_t>(std::min(max_new, tokens));
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool e4m3 = cache->fmt == I8_CODES_E4M3;
-  switch (cache->head_dim) {
-    case 64: return e4m3 ? launch_attention_nt<64, true>(a, st) : launch_attention_nt<64, false>(a, st);
-    case 128: return e4m3 ? launch_attention_nt<128, true>(a, st) : launch_attention_nt<128, false>(a, st);
-    default: return e4m3 ? launch_attention_nt<256, true>(a, st) : launch_attention_nt<256, false>(a, st);
-  }
+  return attention_dispatch(a, cache->head_dim, cache->fmt == I8_CODES_E4M3, ws, ws_bytes, nullptr,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

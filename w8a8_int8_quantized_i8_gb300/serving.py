@@ -294,7 +294,7 @@ def paged_attention(q: torch.Tensor, cache: QuantKVCache, block_tables: torch.Te
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
     with _on_device(dev) as stream:
         lib = load()
-        need = lib.i8_paged_attention_workspace_bytes(Hq, info.kv_heads, D, max_new)
+        need = lib.i8_paged_attention_workspace_bytes(Hq, info.kv_heads, D, info.fmt, min(max_new, T))
         if workspace is None and need:
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         _check(lib.i8_paged_attention(
