@@ -25,12 +25,18 @@
 //
 // The products run transposed: S^T = K q^T and O^T = V^T P^T, so that the
 // tokens and the head dimension fill the 16-row side of the warp MMA
-// (m16n8k16) and the few query rows its 8-wide side.  A warp takes 32 tokens
-// at a time straight from global memory into the MMA's register fragments:
-// the order of the head dimension inside a product and of the output's rows
-// is free, so lane (g, c) = (lane / 4, lane % 4) reads 16 contiguous codes of
-// token g of K, and of tokens 2c, 2c + 1 of V, and no shared memory is used.
+// (m16n8k16) and the few query rows its 8-wide side.  The order of the head
+// dimension inside a product and of the output's rows is free, so lane (g, c)
+// = (lane / 4, lane % 4) takes 16 contiguous codes of token g of K, and of
+// tokens 2c, 2c + 1 of V.
+//
+// Every warp has a ring of its own in shared memory, which its first lane
+// fills by TMA (16 or 32 tokens of a block are one contiguous piece of the
+// cache) and which needs no barrier between warps.  The 128-byte swizzle makes
+// the lanes' 16-byte reads free of bank conflicts: rows 2c, 2c + 1 at chunk g
+// for V, rows g at chunks 2c + j for K.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,7 +48,7 @@
 namespace i8 {
 
 // How the work is split.  An item is a request's row tile (8 * NT rows) of one
-// kv head; its tokens come in units of 128.  The units of all items, request
+// kv head; its tokens come in units of 4 warps' tiles.  The units of all items, request
 // after request, are one line that the resident CTAs cut into equal shares, so
 // ragged lengths balance and one long context fills the GPU.  Nobody but the
 // device knows the lengths: every CTA adds up the requests' units by itself
@@ -53,15 +59,24 @@ namespace i8 {
 // timing.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnTile = 32;  // tokens a warp takes at a time (two halves of 16)
-constexpr int kAttnUnit = kAttnTile * kAttnWarps;
+static_assert(kAttnThreads == 128, "the epilogues' ownership of rows is written for 128 threads");
+
+// Tokens a warp takes at a time, in halves of 16, and its ring's stages.
+template <int D>
+struct AttnTile {
+  static constexpr int HALVES = D == 256 ? 1 : 2;
+  static constexpr int TOKENS = 16 * HALVES;
+  static constexpr int UNIT = TOKENS * kAttnWarps;
+  static constexpr int STAGES = 2;
+  static constexpr int SIDE = TOKENS * D;      // bytes of K, or of V, in a stage
+  static constexpr int STAGE = 2 * SIDE;
+  static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row in one TMA box
+};
 constexpr int kJoinGroups = 4;  // groups of kAttnThreads that share an item's pieces in the join
 
 struct AttnArgs {
   const uint16_t* q;          // [tokens, q_heads, D] bf16
   int64_t ldq_token, ldq_head;
-  const uint8_t* k;           // [blocks, kv_heads, B, D] codes
-  const uint8_t* v;
   const float* k_scale;       // [blocks, kv_heads]
   const float* v_scale;
   const int32_t* table;       // [requests, width]
@@ -76,6 +91,8 @@ struct AttnArgs {
   int64_t blocks;
   int32_t requests, width, block;
   int32_t q_heads, kv_heads, max_new;
+  int32_t unit_cols, unit_rest;  // unit / block, unit % block
+  int32_t box_rows;           // tokens of a TMA box: 16 or 32
   float* pieces;              // workspace: [2 * workers][8 * NT * (D + 2)]
   int4* cut;                  // [2 * workers]: the item begun, but not ended, by a worker
 };
@@ -159,7 +176,7 @@ struct AttnRequest {
   int64_t units;
 };
 
-template <int ROWS>
+template <int ROWS, int UNIT>
 __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   AttnRequest a;
   a.q0 = p.cu_new[r];
@@ -172,7 +189,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
     a.len = min(a.len, p.width * p.block);
   }
   a.tiles = static_cast<int>((static_cast<int64_t>(a.fresh) * (p.q_heads / p.kv_heads) + ROWS - 1) / ROWS);
-  a.per_item = max(1, (a.len + kAttnUnit - 1) / kAttnUnit);  // one even where there is nothing to see
+  a.per_item = max(1, (a.len + UNIT - 1) / UNIT);  // one even where there is nothing to see
   a.units = static_cast<int64_t>(a.per_item) * a.tiles * p.kv_heads;
   return a;
 }
@@ -220,91 +237,160 @@ __device__ __forceinline__ void attn_write(const AttnArgs& p, int q0, int r, int
         l > 0.0f ? (m + (log2f(l) - 10.0f)) * 0.69314718055994531f : -INFINITY;
 }
 
+__device__ __forceinline__ uint4 lds_16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds_8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// Where a place in a token's row lies in a half (16 tokens) of a stage's K or
+// V: boxes of 16 rows, each row's 16-byte chunks xor-ed with the row number
+// (128-byte rows: by row & 7, 64-byte rows: by row / 2 & 3).
+template <int D>
+__device__ __forceinline__ uint32_t attn_place(int row, int byte) {
+  if constexpr (D == 64) return row * 64 + (byte ^ (((row >> 1) & 3) << 4));
+  return (byte >> 7) * (AttnTile<D>::TOKENS * 128) + row * 128 + ((byte & 127) ^ ((row & 7) << 4));
+}
+
+// First head dimension of K chunk j of lane column c (16 codes).
+template <int D>
+__host__ __device__ constexpr int attn_k_dim(int j, int c) {
+  return D == 64 ? c * 16 : (j >> 1) * 128 + (2 * c + (j & 1)) * 16;
+}
+
 // A row tile of a request's rows against tokens [begin, end) of one kv head,
-// in steps of kAttnTile * kAttnWarps; the warp takes every kAttnWarps-th tile.
+// in steps of a unit; the warp takes every kAttnWarps-th tile.  `ring` and
+// `bars`: the shared-memory addresses of the warp's stages and of the barriers
+// on which their copies count; `parity`: a bit for each stage.
 template <int D, bool E4M3, int NT>
-__device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* table, int head,
+__device__ __forceinline__ void attend_tiles(const AttnArgs& p, const void* k_map,
+                                             const void* v_map, const int32_t* table, int head,
                                              const uint32_t (&qf)[NT][D / 16][2],
                                              const float (&rowfac)[NT][2],
                                              const int (&limit)[NT][2], int all_seen, int begin,
-                                             int end, int warp, int lane, AttnState<D, NT>& st) {
-  constexpr int KW = D / 64;   // 16-byte chunks of a token's K row a lane holds
+                                             int end, uint32_t ring, uint32_t bars,
+                                             uint32_t& parity, volatile int* abort_flag, int warp,
+                                             int lane, AttnState<D, NT>& st) {
+  using Tile = AttnTile<D>;
+  constexpr int H = Tile::HALVES;
+  constexpr int S = Tile::STAGES;
+  constexpr int KW = D / 64;   // 16-byte chunks of a token's K row a lane takes
   constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // the same of V (8 bytes at D = 64)
-  constexpr int VB = D / 8 < 16 ? D / 8 : 16;    // contiguous bytes of V a lane reads
+  constexpr int VB = D / 8 < 16 ? D / 8 : 16;    // contiguous bytes of V a lane takes
   const int g = lane >> 2, c = lane & 3;
-  const int64_t head_stride = static_cast<int64_t>(p.block) * D;
+  const int t_first = begin + warp * Tile::TOKENS;
+  if (t_first >= end) return;
 
-  for (int t0 = begin + warp * kAttnTile; t0 < end; t0 += kAttnTile * kAttnWarps) {
-    uint4 kr[2][2][KW];      // [half][token g, g + 8][chunk]
-    uint32_t vr[2][4][VW * 4];
-    float sk[2], sv[2];
-    bool gone[2];            // no such block: its tokens are left out
+  // the block (a column of the table) and the offset in it of the next tile to
+  // look up; ids are looked up a tile ahead of the copies that need them
+  int col = t_first / p.block, off = t_first - col * p.block, t_look = t_first;
+  int next_id[H], next_off[H];
+  auto look_up = [&]() {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = t0 + 16 * h;
-      const int b = t / p.block;
-      int64_t blk = -1;
-      if (t < end) {  // end lies within the table's width
-        blk = table[b];
-        if (blk < 0 || blk >= p.blocks) {
-          if (lane == 0) atomicOr(&g_status, 1u << 7);
-          blk = -1;
-        }
-      }
-      gone[h] = blk < 0;
-      sk[h] = sv[h] = 0.0f;
-      if (blk >= 0) {
-        const int64_t base = (blk * p.kv_heads + head) * head_stride + static_cast<int64_t>(t - b * p.block) * D;
-        const uint8_t* kp = p.k + base;
-        const uint8_t* vp = p.v + base;
+    for (int h = 0; h < H; ++h) {
+      const bool wraps = off + 16 * h >= p.block;
+      next_off[h] = wraps ? off + 16 * h - p.block : off + 16 * h;
+      next_id[h] = t_look + 16 * h < end ? __ldg(table + (wraps ? col + 1 : col)) : -1;
+    }
+    t_look += Tile::UNIT;
+    col += p.unit_cols;
+    off += p.unit_rest;
+    if (off >= p.block) {
+      off -= p.block;
+      ++col;
+    }
+  };
+  float ksc[S][H], vsc[S][H];  // block scales of the tiles in the ring; K's is NaN for a missing block
+  auto issue = [&](int t0, int slot, int into) {
+    if (t0 >= end) return;
+    const uint32_t k_to = ring + slot * Tile::STAGE, v_to = k_to + Tile::SIDE;
+    const uint32_t bar = bars + 8 * slot;
+    uint32_t bytes = 0;
+    bool there[H];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int h = 0; h < H; ++h) {
+      there[h] = next_id[h] >= 0 && next_id[h] < p.blocks;
+      // end lies within the table's width
+      if (!there[h] && t0 + 16 * h < end && lane == 0) atomicOr(&g_status, 1u << 7);
+      bytes += there[h] ? 32u * D : 0u;
+    }
+    // a box of 32 tokens where blocks are a multiple of that: the halves' ids agree
+    const bool whole = H == 2 && p.box_rows == 32;
+    if (whole) bytes = there[0] ? 64u * D : 0u;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-          for (int j = 0; j < KW; ++j)
-            kr[h][i][j] = ld_stream_v4(kp + (g + 8 * i) * D + j * 64 + c * 16);
+      for (int h = 0; h < H; ++h)
+        if (there[h] && !(whole && h == 1)) {
+          const int row = next_id[h] * p.kv_heads + head;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            if constexpr (VB == 16) {
-              const uint4 x = ld_stream_v4(vp + tk * D + j * 128 + g * 16);
-              vr[h][i][4 * j] = x.x;
-              vr[h][i][4 * j + 1] = x.y;
-              vr[h][i][4 * j + 2] = x.z;
-              vr[h][i][4 * j + 3] = x.w;
-            } else {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(vp + tk * D + g * 8));
-              vr[h][i][0] = x.x;
-              vr[h][i][1] = x.y;
-            }
+          for (int b = 0; b < D / Tile::BOX; ++b) {
+            const uint32_t at = b * (Tile::TOKENS * 128) + h * 16 * Tile::BOX;
+            tma_load_3d(k_to + at, k_map, bar, b * Tile::BOX, next_off[h], row);
+            tma_load_3d(v_to + at, v_map, bar, b * Tile::BOX, next_off[h], row);
           }
         }
-        sk[h] = p.k_scale[blk * p.kv_heads + head];
-        sv[h] = p.v_scale[blk * p.kv_heads + head];
-      } else {
+    }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int h = 0; h < H; ++h) {
+      const int64_t row = static_cast<int64_t>(next_id[h]) * p.kv_heads + head;
+      ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : NAN;
+      vsc[into][h] = there[h] ? __ldg(p.v_scale + row) : 0.0f;
+    }
+  };
+
+  look_up();
 #pragma unroll
-          for (int j = 0; j < KW; ++j) kr[h][i][j] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < S - 1; ++i) {
+    issue(t_first + i * Tile::UNIT, i, i);
+    look_up();
+  }
+  int slot = 0;
+#pragma unroll 1
+  for (int t0 = t_first; t0 < end; t0 += Tile::UNIT) {
+    if (!mbar_wait(bars + 8 * slot, (parity >> slot) & 1u, abort_flag)) break;
+    parity ^= 1u << slot;
+    float sk[H], sv[H];
+    bool gone[H];            // no such block: its tokens are left out
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int h = 0; h < H; ++h) {
+      sk[h] = ksc[0][h];
+      sv[h] = vsc[0][h];
+      gone[h] = isnan(sk[h]);
 #pragma unroll
-          for (int j = 0; j < VW * 4; ++j) vr[h][i][j] = 0u;
+      for (int i = 0; i + 2 < S; ++i) {
+        ksc[i][h] = ksc[i + 1][h];
+        vsc[i][h] = vsc[i + 1][h];
       }
     }
+    const uint32_t stage = ring + slot * Tile::STAGE;
+    __syncwarp();  // the whole warp is done with the tile before, whose stage is filled next
+    issue(t0 + (S - 1) * Tile::UNIT, slot == 0 ? S - 1 : slot - 1, S - 2);
+    look_up();
+    slot = slot + 1 == S ? 0 : slot + 1;
     // ---- S^T
-    float s[2][NT][4];
+    float s[H][NT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
+      const uint32_t half = stage + h * 16 * Tile::BOX;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[h][n][i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
-        const uint32_t w0[4] = {kr[h][0][j].x, kr[h][0][j].y, kr[h][0][j].z, kr[h][0][j].w};
-        const uint32_t w1[4] = {kr[h][1][j].x, kr[h][1][j].y, kr[h][1][j].z, kr[h][1][j].w};
+        const uint4 k0 = lds_16(half + attn_place<D>(g, attn_k_dim<D>(j, c)));
+        const uint4 k1 = lds_16(half + attn_place<D>(g + 8, attn_k_dim<D>(j, c)));
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w};
+        const uint32_t w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t a0, a1, a2, a3;
@@ -317,13 +403,13 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
       }
     }
     // ---- softmax
-    const bool masked = t0 + kAttnTile > all_seen || gone[0] || gone[1];
+    const bool masked = t0 + Tile::TOKENS > all_seen || gone[0] || gone[H - 1];
     float top[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s[h][n][i] *= sk[h] * rowfac[n][i & 1];
@@ -332,7 +418,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
           top[n][i & 1] = fmaxf(top[n][i & 1], s[h][n][i]);
         }
     }
-    const float s_ref = fmaxf(st.s_ref, fmaxf(sv[0], sv[1]));
+    const float s_ref = fmaxf(st.s_ref, fmaxf(sv[0], sv[H - 1]));
     const float grow = s_ref > 0.0f ? __fdividef(st.s_ref, s_ref) : 0.0f;
     bool moved = s_ref != st.s_ref;
     float alpha[NT][2];
@@ -362,7 +448,8 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
     }
     // ---- P^T and O^T
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
+      const uint32_t half = stage + Tile::SIDE + h * 16 * Tile::BOX;
       const float vs = s_ref > 0.0f ? __fdividef(sv[h], s_ref) : 0.0f;
       uint32_t b[NT][2];
 #pragma unroll
@@ -377,12 +464,31 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
         b[n][0] = transpose_8x8(pack_f16x2(e[0] * vs, e[1] * vs));
         b[n][1] = transpose_8x8(pack_f16x2(e[2] * vs, e[3] * vs));
       }
+      uint32_t vr[4][D / 32];             // the V words of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          if constexpr (VB == 16) {
+            const uint4 x = lds_16(half + attn_place<D>(tk, j * 128 + g * 16));
+            vr[i][4 * j] = x.x;
+            vr[i][4 * j + 1] = x.y;
+            vr[i][4 * j + 2] = x.z;
+            vr[i][4 * j + 3] = x.w;
+          } else {
+            const uint2 x = lds_8(half + attn_place<D>(tk, g * 8));
+            vr[i][0] = x.x;
+            vr[i][1] = x.y;
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // word j of the V rows: 4 head dimensions, 2 MMAs
         uint32_t f[2][4];                 // [tokens 2c.., 8 + 2c..][head dimension]
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t x = vr[h][2 * i][j], y = vr[h][2 * i + 1][j];
+          const uint32_t x = vr[2 * i][j], y = vr[2 * i + 1][j];
           codes_to_f16<E4M3>(__byte_perm(x, y, 0x5140), f[i][0], f[i][1]);
           codes_to_f16<E4M3>(__byte_perm(x, y, 0x7362), f[i][2], f[i][3]);
         }
@@ -397,12 +503,27 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const int32_t* t
   }
 }
 
+// CTAs an SM that the registers are cut to: as many as the accumulators of the
+// column tiles allow, so that as many rings are in flight.
+template <int D, int NT>
+constexpr int attn_ctas() { return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT == 1 ? 3 : 2; }
+
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
+    kv_attention_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map) {
   constexpr int ROWS = 8 * NT;
   constexpr int FRAG = D / 16 * NT * 4;  // accumulators a lane
   constexpr int PIECE = ROWS * (D + 2);
-  extern __shared__ float sm_o[];        // [warps][FRAG][32]
+  constexpr int UNIT = AttnTile<D>::UNIT;
+  constexpr int S = AttnTile<D>::STAGES;
+  // the warps' rings (on a 1024-byte boundary), and after an item's last tile
+  // [warps][FRAG][32] sums
+  extern __shared__ uint8_t sm_attn[];
+  float* sm_o = reinterpret_cast<float*>(
+      sm_attn + ((1024u - (smem_u32(sm_attn) & 1023u)) & 1023u));
+  __shared__ __align__(8) uint64_t sm_bars[kAttnWarps][S];
+  __shared__ int abort_flag;
   __shared__ float sm_m[kAttnWarps][ROWS], sm_l[kAttnWarps][ROWS];
   __shared__ int64_t sm_scan[kAttnWarps];
   __shared__ int64_t sm_base;
@@ -410,6 +531,18 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int group = p.q_heads / p.kv_heads;
+  const uint32_t ring = smem_u32(sm_o) + warp * (S * AttnTile<D>::STAGE);
+  const uint32_t bars = smem_u32(sm_bars[warp]);
+  uint32_t parity = 0;
+  if (lane < S) mbar_init(bars + 8 * lane, 1);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    tma_prefetch_desc(&k_map);
+    tma_prefetch_desc(&v_map);
+  }
+  fence_mbarrier_init();
+  fence_proxy_async_smem();
+  __syncwarp();
 
   pdl_wait();
   // ---- this CTA's share of the units
@@ -417,7 +550,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
   const int r_lo = min(p.requests, static_cast<int>(threadIdx.x) * chunk);
   const int r_hi = min(p.requests, r_lo + chunk);
   int64_t mine = 0, total;
-  for (int r = r_lo; r < r_hi; ++r) mine += attn_request<ROWS>(p, r).units;
+  for (int r = r_lo; r < r_hi; ++r) mine += attn_request<ROWS, UNIT>(p, r).units;
   int64_t before = attn_scan(mine, total, sm_scan);
   const int64_t workers = min(total, static_cast<int64_t>(gridDim.x));
   if (blockIdx.x >= workers) {
@@ -429,7 +562,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
   if (before <= u && u < before + mine) {
     int r = r_lo;
     for (; r < r_hi - 1; ++r) {
-      const int64_t n = attn_request<ROWS>(p, r).units;
+      const int64_t n = attn_request<ROWS, UNIT>(p, r).units;
       if (u < before + n) break;
       before += n;
     }
@@ -439,14 +572,14 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
   __syncthreads();
   int req = sm_req;
   int64_t base = sm_base;  // the request's first unit
-  AttnRequest rq = attn_request<ROWS>(p, req);
+  AttnRequest rq = attn_request<ROWS, UNIT>(p, req);
   if (threadIdx.x == 0) p.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   // every round ends an item or the share, so there are at most u_end - u
   for (; u < u_end;) {
     for (; u >= base + rq.units && req + 1 < p.requests;) {
       base += rq.units;
-      rq = attn_request<ROWS>(p, ++req);
+      rq = attn_request<ROWS, UNIT>(p, ++req);
     }
     const int64_t item = (u - base) / rq.per_item;
     const int64_t item_u = base + item * rq.per_item;  // the item's first unit
@@ -474,8 +607,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
       uint32_t amax = 0;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        // step j = 4 * chunk + word: head dimensions chunk * 64 + c * 16 + 4 * word ..
-        const int d = (j >> 2) * 64 + c * 16 + (j & 3) * 4;
+        const int d = attn_k_dim<D>(j >> 2, c) + (j & 3) * 4;  // step j = 4 * chunk + word
         w[j] = real ? __ldg(reinterpret_cast<const uint2*>(qp + d)) : make_uint2(0u, 0u);
         const uint32_t a = (w[j].x & 0x7FFF7FFFu), b = (w[j].y & 0x7FFF7FFFu);
         amax = max(amax, max(max(a & 0xFFFFu, a >> 16), max(b & 0xFFFFu, b >> 16)));
@@ -516,11 +648,11 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
         for (int i = 0; i < 4; ++i) st.o[j][n][i] = 0.0f;
     }
     st.s_ref = 0.0f;
-    attend_tiles<D, E4M3, NT>(p, p.table + req * p.ld_table, head, qf, rowfac, limit, least,
-                              first * kAttnUnit, min(most, last * kAttnUnit), warp, lane, st);
+    attend_tiles<D, E4M3, NT>(p, &k_map, &v_map, p.table + req * p.ld_table, head, qf, rowfac, limit, least,
+                              first * UNIT, min(most, last * UNIT), ring, bars, parity, &abort_flag, warp, lane, st);
 
-    // ---- the four warps' parts meet
-    __syncthreads();  // the previous item's have been read
+    // ---- the four warps' parts meet, where the rings were
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -588,6 +720,11 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
       p.cut[2 * blockIdx.x + 1] = make_int4(rq.q0, 0, 0, 0);
     }
     u = item_u + last;
+    if (abort_flag) break;
+    if (u < u_end) {
+      fence_proxy_async_smem();  // the sums' place is filled by copies again
+      __syncthreads();
+    }
   }
   pdl_trigger();
 }

@@ -1,6 +1,7 @@
 // serving_api.cu -- the C ABI of the serving operators (declared in
 // include/i8.h): the norm with the residual's addition and an 8-bit output,
 // block tables, the 8-bit paged cache's append and the attention over it.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -89,7 +90,7 @@ i8_status check_cache(const i8_kv_cache* c) {
   if (c->fmt != I8_CODES_INT8 && c->fmt != I8_CODES_E4M3) return I8_ERR_INVALID_ARG;
   if (c->blocks > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return I8_ERR_INVALID_ARG;
   if (c->block_size % 16 != 0 || c->block_size > 1024 || c->blocks > INT32_MAX ||
-      c->kv_heads > 32767)
+      c->kv_heads > 32767 || c->blocks * c->kv_heads > INT32_MAX)
     return I8_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return I8_ERR_UNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
@@ -105,7 +106,47 @@ int attention_nt(int64_t rows, int64_t head_dim) { return head_dim == 256 || row
 
 template <int D, bool E4M3, int NT>
 size_t attention_smem() {
-  return sizeof(float) * kAttnWarps * (D / 16) * NT * 4 * 32;
+  return 1024 + std::max<size_t>(sizeof(float) * kAttnWarps * (D / 16) * NT * 4 * 32,
+                                 static_cast<size_t>(kAttnWarps) * AttnTile<D>::STAGES * AttnTile<D>::STAGE);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The cache's codes [blocks * kv_heads, block, D] in boxes of `rows` tokens by
+// at most 128 bytes.  A third dimension for the block keeps every coordinate
+// below 2^31 however large the cache is.
+i8_status encode_cache(CUtensorMap* map, const void* base, const i8_kv_cache& c, int rows) {
+  static std::mutex mu;
+  static EncodeTiledFn encode = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                           &q) != cudaSuccess ||
+          q != cudaDriverEntryPointSuccess || !fn)
+        return I8_ERR_CUDA;
+      encode = reinterpret_cast<EncodeTiledFn>(fn);
+    }
+  }
+  // (a cache of no blocks is never read: any extent and address will do)
+  const cuuint64_t D = c.head_dim, B = c.block_size;
+  const cuuint64_t dims[3] = {D, B, std::max<cuuint64_t>(1, static_cast<cuuint64_t>(c.blocks) * c.kv_heads)};
+  const cuuint64_t strides[2] = {D, D * B};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(std::min<cuuint64_t>(D, 128)),
+                             static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? I8_OK
+             : I8_ERR_CUDA;
 }
 
 // CTAs of a kernel that are resident at once.
@@ -136,7 +177,8 @@ size_t attention_ws(int workers) {
 }
 
 template <int D, bool E4M3, int NT>
-i8_status launch_attention(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need, cudaStream_t st) {
+i8_status launch_attention(AttnArgs& a, const i8_kv_cache* cache, void* ws, size_t ws_bytes,
+                           size_t* need, cudaStream_t st) {
   int workers;
   if (i8_status e = attention_workers<D, E4M3, NT>(&workers)) return e;
   const size_t bytes = attention_ws<D, NT>(workers);
@@ -148,9 +190,16 @@ i8_status launch_attention(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need,
   if (!aligned16(ws)) return I8_ERR_ALIGNMENT;
   a.cut = static_cast<int4*>(ws);
   a.pieces = reinterpret_cast<float*>(a.cut + 2 * static_cast<size_t>(workers));
+  a.unit_cols = AttnTile<D>::UNIT / a.block;
+  a.unit_rest = AttnTile<D>::UNIT % a.block;
+  a.box_rows = AttnTile<D>::HALVES == 2 && a.block % 32 == 0 ? 32 : 16;
+  CUtensorMap k_map, v_map;
+  const bool any = cache->blocks > 0;
+  if (i8_status e = encode_cache(&k_map, any ? cache->k : ws, *cache, a.box_rows)) return e;
+  if (i8_status e = encode_cache(&v_map, any ? cache->v : ws, *cache, a.box_rows)) return e;
   const dim3 grid(static_cast<unsigned>(workers));
   if (cudaError_t e = launch_pdl(kv_attention_kernel<D, E4M3, NT>, grid, dim3(kAttnThreads),
-                                 attention_smem<D, E4M3, NT>(), st, a))
+                                 attention_smem<D, E4M3, NT>(), st, a, k_map, v_map))
     return cuda_status(e);
   return cuda_status(launch_pdl(kv_attention_join_kernel<D, NT>, dim3(grid.x, NT),
                                 dim3(kAttnThreads * kJoinGroups), 0, st, a));
@@ -158,24 +207,25 @@ i8_status launch_attention(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need,
 
 // Runs the attention, or with `need` only says how much workspace it wants.
 template <int D, bool E4M3>
-i8_status attention_nt_dispatch(AttnArgs& a, void* ws, size_t ws_bytes, size_t* need, cudaStream_t st) {
+i8_status attention_nt_dispatch(AttnArgs& a, const i8_kv_cache* cache, void* ws, size_t ws_bytes,
+                                size_t* need, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
-  if (attention_nt(rows, D) == 1) return launch_attention<D, E4M3, 1>(a, ws, ws_bytes, need, st);
-  return launch_attention<D, E4M3, D == 256 ? 1 : 2>(a, ws, ws_bytes, need, st);
+  if (attention_nt(rows, D) == 1) return launch_attention<D, E4M3, 1>(a, cache, ws, ws_bytes, need, st);
+  return launch_attention<D, E4M3, D == 256 ? 1 : 2>(a, cache, ws, ws_bytes, need, st);
 }
 
-i8_status attention_dispatch(AttnArgs& a, int head_dim, bool e4m3, void* ws, size_t ws_bytes,
-                             size_t* need, cudaStream_t st) {
+i8_status attention_dispatch(AttnArgs& a, const i8_kv_cache* cache, int head_dim, bool e4m3,
+                             void* ws, size_t ws_bytes, size_t* need, cudaStream_t st) {
   switch (head_dim) {
     case 64:
-      return e4m3 ? attention_nt_dispatch<64, true>(a, ws, ws_bytes, need, st)
-                  : attention_nt_dispatch<64, false>(a, ws, ws_bytes, need, st);
+      return e4m3 ? attention_nt_dispatch<64, true>(a, cache, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<64, false>(a, cache, ws, ws_bytes, need, st);
     case 128:
-      return e4m3 ? attention_nt_dispatch<128, true>(a, ws, ws_bytes, need, st)
-                  : attention_nt_dispatch<128, false>(a, ws, ws_bytes, need, st);
+      return e4m3 ? attention_nt_dispatch<128, true>(a, cache, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<128, false>(a, cache, ws, ws_bytes, need, st);
     case 256:
-      return e4m3 ? attention_nt_dispatch<256, true>(a, ws, ws_bytes, need, st)
-                  : attention_nt_dispatch<256, false>(a, ws, ws_bytes, need, st);
+      return e4m3 ? attention_nt_dispatch<256, true>(a, cache, ws, ws_bytes, need, st)
+                  : attention_nt_dispatch<256, false>(a, cache, ws, ws_bytes, need, st);
   }
   return I8_ERR_UNSUPPORTED;
 }
@@ -302,7 +352,7 @@ size_t i8_paged_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int
   a.kv_heads = static_cast<int32_t>(kv_heads);
   a.max_new = static_cast<int32_t>(max_new);
   size_t need = 0;
-  if (attention_dispatch(a, static_cast<int>(head_dim), fmt == I8_CODES_E4M3, nullptr, 0, &need,
+  if (attention_dispatch(a, nullptr, static_cast<int>(head_dim), fmt == I8_CODES_E4M3, nullptr, 0, &need,
                          nullptr) != I8_OK)
     return 0;
   return need;
@@ -337,8 +387,6 @@ i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head,
   a.q = static_cast<const uint16_t*>(q);
   a.ldq_token = ldq_token;
   a.ldq_head = ldq_head;
-  a.k = static_cast<const uint8_t*>(cache->k);
-  a.v = static_cast<const uint8_t*>(cache->v);
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
   a.table = block_tables;
@@ -358,7 +406,7 @@ i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head,
   a.q_heads = static_cast<int32_t>(q_heads);
   a.kv_heads = cache->kv_heads;
   a.max_new = static_cast<int32_t>(std::min(max_new, tokens));
-  return attention_dispatch(a, cache->head_dim, cache->fmt == I8_CODES_E4M3, ws, ws_bytes, nullptr,
+  return attention_dispatch(a, cache, cache->head_dim, cache->fmt == I8_CODES_E4M3, ws, ws_bytes, nullptr,
                             reinterpret_cast<cudaStream_t>(stream));
 }
 
