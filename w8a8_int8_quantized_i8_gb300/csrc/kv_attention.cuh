@@ -92,7 +92,8 @@ struct AttnArgs {
   int32_t requests, width, block;
   int32_t q_heads, kv_heads, max_new;
   int32_t unit_cols, unit_rest;  // unit / block, unit % block
-  int32_t box_rows;           // tokens of a TMA box: 16 or 32
+  int32_t box_rows;           // tokens of a TMA box
+  int32_t split_rows;         // requests of this many rows a kv head are kv_prefill.cuh's
   float* pieces;              // workspace: [2 * workers][8 * NT * (D + 2)]
   int4* cut;                  // [2 * workers]: the item begun, but not ended, by a worker
 };
@@ -191,6 +192,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   a.tiles = static_cast<int>((static_cast<int64_t>(a.fresh) * (p.q_heads / p.kv_heads) + ROWS - 1) / ROWS);
   a.per_item = max(1, (a.len + UNIT - 1) / UNIT);  // one even where there is nothing to see
   a.units = static_cast<int64_t>(a.per_item) * a.tiles * p.kv_heads;
+  if (static_cast<int64_t>(a.fresh) * (p.q_heads / p.kv_heads) >= p.split_rows) a.units = 0;
   return a;
 }
 

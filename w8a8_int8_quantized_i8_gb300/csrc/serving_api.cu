@@ -13,6 +13,7 @@
 #include "host.h"
 #include "kv_append.cuh"
 #include "kv_attention.cuh"
+#include "kv_prefill.cuh"
 #include "ptx.cuh"
 #include "rmsnorm.cuh"
 
@@ -116,9 +117,10 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // The cache's codes [blocks * kv_heads, block, D] in boxes of `rows` tokens by
-// at most 128 bytes.  A third dimension for the block keeps every coordinate
+// at most 128 bytes, swizzled (the warps' fragments) or as they are.  A third dimension for the block keeps every coordinate
 // below 2^31 however large the cache is.
-i8_status encode_cache(CUtensorMap* map, const void* base, const i8_kv_cache& c, int rows) {
+i8_status encode_cache(CUtensorMap* map, const void* base, const i8_kv_cache& c, int rows,
+                       bool swizzle) {
   static std::mutex mu;
   static EncodeTiledFn encode = nullptr;
   {
@@ -142,7 +144,9 @@ i8_status encode_cache(CUtensorMap* map, const void* base, const i8_kv_cache& c,
   const cuuint32_t elem[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
                 elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                !swizzle  ? CU_TENSOR_MAP_SWIZZLE_NONE
+                : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? I8_OK
@@ -176,6 +180,27 @@ size_t attention_ws(int workers) {
   return static_cast<size_t>(workers) * 2 * (sizeof(int4) + sizeof(float) * 8 * NT * (D + 2));
 }
 
+// Rows of a request and kv head from which the tcgen05 kernel takes it.
+constexpr int kPrefillRows = 96;
+
+template <int D, bool E4M3>
+i8_status launch_prefill(AttnArgs a, const i8_kv_cache* cache, void* ws, cudaStream_t st) {
+  constexpr size_t smem = 1024 + PrefillSmem<D>::BYTES;
+  if (i8_status e = allow_smem<kv_prefill_kernel<D, E4M3>>(smem)) return e;
+  // the largest box of tokens that ends neither inside a block nor inside a tile
+  a.box_rows = 16;
+  while (a.box_rows < kPreTokens && a.block % (2 * a.box_rows) == 0) a.box_rows *= 2;
+  CUtensorMap k_map, v_map;
+  const bool any = cache->blocks > 0;
+  if (i8_status e = encode_cache(&k_map, any ? cache->k : ws, *cache, a.box_rows, false)) return e;
+  if (i8_status e = encode_cache(&v_map, any ? cache->v : ws, *cache, a.box_rows, false)) return e;
+  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
+  const int64_t items = (rows + kPreRows - 1) / kPreRows * a.requests * a.kv_heads;
+  if (items > INT32_MAX) return I8_ERR_UNSUPPORTED;
+  return cuda_status(launch_pdl(kv_prefill_kernel<D, E4M3>, dim3(static_cast<unsigned>(items)),
+                                dim3(kPreThreads), smem, st, a, k_map, v_map));
+}
+
 template <int D, bool E4M3, int NT>
 i8_status launch_attention(AttnArgs& a, const i8_kv_cache* cache, void* ws, size_t ws_bytes,
                            size_t* need, cudaStream_t st) {
@@ -190,13 +215,20 @@ i8_status launch_attention(AttnArgs& a, const i8_kv_cache* cache, void* ws, size
   if (!aligned16(ws)) return I8_ERR_ALIGNMENT;
   a.cut = static_cast<int4*>(ws);
   a.pieces = reinterpret_cast<float*>(a.cut + 2 * static_cast<size_t>(workers));
+  a.split_rows = INT32_MAX;
+  if constexpr (D <= 128) {
+    if (static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads) >= kPrefillRows) {
+      a.split_rows = kPrefillRows;
+      if (i8_status e = launch_prefill<D, E4M3>(a, cache, ws, st)) return e;
+    }
+  }
   a.unit_cols = AttnTile<D>::UNIT / a.block;
   a.unit_rest = AttnTile<D>::UNIT % a.block;
   a.box_rows = AttnTile<D>::HALVES == 2 && a.block % 32 == 0 ? 32 : 16;
   CUtensorMap k_map, v_map;
   const bool any = cache->blocks > 0;
-  if (i8_status e = encode_cache(&k_map, any ? cache->k : ws, *cache, a.box_rows)) return e;
-  if (i8_status e = encode_cache(&v_map, any ? cache->v : ws, *cache, a.box_rows)) return e;
+  if (i8_status e = encode_cache(&k_map, any ? cache->k : ws, *cache, a.box_rows, true)) return e;
+  if (i8_status e = encode_cache(&v_map, any ? cache->v : ws, *cache, a.box_rows, true)) return e;
   const dim3 grid(static_cast<unsigned>(workers));
   if (cudaError_t e = launch_pdl(kv_attention_kernel<D, E4M3, NT>, grid, dim3(kAttnThreads),
                                  attention_smem<D, E4M3, NT>(), st, a, k_map, v_map))
