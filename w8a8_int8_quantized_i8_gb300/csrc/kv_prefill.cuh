@@ -80,22 +80,63 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// Waits for the tcgen05.ld that fills r; naming the registers keeps their uses
+// behind the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
+                                                     unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 32 lanes x 32 consecutive 32-bit columns from the warp's registers.
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 consecutive 32-bit columns, to and from the warp's registers.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void sts_16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -221,38 +262,40 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_at + 32 * q, s[q]);
-      tmem_wait_ld();
+      // S is read twice, in chunks of 32 columns of which the next is on its
+      // way: for the maximum, then for P.  P takes S's place as it goes.
       const PrefillScales& z = sc[j & 3];
-      float f[kPreGranules], b[kPreGranules];
-#pragma unroll
-      for (int g = 0; g < kPreGranules; ++g) {
-        f[g] = z.k[g] * rowfac;
-        b[g] = z.lv[g];
-      }
       const int seen = limit - j * kPreTokens;  // columns below this are seen
-      if (__any_sync(0xFFFFFFFFu, seen < kPreTokens)) {
-#pragma unroll
-        for (int g = 0; g < kPreGranules; ++g) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int col = 16 * g + k;
-            const float x = fmaf(__uint_as_float(s[col >> 5][col & 31]), f[g], b[g]);
-            s[col >> 5][col & 31] = __float_as_uint(col < seen ? x : -INFINITY);
-          }
-          f[g] = 1.0f;
-          b[g] = 0.0f;
-        }
-      }
+      const bool masked = __any_sync(0xFFFFFFFFu, seen < kPreTokens);
+      uint32_t s[2][32];
+      tmem_ld_32x32b_x32(s_at, s[0]);
       float top = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < kPreGranules; ++g) {
-        float x = __uint_as_float(s[g >> 1][16 * (g & 1)]);
+      for (int q = 0; q < 4; ++q) {
+        tmem_wait_ld(s[q & 1]);
+        tmem_ld_32x32b_x32(s_at + 32 * ((q + 1) & 3), s[(q + 1) & 1]);
 #pragma unroll
-        for (int k = 1; k < 16; ++k) x = fmaxf(x, __uint_as_float(s[g >> 1][16 * (g & 1) + k]));
-        top = fmaxf(top, fmaf(x, f[g], b[g]));
+        for (int g = 0; g < 2; ++g) {
+          uint32_t* v = &s[q & 1][16 * g];
+          const float f = z.k[2 * q + g] * rowfac, b = z.lv[2 * q + g];
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = fmaf(__uint_as_float(v[k]), f, b);
+              top = fmaxf(top, 32 * q + 16 * g + k < seen ? x : -INFINITY);
+            }
+          } else {
+            float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+            for (int k = 6; k < 14; k += 4) {
+              x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
+            x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
+            top = fmaxf(top, fmaf(fmaxf(x, y), f, b));
+          }
+        }
       }
       float alpha = 1.0f;
       if (top > R + 8.0f) {  // (-inf + 8 is -inf)
@@ -263,33 +306,49 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && j > 0) {
         // S of this tile was committed after the last product into O, so O is
         // complete
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(o_at + 16 * q, o);
+          tmem_wait_ld(o);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(o_at + 32 * q, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st_32x32b_x32(o_at + 32 * q, o);
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st_32x32b_x16(o_at + 16 * q, o);
         }
       }
       const float ref = (R > -INFINITY ? R : 0.0f) - 6.0f;
-      uint32_t pk[2][32];
+      uint32_t pk[16];
 #pragma unroll
-      for (int g = 0; g < kPreGranules; ++g) {
-        const float shift = b[g] - ref;
-        float sum = 0.0f;
+      for (int q = 0; q < 4; ++q) {
+        tmem_wait_ld(s[q & 1]);
+        if (q < 3) tmem_ld_32x32b_x32(s_at + 32 * (q + 1), s[(q + 1) & 1]);
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const float e0 = ex2(fmaf(__uint_as_float(s[g >> 1][16 * (g & 1) + k]), f[g], shift));
-          const float e1 = ex2(fmaf(__uint_as_float(s[g >> 1][16 * (g & 1) + k + 1]), f[g], shift));
-          sum += e0 + e1;
-          pk[g >> 2][8 * (g & 3) + (k >> 1)] = pack_f16x2(e0, e1);
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t* v = &s[q & 1][16 * g];
+          const float f = z.k[2 * q + g] * rowfac, b = z.lv[2 * q + g] - ref;
+          const unsigned long long ff = f2(f, f), bb = f2(b, b);
+          unsigned long long sum[2];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float e0, e1;
+            f2_split(f2_fma(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, bb), e0, e1);
+            if (masked) {
+              e0 = 32 * q + 16 * g + k < seen ? e0 : -INFINITY;
+              e1 = 32 * q + 16 * g + k + 1 < seen ? e1 : -INFINITY;
+            }
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            const unsigned long long e = f2(e0, e1);
+            sum[(k >> 1) & 1] = k < 4 ? e : f2_add(sum[(k >> 1) & 1], e);
+            pk[8 * g + (k >> 1)] = pack_f16x2(e0, e1);
+          }
+          float s0, s1;
+          f2_split(f2_add(sum[0], sum[1]), s0, s1);
+          l = fmaf(s0 + s1, z.back[2 * q + g], l);
         }
-        l = fmaf(sum, z.back[g], l);
+        // columns 16q .. of P: those of S are read already
+        tmem_st_32x32b_x16(s_at + 16 * q, pk);
       }
-      tmem_st_32x32b_x32(s_at, pk[0]);
-      tmem_st_32x32b_x32(s_at + 32, pk[1]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -308,7 +367,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         uint32_t o[32];
         if (n > 0) {
           tmem_ld_32x32b_x32(o_at + 32 * q, o);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
         }
         if (real) {
 #pragma unroll
