@@ -70,13 +70,32 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_n(uint32_t saddr, uint32_t n
   return d | (static_cast<uint64_t>(n_stride >> 4) << 16);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16, one CTA.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem]^T, kind::f16, one CTA, A in shared memory or in
+// TMEM; and the commit that arrives on `bar` when what was issued is done.  The
+// whole warp calls, its elected lane (the same one every time) issues: kept in
+// converged code the operands stay in uniform registers, where the instruction
+// wants them.  Issued by one lane of a divergent branch, each product of eight
+// took about 980 cycles instead of 512.
+__device__ __forceinline__ void mma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
@@ -156,7 +175,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __shared__ float sm_ref;
   __shared__ uint32_t sm_tmem;
   __shared__ int abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int group = p.q_heads / p.kv_heads;
   const uint32_t base = (smem_u32(sm_pre) + 1023u) & ~1023u;
 
@@ -464,58 +483,62 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     } else if (warp == 9) {
       // ================================================================= products
-      if (lane == 0 && n > 0) {
+      if (n > 0) {
         constexpr uint32_t kIdS = idesc_f16_f32(128, kPreTokens);
         constexpr uint32_t kIdO = idesc_f16_f32(128, D) | (1u << 16);  // B is N-major
         const uint32_t kv0 = base + Sm::KV;
         auto product_s = [&](int t, int slot) {
+          const uint64_t a = smem_desc_sw128(base + Sm::Q + t * Sm::TILE);
+          const uint64_t b = smem_desc_sw128(kv0 + slot * Sm::TILE);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_f16_ss(tmem + t * 128, smem_desc_sw128(base + Sm::Q + t * Sm::TILE + at),
-                       smem_desc_sw128(kv0 + slot * Sm::TILE + at), kIdS, k > 0);
+            const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            mma_f16_ss_warp(tmem + t * 128, a + at, b + at, kIdS, k > 0);
           }
         };
         auto product_o = [&](int t, int slot, bool first) {
+          const uint64_t b = smem_desc_sw128_n(kv0 + slot * Sm::TILE, 16384);
 #pragma unroll
           for (int k = 0; k < kPreTokens / 16; ++k)
-            mma_f16_ts(tmem + 256 + t * D, tmem + t * 128 + 8 * k,
-                       smem_desc_sw128_n(kv0 + slot * Sm::TILE + k * 2048, 16384), kIdO,
-                       !(first && k == 0));
+            mma_f16_ts_warp(tmem + 256 + t * D, tmem + t * 128 + 8 * k, b + k * (2048 >> 4), kIdO,
+                            !(first && k == 0));
         };
         auto wait_kv = [&](int it) {
-          return mbar_wait(smem_u32(&kv_full[it % kPreSlots]), (it / kPreSlots) & 1, &abort_flag);
+          return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&kv_full[it % kPreSlots]),
+                                                   (it / kPreSlots) & 1, &abort_flag));
         };
-        bool ok = mbar_wait(smem_u32(&q_full), 0, &abort_flag) && wait_kv(0);
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&q_full), 0, &abort_flag)) && wait_kv(0);
         if (ok) {
           tc_fence_after();
           for (int t = 0; t < 2; ++t) {
             product_s(t, 0);
-            mma_commit(smem_u32(&s_full[t]));
+            mma_commit_warp(smem_u32(&s_full[t]));
           }
-          mma_commit(smem_u32(&kv_empty[0]));
+          mma_commit_warp(smem_u32(&kv_empty[0]));
         }
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
           const int v_slot = (2 * j + 1) % kPreSlots, k_slot = (2 * j + 2) % kPreSlots;
           const bool more = j + 1 < n;
           ok = wait_kv(2 * j + 1) && (!more || wait_kv(2 * j + 2));
-          for (int t = 0; t < 2 && ok; ++t) {
-            ok = mbar_wait(smem_u32(&p_full[t]), j & 1, &abort_flag);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&p_full[t]), j & 1, &abort_flag));
             if (!ok) break;
             tc_fence_after();
             product_o(t, v_slot, j == 0);
-            if (t == 1) mma_commit(smem_u32(&kv_empty[v_slot]));
+            if (t == 1) mma_commit_warp(smem_u32(&kv_empty[v_slot]));
             if (more) {
               product_s(t, k_slot);
-              mma_commit(smem_u32(&s_full[t]));
+              mma_commit_warp(smem_u32(&s_full[t]));
             }
           }
-          if (ok && more) mma_commit(smem_u32(&kv_empty[k_slot]));
+          if (ok && more) mma_commit_warp(smem_u32(&kv_empty[k_slot]));
         }
-        if (ok) mma_commit(smem_u32(&o_full));
-        else {  // the products in flight end (bounded) before TMEM is freed
-          mma_commit(smem_u32(&drained));
+        if (ok) {
+          mma_commit_warp(smem_u32(&o_full));
+        } else {  // the products in flight end (bounded) before TMEM is freed
+          mma_commit_warp(smem_u32(&drained));
           mbar_wait_bounded(smem_u32(&drained), 0, 1000000000ull);
         }
       }
