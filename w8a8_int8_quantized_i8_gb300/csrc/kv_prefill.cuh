@@ -5,7 +5,7 @@
 // query head of one kv head, token-major) as two tiles of 128, and goes over
 // the keys 128 tokens at a time:
 //   S_t = Q_t K^T  -> TMEM      (fp16 x fp16, exact products, fp32 sums)
-//   P_t = 2^(s + log2 sv - R)   softmax threads, one row each, P back to TMEM
+//   P_t = 2^(s + log2 sv - R)   softmax threads, P back to TMEM
 //   O_t += P_t V   -> TMEM      (A operand from TMEM, V as it lies: N-major)
 // with s = S * sk * scale * log2 e and sv, sk the block's scales.  The two
 // tiles take turns: while one tile's softmax runs, the tensor cores do the
@@ -20,9 +20,10 @@
 // stays below 2^14.  The sum of exponentials is kept in fp32 beside it, each
 // 16 tokens' sum of P times 2^(Lr - log2 sv), Lr a fixed reference.
 //
-// Roles: warps 0-7 softmax (tile = warp / 4; a warp reads the 32 TMEM lanes of
-// its place in the warpgroup), warp 8 copies by TMA and prepares the scales,
-// warp 9 issues the MMAs, warps 10-15 convert.  At 128 head dimensions 208 KB
+// Roles: warps 0-15 softmax (tile = warp / 8; a row has two threads, each for
+// half of the keys, which agree on R once a tile; a warp reads the 32 TMEM
+// lanes of its place in the warpgroup), warp 16 copies by TMA and prepares the
+// scales, warp 17 issues the MMAs, warps 18-23 convert.  At 128 head dimensions 208 KB
 // of shared memory (Q 64, three fp16 tiles 96, three tiles of codes 48) and all
 // of TMEM (S 2 x 128, O 2 x 128 columns): one CTA an SM.
 #pragma once
@@ -37,7 +38,8 @@
 
 namespace i8 {
 
-constexpr int kPreThreads = 512;
+constexpr int kPreThreads = 768;
+constexpr int kPreSoftWarps = 16;
 constexpr int kPreRows = 256;      // rows of an item
 constexpr int kPreTokens = 128;    // tokens of a tile of keys
 constexpr int kPreConvWarps = 6;
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       kv_empty[kPreSlots], sc_full[kPreScales], s_full[2], p_full[2], q_full, o_full, drained;
   __shared__ PrefillScales sc[kPreScales];
   __shared__ float sm_ref;
+  __shared__ float sm_top[2][2][128], sm_sum[2][2][128];  // [tile][half of the keys][row]
   __shared__ uint32_t sm_tmem;
   __shared__ int abort_flag;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -190,9 +193,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int i = 0; i < kPreScales; ++i) mbar_init(smem_u32(&sc_full[i]), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&p_full[i]), kPreSoftWarps / 2);
     }
-    mbar_init(smem_u32(&q_full), 8);
+    mbar_init(smem_u32(&q_full), kPreSoftWarps);
     mbar_init(smem_u32(&o_full), 1);
     mbar_init(smem_u32(&drained), 1);
     tma_prefetch_desc(&k_map);
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int last_row = min(row0 + kPreRows, rows) - 1;
   const int end = min(max(pos0 + last_row / group + 1, 0), rq.len);
   const int n = (end + kPreTokens - 1) / kPreTokens;  // tiles of keys
-  if (warp == 9) {
+  if (warp == kPreSoftWarps + 1) {
     tmem_alloc(smem_u32(&sm_tmem), 512);
     tmem_relinquish();
   }
@@ -224,24 +227,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm_tmem;
 
-  if (warp < 8) {
+  if (warp < kPreSoftWarps) {
     // =================================================================== softmax
-    regs_inc<192>();
-    const int t = warp >> 2;
-    const int row = row0 + t * 128 + (warp & 3) * 32 + lane;
+    regs_inc<96>();
+    const int t = warp >> 3, half = (warp >> 2) & 1;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile
+    const int row = row0 + t * 128 + r;
     const bool real = row < rows;
     const int i = real ? row / group : 0;
     const int hq = head * group + (real ? row - i * group : 0);
     float rowfac;
     {
-      // q's row: its power of two, then fp16 into the swizzled tile
-      const uint16_t* qp = p.q + (static_cast<int64_t>(rq.q0) + i) * p.ldq_token + hq * p.ldq_head;
-      uint4 w[D / 8];
+      // q's row: its power of two, then this thread's half in fp16 into the
+      // swizzled tile
+      const uint4* qp = reinterpret_cast<const uint4*>(
+          p.q + (static_cast<int64_t>(rq.q0) + i) * p.ldq_token + hq * p.ldq_head);
       uint32_t amax = 0;
-#pragma unroll
+#pragma unroll 8
       for (int c = 0; c < D / 8; ++c) {
-        w[c] = real ? __ldg(reinterpret_cast<const uint4*>(qp) + c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t a = x[k] & 0x7FFF7FFFu;
@@ -253,11 +258,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       rowfac = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (E4M3 ? 256.0f : 1.0f) *
                fabsf(p.scale_log2);
       if (p.scale_log2 < 0.0f) up = -up;  // the factor of S is never negative
-      const int r = (warp & 3) * 32 + lane;
       const uint32_t to = base + Sm::Q + t * Sm::TILE + r * 128;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll 4
+      for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+        const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
         uint32_t y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -270,52 +275,57 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     const int limit = real ? min(max(pos0 + i + 1, 0), rq.len) : 0x7FFFFFFF;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
-    const uint32_t s_at = tmem + lanes + t * 128;
-    const uint32_t o_at = tmem + lanes + 256 + t * D;
+    const uint32_t s_at = tmem + lanes + t * 128 + half * 64;  // this half's S
+    const uint32_t p_at = tmem + lanes + t * 128 + half * 32;  // and P
+    const uint32_t o_at = tmem + lanes + 256 + t * D + half * (D / 2);
     float R = -INFINITY, l = 0.0f;
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      ok = mbar_wait(smem_u32(&sc_full[j & 3]), (j >> 2) & 1, &abort_flag) &&
+      ok = ok && mbar_wait(smem_u32(&sc_full[j & 3]), (j >> 2) & 1, &abort_flag) &&
            mbar_wait(smem_u32(&s_full[t]), j & 1, &abort_flag);
       ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      if (!ok) {  // given up: only keep the tile's barrier company
+        named_bar_sync(1 + t, 256);
+        continue;
+      }
       tc_fence_after();
-      // S is read twice, in chunks of 32 columns of which the next is on its
-      // way: for the maximum, then for P.  P takes S's place as it goes.
       const PrefillScales& z = sc[j & 3];
-      const int seen = limit - j * kPreTokens;  // columns below this are seen
-      const bool masked = __any_sync(0xFFFFFFFFu, seen < kPreTokens);
+      const int seen = limit - j * kPreTokens - 64 * half;  // columns below this are seen
+      const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
       uint32_t s[2][32];
       tmem_ld_32x32b_x32(s_at, s[0]);
+      tmem_ld_32x32b_x32(s_at + 32, s[1]);
+      tmem_wait_ld(s[0]);
+      tmem_wait_ld(s[1]);
       float top = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_wait_ld(s[q & 1]);
-        tmem_ld_32x32b_x32(s_at + 32 * ((q + 1) & 3), s[(q + 1) & 1]);
+      for (int g = 0; g < 4; ++g) {
+        uint32_t* v = &s[g >> 1][16 * (g & 1)];
+        const float f = z.k[4 * half + g] * rowfac, b = z.lv[4 * half + g];
+        if (masked) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t* v = &s[q & 1][16 * g];
-          const float f = z.k[2 * q + g] * rowfac, b = z.lv[2 * q + g];
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float x = fmaf(__uint_as_float(v[k]), f, b);
-              top = fmaxf(top, 32 * q + 16 * g + k < seen ? x : -INFINITY);
-            }
-          } else {
-            float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-            float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
-#pragma unroll
-            for (int k = 6; k < 14; k += 4) {
-              x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-              y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-            }
-            x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
-            top = fmaxf(top, fmaf(fmaxf(x, y), f, b));
+          for (int k = 0; k < 16; ++k) {
+            const float x = fmaf(__uint_as_float(v[k]), f, b);
+            top = fmaxf(top, 16 * g + k < seen ? x : -INFINITY);
           }
+        } else {
+          float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+          float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+          for (int k = 6; k < 14; k += 4) {
+            x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+            y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+          }
+          x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
+          top = fmaxf(top, fmaf(fmaxf(x, y), f, b));
         }
       }
+      // the row's two threads agree on the maximum.  Both have read their S
+      // after the barrier, so that either may overwrite any of it with P.
+      sm_top[t][half][r] = top;
+      named_bar_sync(1 + t, 256);
+      top = fmaxf(top, sm_top[t][half ^ 1][r]);
       float alpha = 1.0f;
       if (top > R + 8.0f) {  // (-inf + 8 is -inf)
         alpha = R > -INFINITY ? ex2(R - top) : 0.0f;
@@ -324,9 +334,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && j > 0) {
         // S of this tile was committed after the last product into O, so O is
-        // complete
+        // complete; each thread rescales its half of the head dimensions
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
+        for (int q = 0; q < D / 32; ++q) {
           uint32_t o[16];
           tmem_ld_32x32b_x16(o_at + 16 * q, o);
           tmem_wait_ld(o);
@@ -336,15 +346,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
       const float ref = (R > -INFINITY ? R : 0.0f) - 6.0f;
-      uint32_t pk[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_wait_ld(s[q & 1]);
-        if (q < 3) tmem_ld_32x32b_x32(s_at + 32 * (q + 1), s[(q + 1) & 1]);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint32_t* v = &s[q & 1][16 * g];
-          const float f = z.k[2 * q + g] * rowfac, b = z.lv[2 * q + g] - ref;
+          const uint32_t* v = &s[q][16 * g];
+          const int gr = 4 * half + 2 * q + g;
+          const float f = z.k[gr] * rowfac, b = z.lv[gr] - ref;
           const unsigned long long ff = f2(f, f), bb = f2(b, b);
           unsigned long long sum[2];
 #pragma unroll
@@ -363,34 +372,36 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
           float s0, s1;
           f2_split(f2_add(sum[0], sum[1]), s0, s1);
-          l = fmaf(s0 + s1, z.back[2 * q + g], l);
+          l = fmaf(s0 + s1, z.back[gr], l);
         }
-        // columns 16q .. of P: those of S are read already
-        tmem_st_32x32b_x16(s_at + 16 * q, pk);
+        tmem_st_32x32b_x16(p_at + 16 * q, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
     }
-    // ---- out
+    // ---- out: each thread its half of the head dimensions
+    sm_sum[t][half][r] = l;
+    named_bar_sync(1 + t, 256);
+    l += sm_sum[t][half ^ 1][r];
     if (n > 0 && ok) ok = mbar_wait(smem_u32(&o_full), 0, &abort_flag);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       tc_fence_after();
       const float inv = l > 0.0f ? __fdiv_rn(ex2(sm_ref) * (E4M3 ? 256.0f : 1.0f), l) : 0.0f;
       const int64_t token = static_cast<int64_t>(rq.q0) + i;
-      uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head;
+      uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
+        uint32_t o[16];
         if (n > 0) {
-          tmem_ld_32x32b_x32(o_at + 32 * q, o);
+          tmem_ld_32x32b_x16(o_at + 16 * q, o);
           tmem_wait_ld(o);
         }
         if (real) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
+          for (int k = 0; k < 16; k += 8) {
             uint32_t y[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -399,18 +410,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
               y[m] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            *reinterpret_cast<uint4*>(to + 32 * q + k) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(to + 16 * q + k) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
       }
-      if (real && p.lse)
+      if (real && p.lse && half == 0)
         p.lse[token * p.q_heads + hq] =
             l > 0.0f ? (R - sm_ref - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
     tc_fence_before();
   } else {
-    regs_dec<64>();
-    if (warp == 8) {
+    regs_dec<48>();
+    if (warp == kPreSoftWarps) {
       // ================================================================= copies
       const int32_t* table = p.table + req * p.ld_table;
       const int boxes = kPreTokens / p.box_rows;
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           mbar_wait_bounded(smem_u32(&raw_full[at % kPreSlots]), (at / kPreSlots) & 1, 1000000ull);
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == kPreSoftWarps + 1) {
       // ================================================================= products
       if (n > 0) {
         constexpr uint32_t kIdS = idesc_f16_f32(128, kPreTokens);
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       __syncwarp();
     } else {
       // ================================================================= conversion
-      const int cw = warp - 10;
+      const int cw = warp - kPreSoftWarps - 2;
       bool ok = true;
 #pragma unroll 1
       for (int item = 0; item < 2 * n && ok; ++item) {
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
   __syncthreads();
   pdl_trigger();
-  if (warp == 9) {
+  if (warp == kPreSoftWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
