@@ -20,11 +20,11 @@ from .binding import (I8Error, e4m3_workspace_bytes, f16codes_workspace_bytes,
                       quant_weight_perchannel_e4m3, set_option, sync_check, widen_weight_codes,
                       workspace_bytes)
 from .serving import (BlockPlan, QuantKVCache, add_rmsnorm_quant_act_pertoken, build_block_tables,
-                      kv_cache_append, paged_attention)
+                      kv_cache_append, paged_attention, paged_attention_workspace_bytes)
 
 __all__ = [
     "BlockPlan", "QuantKVCache", "add_rmsnorm_quant_act_pertoken", "build_block_tables",
-    "kv_cache_append", "paged_attention",
+    "kv_cache_append", "paged_attention", "paged_attention_workspace_bytes",
     "I8Error", "e4m3_workspace_bytes", "f16codes_workspace_bytes", "gelu_quant_act_pertoken",
     "gemm_dequant_bias_bf16_f16codes", "gemm_int32_f16codes", "get_option", "linear_f16codes",
     "quant_act_pertoken_f16codes", "gemm_dequant_bias_bf16", "gemm_e4m3_dequant_bias_bf16",

@@ -22,9 +22,8 @@
 
 namespace i8 {
 
-constexpr int kTableThreads = 512;
-constexpr int kTableMaxRequests = 16384;  // two words a request in shared memory: 128 KB
-constexpr int kTableTokensPerThread = 4;
+constexpr int kTableThreads = 1024;
+constexpr int kTableMaxRequests = 16384;  // three words a request in shared memory: 192 KB
 
 struct TableArgs {
   const int32_t* context;
@@ -43,7 +42,19 @@ struct TableArgs {
   int32_t requests;
   int32_t width;
   int32_t block;
+  int32_t shift;  // log2 of block, or -1
 };
+
+// Lengths are below 2^31, so positions fit 32 unsigned bits.
+__device__ __forceinline__ uint32_t table_column(const TableArgs& p, uint32_t position) {
+  return p.shift >= 0 ? position >> p.shift : position / static_cast<uint32_t>(p.block);
+}
+// Blocks that n tokens take, at most the table's width.
+__device__ __forceinline__ int table_blocks(const TableArgs& p, uint32_t n) {
+  const uint32_t whole = table_column(p, n);
+  return static_cast<int>(min(whole + (whole * static_cast<uint32_t>(p.block) < n ? 1u : 0u),
+                              static_cast<uint32_t>(p.width)));
+}
 
 __device__ __forceinline__ int32_t saturate_i32(int64_t v) {
   return static_cast<int32_t>(v > INT32_MAX ? INT32_MAX : v);
@@ -88,39 +99,44 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
   extern __shared__ int32_t sm_dyn[];
   __shared__ int64_t sm_scan[kTableThreads / 32][2];
   __shared__ int sm_lost;
-  int32_t* cu = sm_dyn;                    // [requests + 1]
-  int32_t* first = sm_dyn + p.requests + 1;  // [requests]: free-list index of column 0, were it fresh
+  int32_t* cu = sm_dyn;                      // [requests + 1]
+  int32_t* first = cu + p.requests + 1;      // [requests]: free-list index of column 0, were it fresh
+  int32_t* ctxs = first + p.requests;        // [requests]
   const int tid = threadIdx.x;
   if (tid == 0) sm_lost = 0;
 
   pdl_wait();
   const int64_t taken = p.taken ? max(0, *p.taken) : 0;
-  int64_t base_t = 0, base_b = taken;
-  for (int r0 = 0; r0 < p.requests; r0 += kTableThreads) {
-    const int r = r0 + tid;
-    int64_t ctx = 0, nw = 0;
-    if (r < p.requests) {
-      ctx = max(0, p.context[r]);
-      nw = max(0, p.news[r]);
+  // consecutive requests a thread, one scan of the threads' sums
+  const int each = (p.requests + kTableThreads - 1) / kTableThreads;
+  const int r_lo = min(p.requests, tid * each), r_hi = min(p.requests, r_lo + each);
+  int64_t t = 0, b = 0, base_t, base_b;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const int ctx = max(0, p.context[r]), nw = max(0, p.news[r]);
+    ctxs[r] = ctx;
+    cu[r] = nw;
+    t += nw;
+    b += table_blocks(p, static_cast<uint32_t>(ctx) + nw) - table_blocks(p, ctx);
+  }
+  scan_pair(t, b, base_t, base_b, sm_scan);
+  b += taken;
+  base_b += taken;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const int ctx = ctxs[r], nw = cu[r];
+    const int held = table_blocks(p, ctx), need = table_blocks(p, static_cast<uint32_t>(ctx) + nw);
+    cu[r] = saturate_i32(t);
+    // clamped to the free list's end: beyond it every index is out of blocks
+    first[r] = static_cast<int32_t>(min(b, p.n_free) - held);
+    if (blockIdx.x == 0) {
+      p.cu_new[r] = saturate_i32(t);
+      const int64_t len = static_cast<int64_t>(ctx) + nw;
+      p.seq_lens[r] = saturate_i32(len);
+      const int64_t have = held + min(static_cast<int64_t>(need - held), max(static_cast<int64_t>(0), p.n_free - b));
+      const int64_t lost = len - max(static_cast<int64_t>(ctx), min(len, have * p.block));
+      if (lost > 0) atomicAdd(&sm_lost, saturate_i32(lost));
     }
-    const int64_t held = min((ctx + p.block - 1) / p.block, static_cast<int64_t>(p.width));
-    const int64_t need = min((ctx + nw + p.block - 1) / p.block, static_cast<int64_t>(p.width));
-    int64_t t = nw, b = need - held, tt, tb;
-    scan_pair(t, b, tt, tb, sm_scan);
-    if (r < p.requests) {
-      cu[r] = saturate_i32(base_t + t);
-      // clamped to the free list's end: beyond it every index is out of blocks
-      first[r] = static_cast<int32_t>(min(base_b + b, p.n_free) - held);
-      if (blockIdx.x == 0) {
-        p.cu_new[r] = saturate_i32(base_t + t);
-        p.seq_lens[r] = saturate_i32(ctx + nw);
-        const int64_t have = held + min(need - held, max(static_cast<int64_t>(0), p.n_free - base_b - b));
-        const int64_t lost = ctx + nw - max(ctx, min(ctx + nw, have * p.block));
-        if (lost > 0) atomicAdd(&sm_lost, saturate_i32(lost));
-      }
-    }
-    base_t += tt;
-    base_b += tb;
+    t += nw;
+    b += need - held;
   }
   if (tid == 0) cu[p.requests] = saturate_i32(base_t);
   __syncthreads();
@@ -136,57 +152,43 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
   const int lane = tid & 31;
   const int warps = static_cast<int>(gridDim.x) * (kTableThreads / 32);
   for (int r = blockIdx.x * (kTableThreads / 32) + (tid >> 5); r < p.requests; r += warps) {
-    const int64_t ctx = max(0, p.context[r]), nw = max(0, p.news[r]);
-    const int held = static_cast<int>(min((ctx + p.block - 1) / p.block, static_cast<int64_t>(p.width)));
-    const int need = static_cast<int>(min((ctx + nw + p.block - 1) / p.block, static_cast<int64_t>(p.width)));
+    const int held = table_blocks(p, ctxs[r]);
+    const int need = table_blocks(p, static_cast<uint32_t>(ctxs[r]) + (cu[r + 1] - cu[r]));
     for (int c = held + lane; c < need; c += 32) {
       const int64_t at = static_cast<int64_t>(first[r]) + c;
       p.table[r * p.ld_table + c] = at < p.n_free ? p.free_blocks[at] : -1;
     }
   }
 
-  // the tokens: a few consecutive ones a thread, one search for the first
+  // the tokens, one a thread
   const int total = cu[p.requests];
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTableThreads * kTableTokensPerThread;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kTableThreads + tid) * kTableTokensPerThread;
-       t0 < p.max_tokens; t0 += stride) {
-    int r = 0;
-    if (t0 < total) {
-      int lo = 0, hi = p.requests;  // the last request with cu[r] <= t0 and tokens of its own
-      for (int step = 0; step < 32 && hi - lo > 1; ++step) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t0) lo = mid;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTableThreads;
+  for (int64_t tk = static_cast<int64_t>(blockIdx.x) * kTableThreads + tid; tk < p.max_tokens; tk += stride) {
+    int64_t slot = -1;
+    int pos = 0;
+    if (tk < total) {
+      int r = 0, hi = p.requests;  // the last request with cu[r] <= tk: it has tokens
+      for (int step = 0; step < 32 && hi - r > 1; ++step) {
+        const int mid = (r + hi) >> 1;
+        if (cu[mid] <= tk) r = mid;
         else hi = mid;
       }
-      r = lo;
-    }
-#pragma unroll
-    for (int j = 0; j < kTableTokensPerThread; ++j) {
-      const int64_t t = t0 + j;
-      if (t >= p.max_tokens) break;
-      int64_t slot = -1;
-      int pos = 0;
-      if (t < total) {
-        for (int skip = 0; skip < p.requests && cu[r + 1] <= t; ++skip) ++r;  // empty requests
-        const int64_t ctx = max(0, p.context[r]);
-        const int64_t at = ctx + t - cu[r];
-        pos = saturate_i32(at);
-        const int64_t c = at / p.block;
-        if (c < p.width) {
-          const int64_t held = (ctx + p.block - 1) / p.block;
-          int64_t blk;
-          if (c < held) {
-            blk = p.table[r * p.ld_table + c];
-          } else {
-            const int64_t f = first[r] + c;
-            blk = f < p.n_free ? p.free_blocks[f] : -1;
-          }
-          if (blk >= 0) slot = blk * p.block + at % p.block;
+      const uint32_t ctx = ctxs[r], at = ctx + static_cast<uint32_t>(tk - cu[r]);
+      pos = saturate_i32(at);
+      const uint32_t c = table_column(p, at);
+      if (c < static_cast<uint32_t>(p.width)) {
+        int64_t blk;
+        if (c < static_cast<uint32_t>(table_blocks(p, ctx))) {
+          blk = p.table[r * p.ld_table + c];
+        } else {
+          const int64_t f = static_cast<int64_t>(first[r]) + c;
+          blk = f < p.n_free ? p.free_blocks[f] : -1;
         }
+        if (blk >= 0) slot = blk * p.block + (at - c * static_cast<uint32_t>(p.block));
       }
-      p.slots[t] = slot;
-      p.positions[t] = pos;
     }
+    p.slots[tk] = slot;
+    p.positions[tk] = pos;
   }
 }
 

@@ -15,8 +15,12 @@
 // costs that token only, except when it is the loudest of its block yet.
 //
 // Every run is handled by one warp (short runs, a decode step) or one CTA
-// (long runs, a prefill), whole: no two CTAs write a block, no atomics.  The
-// second read of the run's rows (for the codes) hits L1 / L2.
+// (long runs, a prefill), whole: no two CTAs write a block, no atomics.  A run
+// of up to 8 vectors a thread stays in registers between the maximum and the
+// codes; of a longer one the rest is read again (from L1 / L2).
+//
+// Finding the runs is a chain of short dependent steps, so the slots that they
+// need go to shared memory first, in one load a thread.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -30,7 +34,9 @@ namespace i8 {
 
 constexpr int kAppendThreads = 128;
 constexpr int kAppendMaxWindow = 32;  // tokens a CTA looks for runs in
-constexpr int kAppendShortRun = 2;    // runs up to this are one warp's work
+constexpr int kAppendShortRun = 8;    // runs up to this are one warp's work
+constexpr int kAppendKeep = 8;        // vectors a thread keeps
+constexpr int kAppendSlots = 256;     // slots in shared memory: the one before the window, then on
 
 struct AppendSide {
   const uint16_t* src;        // bf16 [tokens, heads, D]
@@ -46,7 +52,7 @@ struct AppendArgs {
   int64_t blocks;
   int32_t heads;
   int32_t block;
-  int32_t dim;
+  int32_t dim_shift;   // log2 of the head dimension
   int32_t window;
 };
 
@@ -80,12 +86,26 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
 struct AppendRun {
   int64_t slot;  // of its first token
   int64_t at;    // its first token
+  int64_t block;
+  int off;       // its first offset in the block
   int span;
   int count;
 };
 
+// The step's slots: the window's neighbourhood from shared memory.
+struct AppendSlots {
+  const int64_t* all;
+  const int64_t* near;  // [kAppendSlots] from token w0 - 1 on
+  int64_t w0;
+  __device__ __forceinline__ int64_t operator[](int64_t t) const {
+    const int64_t i = t - w0 + 1;
+    return i >= 0 && i < kAppendSlots ? near[i] : all[t];
+  }
+};
+
 // The first token from t on that is not skipped, or T (the whole warp calls).
-__device__ __forceinline__ int64_t next_token(const int64_t* slots, int64_t t, int64_t T, int lane) {
+__device__ __forceinline__ int64_t next_token(const AppendSlots& slots, int64_t t, int64_t T,
+                                              int lane) {
   for (; t < T; t += 256) {
     int first = 256;
 #pragma unroll
@@ -101,19 +121,21 @@ __device__ __forceinline__ int64_t next_token(const int64_t* slots, int64_t t, i
 
 // Extends a run from its first token to its last (the whole warp calls).
 // Every round finds tokens of the run or ends, so there are at most `most`.
-__device__ __forceinline__ void run_extent(const AppendArgs& p, AppendRun& r, int most, int lane) {
+__device__ __forceinline__ void run_extent(const AppendSlots& slots, int64_t T, AppendRun& r,
+                                           int most, int lane) {
   int64_t t = r.at + 1;
-  for (int round = 0; round < most && r.count < most; ++round) {
-    const bool goes_on = r.count + lane < most && t + lane < p.tokens &&
-                         p.slots[t + lane] == r.slot + r.count + lane;
+  for (int round = 0; round < most && r.count < most && t < T; ++round) {
+    const bool goes_on = r.count + lane < most && t + lane < T &&
+                         slots[t + lane] == r.slot + r.count + lane;
     const unsigned on = __ballot_sync(0xFFFFFFFFu, goes_on);
     const int n = __popc(on & ~(on + 1));  // the low ones of `on`
     r.count += n;
     t += n;
     if (n > 0) r.span = static_cast<int>(t - r.at);
     if (n == 32 || r.count == most) continue;
-    t = next_token(p.slots, t, p.tokens, lane);
-    if (t >= p.tokens || p.slots[t] != r.slot + r.count) break;
+    if (t >= T || slots[t] >= 0) break;    // another block's token
+    t = next_token(slots, t, T, lane);
+    if (t >= T || slots[t] != r.slot + r.count) break;
   }
 }
 
@@ -126,19 +148,34 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   const int64_t s0 = run.slot;
   const int64_t* slots = p.slots + run.at;
   const bool gaps = run.span != run.count;
-  const int64_t blk = s0 / p.block;
-  const int off = static_cast<int>(s0 - blk * p.block);
-  const int vecs = p.dim >> 3;  // 16-byte vectors a token
+  const int64_t blk = run.block;
+  const int off = run.off;
+  const int vs = p.dim_shift - 3;  // 16-byte vectors a token: 1 << vs
   const uint16_t* src = a.src + run.at * a.ld_token + head * a.ld_head;
   float* sp = a.scale + blk * p.heads + head;
-  uint8_t* dst = a.codes + ((blk * p.heads + head) * p.block) * p.dim;
+  uint8_t* dst = a.codes + (((blk * p.heads + head) * p.block) << p.dim_shift);
   const float s_old = off > 0 ? *sp : 0.0f;
 
   uint32_t amax2 = 0;
-  const int n = run.span * vecs;
+  const int n = run.span << vs;
+  uint4 keep[kAppendKeep];
+#pragma unroll
+  for (int q = 0; q < kAppendKeep; ++q) {
+    const int i = me + q * threads, t = i >> vs, c = i - (t << vs);
+    keep[q] = make_uint4(0u, 0u, 0u, 0u);  // (skipped tokens and the run's end: nothing louder)
+    if (i < n && !(gaps && slots[t] < 0))
+      keep[q] = *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8);
+  }
+#pragma unroll
+  for (int q = 0; q < kAppendKeep; ++q) {
+    amax2 = absmax_bf16x2(amax2, keep[q].x);
+    amax2 = absmax_bf16x2(amax2, keep[q].y);
+    amax2 = absmax_bf16x2(amax2, keep[q].z);
+    amax2 = absmax_bf16x2(amax2, keep[q].w);
+  }
 #pragma unroll 4
-  for (int i = me; i < n; i += threads) {
-    const int t = i / vecs, c = i - t * vecs;
+  for (int i = me + kAppendKeep * threads; i < n; i += threads) {
+    const int t = i >> vs, c = i - (t << vs);
     if (gaps && slots[t] < 0) continue;
     const uint4 v = *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8);
     amax2 = absmax_bf16x2(amax2, v.x);
@@ -164,7 +201,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   if (s > s_old && off > 0) {
     const float ratio = __fdiv_rn(s_old, s);
     uint2* old = reinterpret_cast<uint2*>(dst);
-    for (int i = me; i < off * vecs; i += threads) {
+    for (int i = me; i < off << vs; i += threads) {
       uint2 w = old[i];
       w.x = E4M3 ? rescale_e4m3x4(w.x, ratio) : rescale_s8x4(w.x, ratio);
       w.y = E4M3 ? rescale_e4m3x4(w.y, ratio) : rescale_s8x4(w.y, ratio);
@@ -174,16 +211,14 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   const bool fast = s >= 0x1p-126f;
   const float r = __frcp_rn(s);
   const unsigned long long rr = f2(r, r);
-  uint2* out = reinterpret_cast<uint2*>(dst + off * p.dim);
-#pragma unroll 4
-  for (int i = me; i < n; i += threads) {
-    const int t = i / vecs, c = i - t * vecs;
+  uint2* out = reinterpret_cast<uint2*>(dst + (off << p.dim_shift));
+  auto code = [&](int i, const uint4& v) {
+    const int t = i >> vs;
     int to = i;
     if (gaps) {
-      if (slots[t] < 0) continue;
-      to = static_cast<int>(slots[t] - s0) * vecs + c;
+      if (slots[t] < 0) return;
+      to = (static_cast<int>(slots[t] - s0) << vs) + i - (t << vs);
     }
-    const uint4 v = *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8);
     uint2 w = make_uint2(0u, 0u);
     if (s != 0.0f) {
       if constexpr (E4M3) {
@@ -195,54 +230,68 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
       }
     }
     out[to] = w;
+  };
+#pragma unroll
+  for (int q = 0; q < kAppendKeep; ++q)
+    if (me + q * threads < n) code(me + q * threads, keep[q]);
+  for (int i = me + kAppendKeep * threads; i < n; i += threads) {
+    const int t = i >> vs, c = i - (t << vs);
+    if (gaps && slots[t] < 0) continue;
+    code(i, *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8));
   }
 }
 
 // grid (windows of tokens, 2 * heads).
 template <bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs p) {
   __shared__ uint32_t red[kAppendThreads / 32];
   __shared__ AppendRun run[kAppendMaxWindow];
   __shared__ int n_runs;
+  __shared__ int64_t near[kAppendSlots];
   const bool values = blockIdx.y & 1;
   const int head = blockIdx.y >> 1;
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * p.window;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   pdl_wait();
+  for (int i = threadIdx.x; i < kAppendSlots; i += kAppendThreads) {
+    const int64_t t = w0 - 1 + i;
+    near[i] = t >= 0 && t < p.tokens ? p.slots[t] : -1;
+  }
+  __syncthreads();
   // warp 0 finds the runs that start in this window: lane j looks at token j
   if (warp == 0) {
+    const AppendSlots slots{p.slots, near, w0};
     const int64_t t = w0 + lane;
     bool starts = false;
-    int64_t s = -1;
-    if (lane < p.window && t < p.tokens) {
-      s = p.slots[t];
-      if (s >= 0) {
-        const int64_t blk = s / p.block;
-        int64_t before = -1;  // the slot of the last token before it that is not skipped
-        for (int64_t u = t - 1; u >= 0 && before < 0; --u) before = p.slots[u];
-        starts = true;
-        if (before >= 0 && before / p.block == blk) {
-          starts = false;  // inside a run
-          if (before + 1 != s) atomicOr(&g_status, 1u << 7);  // out of order: not written
-        }
-        if (starts && blk >= p.blocks) {
-          starts = false;
-          atomicOr(&g_status, 1u << 7);
-        }
+    int64_t s = -1, blk = 0;
+    if (lane < p.window && t < p.tokens) s = near[lane + 1];
+    if (s >= 0) {
+      blk = s / p.block;
+      int64_t before = near[lane];  // the slot of the last token before it that is not skipped
+      if (before < 0)
+        for (int64_t u = t - 2; u >= 0 && before < 0; --u) before = slots[u];
+      starts = true;
+      if (before >= 0 && before >= blk * p.block && before < (blk + 1) * p.block) {
+        starts = false;  // inside a run
+        if (before + 1 != s) atomicOr(&g_status, 1u << 7);  // out of order: not written
+      }
+      if (starts && blk >= p.blocks) {
+        starts = false;
+        atomicOr(&g_status, 1u << 7);
       }
     }
-    // a run goes on as long as the slots do, by one and inside the block
     const unsigned mask = __ballot_sync(0xFFFFFFFFu, starts);
     int i = 0;
     for (unsigned left = mask; left != 0; left &= left - 1, ++i) {
       const int at = __ffs(left) - 1;
       AppendRun r;
       r.slot = __shfl_sync(0xFFFFFFFFu, s, at);
+      r.block = __shfl_sync(0xFFFFFFFFu, blk, at);
+      r.off = static_cast<int>(r.slot - r.block * p.block);
       r.at = w0 + at;
       r.span = r.count = 1;
-      const int most = static_cast<int>(p.block - r.slot % p.block);
-      run_extent(p, r, most, lane);
+      run_extent(slots, p.tokens, r, p.block - r.off, lane);
       if (lane == 0) run[i] = r;
     }
     if (lane == 0) n_runs = __popc(mask);

@@ -324,15 +324,17 @@ i8_status i8_build_block_tables(const int32_t* context_lens, const int32_t* new_
     return I8_ERR_ALIGNMENT;
   TableArgs a{context_lens, new_lens, block_tables, free_blocks, taken, cu_new, seq_lens, slots,
               positions, counts, ld_table, n_free, max_tokens, static_cast<int32_t>(requests),
-              static_cast<int32_t>(width), static_cast<int32_t>(block_size)};
+              static_cast<int32_t>(width), static_cast<int32_t>(block_size), -1};
+  if ((block_size & (block_size - 1)) == 0)
+    for (a.shift = 0; (int64_t{1} << a.shift) < block_size;) ++a.shift;
   int sms;
   if (i8_status e = device_sms(&sms)) return e;
-  const size_t smem = sizeof(int32_t) * (2 * static_cast<size_t>(requests) + 1);
-  if (i8_status e = allow_smem<block_tables_kernel>(sizeof(int32_t) * (2 * kTableMaxRequests + 1)))
+  const size_t smem = sizeof(int32_t) * (3 * static_cast<size_t>(requests) + 1);
+  if (i8_status e = allow_smem<block_tables_kernel>(sizeof(int32_t) * (3 * kTableMaxRequests + 1)))
     return e;
-  const int64_t per = kTableThreads * kTableTokensPerThread;
   const int64_t grid = std::max<int64_t>(
-      1, std::min<int64_t>(sms, std::max((max_tokens + per - 1) / per, requests / (kTableThreads / 32))));
+      1, std::min<int64_t>(sms, std::max((max_tokens + kTableThreads - 1) / kTableThreads,
+                                         requests / (kTableThreads / 32))));
   return cuda_status(launch_pdl(block_tables_kernel, dim3(static_cast<unsigned>(grid)),
                                 dim3(kTableThreads), smem, reinterpret_cast<cudaStream_t>(stream), a));
 }
@@ -361,7 +363,7 @@ i8_status i8_kv_cache_append(const void* k, int64_t ldk_token, int64_t ldk_head,
   a.blocks = cache->blocks;
   a.heads = cache->kv_heads;
   a.block = cache->block_size;
-  a.dim = cache->head_dim;
+  a.dim_shift = cache->head_dim == 64 ? 6 : cache->head_dim == 128 ? 7 : 8;
   const int64_t units = tokens * 2 * cache->kv_heads;
   a.window = static_cast<int32_t>(std::min<int64_t>(
       kAppendMaxWindow, std::max<int64_t>(kAppendThreads / 32, units / (static_cast<int64_t>(sms) * 16))));

@@ -17,6 +17,7 @@ raises I8_ERR_DEVICE_DATA.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -24,6 +25,15 @@ import torch
 from .binding import _FMT, KVCacheInfo, _check, load
 
 _CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_bf16, _i32, _i64, _f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = load()
+    return _lib
 
 
 class BlockPlan(NamedTuple):
@@ -68,27 +78,23 @@ class QuantKVCache(NamedTuple):
         return self.k.shape[2]
 
 
-class _on_device:
-    """The stream to launch on, with the tensors' device made current for the
-    call (nothing to do where it is already)."""
-    __slots__ = ("device", "guard")
-
-    def __init__(self, device):
-        self.device, self.guard = device, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _call(fn: str, index: int, *args) -> None:
+    """Calls the library on the current stream of device `index`, made the
+    current device for the call where it is not."""
+    lib = _library()
+    if index == torch.cuda.current_device():
+        status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, fn)
 
 
-def _need(t, dtype, name, ndim, device=None):
+# The checks below cost the host a microsecond or so each, as much as a launch,
+# so each is one expression over cheap attributes; _explain says what was wrong.
+
+def _explain(t, dtype, name, ndim, index=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -97,58 +103,92 @@ def _need(t, dtype, name, ndim, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must be {ndim}-D")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
 
 
-def _vector(t, dtype, name, n, device):
-    _need(t, dtype, name, 1, device)
+def _vector(t, dtype, name, n, index):
+    """The address of a contiguous vector of n elements."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 1
+            and t.shape[0] == n and t.is_contiguous() and index >= 0):
+        return t.data_ptr()
+    _explain(t, dtype, name, 1, index)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} elements, got {t.shape[0]}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t, name, rows, cols, device):
-    """Row stride of a bf16 matrix with unit stride along its rows."""
-    _need(t, torch.bfloat16, name, 2, device)
-    if tuple(t.shape) != (rows, cols):
+def _rows(t, dtype, name, rows, cols, index):
+    """(address, row stride) of a matrix with unit stride along its rows."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 2
+            and index >= 0):
+        _explain(t, dtype, name, 2, index)
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit stride along K")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
     if rows <= 1:
-        return cols
-    if t.stride(0) < cols:
+        return t.data_ptr(), cols       # the stride of a single row says nothing
+    if ld < cols:
         raise ValueError(f"{name} rows overlap")
-    return t.stride(0)
+    return t.data_ptr(), ld
 
 
-def _heads(t, name, device, head_dim=None):
-    """(token, head) strides of a bf16 [tokens, heads, head_dim] tensor."""
-    _need(t, torch.bfloat16, name, 3, device)
-    if head_dim is not None and t.shape[2] != head_dim:
-        raise ValueError(f"{name} must have head_dim {head_dim}, got {t.shape[2]}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+def _heads(t, name, shape, index):
+    """(address, token stride, head stride) of a bf16 [tokens, heads, head_dim]."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _bf16 and t.get_device() == index and t.dim() == 3
+            and index >= 0):
+        _explain(t, _bf16, name, 3, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    token, head, unit = t.stride()
+    if unit != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit stride along head_dim")
-    # a stride along a dimension of one element says nothing
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    # the stride along a dimension of one element says nothing
+    return t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
-def _cache(cache: QuantKVCache, device) -> KVCacheInfo:
-    k, v, ks, vs = cache.k, cache.v, cache.k_scale, cache.v_scale
+def _cache(cache: QuantKVCache, index: int) -> KVCacheInfo:
+    k, v, ks, vs = cache
     fmt = _CODES.get(k.dtype) if isinstance(k, torch.Tensor) else None
     if fmt is None:
         raise TypeError("the cache's codes must be int8 or float8_e4m3fn")
-    _need(k, k.dtype, "cache.k", 4, device)
-    _need(v, k.dtype, "cache.v", 4, device)
-    _need(ks, torch.float32, "cache.k_scale", 2, device)
-    _need(vs, torch.float32, "cache.v_scale", 2, device)
-    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
-        raise ValueError("the cache's shapes do not agree")
-    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+    shape = k.shape
+    if not (k.dim() == 4 and isinstance(v, torch.Tensor) and v.dtype is k.dtype and v.shape == shape
+            and isinstance(ks, torch.Tensor) and ks.dtype is _f32 and ks.shape == shape[:2]
+            and isinstance(vs, torch.Tensor) and vs.dtype is _f32 and vs.shape == shape[:2]
+            and index >= 0 and k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == index
+            and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        _explain(k, k.dtype, "cache.k", 4, index)
+        _explain(v, k.dtype, "cache.v", 4, index)
+        _explain(ks, _f32, "cache.k_scale", 2, index)
+        _explain(vs, _f32, "cache.v_scale", 2, index)
+        if v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+            raise ValueError("the cache's shapes do not agree")
         raise ValueError("the cache must be contiguous")
-    return KVCacheInfo(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.shape[0],
-                       k.shape[2], k.shape[1], k.shape[3], fmt)
+    blocks, heads, block, dim = shape
+    return KVCacheInfo(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), blocks, block, heads, dim, fmt)
+
+
+def _device_index(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(q_heads, kv_heads, head_dim, fmt, max_new, index) -> int:
+    with torch.cuda.device(index):
+        return _library().i8_paged_attention_workspace_bytes(q_heads, kv_heads, head_dim, fmt, max_new)
+
+
+def paged_attention_workspace_bytes(q_heads: int, cache: QuantKVCache, max_new: int) -> int:
+    """Bytes of workspace that paged_attention needs for these sizes."""
+    info = _cache(cache, _device_index(cache.k, "cache.k"))
+    return _attention_workspace(q_heads, info.kv_heads, info.head_dim, info.fmt, max_new, cache.k.get_device())
 
 
 def add_rmsnorm_quant_act_pertoken(x: torch.Tensor, residual: torch.Tensor | None = None,
@@ -164,28 +204,29 @@ def add_rmsnorm_quant_act_pertoken(x: torch.Tensor, residual: torch.Tensor | Non
         raise ValueError(f"fmt must be one of {sorted(_FMT)}")
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a 2-D bf16 CUDA tensor")
+    index = _device_index(x, "x")
     M, K = x.shape
     dev = x.device
-    ldx = _matrix(x, "x", M, K, None)
-    ldr = _matrix(residual, "residual", M, K, dev) if residual is not None else 0
-    if weight is not None:
-        _vector(weight, torch.bfloat16, "weight", K, dev)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without a residual")
+    xp, ldx = _rows(x, _bf16, "x", M, K, index)
+    wp = _vector(weight, _bf16, "weight", K, index) if weight is not None else None
     code, dtype = _FMT[fmt]
     q = torch.empty((M, K), dtype=dtype, device=dev)
-    s = torch.empty((M,), dtype=torch.float32, device=dev)
-    h = residual_out
-    if residual is not None and h is None:
-        h = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    ldh = _matrix(h, "residual_out", M, K, dev) if h is not None else 0
-    with _on_device(dev) as stream:
-        _check(load().i8_add_rmsnorm_quant_act_pertoken(
-            x.data_ptr(), M, K, ldx, residual.data_ptr() if residual is not None else None, ldr,
-            weight.data_ptr() if weight is not None else None, eps, code, q.data_ptr(), K,
-            s.data_ptr(), h.data_ptr() if h is not None else None, ldh, stream),
-            "i8_add_rmsnorm_quant_act_pertoken")
-    return (q, s) if h is None else (q, s, h)
+    s = torch.empty((M,), dtype=_f32, device=dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        _call("i8_add_rmsnorm_quant_act_pertoken", index, xp, M, K, ldx, None, 0, wp, eps, code,
+              q.data_ptr(), K, s.data_ptr(), None, 0)
+        return q, s
+    rp, ldr = _rows(residual, _bf16, "residual", M, K, index)
+    if residual_out is None:
+        residual_out = torch.empty((M, K), dtype=_bf16, device=dev)
+        hp, ldh = residual_out.data_ptr(), K
+    else:
+        hp, ldh = _rows(residual_out, _bf16, "residual_out", M, K, index)
+    _call("i8_add_rmsnorm_quant_act_pertoken", index, xp, M, K, ldx, rp, ldr, wp, eps, code,
+          q.data_ptr(), K, s.data_ptr(), hp, ldh)
+    return q, s, residual_out
 
 
 def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
@@ -196,39 +237,30 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, block
     views allowed) gets the blocks that the new tokens need, from
     ``free_blocks`` (int32) in request order, beginning at entry ``taken``
     (int32 [1]; None: 0).  See i8_build_block_tables for the outputs."""
-    dev = context_lens.device
+    index = _device_index(context_lens, "context_lens")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be 1-D")
     R = context_lens.shape[0]
-    _vector(context_lens, torch.int32, "context_lens", R, None)
-    _vector(new_lens, torch.int32, "new_lens", R, dev)
-    _need(block_tables, torch.int32, "block_tables", 2, dev)
+    ctx = _vector(context_lens, _i32, "context_lens", R, index)
+    new = _vector(new_lens, _i32, "new_lens", R, index)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise TypeError("block_tables must be a 2-D int32 CUDA tensor")
     width = block_tables.shape[1]
-    if block_tables.shape[0] != R:
-        raise ValueError("block_tables must have a row for each request")
-    if width > 1 and block_tables.stride(1) != 1:
-        raise ValueError("block_tables must have unit stride along its rows")
-    ld = block_tables.stride(0) if R > 1 else width
-    if ld < width:
-        raise ValueError("block_tables rows overlap")
-    _vector(free_blocks, torch.int32, "free_blocks", free_blocks.shape[0], dev)
-    if taken is not None:
-        _vector(taken, torch.int32, "taken", 1, dev)
+    table, ld = _rows(block_tables, _i32, "block_tables", R, width, index)
+    if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
+        raise TypeError("free_blocks must be a 1-D int32 CUDA tensor")
+    free, n_free = _vector(free_blocks, _i32, "free_blocks", free_blocks.shape[0], index), free_blocks.shape[0]
     if max_tokens < 0 or block_size <= 0:
         raise ValueError("max_tokens must be >= 0 and block_size > 0")
     if out is None:
-        out = BlockPlan.empty(R, max_tokens, dev)
-    else:
-        _vector(out.cu_new, torch.int32, "out.cu_new", R + 1, dev)
-        _vector(out.seq_lens, torch.int32, "out.seq_lens", R, dev)
-        _vector(out.slots, torch.int64, "out.slots", max_tokens, dev)
-        _vector(out.positions, torch.int32, "out.positions", max_tokens, dev)
-        _vector(out.counts, torch.int32, "out.counts", 3, dev)
-    with _on_device(dev) as stream:
-        _check(load().i8_build_block_tables(
-            context_lens.data_ptr(), new_lens.data_ptr(), R, block_tables.data_ptr(), width, ld,
-            free_blocks.data_ptr(), free_blocks.shape[0],
-            taken.data_ptr() if taken is not None else None, block_size, max_tokens,
-            out.cu_new.data_ptr(), out.seq_lens.data_ptr(), out.slots.data_ptr(),
-            out.positions.data_ptr(), out.counts.data_ptr(), stream), "i8_build_block_tables")
+        out = BlockPlan.empty(R, max_tokens, context_lens.device)
+    cu, lens, slots, positions, counts = out
+    _call("i8_build_block_tables", index, ctx, new, R, table, width, ld, free, n_free,
+          _vector(taken, _i32, "taken", 1, index) if taken is not None else None, block_size, max_tokens,
+          _vector(cu, _i32, "out.cu_new", R + 1, index), _vector(lens, _i32, "out.seq_lens", R, index),
+          _vector(slots, _i64, "out.slots", max_tokens, index),
+          _vector(positions, _i32, "out.positions", max_tokens, index),
+          _vector(counts, _i32, "out.counts", 3, index))
     return out
 
 
@@ -238,17 +270,14 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
     (views of the fused projection's output allowed), into their slots
     (int64 [T], as build_block_tables gives them; negative: skipped).  A block
     whose tokens get louder is re-coded with its new scale."""
-    dev = k.device
-    info = _cache(cache, dev)
-    kt, kh = _heads(k, "k", None, info.head_dim)
-    vt, vh = _heads(v, "v", dev, info.head_dim)
-    T = k.shape[0]
-    if k.shape[1] != info.kv_heads or v.shape != k.shape:
-        raise ValueError("k and v must be [T, kv_heads, head_dim] of the cache")
-    _vector(slots, torch.int64, "slots", T, dev)
-    with _on_device(dev) as stream:
-        _check(load().i8_kv_cache_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(),
-                                         T, ctypes.byref(info), stream), "i8_kv_cache_append")
+    index = _device_index(k, "k")
+    info = _cache(cache, index)
+    T = k.shape[0] if k.dim() else 0
+    shape = (T, info.kv_heads, info.head_dim)
+    kp, kt, kh = _heads(k, "k", shape, index)
+    vp, vt, vh = _heads(v, "v", shape, index)
+    _call("i8_kv_cache_append", index, kp, kt, kh, vp, vt, vh, _vector(slots, _i64, "slots", T, index), T,
+          ctypes.byref(info))
     return cache
 
 
@@ -265,43 +294,39 @@ def paged_attention(q: torch.Tensor, cache: QuantKVCache, block_tables: torch.Te
     Returns out [T, q_heads, head_dim] bf16, and with ``want_lse`` also the
     natural log of the sum of exponentials, fp32 [T, q_heads] (-inf for a row
     that sees nothing, whose output is 0).  Rows of no request are not written."""
-    dev = q.device
-    info = _cache(cache, dev)
-    qt, qh = _heads(q, "q", None, info.head_dim)
-    T, Hq, D = q.shape
-    R, width = seq_lens.shape[0], block_tables.shape[1]
-    _vector(seq_lens, torch.int32, "seq_lens", R, dev)
-    _vector(cu_new, torch.int32, "cu_new", R + 1, dev)
-    _need(block_tables, torch.int32, "block_tables", 2, dev)
-    if block_tables.shape[0] != R:
-        raise ValueError("block_tables must have a row for each request")
-    if width > 1 and block_tables.stride(1) != 1:
-        raise ValueError("block_tables must have unit stride along its rows")
-    ld = block_tables.stride(0) if R > 1 else width
-    if ld < width:
-        raise ValueError("block_tables rows overlap")
-    if Hq == 0 or Hq % info.kv_heads:
-        raise ValueError("q_heads must be a multiple of kv_heads")
-    if max_new is None:
-        max_new = T
+    index = _device_index(q, "q")
+    info = _cache(cache, index)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D")
+    T, Hq, D = shape = q.shape
+    if D != info.head_dim or Hq == 0 or Hq % info.kv_heads:
+        raise ValueError("q must be [T, q_heads, head_dim] with the cache's head_dim and a multiple of its kv_heads")
+    qp, qt, qh = _heads(q, "q", shape, index)
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise TypeError("seq_lens must be a 1-D int32 CUDA tensor")
+    R = seq_lens.shape[0]
+    lens = _vector(seq_lens, _i32, "seq_lens", R, index)
+    cu = _vector(cu_new, _i32, "cu_new", R + 1, index)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise TypeError("block_tables must be a 2-D int32 CUDA tensor")
+    width = block_tables.shape[1]
+    table, ld = _rows(block_tables, _i32, "block_tables", R, width, index)
+    max_new = T if max_new is None else min(max_new, T)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    ot, oh = _heads(out, "out", dev, D)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if (T > 1 and ot < D) or (Hq > 1 and oh < D):
-        raise ValueError("out's rows overlap")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    with _on_device(dev) as stream:
-        lib = load()
-        need = lib.i8_paged_attention_workspace_bytes(Hq, info.kv_heads, D, info.fmt, min(max_new, T))
-        if workspace is None and need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check(lib.i8_paged_attention(
-            q.data_ptr(), qt, qh, T, Hq, ctypes.byref(info), block_tables.data_ptr(), width, ld,
-            seq_lens.data_ptr(), cu_new.data_ptr(), R, max_new, D ** -0.5 if scale is None else scale,
-            out.data_ptr(), ot, oh, lse.data_ptr() if lse is not None else None,
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, stream),
-            "i8_paged_attention")
+        out = torch.empty(shape, dtype=_bf16, device=q.device)
+        op, ot, oh = out.data_ptr(), Hq * D, D
+    else:
+        op, ot, oh = _heads(out, "out", shape, index)
+        if (T > 1 and ot < D) or (Hq > 1 and oh < D):
+            raise ValueError("out's rows overlap")
+    lse = torch.empty((T, Hq), dtype=_f32, device=q.device) if want_lse else None
+    if workspace is None:
+        need = _attention_workspace(Hq, info.kv_heads, D, info.fmt, max_new, index)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    _call("i8_paged_attention", index, qp, qt, qh, T, Hq, ctypes.byref(info), table, width, ld, lens, cu, R,
+          max_new, D ** -0.5 if scale is None else scale, op, ot, oh,
+          lse.data_ptr() if want_lse else None, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return (out, lse) if want_lse else out
