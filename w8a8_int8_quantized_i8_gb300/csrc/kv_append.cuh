@@ -16,7 +16,7 @@
 //
 // Every run is handled by one warp (short runs, a decode step) or one CTA
 // (long runs, a prefill), whole: no two CTAs write a block, no atomics.  A run
-// of up to 8 vectors a thread stays in registers between the maximum and the
+// of up to 4 vectors a thread stays in registers between the maximum and the
 // codes; of a longer one the rest is read again (from L1 / L2).
 //
 // Finding the runs is a chain of short dependent steps, so the slots that they
@@ -35,7 +35,7 @@ namespace i8 {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendMaxWindow = 32;  // tokens a CTA looks for runs in
 constexpr int kAppendShortRun = 8;    // runs up to this are one warp's work
-constexpr int kAppendKeep = 8;        // vectors a thread keeps
+constexpr int kAppendKeep = 4;        // vectors a thread keeps
 constexpr int kAppendSlots = 256;     // slots in shared memory: the one before the window, then on
 
 struct AppendSide {
@@ -243,7 +243,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
 
 // grid (windows of tokens, 2 * heads).
 template <bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const AppendArgs p) {
   __shared__ uint32_t red[kAppendThreads / 32];
   __shared__ AppendRun run[kAppendMaxWindow];
   __shared__ int n_runs;
@@ -305,11 +305,22 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
   a.ld_head = values ? p.v.ld_head : p.k.ld_head;
   a.codes = values ? p.v.codes : p.k.codes;
   a.scale = values ? p.v.scale : p.k.scale;
-  for (int i = warp; i < runs; i += kAppendThreads / 32)
-    if (run[i].span <= kAppendShortRun) append_run<E4M3>(p, a, head, run[i], lane, 32, nullptr);
-  for (int i = 0; i < runs; ++i)
-    if (run[i].span > kAppendShortRun)
-      append_run<E4M3>(p, a, head, run[i], threadIdx.x, kAppendThreads, red);
+  // the short runs first, a warp each, then the long ones, the CTA together:
+  // one call of append_run for both, so that it is in the code once
+  bool solo = true;
+  int i = warp;
+  for (int step = 0; step < 2 * kAppendMaxWindow + 2; ++step) {
+    for (; i < runs && (run[i].span <= kAppendShortRun) != solo;) i += solo ? kAppendThreads / 32 : 1;
+    if (i >= runs) {
+      if (!solo) break;
+      solo = false;
+      i = 0;
+      continue;
+    }
+    append_run<E4M3>(p, a, head, run[i], solo ? lane : threadIdx.x, solo ? 32 : kAppendThreads,
+                     solo ? nullptr : red);
+    i += solo ? kAppendThreads / 32 : 1;
+  }
 }
 
 }  // namespace i8
