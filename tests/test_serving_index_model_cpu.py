@@ -44,11 +44,11 @@ def test_the_model_is_the_source():
     assert "if constexpr (D == 64) return row * 64 + (byte ^ (((row >> 1) & 3) << 4));" in src
     assert "return (byte >> 7) * (AttnTile<D>::TOKENS * 128) + row * 128 + ((byte & 127) ^ ((row & 7) << 4));" in src
     assert "return D == 64 ? c * 16 : (j >> 1) * 128 + (2 * c + (j & 1)) * 16;" in src
-    assert "lds_16(half + attn_place<D>(g, attn_k_dim<D>(j, c)))" in src
+    assert "lds_16(stage + h * 16 * Tile::BOX + attn_place<D>(g + 8 * i, attn_k_dim<D>(j, c)))" in src
     assert "lds_16(half + attn_place<D>(tk, j * 128 + g * 16))" in src
     assert "lds_8(half + attn_place<D>(tk, g * 8))" in src
     # every innermost TMA coordinate is a multiple of a box, 64 or 128 bytes
-    assert src.count("tma_load_3d(") == 2 and src.count("bar, b * Tile::BOX, next_off[h], row)") == 2
+    assert src.count("tma_load_3d(") == 2 and src.count("bar, b * Tile::BOX, f.next_off[h], row)") == 2
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])

@@ -10,18 +10,17 @@
 // request's new tokens, are the rows r = i * G + g that read the same keys.
 //
 // Arithmetic:
-//   * the codes are exact in fp16 (int8: |c| <= 127; E4M3: 4 significant bits;
-//     read with fp16's exponent bias they are 2^-8 times their value, which the
-//     scale makes good).  A row of q, bf16, is multiplied by the power of two
-//     that brings its largest element into [2^14, 2^15): exact in fp16 except
-//     for elements below 2^-28 of the largest, which keep an absolute error of
+//   * the codes are exact in fp16 (int8: |c| <= 127; E4M3: 4 significant bits,
+//     2^-9 to 448).  A row of q, bf16, is multiplied by the power of two that
+//     brings its largest element into [2^14, 2^15): exact in fp16 except for
+//     elements below 2^-28 of the largest, which keep an absolute error of
 //     2^-40 of it.  So q . ck is a sum of exact products in fp32;
 //   * softmax statistics and sums are fp32;
-//   * P is rounded to fp16 (11 bits) for the second product, as
-//     2^10 e^(S - M) sv / s_ref with s_ref the largest sv met so far: at most
-//     2^10, and what lies 2^-35 below the maximum vanishes;
-//   * both running references, M and s_ref, only grow; the accumulator is
-//     rescaled when one does.
+//   * P is rounded to fp16 (11 bits) for the second product, as 2^(10 + s - R)
+//     with s = log2(e) S + log2 sv, the log of a term's weight in O, and R its
+//     running maximum in the row: at most 2^10, and what lies 2^-35 below the
+//     maximum vanishes.  The sum of exponentials adds P / sv, in fp32.  (A
+//     block of zeros counts with the block before it for sv.)
 //
 // The products run transposed: S^T = K q^T and O^T = V^T P^T, so that the
 // tokens and the head dimension fill the 16-row side of the warp MMA
@@ -72,6 +71,7 @@ struct AttnTile {
   static constexpr int STAGE = 2 * SIDE;
   static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row in one TMA box
 };
+constexpr int kAttnMeet = 4;    // m-tiles of O^T a warp's parts meet by at a time
 constexpr int kJoinGroups = 4;  // groups of kAttnThreads that share an item's pieces in the join
 
 struct AttnArgs {
@@ -108,19 +108,24 @@ __device__ __forceinline__ float ex2(float x) {
 template <bool E4M3>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (E4M3) {
-    // sign to bit 15, the seven other bits to 13..7: 2^-8 times the value
-    const uint32_t a = __byte_perm(w, 0u, 0x1404);
-    const uint32_t b = __byte_perm(w, 0u, 0x3424);
-    lo = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u);
-    hi = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   } else {
     s8x4_to_f16x4(w, lo, hi);
   }
 }
 
+// E4M3 NaN codes, which places that hold no token may contain, as zeros (the
+// product's 0 * NaN would spread).
+__device__ __forceinline__ uint32_t without_nan_codes(uint32_t w) {
+  return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -142,9 +147,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 template <int D, int NT>
 struct AttnState {
   float o[D / 16][NT][4];  // O^T: rows d, columns 8 * nt + 2c + {0, 1}
-  float m[NT][2];          // running maximum of S (log2 units) of those columns
-  float l[NT][2];          // this lane's share of the sum of 2^(10 + S - m)
-  float s_ref;             // largest block scale of V so far
+  float m[NT][2];          // running maximum R of those columns
+  float l[NT][2];          // this lane's share of the sum of 2^(10 + log2(e) S - R)
+};
+
+// A warp's feed: where its copies of a segment of keys stand.
+template <int D>
+struct AttnFeed {
+  using Tile = AttnTile<D>;
+  static constexpr int H = Tile::HALVES;
+  static constexpr int S = Tile::STAGES;
+  const int32_t* table;     // the request's blocks
+  int head;
+  int t_first, end;         // the warp's first token of the segment, the segment's end
+  int t_look, col, off;     // the next tile to look up: token, column of the table, offset in the block
+  int next_id[H], next_off[H];  // looked up, not yet copied
+  float ksc[S][H], vsc[S][H];   // block scales of the tiles in the ring; K's is NaN for a missing block
 };
 
 // Adds the calls' values up over the CTA: returns the exclusive sum before
@@ -268,19 +286,105 @@ __host__ __device__ constexpr int attn_k_dim(int j, int c) {
   return D == 64 ? c * 16 : (j >> 1) * 128 + (2 * c + (j & 1)) * 16;
 }
 
-// A row tile of a request's rows against tokens [begin, end) of one kv head,
-// in steps of a unit; the warp takes every kAttnWarps-th tile.  `ring` and
-// `bars`: the shared-memory addresses of the warp's stages and of the barriers
-// on which their copies count; `parity`: a bit for each stage.
+template <int D>
+__device__ __forceinline__ void feed_look_up(const AttnArgs& p, AttnFeed<D>& f) {
+  using Tile = AttnTile<D>;
+#pragma unroll
+  for (int h = 0; h < Tile::HALVES; ++h) {
+    const bool wraps = f.off + 16 * h >= p.block;
+    f.next_off[h] = wraps ? f.off + 16 * h - p.block : f.off + 16 * h;
+    f.next_id[h] = f.t_look + 16 * h < f.end ? __ldg(f.table + (wraps ? f.col + 1 : f.col)) : -1;
+  }
+  f.t_look += Tile::UNIT;
+  f.col += p.unit_cols;
+  f.off += p.unit_rest;
+  if (f.off >= p.block) {
+    f.off -= p.block;
+    ++f.col;
+  }
+}
+
+// Starts the copies of the tile at t0, whose blocks have been looked up, into
+// stage `slot`; its scales go to place `into` of the feed.
+template <int D>
+__device__ __forceinline__ void feed_issue(const AttnArgs& p, AttnFeed<D>& f, const void* k_map,
+                                           const void* v_map, uint32_t ring, uint32_t bars,
+                                           int lane, int t0, int slot, int into) {
+  using Tile = AttnTile<D>;
+  constexpr int H = Tile::HALVES;
+  if (t0 >= f.end) return;
+  const uint32_t k_to = ring + slot * Tile::STAGE, v_to = k_to + Tile::SIDE;
+  const uint32_t bar = bars + 8 * slot;
+  uint32_t bytes = 0;
+  bool there[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    there[h] = f.next_id[h] >= 0 && f.next_id[h] < p.blocks;
+    // end lies within the table's width
+    if (!there[h] && t0 + 16 * h < f.end && lane == 0) atomicOr(&g_status, 1u << 7);
+    bytes += there[h] ? 32u * D : 0u;
+  }
+  // a box of 32 tokens where blocks are a multiple of that: the halves' ids agree
+  const bool whole = H == 2 && p.box_rows == 32;
+  if (whole) bytes = there[0] ? 64u * D : 0u;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (there[h] && !(whole && h == 1)) {
+        const int row = f.next_id[h] * p.kv_heads + f.head;
+#pragma unroll
+        for (int b = 0; b < D / Tile::BOX; ++b) {
+          const uint32_t at = b * (Tile::TOKENS * 128) + h * 16 * Tile::BOX;
+          tma_load_3d(k_to + at, k_map, bar, b * Tile::BOX, f.next_off[h], row);
+          tma_load_3d(v_to + at, v_map, bar, b * Tile::BOX, f.next_off[h], row);
+        }
+      }
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int64_t row = static_cast<int64_t>(f.next_id[h]) * p.kv_heads + f.head;
+    f.ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : NAN;
+    f.vsc[into][h] = there[h] ? __ldg(p.v_scale + row) : 0.0f;
+  }
+}
+
+// Begins a segment, tokens [begin, end) of one kv head: the warp takes every
+// kAttnWarps-th tile; its ring is filled but for the stage that the first
+// round of attend_tiles fills.
+template <int D>
+__device__ __forceinline__ void feed_begin(const AttnArgs& p, AttnFeed<D>& f, const void* k_map,
+                                           const void* v_map, const int32_t* table, int head,
+                                           int begin, int end, uint32_t ring, uint32_t bars,
+                                           int warp, int lane) {
+  using Tile = AttnTile<D>;
+  f.table = table;
+  f.head = head;
+  f.t_first = f.t_look = begin + warp * Tile::TOKENS;
+  f.end = end;
+  if (f.t_first >= end) return;
+  f.col = f.t_first / p.block;
+  f.off = f.t_first - f.col * p.block;
+  feed_look_up(p, f);
+#pragma unroll
+  for (int i = 0; i < Tile::STAGES - 1; ++i) {
+    feed_issue(p, f, k_map, v_map, ring, bars, lane, f.t_first + i * Tile::UNIT, i, i);
+    feed_look_up(p, f);
+  }
+}
+
+// A row tile of a request's rows against the segment that the feed has begun.
+// `ring` and `bars`: the shared-memory addresses of the warp's stages and of
+// the barriers on which their copies count; `parity`: a bit for each stage.
 template <int D, bool E4M3, int NT>
-__device__ __forceinline__ void attend_tiles(const AttnArgs& p, const void* k_map,
-                                             const void* v_map, const int32_t* table, int head,
+__device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, const void* k_map,
+                                             const void* v_map,
                                              const uint32_t (&qf)[NT][D / 16][2],
                                              const float (&rowfac)[NT][2],
-                                             const int (&limit)[NT][2], int all_seen, int begin,
-                                             int end, uint32_t ring, uint32_t bars,
-                                             uint32_t& parity, volatile int* abort_flag, int warp,
-                                             int lane, AttnState<D, NT>& st) {
+                                             const int (&limit)[NT][2], int all_seen,
+                                             uint32_t ring, uint32_t bars, uint32_t& parity,
+                                             volatile int* abort_flag, int lane,
+                                             AttnState<D, NT>& st) {
   using Tile = AttnTile<D>;
   constexpr int H = Tile::HALVES;
   constexpr int S = Tile::STAGES;
@@ -288,147 +392,105 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const void* k_ma
   constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // the same of V (8 bytes at D = 64)
   constexpr int VB = D / 8 < 16 ? D / 8 : 16;    // contiguous bytes of V a lane takes
   const int g = lane >> 2, c = lane & 3;
-  const int t_first = begin + warp * Tile::TOKENS;
-  if (t_first >= end) return;
-
-  // the block (a column of the table) and the offset in it of the next tile to
-  // look up; ids are looked up a tile ahead of the copies that need them
-  int col = t_first / p.block, off = t_first - col * p.block, t_look = t_first;
-  int next_id[H], next_off[H];
-  auto look_up = [&]() {
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const bool wraps = off + 16 * h >= p.block;
-      next_off[h] = wraps ? off + 16 * h - p.block : off + 16 * h;
-      next_id[h] = t_look + 16 * h < end ? __ldg(table + (wraps ? col + 1 : col)) : -1;
-    }
-    t_look += Tile::UNIT;
-    col += p.unit_cols;
-    off += p.unit_rest;
-    if (off >= p.block) {
-      off -= p.block;
-      ++col;
-    }
-  };
-  float ksc[S][H], vsc[S][H];  // block scales of the tiles in the ring; K's is NaN for a missing block
-  auto issue = [&](int t0, int slot, int into) {
-    if (t0 >= end) return;
-    const uint32_t k_to = ring + slot * Tile::STAGE, v_to = k_to + Tile::SIDE;
-    const uint32_t bar = bars + 8 * slot;
-    uint32_t bytes = 0;
-    bool there[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      there[h] = next_id[h] >= 0 && next_id[h] < p.blocks;
-      // end lies within the table's width
-      if (!there[h] && t0 + 16 * h < end && lane == 0) atomicOr(&g_status, 1u << 7);
-      bytes += there[h] ? 32u * D : 0u;
-    }
-    // a box of 32 tokens where blocks are a multiple of that: the halves' ids agree
-    const bool whole = H == 2 && p.box_rows == 32;
-    if (whole) bytes = there[0] ? 64u * D : 0u;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (there[h] && !(whole && h == 1)) {
-          const int row = next_id[h] * p.kv_heads + head;
-#pragma unroll
-          for (int b = 0; b < D / Tile::BOX; ++b) {
-            const uint32_t at = b * (Tile::TOKENS * 128) + h * 16 * Tile::BOX;
-            tma_load_3d(k_to + at, k_map, bar, b * Tile::BOX, next_off[h], row);
-            tma_load_3d(v_to + at, v_map, bar, b * Tile::BOX, next_off[h], row);
-          }
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t row = static_cast<int64_t>(next_id[h]) * p.kv_heads + head;
-      ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : NAN;
-      vsc[into][h] = there[h] ? __ldg(p.v_scale + row) : 0.0f;
-    }
-  };
-
-  look_up();
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    issue(t_first + i * Tile::UNIT, i, i);
-    look_up();
-  }
   int slot = 0;
+  float last_sv = 0x1p-60f;    // of the last block that is not all zeros
 #pragma unroll 1
-  for (int t0 = t_first; t0 < end; t0 += Tile::UNIT) {
+  for (int t0 = f.t_first; t0 < f.end; t0 += Tile::UNIT) {
     if (!mbar_wait(bars + 8 * slot, (parity >> slot) & 1u, abort_flag)) break;
     parity ^= 1u << slot;
-    float sk[H], sv[H];
-    bool gone[H];            // no such block: its tokens are left out
+    float sk[H], lv[H], back[H];  // log2 sv and 1 / sv
+    bool gone[H];                 // no such block: its tokens are left out
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      sk[h] = ksc[0][h];
-      sv[h] = vsc[0][h];
+      sk[h] = f.ksc[0][h];
       gone[h] = isnan(sk[h]);
+      if (f.vsc[0][h] > 0.0f) last_sv = f.vsc[0][h];
+      lv[h] = __log2f(last_sv);
+      back[h] = __fdividef(1.0f, last_sv);
 #pragma unroll
       for (int i = 0; i + 2 < S; ++i) {
-        ksc[i][h] = ksc[i + 1][h];
-        vsc[i][h] = vsc[i + 1][h];
+        f.ksc[i][h] = f.ksc[i + 1][h];
+        f.vsc[i][h] = f.vsc[i + 1][h];
       }
     }
     const uint32_t stage = ring + slot * Tile::STAGE;
     __syncwarp();  // the whole warp is done with the tile before, whose stage is filled next
-    issue(t0 + (S - 1) * Tile::UNIT, slot == 0 ? S - 1 : slot - 1, S - 2);
-    look_up();
+    feed_issue(p, f, k_map, v_map, ring, bars, lane, t0 + (S - 1) * Tile::UNIT,
+               slot == 0 ? S - 1 : slot - 1, S - 2);
+    feed_look_up(p, f);
     slot = slot + 1 == S ? 0 : slot + 1;
-    // ---- S^T
+    // ---- S^T: all reads first, the halves' products in turn (a warp has few
+    // neighbours on its scheduler to hide its latencies)
+    uint4 kr[H][2][KW];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < KW; ++j)
+          kr[h][i][j] = lds_16(stage + h * 16 * Tile::BOX + attn_place<D>(g + 8 * i, attn_k_dim<D>(j, c)));
     float s[H][NT][4];
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const uint32_t half = stage + h * 16 * Tile::BOX;
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[h][n][i] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < KW; ++j) {
-        const uint4 k0 = lds_16(half + attn_place<D>(g, attn_k_dim<D>(j, c)));
-        const uint4 k1 = lds_16(half + attn_place<D>(g + 8, attn_k_dim<D>(j, c)));
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w};
-        const uint32_t w1[4] = {k1.x, k1.y, k1.z, k1.w};
+    for (int j = 0; j < 4 * KW; ++j)  // word j % 4 of chunk j / 4
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a0, a1, a2, a3;
-          codes_to_f16<E4M3>(w0[i], a0, a2);
-          codes_to_f16<E4M3>(w1[i], a1, a3);
+      for (int h = 0; h < H; ++h) {
+        const uint4 k0 = kr[h][0][j >> 2], k1 = kr[h][1][j >> 2];
+        const uint32_t w0 = (j & 3) == 0 ? k0.x : (j & 3) == 1 ? k0.y : (j & 3) == 2 ? k0.z : k0.w;
+        const uint32_t w1 = (j & 3) == 0 ? k1.x : (j & 3) == 1 ? k1.y : (j & 3) == 2 ? k1.z : k1.w;
+        uint32_t a0, a1, a2, a3;
+        codes_to_f16<E4M3>(w0, a0, a2);
+        codes_to_f16<E4M3>(w1, a1, a3);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_16816(s[h][n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+        for (int n = 0; n < NT; ++n) mma_16816(s[h][n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+      }
+    // ---- V's codes, read while the softmax runs
+    uint32_t vr[H][4][D / 32];  // the words of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
+        const uint32_t half = stage + Tile::SIDE + h * 16 * Tile::BOX;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          if constexpr (VB == 16) {
+            const uint4 x = lds_16(half + attn_place<D>(tk, j * 128 + g * 16));
+            vr[h][i][4 * j] = x.x;
+            vr[h][i][4 * j + 1] = x.y;
+            vr[h][i][4 * j + 2] = x.z;
+            vr[h][i][4 * j + 3] = x.w;
+          } else {
+            const uint2 x = lds_8(half + attn_place<D>(tk, g * 8));
+            vr[h][i][0] = x.x;
+            vr[h][i][1] = x.y;
+          }
         }
       }
-    }
     // ---- softmax
     const bool masked = t0 + Tile::TOKENS > all_seen || gone[0] || gone[H - 1];
-    float top[NT][2];
+    bool moved = false;
+    float alpha[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      top[n][0] = top[n][1] = -INFINITY;
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[h][n][i] *= sk[h] * rowfac[n][i & 1];
+          s[h][n][i] = fmaf(s[h][n][i], sk[h] * rowfac[n][i & 1], lv[h]);
           if (masked && (gone[h] || t0 + 16 * h + g + 8 * (i >> 1) >= limit[n][i & 1]))
             s[h][n][i] = -INFINITY;
-          top[n][i & 1] = fmaxf(top[n][i & 1], s[h][n][i]);
+          top[i & 1] = fmaxf(top[i & 1], s[h][n][i]);
         }
-    }
-    const float s_ref = fmaxf(st.s_ref, fmaxf(sv[0], sv[H - 1]));
-    const float grow = s_ref > 0.0f ? __fdividef(st.s_ref, s_ref) : 0.0f;
-    bool moved = s_ref != st.s_ref;
-    float alpha[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = top[n][i];
+        float x = top[i];
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
@@ -439,20 +501,18 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const void* k_ma
         st.m[n][i] = m;
         st.l[n][i] *= alpha[n][i];
       }
-    st.s_ref = s_ref;
+    }
     if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st.o[j][n][i] *= alpha[n][i & 1] * grow;
+          for (int i = 0; i < 4; ++i) st.o[j][n][i] *= alpha[n][i & 1];
     }
     // ---- P^T and O^T
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const uint32_t half = stage + Tile::SIDE + h * 16 * Tile::BOX;
-      const float vs = s_ref > 0.0f ? __fdividef(sv[h], s_ref) : 0.0f;
       uint32_t b[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -460,37 +520,25 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, const void* k_ma
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float m = st.m[n][i & 1];
+          // (where the row has seen nothing, s and m are -inf both: 0, not NaN)
           e[i] = s[h][n][i] > -INFINITY ? ex2(s[h][n][i] - m + 10.0f) : 0.0f;
-          st.l[n][i & 1] += e[i];
+          st.l[n][i & 1] = fmaf(e[i], back[h], st.l[n][i & 1]);
         }
-        b[n][0] = transpose_8x8(pack_f16x2(e[0] * vs, e[1] * vs));
-        b[n][1] = transpose_8x8(pack_f16x2(e[2] * vs, e[3] * vs));
+        b[n][0] = transpose_8x8(pack_f16x2(e[0], e[1]));
+        b[n][1] = transpose_8x8(pack_f16x2(e[2], e[3]));
       }
-      uint32_t vr[4][D / 32];             // the V words of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+      if (E4M3 && masked) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          if constexpr (VB == 16) {
-            const uint4 x = lds_16(half + attn_place<D>(tk, j * 128 + g * 16));
-            vr[i][4 * j] = x.x;
-            vr[i][4 * j + 1] = x.y;
-            vr[i][4 * j + 2] = x.z;
-            vr[i][4 * j + 3] = x.w;
-          } else {
-            const uint2 x = lds_8(half + attn_place<D>(tk, g * 8));
-            vr[i][0] = x.x;
-            vr[i][1] = x.y;
-          }
-        }
+          for (int j = 0; j < D / 32; ++j) vr[h][i][j] = without_nan_codes(vr[h][i][j]);
       }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // word j of the V rows: 4 head dimensions, 2 MMAs
         uint32_t f[2][4];                 // [tokens 2c.., 8 + 2c..][head dimension]
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t x = vr[2 * i][j], y = vr[2 * i + 1][j];
+          const uint32_t x = vr[h][2 * i][j], y = vr[h][2 * i + 1][j];
           codes_to_f16<E4M3>(__byte_perm(x, y, 0x5140), f[i][0], f[i][1]);
           codes_to_f16<E4M3>(__byte_perm(x, y, 0x7362), f[i][2], f[i][3]);
         }
@@ -515,15 +563,12 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
     kv_attention_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map) {
   constexpr int ROWS = 8 * NT;
-  constexpr int FRAG = D / 16 * NT * 4;  // accumulators a lane
   constexpr int PIECE = ROWS * (D + 2);
   constexpr int UNIT = AttnTile<D>::UNIT;
   constexpr int S = AttnTile<D>::STAGES;
-  // the warps' rings (on a 1024-byte boundary), and after an item's last tile
-  // [warps][FRAG][32] sums
+  // the warps' rings, on a 1024-byte boundary
   extern __shared__ uint8_t sm_attn[];
-  float* sm_o = reinterpret_cast<float*>(
-      sm_attn + ((1024u - (smem_u32(sm_attn) & 1023u)) & 1023u));
+  __shared__ float sm_o[kAttnWarps * kAttnMeet * NT * 4 * 32];  // where the warps' parts meet
   __shared__ __align__(8) uint64_t sm_bars[kAttnWarps][S];
   __shared__ int abort_flag;
   __shared__ float sm_m[kAttnWarps][ROWS], sm_l[kAttnWarps][ROWS];
@@ -533,7 +578,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int group = p.q_heads / p.kv_heads;
-  const uint32_t ring = smem_u32(sm_o) + warp * (S * AttnTile<D>::STAGE);
+  const uint32_t ring = ((smem_u32(sm_attn) + 1023u) & ~1023u) + warp * (S * AttnTile<D>::STAGE);
   const uint32_t bars = smem_u32(sm_bars[warp]);
   uint32_t parity = 0;
   if (lane < S) mbar_init(bars + 8 * lane, 1);
@@ -572,39 +617,61 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
     sm_base = before;
   }
   __syncthreads();
-  int req = sm_req;
-  int64_t base = sm_base;  // the request's first unit
-  AttnRequest rq = attn_request<ROWS, UNIT>(p, req);
   if (threadIdx.x == 0) p.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-  // every round ends an item or the share, so there are at most u_end - u
-  for (; u < u_end;) {
+  // A segment: the part of an item in this share.
+  struct Segment {
+    int q0, fresh, len, rows;  // of the request
+    int head, row0;
+    int first, last, per_item; // units of the item
+    int64_t item_u;            // the item's first unit
+  };
+  int req = sm_req;
+  int64_t base = sm_base;      // the request's first unit
+  AttnRequest rq = attn_request<ROWS, UNIT>(p, req);
+  AttnFeed<D> feed;
+  // finds the segment at u, begins its copies and moves u past it
+  auto begin_segment = [&](Segment& sg) {
     for (; u >= base + rq.units && req + 1 < p.requests;) {
       base += rq.units;
       rq = attn_request<ROWS, UNIT>(p, ++req);
     }
     const int64_t item = (u - base) / rq.per_item;
-    const int64_t item_u = base + item * rq.per_item;  // the item's first unit
-    const int first = static_cast<int>(u - item_u);
-    const int last = static_cast<int>(min(static_cast<int64_t>(rq.per_item), u_end - item_u));
-    const int head = static_cast<int>(item / rq.tiles);
-    const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * rq.tiles) * ROWS;
-    const int rows = rq.fresh * group;
-    const int pos0 = rq.len - rq.fresh;  // position of the request's first new token
+    sg.q0 = rq.q0;
+    sg.fresh = rq.fresh;
+    sg.len = rq.len;
+    sg.rows = rq.fresh * group;
+    sg.per_item = rq.per_item;
+    sg.item_u = base + item * rq.per_item;
+    sg.first = static_cast<int>(u - sg.item_u);
+    sg.last = static_cast<int>(min(static_cast<int64_t>(rq.per_item), u_end - sg.item_u));
+    sg.head = static_cast<int>(item / rq.tiles);
+    sg.row0 = static_cast<int>(item - static_cast<int64_t>(sg.head) * rq.tiles) * ROWS;
+    const int newest = (min(sg.row0 + ROWS, sg.rows) - 1) / group;  // new token of the tile's last row
+    const int most = min(max(sg.len - sg.fresh + newest + 1, 0), sg.len);
+    feed_begin<D>(p, feed, &k_map, &v_map, p.table + req * p.ld_table, sg.head, sg.first * UNIT,
+                  min(most, sg.last * UNIT), ring, bars, warp, lane);
+    u = sg.item_u + sg.last;
+  };
+  // every round ends an item or the share, so there are at most u_end - u
+  for (; u < u_end;) {
+    Segment sg;
+    begin_segment(sg);                   // its first keys come while q is read
+    const int pos0 = sg.len - sg.fresh;  // position of the request's first new token
 
     // q fragments (column n of a tile is row g) and what the lane's two columns
     // of S^T need: their factor and the first position that they do not see
     uint32_t qf[NT][D / 16][2];
     float rowfac[NT][2];
     int limit[NT][2];
-    int most = 0, least = 0x7FFFFFFF;
+    int least = 0x7FFFFFFF;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = row0 + 8 * n + g;
-      const bool real = r < rows;
+      const int r = sg.row0 + 8 * n + g;
+      const bool real = r < sg.rows;
       const int i = real ? r / group : 0;
-      const uint16_t* qp = p.q + (static_cast<int64_t>(rq.q0) + i) * p.ldq_token +
-                           (head * group + (real ? r - i * group : 0)) * p.ldq_head;
+      const uint16_t* qp = p.q + (static_cast<int64_t>(sg.q0) + i) * p.ldq_token +
+                           (sg.head * group + (real ? r - i * group : 0)) * p.ldq_head;
       uint2 w[D / 16];
       uint32_t amax = 0;
 #pragma unroll
@@ -626,17 +693,15 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
         qf[n][j][1] = pack_f16x2(__uint_as_float(w[j].y << 16) * up, __uint_as_float(w[j].y & 0xFFFF0000u) * up);
       }
       // row g's exponent and limit go to the lanes whose columns 2c, 2c + 1 it is
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (E4M3 ? 256.0f : 1.0f) * p.scale_log2;
-      const int lim = real ? min(max(pos0 + i + 1, 0), rq.len) : 0;
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * p.scale_log2;
+      const int lim = real ? min(max(pos0 + i + 1, 0), sg.len) : 0;
 #pragma unroll
       for (int i2 = 0; i2 < 2; ++i2) {
         rowfac[n][i2] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i2) * 4);
         limit[n][i2] = __shfl_sync(0xFFFFFFFFu, lim, (2 * c + i2) * 4);
       }
-      most = max(most, lim);
       least = min(least, real ? lim : 0x7FFFFFFF);
     }
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
     least = __reduce_min_sync(0xFFFFFFFFu, least);
 
     AttnState<D, NT> st;
@@ -649,12 +714,9 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.o[j][n][i] = 0.0f;
     }
-    st.s_ref = 0.0f;
-    attend_tiles<D, E4M3, NT>(p, &k_map, &v_map, p.table + req * p.ld_table, head, qf, rowfac, limit, least,
-                              first * UNIT, min(most, last * UNIT), ring, bars, parity, &abort_flag, warp, lane, st);
-
-    // ---- the four warps' parts meet, where the rings were
-    __syncthreads();
+    attend_tiles<D, E4M3, NT>(p, feed, &k_map, &v_map, qf, rowfac, limit, least, ring, bars, parity,
+                              &abort_flag, lane, st);
+    // ---- the four warps' parts meet
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -668,66 +730,81 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
           sm_l[warp][8 * n + 2 * c + i] = l;
         }
       }
-    const float unit = st.s_ref * (E4M3 ? 256.0f : 1.0f);
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sm_o[(warp * FRAG + (j * NT + n) * 4 + i) * 32 + lane] = st.o[j][n][i] * unit;
-    __syncthreads();
-    const bool whole = first == 0 && last == rq.per_item;
+    const bool whole = sg.first == 0 && sg.last == sg.per_item;
     // a piece of an item begun earlier goes to the first slot, of one that
     // goes on to the second
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0);
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (sg.first == 0 ? 1 : 0);
     float* piece = p.pieces + slot * PIECE;
+    // through kAttnMeet m-tiles' worth of shared memory at a time: in turn, a
+    // thread of either half of the CTA finds the m-tiles that it owns there
+    float o[NT][D / 16];
+#pragma unroll
+    for (int part = 0; part < D / 16 / kAttnMeet; ++part) {
+      // m-tiles 2 * part + {0, 1} of each half of the head dimension's m-tiles
+#pragma unroll
+      for (int x = 0; x < kAttnMeet; ++x) {
+        const int j = (x / (kAttnMeet / 2)) * (D / 32) + part * (kAttnMeet / 2) + x % (kAttnMeet / 2);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sm_o[((warp * kAttnMeet + x) * NT * 4 + n * 4 + i) * 32 + lane] = st.o[j][n][i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = 8 * n + attn_own_row(threadIdx.x);
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w][row]);
+#pragma unroll
+        for (int k = 0; k < kAttnMeet; ++k) o[n][part * kAttnMeet + k] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+          const float f = sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f;
+#pragma unroll
+          for (int k = 0; k < kAttnMeet; ++k) {
+            const int x = static_cast<int>(threadIdx.x >> 6) * (kAttnMeet / 2) + (k >> 1);
+            const int i = 2 * (k & 1) + ((threadIdx.x >> 5) & 1);
+            o[n][part * kAttnMeet + k] = fmaf(
+                f, sm_o[((w * kAttnMeet + x) * NT * 4 + n * 4 + i) * 32 + lane], o[n][part * kAttnMeet + k]);
+          }
+        }
+      }
+      if (part + 1 < D / 16 / kAttnMeet) __syncthreads();  // read, before the next part
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = 8 * n + attn_own_row(threadIdx.x);
-      float m = -INFINITY;
+      float m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w][row]);
-      float l = 0.0f, o[D / 16];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) o[k] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float f = sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f;
-        l = fmaf(f, sm_l[w][row], l);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int j = static_cast<int>(threadIdx.x >> 6) * (D / 32) + (k >> 1);
-          const int i = 2 * (k & 1) + ((threadIdx.x >> 5) & 1);
-          o[k] = fmaf(f, sm_o[(w * FRAG + (j * NT + n) * 4 + i) * 32 + lane], o[k]);
-        }
-      }
+      for (int w = 0; w < kAttnWarps; ++w)
+        l = fmaf(sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f, sm_l[w][row], l);
       if (whole) {
-        if (row0 + row < rows) attn_write<D>(p, rq.q0, row0 + row, head, threadIdx.x, o, m, l);
+        if (sg.row0 + row < sg.rows) attn_write<D>(p, sg.q0, sg.row0 + row, sg.head, threadIdx.x, o[n], m, l);
       } else {
         float* to = piece + (n * kAttnThreads + threadIdx.x) * (D / 16);
 #pragma unroll
         for (int k = 0; k < D / 16; k += 4)
-          *reinterpret_cast<float4*>(to + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          *reinterpret_cast<float4*>(to + k) = make_float4(o[n][k], o[n][k + 1], o[n][k + 2], o[n][k + 3]);
         if (attn_own_dim<D>(threadIdx.x) == 0) {
           piece[ROWS * D + 2 * row] = m;
           piece[ROWS * D + 2 * row + 1] = l;
         }
       }
     }
-    if (!whole && first == 0 && threadIdx.x == 0) {
+    if (!whole && sg.first == 0 && threadIdx.x == 0) {
       // the worker that holds the item's last unit
-      const int64_t w_end = ((item_u + rq.per_item) * workers - 1) / total;
-      p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), head, row0, rows);
-      p.cut[2 * blockIdx.x + 1] = make_int4(rq.q0, 0, 0, 0);
+      const int64_t w_end = ((sg.item_u + sg.per_item) * workers - 1) / total;
+      p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), sg.head, sg.row0, sg.rows);
+      p.cut[2 * blockIdx.x + 1] = make_int4(sg.q0, 0, 0, 0);
     }
-    u = item_u + last;
+    __syncthreads();  // the sums have been read
     if (abort_flag) break;
-    if (u < u_end) {
-      fence_proxy_async_smem();  // the sums' place is filled by copies again
-      __syncthreads();
-    }
   }
+  // (not earlier: CTAs of the join beside those still at work cost 20 %)
   pdl_trigger();
 }
 

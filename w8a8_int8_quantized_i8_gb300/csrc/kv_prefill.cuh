@@ -11,9 +11,7 @@
 // tiles take turns: while one tile's softmax runs, the tensor cores do the
 // other's O and next S.
 //
-// Codes are converted to fp16 once a CTA and serve all 256 rows (int8: |c| <=
-// 127 exact; E4M3 read with fp16's exponent bias, 2^-8 of its value, exact;
-// the scale makes it good).  q is scaled per row by a power of two as in
+// Codes are converted to fp16, exactly, once a CTA and serve all 256 rows.  q is scaled per row by a power of two as in
 // kv_attention.cuh.  R is a row's running maximum of s + log2 sv, the log of a
 // term's weight in O; it moves only when it grows by more than 2^8, so that O
 // in TMEM is rarely rescaled, and P, held in fp16 as 2^(6 + s + log2 sv - R),
@@ -177,13 +175,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __shared__ float sm_ref;
   __shared__ float sm_top[2][2][128], sm_sum[2][2][128];  // [tile][half of the keys][row]
   __shared__ uint32_t sm_tmem;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, sm_gaps;  // sm_gaps: some block was missing so far
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int group = p.q_heads / p.kv_heads;
   const uint32_t base = (smem_u32(sm_pre) + 1023u) & ~1023u;
 
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    abort_flag = sm_gaps = 0;
     for (int i = 0; i < kPreSlots; ++i) {
       mbar_init(smem_u32(&raw_full[i]), 1);
       mbar_init(smem_u32(&raw_empty[i]), kPreConvWarps);
@@ -255,8 +253,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       const int e = 14 - max(static_cast<int>(amax >> 7) - 127, -100);
       float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      rowfac = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (E4M3 ? 256.0f : 1.0f) *
-               fabsf(p.scale_log2);
+      rowfac = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(p.scale_log2);
       if (p.scale_log2 < 0.0f) up = -up;  // the factor of S is never negative
       const uint32_t to = base + Sm::Q + t * Sm::TILE + r * 128;
 #pragma unroll 4
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.0f ? __fdiv_rn(ex2(sm_ref) * (E4M3 ? 256.0f : 1.0f), l) : 0.0f;
+      const float inv = l > 0.0f ? __fdiv_rn(ex2(sm_ref), l) : 0.0f;
       const int64_t token = static_cast<int64_t>(rq.q0) + i;
       uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
 #pragma unroll
@@ -441,6 +438,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               lv = sv > 0.0f ? log2f(sv) : -1000.0f;
             } else {
               atomicOr(&g_status, 1u << 7);
+              sm_gaps = 1;
             }
           }
         }
@@ -567,6 +565,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (!ok) break;
         const uint32_t from = base + Sm::CODES + slot * Sm::RAW;
         const uint32_t to = base + Sm::KV + slot * Sm::TILE;
+        // the last tile may end inside a box, and a missing block leaves what
+        // was there before
+        const bool strange = E4M3 && (item >= 2 * n - 2 || *static_cast<volatile int*>(&sm_gaps));
         // 8 rows a step (16 at 64 head dimensions).  Eight neighbouring lanes
         // read 128 bytes on different banks and write eight different chunks
         // of the swizzle: at 128 head dimensions the lanes of the row's second
@@ -583,7 +584,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               c = lane & 3;
               r = r0 + 8 * pass + (lane >> 2);
             }
-            const uint4 w = lds_16(from + r * D + c * 16);
+            uint4 w = lds_16(from + r * D + c * 16);
+            if (strange)
+              w = make_uint4(without_nan_codes(w.x), without_nan_codes(w.y), without_nan_codes(w.z),
+                             without_nan_codes(w.w));
             uint32_t h[8];
             codes_to_f16<E4M3>(w.x, h[0], h[1]);
             codes_to_f16<E4M3>(w.y, h[2], h[3]);

@@ -107,8 +107,7 @@ int attention_nt(int64_t rows, int64_t head_dim) { return head_dim == 256 || row
 
 template <int D, bool E4M3, int NT>
 size_t attention_smem() {
-  return 1024 + std::max<size_t>(sizeof(float) * kAttnWarps * (D / 16) * NT * 4 * 32,
-                                 static_cast<size_t>(kAttnWarps) * AttnTile<D>::STAGES * AttnTile<D>::STAGE);
+  return 1024 + static_cast<size_t>(kAttnWarps) * AttnTile<D>::STAGES * AttnTile<D>::STAGE;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
