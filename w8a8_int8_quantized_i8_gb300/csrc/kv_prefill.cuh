@@ -1,9 +1,9 @@
 // kv_prefill.cuh -- the paged attention of kv_attention.cuh for requests with
 // many rows (chunks of prompts), on the tensor cores of tcgen05.
 //
-// The same formula and cache.  A CTA takes 256 rows of a request (new token x
-// query head of one kv head, token-major) as two tiles of 128, and goes over
-// the keys 128 tokens at a time:
+// The same formula and cache.  An item is 256 rows of a request (new token x
+// query head of one kv head, token-major) as two tiles of 128; a CTA goes over
+// its keys 128 tokens at a time:
 //   S_t = Q_t K^T  -> TMEM      (fp16 x fp16, exact products, fp32 sums)
 //   P_t = 2^(s + log2 sv - R)   softmax threads, P back to TMEM
 //   O_t += P_t V   -> TMEM      (A operand from TMEM, V as it lies: N-major)
@@ -44,6 +44,7 @@ constexpr int kPreConvWarps = 6;
 constexpr int kPreSlots = 3;       // stages of codes, and of fp16 tiles
 constexpr int kPreScales = 4;      // stages of block scales
 constexpr int kPreGranules = kPreTokens / 16;
+constexpr int kPreJoinRows = 8;    // rows of an item that a CTA of the join takes
 
 template <int D>
 struct PrefillSmem {
@@ -56,11 +57,60 @@ struct PrefillSmem {
   static constexpr int BYTES = CODES + kPreSlots * RAW;
 };
 
-struct PrefillScales {   // of the 16-token granules of a tile
+struct PrefillScales {   // of the 16-token granules of a tile, and the tile's place
   float k[kPreGranules];
   float lv[kPreGranules];     // log2 of V's
   float back[kPreGranules];   // 2^(Lr - lv)
+  float ref;                  // Lr
+  int begins, ends;           // it is a segment's first, last
+  int strange;                // places in it may hold codes that are no token's
 };
+
+// Where a CTA stands in the line of all items' tiles of keys (the units).  An
+// item's keys end with its last row's; its row tiles go from the last to the
+// first, head after head, request after request.
+struct PrefillCursor {
+  AttnRequest rq;
+  int req, head, tile, n;     // the item and its units
+  int64_t item_u;             // its first unit
+};
+
+// The tokens that a row tile sees.
+__device__ __forceinline__ int prefill_end(const AttnRequest& rq, int group, int tile) {
+  const int last = min((tile + 1) * kPreRows, rq.fresh * group) - 1;
+  return min(max(rq.len - rq.fresh + last / group + 1, 0), rq.len);
+}
+// Units of a row tile: one even where it sees nothing.
+__device__ __forceinline__ int prefill_units(const AttnRequest& rq, int group, int tile) {
+  return max(1, (prefill_end(rq, group, tile) + kPreTokens - 1) / kPreTokens);
+}
+__device__ __forceinline__ AttnRequest prefill_request(const AttnArgs& p, int r) {
+  AttnRequest rq = attn_request<kPreRows, kPreTokens>(p, r);
+  const int group = p.q_heads / p.kv_heads;
+  rq.units = 0;
+  if (static_cast<int64_t>(rq.fresh) * group < p.split_rows) rq.tiles = 0;
+  for (int t = 0; t < rq.tiles; ++t) rq.units += prefill_units(rq, group, t);
+  rq.units *= p.kv_heads;
+  return rq;
+}
+// Moves the cursor to the item that holds unit u, at or behind the cursor's.
+__device__ __forceinline__ void prefill_seek(const AttnArgs& p, PrefillCursor& c, int64_t u) {
+  const int group = p.q_heads / p.kv_heads;
+  for (; u >= c.item_u + c.n;) {
+    c.item_u += c.n;
+    if (--c.tile < 0) {
+      if (++c.head == p.kv_heads) {
+        c.head = 0;
+        for (++c.req; c.req < p.requests; ++c.req) {  // (a unit behind it: there is one)
+          c.rq = prefill_request(p, c.req);
+          if (c.rq.tiles > 0) break;
+        }
+      }
+      c.tile = c.rq.tiles - 1;
+    }
+    c.n = prefill_units(c.rq, group, c.tile);
+  }
+}
 
 // An N-major (transposed) operand stored with the 128-byte swizzle: rows of
 // 128 bytes (64 values along N) for each k, 8-row groups 1024 bytes apart along
@@ -168,20 +218,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     kv_prefill_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
   using Sm = PrefillSmem<D>;
+  constexpr int PIECE = kPreRows * (D + 2);
   extern __shared__ uint8_t sm_pre[];
   __shared__ __align__(8) uint64_t raw_full[kPreSlots], raw_empty[kPreSlots], kv_full[kPreSlots],
       kv_empty[kPreSlots], sc_full[kPreScales], s_full[2], p_full[2], q_full, o_full, drained;
   __shared__ PrefillScales sc[kPreScales];
-  __shared__ float sm_ref;
   __shared__ float sm_top[2][2][128], sm_sum[2][2][128];  // [tile][half of the keys][row]
+  __shared__ int64_t sm_scan[kAttnWarps], sm_base;
+  __shared__ int sm_req;
   __shared__ uint32_t sm_tmem;
-  __shared__ int abort_flag, sm_gaps;  // sm_gaps: some block was missing so far
+  __shared__ int abort_flag;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int group = p.q_heads / p.kv_heads;
   const uint32_t base = (smem_u32(sm_pre) + 1023u) & ~1023u;
 
   if (threadIdx.x == 0) {
-    abort_flag = sm_gaps = 0;
+    abort_flag = 0;
     for (int i = 0; i < kPreSlots; ++i) {
       mbar_init(smem_u32(&raw_full[i]), 1);
       mbar_init(smem_u32(&raw_empty[i]), kPreConvWarps);
@@ -202,20 +254,46 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
 
   pdl_wait();
-  // ---- the item: row tiles of a request from the last (the longest) to the first
-  const int tiles_max = static_cast<int>((static_cast<int64_t>(p.max_new) * group + kPreRows - 1) / kPreRows);
-  const int head = blockIdx.x % p.kv_heads;
-  const int req = static_cast<int>(blockIdx.x / p.kv_heads) % p.requests;
-  const int back = static_cast<int>(blockIdx.x / p.kv_heads) / p.requests;
-  const AttnRequest rq = attn_request<kPreRows, kPreTokens>(p, req);
-  const int rows = rq.fresh * group;
-  const int tile = rq.tiles - 1 - back;
-  if (rows < p.split_rows || tile < 0 || tiles_max <= 0) return;  // (the whole CTA)
-  const int row0 = tile * kPreRows;
-  const int pos0 = rq.len - rq.fresh;
-  const int last_row = min(row0 + kPreRows, rows) - 1;
-  const int end = min(max(pos0 + last_row / group + 1, 0), rq.len);
-  const int n = (end + kPreTokens - 1) / kPreTokens;  // tiles of keys
+  // ---- this CTA's share of the units
+  int64_t mine = 0, total, before = 0;
+  const int chunk = (p.requests + kAttnThreads - 1) / kAttnThreads;
+  const int r_lo = min(p.requests, static_cast<int>(threadIdx.x) * chunk);
+  const int r_hi = min(p.requests, r_lo + chunk);
+  if (threadIdx.x < kAttnThreads)
+    for (int r = r_lo; r < r_hi; ++r) mine += prefill_request(p, r).units;
+  {
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (warp < kAttnWarps && lane == 31) sm_scan[warp] = x;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      if (w < warp) before += sm_scan[w];
+      total += sm_scan[w];
+    }
+    before += x - mine;
+  }
+  const int64_t workers = min(total, static_cast<int64_t>(gridDim.x));
+  if (threadIdx.x == 0) p.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (blockIdx.x >= workers) return;  // (the whole CTA)
+  const int64_t u_begin = blockIdx.x * total / workers;
+  const int64_t u_end = (blockIdx.x + 1) * total / workers;
+  const int tiles = static_cast<int>(u_end - u_begin);
+  if (threadIdx.x < kAttnThreads && before <= u_begin && u_begin < before + mine) {
+    int r = r_lo;
+    for (; r < r_hi - 1; ++r) {
+      const int64_t n = prefill_request(p, r).units;
+      if (u_begin < before + n) break;
+      before += n;
+    }
+    sm_req = r;
+    sm_base = before;
+  }
   if (warp == kPreSoftWarps + 1) {
     tmem_alloc(smem_u32(&sm_tmem), 512);
     tmem_relinquish();
@@ -224,208 +302,258 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm_tmem;
+  // the first item: over the request's heads that lie before it at once
+  auto first_item = [&](PrefillCursor& c) {
+    c.req = sm_req;
+    c.rq = prefill_request(p, c.req);
+    const int64_t per_head = c.rq.units / p.kv_heads;
+    c.head = static_cast<int>((u_begin - sm_base) / per_head);
+    c.item_u = sm_base + c.head * per_head;
+    c.tile = c.rq.tiles - 1;
+    c.n = prefill_units(c.rq, group, c.tile);
+    prefill_seek(p, c, u_begin);
+  };
 
   if (warp < kPreSoftWarps) {
     // =================================================================== softmax
     regs_inc<96>();
     const int t = warp >> 3, half = (warp >> 2) & 1;
     const int r = (warp & 3) * 32 + lane;  // row of the tile
-    const int row = row0 + t * 128 + r;
-    const bool real = row < rows;
-    const int i = real ? row / group : 0;
-    const int hq = head * group + (real ? row - i * group : 0);
-    float rowfac;
-    {
-      // q's row: its power of two, then this thread's half in fp16 into the
-      // swizzled tile
-      const uint4* qp = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(rq.q0) + i) * p.ldq_token + hq * p.ldq_head);
-      uint32_t amax = 0;
-#pragma unroll 8
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a = x[k] & 0x7FFF7FFFu;
-          amax = max(amax, max(a & 0xFFFFu, a >> 16));
-        }
-      }
-      const int e = 14 - max(static_cast<int>(amax >> 7) - 127, -100);
-      float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      rowfac = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(p.scale_log2);
-      if (p.scale_log2 < 0.0f) up = -up;  // the factor of S is never negative
-      const uint32_t to = base + Sm::Q + t * Sm::TILE + r * 128;
-#pragma unroll 4
-      for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
-        const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          y[k] = pack_f16x2(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
-        sts_16(to + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_full));
-    }
-    const int limit = real ? min(max(pos0 + i + 1, 0), rq.len) : 0x7FFFFFFF;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     const uint32_t s_at = tmem + lanes + t * 128 + half * 64;  // this half's S
     const uint32_t p_at = tmem + lanes + t * 128 + half * 32;  // and P
     const uint32_t o_at = tmem + lanes + 256 + t * D + half * (D / 2);
-    float R = -INFINITY, l = 0.0f;
+    PrefillCursor cur;
+    first_item(cur);
     bool ok = true;
+    int jt = 0, seg = 0;  // tiles and segments done
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      ok = ok && mbar_wait(smem_u32(&sc_full[j & 3]), (j >> 2) & 1, &abort_flag) &&
-           mbar_wait(smem_u32(&s_full[t]), j & 1, &abort_flag);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) {  // given up: only keep the tile's barrier company
-        named_bar_sync(1 + t, 256);
-        continue;
-      }
-      tc_fence_after();
-      const PrefillScales& z = sc[j & 3];
-      const int seen = limit - j * kPreTokens - 64 * half;  // columns below this are seen
-      const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
-      uint32_t s[2][32];
-      tmem_ld_32x32b_x32(s_at, s[0]);
-      tmem_ld_32x32b_x32(s_at + 32, s[1]);
-      tmem_wait_ld(s[0]);
-      tmem_wait_ld(s[1]);
-      float top = -INFINITY;
+    for (int64_t u = u_begin; u < u_end; ++seg) {
+      prefill_seek(p, cur, u);
+      const int first = static_cast<int>(u - cur.item_u);
+      const int last = static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u));
+      const int rows = cur.rq.fresh * group, row0 = cur.tile * kPreRows;
+      const int row = row0 + t * 128 + r;
+      const bool real = row < rows;
+      const int i = real ? row / group : 0;
+      const int hq = cur.head * group + (real ? row - i * group : 0);
+      const int64_t token = static_cast<int64_t>(cur.rq.q0) + i;
+      float rowfac;
+      {
+        // q's row: its power of two, then this thread's half in fp16 into the
+        // swizzled tile (which the segment before has been done with since its
+        // o_full)
+        const uint4* qp = reinterpret_cast<const uint4*>(p.q + token * p.ldq_token + hq * p.ldq_head);
+        uint32_t amax = 0;
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t* v = &s[g >> 1][16 * (g & 1)];
-        const float f = z.k[4 * half + g] * rowfac, b = z.lv[4 * half + g];
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float x = fmaf(__uint_as_float(v[k]), f, b);
-            top = fmaxf(top, 16 * g + k < seen ? x : -INFINITY);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = x[k] & 0x7FFF7FFFu;
+            amax = max(amax, max(a & 0xFFFFu, a >> 16));
           }
-        } else {
-          float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-          float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
-#pragma unroll
-          for (int k = 6; k < 14; k += 4) {
-            x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-            y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-          }
-          x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
-          top = fmaxf(top, fmaf(fmaxf(x, y), f, b));
         }
+        const int e = 14 - max(static_cast<int>(amax >> 7) - 127, -100);
+        float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        rowfac = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(p.scale_log2);
+        if (p.scale_log2 < 0.0f) up = -up;  // the factor of S is never negative
+        const uint32_t to = base + Sm::Q + t * Sm::TILE + r * 128;
+#pragma unroll 4
+        for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+          const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pack_f16x2(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xFFFF0000u) * up);
+          sts_16(to + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&q_full));
       }
-      // the row's two threads agree on the maximum.  Both have read their S
-      // after the barrier, so that either may overwrite any of it with P.
-      sm_top[t][half][r] = top;
-      named_bar_sync(1 + t, 256);
-      top = fmaxf(top, sm_top[t][half ^ 1][r]);
-      float alpha = 1.0f;
-      if (top > R + 8.0f) {  // (-inf + 8 is -inf)
-        alpha = R > -INFINITY ? ex2(R - top) : 0.0f;
-        R = top;
-        l *= alpha;
-      }
-      if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && j > 0) {
-        // S of this tile was committed after the last product into O, so O is
-        // complete; each thread rescales its half of the head dimensions
+      const int limit =
+          real ? min(max(cur.rq.len - cur.rq.fresh + i + 1, 0), cur.rq.len) : 0x7FFFFFFF;
+      float R = -INFINITY, l = 0.0f, Lr = 0.0f;
 #pragma unroll 1
+      for (int j = first; j < last; ++j, ++jt) {
+        ok = ok && mbar_wait(smem_u32(&sc_full[jt & 3]), (jt >> 2) & 1, &abort_flag) &&
+             mbar_wait(smem_u32(&s_full[t]), jt & 1, &abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) {  // given up: only keep the tile's barrier company
+          named_bar_sync(1 + t, 256);
+          continue;
+        }
+        tc_fence_after();
+        const PrefillScales& z = sc[jt & 3];
+        if (j == first) Lr = z.ref;
+        const int seen = limit - j * kPreTokens - 64 * half;  // columns below this are seen
+        const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(s_at, s[0]);
+        tmem_ld_32x32b_x32(s_at + 32, s[1]);
+        tmem_wait_ld(s[0]);
+        tmem_wait_ld(s[1]);
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t* v = &s[g >> 1][16 * (g & 1)];
+          const float f = z.k[4 * half + g] * rowfac, b = z.lv[4 * half + g];
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = fmaf(__uint_as_float(v[k]), f, b);
+              top = fmaxf(top, 16 * g + k < seen ? x : -INFINITY);
+            }
+          } else {
+            float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+            for (int k = 6; k < 14; k += 4) {
+              x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
+            x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
+            top = fmaxf(top, fmaf(fmaxf(x, y), f, b));
+          }
+        }
+        // the row's two threads agree on the maximum.  Both have read their S
+        // after the barrier, so that either may overwrite any of it with P.
+        sm_top[t][half][r] = top;
+        named_bar_sync(1 + t, 256);
+        top = fmaxf(top, sm_top[t][half ^ 1][r]);
+        float alpha = 1.0f;
+        if (top > R + 8.0f) {  // (-inf + 8 is -inf)
+          alpha = R > -INFINITY ? ex2(R - top) : 0.0f;
+          R = top;
+          l *= alpha;
+        }
+        if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && j > first) {
+          // S of this tile was committed after the last product into O, so O
+          // is complete; each thread rescales its half of the head dimensions
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_at + 16 * q, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st_32x32b_x16(o_at + 16 * q, o);
+          }
+        }
+        const float ref = (R > -INFINITY ? R : 0.0f) - 6.0f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t* v = &s[q][16 * g];
+            const int gr = 4 * half + 2 * q + g;
+            const float f = z.k[gr] * rowfac, b = z.lv[gr] - ref;
+            const unsigned long long ff = f2(f, f), bb = f2(b, b);
+            unsigned long long sum[2];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float e0, e1;
+              f2_split(f2_fma(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, bb), e0, e1);
+              if (masked) {
+                e0 = 32 * q + 16 * g + k < seen ? e0 : -INFINITY;
+                e1 = 32 * q + 16 * g + k + 1 < seen ? e1 : -INFINITY;
+              }
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              const unsigned long long e = f2(e0, e1);
+              sum[(k >> 1) & 1] = k < 4 ? e : f2_add(sum[(k >> 1) & 1], e);
+              pk[8 * g + (k >> 1)] = pack_f16x2(e0, e1);
+            }
+            float s0, s1;
+            f2_split(f2_add(sum[0], sum[1]), s0, s1);
+            l = fmaf(s0 + s1, z.back[gr], l);
+          }
+          tmem_st_32x32b_x16(p_at + 16 * q, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+      }
+      // ---- out: each thread its half of the head dimensions
+      sm_sum[t][half][r] = l;
+      named_bar_sync(1 + t, 256);
+      l = (l + sm_sum[t][half ^ 1][r]) * ex2(-Lr);  // the sum of 2^(6 + s - R)
+      ok = ok && mbar_wait(smem_u32(&o_full), seg & 1, &abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) {
+        tc_fence_after();
+        const bool whole = first == 0 && last == cur.n;
+        const float inv = whole ? (l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f) : 1.0f;
+        uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
+        // a piece of an item begun earlier goes to the first slot, of one that
+        // goes on to the second
+        float* piece = p.pieces + (2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0)) * PIECE;
+        float* part = piece + (t * 128 + r) * D + half * (D / 2);
+#pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[16];
           tmem_ld_32x32b_x16(o_at + 16 * q, o);
           tmem_wait_ld(o);
+          if (whole && real) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st_32x32b_x16(o_at + 16 * q, o);
-        }
-      }
-      const float ref = (R > -INFINITY ? R : 0.0f) - 6.0f;
+            for (int k = 0; k < 16; k += 8) {
+              uint32_t y[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t* v = &s[q][16 * g];
-          const int gr = 4 * half + 2 * q + g;
-          const float f = z.k[gr] * rowfac, b = z.lv[gr] - ref;
-          const unsigned long long ff = f2(f, f), bb = f2(b, b);
-          unsigned long long sum[2];
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float e0, e1;
-            f2_split(f2_fma(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, bb), e0, e1);
-            if (masked) {
-              e0 = 32 * q + 16 * g + k < seen ? e0 : -INFINITY;
-              e1 = 32 * q + 16 * g + k + 1 < seen ? e1 : -INFINITY;
+              for (int m = 0; m < 4; ++m) {
+                const float lo = l > 0.0f ? __uint_as_float(o[k + 2 * m]) * inv : 0.0f;
+                const float hi = l > 0.0f ? __uint_as_float(o[k + 2 * m + 1]) * inv : 0.0f;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+                y[m] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(to + 16 * q + k) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            const unsigned long long e = f2(e0, e1);
-            sum[(k >> 1) & 1] = k < 4 ? e : f2_add(sum[(k >> 1) & 1], e);
-            pk[8 * g + (k >> 1)] = pack_f16x2(e0, e1);
+          } else if (!whole) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(part + 16 * q + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           }
-          float s0, s1;
-          f2_split(f2_add(sum[0], sum[1]), s0, s1);
-          l = fmaf(s0 + s1, z.back[gr], l);
         }
-        tmem_st_32x32b_x16(p_at + 16 * q, pk);
+        if (half == 0) {
+          if (!whole) {
+            piece[kPreRows * D + 2 * (t * 128 + r)] = R;
+            piece[kPreRows * D + 2 * (t * 128 + r) + 1] = l;
+          } else if (real && p.lse) {
+            p.lse[token * p.q_heads + hq] =
+                l > 0.0f ? (R - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          }
+        }
+        if (!whole && first == 0 && threadIdx.x == 0) {
+          // the worker that holds the item's last unit
+          const int64_t w_end = ((cur.item_u + cur.n) * workers - 1) / total;
+          p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), cur.head, row0, rows);
+          p.cut[2 * blockIdx.x + 1] = make_int4(cur.rq.q0, 0, 0, 0);
+        }
       }
-      tmem_wait_st();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+      u = cur.item_u + last;
     }
-    // ---- out: each thread its half of the head dimensions
-    sm_sum[t][half][r] = l;
-    named_bar_sync(1 + t, 256);
-    l += sm_sum[t][half ^ 1][r];
-    if (n > 0 && ok) ok = mbar_wait(smem_u32(&o_full), 0, &abort_flag);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok) {
-      tc_fence_after();
-      const float inv = l > 0.0f ? __fdiv_rn(ex2(sm_ref), l) : 0.0f;
-      const int64_t token = static_cast<int64_t>(rq.q0) + i;
-      uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[16];
-        if (n > 0) {
-          tmem_ld_32x32b_x16(o_at + 16 * q, o);
-          tmem_wait_ld(o);
-        }
-        if (real) {
-#pragma unroll
-          for (int k = 0; k < 16; k += 8) {
-            uint32_t y[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float lo = l > 0.0f ? __uint_as_float(o[k + 2 * m]) * inv : 0.0f;
-              const float hi = l > 0.0f ? __uint_as_float(o[k + 2 * m + 1]) * inv : 0.0f;
-              const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-              y[m] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            *reinterpret_cast<uint4*>(to + 16 * q + k) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
-      }
-      if (real && p.lse && half == 0)
-        p.lse[token * p.q_heads + hq] =
-            l > 0.0f ? (R - sm_ref - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
-    }
-    tc_fence_before();
   } else {
     regs_dec<48>();
     if (warp == kPreSoftWarps) {
       // ================================================================= copies
-      const int32_t* table = p.table + req * p.ld_table;
       const int boxes = kPreTokens / p.box_rows;
-      int item = 0;
+      PrefillCursor cur;
+      first_item(cur);
+      int item = 0, jt = 0;
+      float ref = 0.0f;
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
+      for (int64_t u = u_begin; u < u_end && ok; ++u, ++jt) {
+        prefill_seek(p, cur, u);
+        const int j = static_cast<int>(u - cur.item_u);
+        const int end = prefill_end(cur.rq, group, cur.tile);
+        const int32_t* table = p.table + cur.req * p.ld_table;
+        const bool begins = u == u_begin || j == 0, ends = u + 1 == u_end || j + 1 == cur.n;
         // scales, a lane a granule
         float sk = 0.0f, lv = -INFINITY;
         if (lane < kPreGranules) {
@@ -433,31 +561,37 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (tk < end) {
             const int64_t blk = __ldg(table + tk / p.block);  // end lies within the table's width
             if (blk >= 0 && blk < p.blocks) {
-              sk = __ldg(p.k_scale + blk * p.kv_heads + head);
-              const float sv = __ldg(p.v_scale + blk * p.kv_heads + head);
+              sk = __ldg(p.k_scale + blk * p.kv_heads + cur.head);
+              const float sv = __ldg(p.v_scale + blk * p.kv_heads + cur.head);
               lv = sv > 0.0f ? log2f(sv) : -1000.0f;
             } else {
               atomicOr(&g_status, 1u << 7);
-              sm_gaps = 1;
             }
           }
         }
-        float ref = lv;
+        if (begins) {
+          float x = lv;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
-        ref = __shfl_sync(0xFFFFFFFFu, ref, 0);
-        if (j == 0 && lane == 0) sm_ref = ref > -500.0f ? ref : 0.0f;
-        __syncwarp();
-        ref = sm_ref;
+          for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+          x = __shfl_sync(0xFFFFFFFFu, x, 0);
+          ref = x > -500.0f ? x : 0.0f;
+        }
         if (lv == -1000.0f) lv = ref - 60.0f;  // a block of zeros: its weight does not matter
-        PrefillScales& z = sc[j & 3];
+        const bool gap = __any_sync(0xFFFFFFFFu, lane < kPreGranules && lv == -INFINITY);
+        PrefillScales& z = sc[jt & 3];
         if (lane < kPreGranules) {
           z.k[lane] = sk;
           z.lv[lane] = lv;
           z.back[lane] = lv > -INFINITY ? ex2(ref - lv) : 0.0f;
         }
+        if (lane == 0) {
+          z.ref = ref;
+          z.begins = begins;
+          z.ends = ends;
+          z.strange = gap || (j + 1) * kPreTokens > end;
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sc_full[j & 3]));
+        if (lane == 0) mbar_arrive(smem_u32(&sc_full[jt & 3]));
         // the codes, a lane a box
         const int tb = j * kPreTokens + lane * p.box_rows;
         int64_t blk = -1;
@@ -481,7 +615,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (blk >= 0)
             tma_load_3d(base + Sm::CODES + slot * Sm::RAW + lane * p.box_rows * D,
                         side ? static_cast<const void*>(&v_map) : &k_map, bar, 0, off,
-                        static_cast<int>(blk) * p.kv_heads + head);
+                        static_cast<int>(blk) * p.kv_heads + cur.head);
         }
       }
       if (!ok) {  // let the copies in flight land (bounded) before the CTA ends
@@ -492,72 +626,82 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     } else if (warp == kPreSoftWarps + 1) {
       // ================================================================= products
-      if (n > 0) {
-        constexpr uint32_t kIdS = idesc_f16_f32(128, kPreTokens);
-        constexpr uint32_t kIdO = idesc_f16_f32(128, D) | (1u << 16);  // B is N-major
-        const uint32_t kv0 = base + Sm::KV;
-        auto product_s = [&](int t, int slot) {
-          const uint64_t a = smem_desc_sw128(base + Sm::Q + t * Sm::TILE);
-          const uint64_t b = smem_desc_sw128(kv0 + slot * Sm::TILE);
+      constexpr uint32_t kIdS = idesc_f16_f32(128, kPreTokens);
+      constexpr uint32_t kIdO = idesc_f16_f32(128, D) | (1u << 16);  // B is N-major
+      const uint32_t kv0 = base + Sm::KV;
+      auto product_s = [&](int t, int slot) {
+        const uint64_t a = smem_desc_sw128(base + Sm::Q + t * Sm::TILE);
+        const uint64_t b = smem_desc_sw128(kv0 + slot * Sm::TILE);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            mma_f16_ss_warp(tmem + t * 128, a + at, b + at, kIdS, k > 0);
-          }
-        };
-        auto product_o = [&](int t, int slot, bool first) {
-          const uint64_t b = smem_desc_sw128_n(kv0 + slot * Sm::TILE, 16384);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          mma_f16_ss_warp(tmem + t * 128, a + at, b + at, kIdS, k > 0);
+        }
+      };
+      auto product_o = [&](int t, int slot, bool first) {
+        const uint64_t b = smem_desc_sw128_n(kv0 + slot * Sm::TILE, 16384);
 #pragma unroll
-          for (int k = 0; k < kPreTokens / 16; ++k)
-            mma_f16_ts_warp(tmem + 256 + t * D, tmem + t * 128 + 8 * k, b + k * (2048 >> 4), kIdO,
-                            !(first && k == 0));
-        };
-        auto wait_kv = [&](int it) {
-          return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&kv_full[it % kPreSlots]),
-                                                   (it / kPreSlots) & 1, &abort_flag));
-        };
-        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&q_full), 0, &abort_flag)) && wait_kv(0);
-        if (ok) {
+        for (int k = 0; k < kPreTokens / 16; ++k)
+          mma_f16_ts_warp(tmem + 256 + t * D, tmem + t * 128 + 8 * k, b + k * (2048 >> 4), kIdO,
+                          !(first && k == 0));
+      };
+      auto wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, &abort_flag)) != 0;
+      };
+      auto wait_kv = [&](int it) { return wait(&kv_full[it % kPreSlots], (it / kPreSlots) & 1); };
+      auto flag = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0) != 0; };
+      int seg = 0;
+      bool ok = true, begins = true;  // (tile 0 begins a segment)
+#pragma unroll 1
+      for (int j = 0; j < tiles && ok; ++j) {
+        // K's arrival says that the tile's place has been written down
+        const int k_slot = (2 * j) % kPreSlots, v_slot = (2 * j + 1) % kPreSlots;
+        const int next_slot = (2 * j + 2) % kPreSlots;
+        if (begins) {
+          // a segment's first S: its q has come, and the last one's O was read before that
+          ok = wait_kv(2 * j) && wait(&q_full, seg & 1);
+          if (!ok) break;
           tc_fence_after();
+#pragma unroll
           for (int t = 0; t < 2; ++t) {
-            product_s(t, 0);
+            product_s(t, k_slot);
             mma_commit_warp(smem_u32(&s_full[t]));
           }
-          mma_commit_warp(smem_u32(&kv_empty[0]));
+          mma_commit_warp(smem_u32(&kv_empty[k_slot]));
         }
-#pragma unroll 1
-        for (int j = 0; j < n && ok; ++j) {
-          const int v_slot = (2 * j + 1) % kPreSlots, k_slot = (2 * j + 2) % kPreSlots;
-          const bool more = j + 1 < n;
-          ok = wait_kv(2 * j + 1) && (!more || wait_kv(2 * j + 2));
+        const bool ends = flag(sc[j & 3].ends);
+        ok = wait_kv(2 * j + 1) && (ends || wait_kv(2 * j + 2));
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&p_full[t]), j & 1, &abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            product_o(t, v_slot, j == 0);
-            if (t == 1) mma_commit_warp(smem_u32(&kv_empty[v_slot]));
-            if (more) {
-              product_s(t, k_slot);
-              mma_commit_warp(smem_u32(&s_full[t]));
-            }
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && wait(&p_full[t], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          product_o(t, v_slot, begins);
+          if (t == 1) mma_commit_warp(smem_u32(&kv_empty[v_slot]));
+          if (!ends) {
+            product_s(t, next_slot);
+            mma_commit_warp(smem_u32(&s_full[t]));
           }
-          if (ok && more) mma_commit_warp(smem_u32(&kv_empty[k_slot]));
         }
-        if (ok) {
+        if (!ok) break;
+        if (ends) {
           mma_commit_warp(smem_u32(&o_full));
-        } else {  // the products in flight end (bounded) before TMEM is freed
-          mma_commit_warp(smem_u32(&drained));
-          mbar_wait_bounded(smem_u32(&drained), 0, 1000000000ull);
+          ++seg;
+        } else {
+          mma_commit_warp(smem_u32(&kv_empty[next_slot]));
         }
+        begins = ends;
       }
-      __syncwarp();
+      if (!ok) {  // the products in flight end (bounded) before TMEM is freed
+        mma_commit_warp(smem_u32(&drained));
+        mbar_wait_bounded(smem_u32(&drained), 0, 1000000000ull);
+      }
     } else {
       // ================================================================= conversion
       const int cw = warp - kPreSoftWarps - 2;
       bool ok = true;
 #pragma unroll 1
-      for (int item = 0; item < 2 * n && ok; ++item) {
+      for (int item = 0; item < 2 * tiles && ok; ++item) {
         const int slot = item % kPreSlots, round = item / kPreSlots;
         ok = mbar_wait(smem_u32(&raw_full[slot]), round & 1, &abort_flag) &&
              (round == 0 || mbar_wait(smem_u32(&kv_empty[slot]), (round - 1) & 1, &abort_flag));
@@ -565,9 +709,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (!ok) break;
         const uint32_t from = base + Sm::CODES + slot * Sm::RAW;
         const uint32_t to = base + Sm::KV + slot * Sm::TILE;
-        // the last tile may end inside a box, and a missing block leaves what
-        // was there before
-        const bool strange = E4M3 && (item >= 2 * n - 2 || *static_cast<volatile int*>(&sm_gaps));
+        // places that hold no token may hold NaN codes
+        const bool strange = E4M3 && sc[(item >> 1) & 3].strange != 0;
         // 8 rows a step (16 at 64 head dimensions).  Eight neighbouring lanes
         // read 128 bytes on different banks and write eight different chunks
         // of the swizzle: at 128 head dimensions the lanes of the row's second
@@ -614,6 +757,63 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the pieces of the items that workers began and did not end, in the
+// order of the keys: CTA (w, i) rows kPreJoinRows * i .. of worker w's item, a
+// warp a row.
+template <int D>
+__global__ void __launch_bounds__(32 * kPreJoinRows) kv_prefill_join_kernel(const AttnArgs p) {
+  constexpr int PIECE = kPreRows * (D + 2);
+  constexpr int V = D / 32;
+  const int w0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kPreJoinRows + (threadIdx.x >> 5);
+  pdl_wait();
+  const int4 cut = p.cut[2 * w0];
+  pdl_trigger();
+  const int r = cut.z + row;
+  if (cut.x < 0 || r >= cut.w) return;
+  const int q0 = p.cut[2 * w0 + 1].x;
+  const int pieces = cut.x - w0 + 1;
+  float m = -INFINITY, l = 0.0f, o[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float* piece = p.pieces + (i == 0 ? 2 * static_cast<int64_t>(w0) + 1 : 2 * (static_cast<int64_t>(w0) + i)) * PIECE;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece + kPreRows * D) + row);
+    float v[V];
+    if constexpr (V == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(piece + row * D) + lane);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(piece + row * D) + lane);
+      v[0] = x.x, v[1] = x.y;
+    }
+    const float top = fmaxf(m, ml.x);
+    const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
+    const float add = ml.x > -INFINITY ? ex2(ml.x - top) : 0.0f;
+    m = top;
+    l = l * keep + ml.y * add;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = o[k] * keep + v[k] * add;
+  }
+  const int group = p.q_heads / p.kv_heads;
+  const int i = r / group, hq = cut.y * group + r - i * group;
+  const int64_t token = static_cast<int64_t>(q0) + i;
+  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+  uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + lane * V;
+  uint32_t y[V / 2];
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    y[k] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint32_t*>(to) = y[0];
+  if (p.lse && lane == 0)
+    p.lse[token * p.q_heads + hq] =
+        l > 0.0f ? (m - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace i8

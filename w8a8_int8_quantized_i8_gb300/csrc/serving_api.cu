@@ -182,22 +182,30 @@ size_t attention_ws(int workers) {
 // Rows of a request and kv head from which the tcgen05 kernel takes it.
 constexpr int kPrefillRows = 96;
 
+template <int D>
+size_t prefill_ws(int sms) {
+  return static_cast<size_t>(sms) * 2 * (sizeof(int4) + sizeof(float) * kPreRows * (D + 2));
+}
+
 template <int D, bool E4M3>
-i8_status launch_prefill(AttnArgs a, const i8_kv_cache* cache, void* ws, cudaStream_t st) {
+i8_status launch_prefill(AttnArgs a, const i8_kv_cache* cache, void* ws, int sms, cudaStream_t st) {
   constexpr size_t smem = 1024 + PrefillSmem<D>::BYTES;
   if (i8_status e = allow_smem<kv_prefill_kernel<D, E4M3>>(smem)) return e;
   // the largest box of tokens that ends neither inside a block nor inside a tile
   a.box_rows = 16;
   while (a.box_rows < kPreTokens && a.block % (2 * a.box_rows) == 0) a.box_rows *= 2;
+  a.cut = static_cast<int4*>(ws);
+  a.pieces = reinterpret_cast<float*>(a.cut + 2 * static_cast<size_t>(sms));
   CUtensorMap k_map, v_map;
   const bool any = cache->blocks > 0;
   if (i8_status e = encode_cache(&k_map, any ? cache->k : ws, *cache, a.box_rows, false)) return e;
   if (i8_status e = encode_cache(&v_map, any ? cache->v : ws, *cache, a.box_rows, false)) return e;
-  const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads);
-  const int64_t items = (rows + kPreRows - 1) / kPreRows * a.requests * a.kv_heads;
-  if (items > INT32_MAX) return I8_ERR_UNSUPPORTED;
-  return cuda_status(launch_pdl(kv_prefill_kernel<D, E4M3>, dim3(static_cast<unsigned>(items)),
-                                dim3(kPreThreads), smem, st, a, k_map, v_map));
+  const dim3 grid(static_cast<unsigned>(sms));
+  if (cudaError_t e = launch_pdl(kv_prefill_kernel<D, E4M3>, grid, dim3(kPreThreads), smem, st, a,
+                                 k_map, v_map))
+    return cuda_status(e);
+  return cuda_status(launch_pdl(kv_prefill_join_kernel<D>, dim3(grid.x, kPreRows / kPreJoinRows),
+                                dim3(32 * kPreJoinRows), 0, st, a));
 }
 
 template <int D, bool E4M3, int NT>
@@ -205,7 +213,15 @@ i8_status launch_attention(AttnArgs& a, const i8_kv_cache* cache, void* ws, size
                            size_t* need, cudaStream_t st) {
   int workers;
   if (i8_status e = attention_workers<D, E4M3, NT>(&workers)) return e;
-  const size_t bytes = attention_ws<D, NT>(workers);
+  // both kernels' pieces: the calls that follow one another may overlap
+  const size_t own = attention_ws<D, NT>(workers);
+  size_t bytes = own;
+  const bool many = D <= 128 && static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads) >= kPrefillRows;
+  int sms = 0;
+  if (many) {
+    if (i8_status e = device_sms(&sms)) return e;
+    if constexpr (D <= 128) bytes += prefill_ws<D>(sms);
+  }
   if (need) {
     *need = bytes;
     return I8_OK;
@@ -216,9 +232,9 @@ i8_status launch_attention(AttnArgs& a, const i8_kv_cache* cache, void* ws, size
   a.pieces = reinterpret_cast<float*>(a.cut + 2 * static_cast<size_t>(workers));
   a.split_rows = INT32_MAX;
   if constexpr (D <= 128) {
-    if (static_cast<int64_t>(a.max_new) * (a.q_heads / a.kv_heads) >= kPrefillRows) {
+    if (many) {
       a.split_rows = kPrefillRows;
-      if (i8_status e = launch_prefill<D, E4M3>(a, cache, ws, st)) return e;
+      if (i8_status e = launch_prefill<D, E4M3>(a, cache, static_cast<char*>(ws) + own, sms, st)) return e;
     }
   }
   a.unit_cols = AttnTile<D>::UNIT / a.block;
