@@ -57,14 +57,24 @@ struct PrefillSmem {
   static constexpr int BYTES = CODES + kPreSlots * RAW;
 };
 
-struct PrefillScales {   // of the 16-token granules of a tile, and the tile's place
+struct PrefillScales {   // of the 16-token granules of a tile, and its place
   float k[kPreGranules];
   float lv[kPreGranules];     // log2 of V's
   float back[kPreGranules];   // 2^(Lr - lv)
   float ref;                  // Lr
-  int begins, ends;           // it is a segment's first, last
+  int ends;                   // it is a segment's last
   int strange;                // places in it may hold codes that are no token's
 };
+
+// The part of an item in a CTA's share, written down by the warp that copies:
+// the softmax threads have no registers to spare for finding it themselves.
+struct PrefillSegment {
+  int q0, fresh, len;      // of the request
+  int head, row0;
+  int first, last, n;      // its units, of the item's n
+  int64_t item_u;          // the item's first unit
+};
+constexpr int kPreSegments = 8;  // stages of them: the copies run at most three tiles ahead
 
 // Where a CTA stands in the line of all items' tiles of keys (the units).  An
 // item's keys end with its last row's; its row tiles go from the last to the
@@ -221,8 +231,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   constexpr int PIECE = kPreRows * (D + 2);
   extern __shared__ uint8_t sm_pre[];
   __shared__ __align__(8) uint64_t raw_full[kPreSlots], raw_empty[kPreSlots], kv_full[kPreSlots],
-      kv_empty[kPreSlots], sc_full[kPreScales], s_full[2], p_full[2], q_full, o_full, drained;
+      kv_empty[kPreSlots], sc_full[kPreScales], s_full[2], p_full[2], sum_full[2], q_full,
+      o_full, drained;
   __shared__ PrefillScales sc[kPreScales];
+  __shared__ PrefillSegment segs[kPreSegments];
   __shared__ float sm_top[2][2][128], sm_sum[2][2][128];  // [tile][half of the keys][row]
   __shared__ int64_t sm_scan[kAttnWarps], sm_base;
   __shared__ int sm_req;
@@ -244,6 +256,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_full[i]), kPreSoftWarps / 2);
+      mbar_init(smem_u32(&sum_full[i]), kPreSoftWarps / 2);
     }
     mbar_init(smem_u32(&q_full), kPreSoftWarps);
     mbar_init(smem_u32(&o_full), 1);
@@ -323,27 +336,31 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const uint32_t s_at = tmem + lanes + t * 128 + half * 64;  // this half's S
     const uint32_t p_at = tmem + lanes + t * 128 + half * 32;  // and P
     const uint32_t o_at = tmem + lanes + 256 + t * D + half * (D / 2);
-    PrefillCursor cur;
-    first_item(cur);
     bool ok = true;
-    int jt = 0, seg = 0;  // tiles and segments done
+    int jt = 0;  // tiles done
+    // whatever happens, every warp of the tile passes its barrier `tiles` times
 #pragma unroll 1
-    for (int64_t u = u_begin; u < u_end; ++seg) {
-      prefill_seek(p, cur, u);
-      const int first = static_cast<int>(u - cur.item_u);
-      const int last = static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u));
-      const int rows = cur.rq.fresh * group, row0 = cur.tile * kPreRows;
-      const int row = row0 + t * 128 + r;
-      const bool real = row < rows;
+    for (int seg = 0; jt < tiles; ++seg) {
+      // the first tile's scales say that the segment is written down
+      ok = __all_sync(0xFFFFFFFFu,
+                      ok && mbar_wait(smem_u32(&sc_full[jt & 3]), (jt >> 2) & 1, &abort_flag));
+      if (!ok) {
+        for (; jt < tiles; ++jt) named_bar_sync(1 + t, 256);
+        break;
+      }
+      const PrefillSegment& sg = segs[seg & (kPreSegments - 1)];
+      const int first = sg.first, last = sg.last;
+      const int row = sg.row0 + t * 128 + r;
+      const bool real = row < sg.fresh * group;
       const int i = real ? row / group : 0;
-      const int hq = cur.head * group + (real ? row - i * group : 0);
-      const int64_t token = static_cast<int64_t>(cur.rq.q0) + i;
       float rowfac;
       {
         // q's row: its power of two, then this thread's half in fp16 into the
         // swizzled tile (which the segment before has been done with since its
         // o_full)
-        const uint4* qp = reinterpret_cast<const uint4*>(p.q + token * p.ldq_token + hq * p.ldq_head);
+        const int hq = sg.head * group + (real ? row - i * group : 0);
+        const uint4* qp = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<int64_t>(sg.q0) + i) * p.ldq_token + hq * p.ldq_head);
         uint32_t amax = 0;
 #pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
@@ -375,7 +392,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&q_full));
       }
       const int limit =
-          real ? min(max(cur.rq.len - cur.rq.fresh + i + 1, 0), cur.rq.len) : 0x7FFFFFFF;
+          real ? min(max(sg.len - sg.fresh + i + 1, 0), sg.len) : 0x7FFFFFFF;
       float R = -INFINITY, l = 0.0f, Lr = 0.0f;
 #pragma unroll 1
       for (int j = first; j < last; ++j, ++jt) {
@@ -481,13 +498,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       // ---- out: each thread its half of the head dimensions
       sm_sum[t][half][r] = l;
-      named_bar_sync(1 + t, 256);
-      l = (l + sm_sum[t][half ^ 1][r]) * ex2(-Lr);  // the sum of 2^(6 + s - R)
-      ok = ok && mbar_wait(smem_u32(&o_full), seg & 1, &abort_flag);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sum_full[t]));
+      ok = ok && mbar_wait(smem_u32(&sum_full[t]), seg & 1, &abort_flag) &&
+           mbar_wait(smem_u32(&o_full), seg & 1, &abort_flag);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
         tc_fence_after();
-        const bool whole = first == 0 && last == cur.n;
+        l = (l + sm_sum[t][half ^ 1][r]) * ex2(-Lr);  // the sum of 2^(6 + s - R)
+        const int hq = sg.head * group + (real ? row - i * group : 0);
+        const int64_t token = static_cast<int64_t>(sg.q0) + i;
+        const bool whole = first == 0 && last == sg.n;
         const float inv = whole ? (l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f) : 1.0f;
         uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
         // a piece of an item begun earlier goes to the first slot, of one that
@@ -529,13 +550,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (!whole && first == 0 && threadIdx.x == 0) {
           // the worker that holds the item's last unit
-          const int64_t w_end = ((cur.item_u + cur.n) * workers - 1) / total;
-          p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), cur.head, row0, rows);
-          p.cut[2 * blockIdx.x + 1] = make_int4(cur.rq.q0, 0, 0, 0);
+          const int64_t w_end = ((sg.item_u + sg.n) * workers - 1) / total;
+          p.cut[2 * blockIdx.x] = make_int4(static_cast<int>(w_end), sg.head, sg.row0, sg.fresh * group);
+          p.cut[2 * blockIdx.x + 1] = make_int4(sg.q0, 0, 0, 0);
         }
       }
       tc_fence_before();
-      u = cur.item_u + last;
     }
   } else {
     regs_dec<48>();
@@ -544,7 +564,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int boxes = kPreTokens / p.box_rows;
       PrefillCursor cur;
       first_item(cur);
-      int item = 0, jt = 0;
+      int item = 0, jt = 0, seg = -1;
       float ref = 0.0f;
       bool ok = true;
 #pragma unroll 1
@@ -575,6 +595,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
           x = __shfl_sync(0xFFFFFFFFu, x, 0);
           ref = x > -500.0f ? x : 0.0f;
+          ++seg;
+          if (lane == 0)
+            segs[seg & (kPreSegments - 1)] = {
+                cur.rq.q0, cur.rq.fresh, cur.rq.len, cur.head, cur.tile * kPreRows, j,
+                static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u)), cur.n, cur.item_u};
         }
         if (lv == -1000.0f) lv = ref - 60.0f;  // a block of zeros: its weight does not matter
         const bool gap = __any_sync(0xFFFFFFFFu, lane < kPreGranules && lv == -INFINITY);
@@ -586,7 +611,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (lane == 0) {
           z.ref = ref;
-          z.begins = begins;
           z.ends = ends;
           z.strange = gap || (j + 1) * kPreTokens > end;
         }
