@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, &abort_flag)) != 0;
       };
       auto wait_kv = [&](int it) { return wait(&kv_full[it % kPreSlots], (it / kPreSlots) & 1); };
-      auto flag = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0) != 0; };
+      auto flag = [&](int v) { return __any_sync(0xFFFFFFFFu, v != 0) != 0; };  // uniform
       int seg = 0;
       bool ok = true, begins = true;  // (tile 0 begins a segment)
 #pragma unroll 1
