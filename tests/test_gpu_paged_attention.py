@@ -221,3 +221,81 @@ def test_lengths_out_of_range_are_reported():
         assert e.value.status == 7, (lens, cu)
         assert torch.isfinite(out[:0].float()).all()
     _check(st, *_run(st, max_new=1))                       # the context is as good as before
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,news,heads", [
+    ([5000], [30], (4, 1)),                       # a few rows, a long context: one item over all SMs
+    ([129, 1, 4000, 260], [129, 1, 200, 33], (8, 2)),   # some requests by either kernel
+    ([0, 50, 700], [100, 97, 96], (1, 1)),        # rows that see nothing, odd counts
+    ([256, 128, 385], [256, 128, 385], (3, 3)),   # whole prompts that end on and past a tile
+])
+def test_many_rows(lens, news, heads, D, fmt):
+    st = _state(lens, news, 48 if D == 64 else 64, *heads, D, fmt, 21)
+    out, lse = _run(st)
+    _check(st, out, lse)
+    again, _ = _run(st)
+    assert torch.equal(out, again)
+
+
+def test_many_rows_zero_and_uneven_blocks():
+    st = _state([700, 300], [200, 300], 16, 4, 2, 128, "int8", 22)
+    for r, n in enumerate(st["lens"]):
+        for i, b in enumerate(st["table"][r][: -(-n // 16)]):
+            f = [1.0, 1e-3, 0.0, 1e2, 0.0, 1.0, 10.0][(i + r) % 7]
+            st["scale"]["v"][b] *= f
+            if f == 0.0:
+                for c in "kv":
+                    st["code"][c][b] = 0
+                st["scale"]["k"][b] = 0.0
+    _check(st, *_run(st))
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 3.0])
+def test_many_rows_other_scales(scale):
+    st = _state([400, 130], [120, 130], 32, 2, 1, 64, "e4m3", 23)
+    _check(st, *_run(st, scale=scale), scale=scale)
+    few = _state([400, 130], [1, 2], 32, 2, 1, 64, "e4m3", 23)
+    _check(few, *_run(few, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_missing_blocks(D):
+    st = _state([500, 300], [150, 120], 16, 4, 2, D, "e4m3", 24)
+    st["table"][0][3], st["table"][0][20], st["table"][1][0], st["table"][1][18] = -1, 10 ** 6, -7, 2 ** 31 - 1
+    out, lse = i8.paged_attention(st["q"].cuda(), _cache(st), _table(st), _i32(st["lens"]), _i32(st["cu"]), want_lse=True)
+    with pytest.raises(i8.I8Error) as e:
+        i8.sync_check()
+    assert e.value.status == 7
+    _check(st, out, lse)
+
+
+def test_many_rows_in_a_graph_and_on_another_stream():
+    st = _state([300, 900], [150, 200], 64, 4, 2, 128, "int8", 25)
+    cache, tab, lens, cu, q = _cache(st), _table(st), _i32(st["lens"]), _i32(st["cu"]), st["q"].cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = i8.paged_attention(q, cache, tab, lens, cu, max_new=200, want_lse=True)
+    side.synchronize()
+    _check(st, out, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = i8.paged_attention(q, cache, tab, lens, cu, max_new=200, want_lse=True)
+    st["lens"] = [260, 640]
+    lens.copy_(_i32(st["lens"]))
+    graph.replay()
+    i8.sync_check()
+    _check(st, out, lse)
+
+
+def test_workspace_of_the_caller():
+    st = _state([300, 40], [100, 1], 16, 4, 2, 128, "int8", 26)
+    cache = _cache(st)
+    need = i8.paged_attention_workspace_bytes(4, cache, 100)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    _check(st, *_run(st, max_new=100, workspace=ws))
+    with pytest.raises(i8.I8Error) as e:
+        _run(st, max_new=100, workspace=ws[: need - 16])
+    assert e.value.status == 4
