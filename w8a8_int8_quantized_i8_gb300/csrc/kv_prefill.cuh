@@ -130,28 +130,49 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_n(uint32_t saddr, uint32_t n
   return d | (static_cast<uint64_t>(n_stride >> 4) << 16);
 }
 
-// D[tmem] (+)= A * B[smem]^T, kind::f16, one CTA, A in shared memory or in
-// TMEM; and the commit that arrives on `bar` when what was issued is done.  The
-// whole warp calls, its elected lane (the same one every time) issues: kept in
-// converged code the operands stay in uniform registers, where the instruction
-// wants them.  Issued by one lane of a divergent branch, each product of eight
-// took about 980 cycles instead of 512.
-__device__ __forceinline__ void mma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// A product of 128 rows, kind::f16, one CTA: D[tmem] (+)= A * B[smem]^T over
+// D / 16 steps of K (A in shared memory, both K-major in 64-value groups 16 KB
+// apart) or over 8 (A in TMEM, B N-major); and the commit that arrives on `bar`
+// when what was issued is done.  The whole warp calls, its elected lane (the
+// same one every time) issues: in converged code, and a product in one piece,
+// the operands stay in the uniform registers that the instruction wants.
+// Issued step by step from a lane's own branch a product took 980 cycles
+// instead of 512.
+#define I8_MMA_SS(OFF, P)                                                                  \
+  "add.s64 a, %1, " OFF ";\n\tadd.s64 b, %2, " OFF ";\n\t"                                \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " P ";\n\t"
+#define I8_MMA_TS(OFF_A, OFF_B, P)                                                         \
+  "add.s32 a, %1, " OFF_A ";\n\tadd.s64 b, %2, " OFF_B ";\n\t"                            \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, " P ";\n\t"
+template <int D>
+__device__ __forceinline__ void mma_product_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc) {
+  if constexpr (D == 128)
+    asm volatile("{\n\t.reg .pred n, y, q;\n\t.reg .b64 a, b;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+                 "setp.ne.u32 n, 0, 0;\n\tsetp.eq.u32 y, 0, 0;\n\t"
+                 I8_MMA_SS("0", "n") I8_MMA_SS("2", "y") I8_MMA_SS("4", "y") I8_MMA_SS("6", "y")
+                 I8_MMA_SS("1024", "y") I8_MMA_SS("1026", "y") I8_MMA_SS("1028", "y")
+                 I8_MMA_SS("1030", "y") "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred n, y, q;\n\t.reg .b64 a, b;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+                 "setp.ne.u32 n, 0, 0;\n\tsetp.eq.u32 y, 0, 0;\n\t"
+                 I8_MMA_SS("0", "n") I8_MMA_SS("2", "y") I8_MMA_SS("4", "y") I8_MMA_SS("6", "y")
+                 "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
+                 : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+__device__ __forceinline__ void mma_product_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, bool accumulate) {
+  asm volatile("{\n\t.reg .pred n, y, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+               "setp.ne.u32 n, %4, 0;\n\tsetp.eq.u32 y, 0, 0;\n\t"
+               I8_MMA_TS("0", "0", "n") I8_MMA_TS("8", "128", "y") I8_MMA_TS("16", "256", "y")
+               I8_MMA_TS("24", "384", "y") I8_MMA_TS("32", "512", "y") I8_MMA_TS("40", "640", "y")
+               I8_MMA_TS("48", "768", "y") I8_MMA_TS("56", "896", "y") "}" ::"r"(d_tmem),
+               "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+               : "memory");
 }
+#undef I8_MMA_SS
+#undef I8_MMA_TS
 __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
@@ -654,20 +675,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       constexpr uint32_t kIdO = idesc_f16_f32(128, D) | (1u << 16);  // B is N-major
       const uint32_t kv0 = base + Sm::KV;
       auto product_s = [&](int t, int slot) {
-        const uint64_t a = smem_desc_sw128(base + Sm::Q + t * Sm::TILE);
-        const uint64_t b = smem_desc_sw128(kv0 + slot * Sm::TILE);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          mma_f16_ss_warp(tmem + t * 128, a + at, b + at, kIdS, k > 0);
-        }
+        mma_product_ss<D>(tmem + t * 128, smem_desc_sw128(base + Sm::Q + t * Sm::TILE),
+                          smem_desc_sw128(kv0 + slot * Sm::TILE), kIdS);
       };
       auto product_o = [&](int t, int slot, bool first) {
-        const uint64_t b = smem_desc_sw128_n(kv0 + slot * Sm::TILE, 16384);
-#pragma unroll
-        for (int k = 0; k < kPreTokens / 16; ++k)
-          mma_f16_ts_warp(tmem + 256 + t * D, tmem + t * 128 + 8 * k, b + k * (2048 >> 4), kIdO,
-                          !(first && k == 0));
+        mma_product_ts(tmem + 256 + t * D, tmem + t * 128,
+                       smem_desc_sw128_n(kv0 + slot * Sm::TILE, 16384), kIdO, !first);
       };
       auto wait = [&](uint64_t* bar, int parity) {
         return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity, &abort_flag)) != 0;
