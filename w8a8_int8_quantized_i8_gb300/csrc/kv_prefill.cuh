@@ -815,25 +815,40 @@ __global__ void __launch_bounds__(32 * kPreJoinRows) kv_prefill_join_kernel(cons
   float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float* piece = p.pieces + (i == 0 ? 2 * static_cast<int64_t>(w0) + 1 : 2 * (static_cast<int64_t>(w0) + i)) * PIECE;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece + kPreRows * D) + row);
-    float v[V];
-    if constexpr (V == 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(piece + row * D) + lane);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(piece + row * D) + lane);
-      v[0] = x.x, v[1] = x.y;
-    }
-    const float top = fmaxf(m, ml.x);
-    const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
-    const float add = ml.x > -INFINITY ? ex2(ml.x - top) : 0.0f;
-    m = top;
-    l = l * keep + ml.y * add;
+  // two pieces at a time, both on their way before either is used (most items
+  // are cut once)
+#pragma unroll 1
+  for (int i = 0; i < pieces; i += 2) {
+    float2 ml[2];
+    float v[2][V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = o[k] * keep + v[k] * add;
+    for (int x = 0; x < 2; ++x) {
+      ml[x] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[x][k] = 0.0f;
+      if (i + x < pieces) {
+        const int64_t slot = i + x == 0 ? 2 * static_cast<int64_t>(w0) + 1 : 2 * (static_cast<int64_t>(w0) + i + x);
+        const float* piece = p.pieces + slot * PIECE;
+        ml[x] = __ldcg(reinterpret_cast<const float2*>(piece + kPreRows * D) + row);
+        if constexpr (V == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(piece + row * D) + lane);
+          v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(piece + row * D) + lane);
+          v[x][0] = y.x, v[x][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float top = fmaxf(m, ml[x].x);
+      const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
+      const float add = ml[x].x > -INFINITY ? ex2(ml[x].x - top) : 0.0f;
+      m = top;
+      l = l * keep + ml[x].y * add;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = o[k] * keep + v[x][k] * add;
+    }
   }
   const int group = p.q_heads / p.kv_heads;
   const int i = r / group, hq = cut.y * group + r - i * group;

@@ -179,7 +179,11 @@ size_t attention_ws(int workers) {
   return static_cast<size_t>(workers) * 2 * (sizeof(int4) + sizeof(float) * 8 * NT * (D + 2));
 }
 
-// Rows of a request and kv head from which the tcgen05 kernel takes it.
+// Rows of a request and kv head from which the tcgen05 kernel takes it.  It
+// always pays for 256 rows; the warp kernel reads and converts the keys again
+// for every 16.  us by the warp kernel / by tcgen05, 8 requests of 4096 tokens
+// and 8 kv heads of 128: 64 rows 39 / 58, 96 rows 85 / 63, 128 rows 64 / 59, 256
+// rows 117 / 66; one request of 32768: 64 rows 57 / 57, 128 rows 101 / 59.
 constexpr int kPrefillRows = 96;
 
 template <int D>
