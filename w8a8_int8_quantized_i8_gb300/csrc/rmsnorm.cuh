@@ -12,6 +12,11 @@
 // are summed.  h and t are fp32 (h is rounded to bf16 only where it is stored;
 // the norm uses the unrounded sum), and the row is never rounded to bf16
 // between the norm and the quantizer: one rounding, to the 8-bit code.
+//
+// Bound by HBM: 2 + 2 bytes read and 2 + 1 written an element.  A row a CTA, as
+// in the quantizer: small CTAs spread evenly, each element is read once and
+// stays in registers.  16384 x 3072, E4M3: 58.6 us, 6.0 TB/s (89 % of the
+// measured copy rate); one row of 3072: 2.9 us, a launch.
 #pragma once
 #include <cuda_bf16.h>
 
