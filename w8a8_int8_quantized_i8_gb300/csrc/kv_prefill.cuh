@@ -11,12 +11,13 @@
 // tiles take turns: while one tile's softmax runs, the tensor cores do the
 // other's O and next S.
 //
-// Codes are converted to fp16, exactly, once a CTA and serve all 256 rows.  q is scaled per row by a power of two as in
-// kv_attention.cuh.  R is a row's running maximum of s + log2 sv, the log of a
-// term's weight in O; it moves only when it grows by more than 2^8, so that O
-// in TMEM is rarely rescaled, and P, held in fp16 as 2^(6 + s + log2 sv - R),
-// stays below 2^14.  The sum of exponentials is kept in fp32 beside it, each
-// 16 tokens' sum of P times 2^(Lr - log2 sv), Lr a fixed reference.
+// Codes are converted to fp16, exactly, once a CTA and serve all 256 rows.  q is
+// scaled per row by a power of two as in kv_attention.cuh.  R is a row's running
+// maximum of s + log2 sv, the log of a term's weight in O; it moves only when it
+// grows by more than 8 (2^8 in weight), so that O in TMEM is rarely rescaled,
+// and P, held in fp16 as 2^(6 + s + log2 sv - R), stays below 2^14.  The sum of
+// exponentials is kept in fp32 beside it, each 16 tokens' sum of P times
+// 2^(Lr - log2 sv), Lr a fixed reference.
 //
 // Bound by shared memory's bandwidth: a tile of keys takes about 4700 cycles, of
 // which S's operands (512 a row tile), O's (256), and the conversion's reads and
@@ -32,9 +33,9 @@
 // Roles: warps 0-15 softmax (tile = warp / 8; a row has two threads, each for
 // half of the keys, which agree on R once a tile; a warp reads the 32 TMEM
 // lanes of its place in the warpgroup), warp 16 copies by TMA and prepares the
-// scales, warp 17 issues the MMAs, warps 18-23 convert.  At 128 head dimensions 208 KB
-// of shared memory (Q 64, three fp16 tiles 96, three tiles of codes 48) and all
-// of TMEM (S 2 x 128, O 2 x 128 columns): one CTA an SM.
+// scales, warp 17 issues the MMAs, warps 18-23 convert.  At 128 head dimensions
+// 208 KB of shared memory (Q 64, three fp16 tiles 96, three tiles of codes 48)
+// and all of TMEM (S 2 x 128, O 2 x 128 columns): one CTA an SM.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
