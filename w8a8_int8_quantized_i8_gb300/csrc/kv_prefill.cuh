@@ -19,9 +19,11 @@
 // exponentials is kept in fp32 beside it, each 16 tokens' sum of P times
 // 2^(Lr - log2 sv), Lr a fixed reference.
 //
-// Bound by shared memory's bandwidth: a tile of keys takes about 4700 cycles, of
-// which S's operands (512 a row tile), O's (256), and the conversion's reads and
-// writes (1000) are 2560 at 128 bytes a cycle, the products alone 2048.  Four
+// Bound by a row tile's chain: S, softmax (about 2400 cycles and the barriers
+// around it), P, O.  TMEM is full, so a tile has one S buffer and its next S
+// waits for its P to be used; the two tiles in turn take about 4700 cycles a
+// tile of keys, of which the products take 2950 (2048 at the nominal rate: S
+// reads both operands from shared memory, which the conversion uses too).  Four
 // requests, 5357 new tokens, contexts to 8000, 32 query and 8 kv heads of 128:
 // 556 us, 46 % of the measured bf16 rate (warp MMA: 4224 us).  Two softmax
 // threads a row against one: 510 against 543 us; 8 converting warps against 6:
