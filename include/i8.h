@@ -347,7 +347,8 @@ i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_
  * rows cu_new[r] .. cu_new[r + 1] of q, the last ones of its seq_lens[r]
  * tokens; each sees the positions up to its own.  A row that sees nothing
  * (a request whose seq_len is less than its count of new tokens) gives 0, and
- * -inf in lse.
+ * -inf in lse.  Tokens of a sequence that have no block (an id out of range,
+ * or a place past the table's width) are absent, and reported.
  *   q, out [tokens, q_heads, head_dim] bf16, element strides between tokens
  *   and heads (% 8 == 0); lse [tokens, q_heads] fp32 or NULL: the natural log
  *   of the sum of exponentials

@@ -140,3 +140,73 @@ def attention_reference(q, k, v, k_scale, v_scale, table, lens, cu, scale):
                 lse_bound[cu[r]:cu[r + 1], j] = delta[:, 0] * 2 + 2.0 ** -22 * lse[cu[r]:cu[r + 1], j].abs().clamp(max=1e6) \
                     + n * 2.0 ** -24
     return out, lse, bound, lse_bound
+
+
+def attention_definition(q, k, v, k_scale, v_scale, table, lens, cu, scale, code_max):
+    """(out, lse, bound on out, bound on lse) in fp64, as attention_reference,
+    for values far apart and for NaN: a row's result depends on the tokens that
+    it sees and on nothing else.  A sequence's tokens past its table, or without
+    a block, are absent; rows keep their positions.  code_max is the format's
+    largest code.  What P's fp16 loses is counted from the row's own largest
+    term: half the spacing 2^-24 of fp16's subnormals, of at least 2^6."""
+    T, Hq, D = q.shape
+    P, Hkv, B, _ = k.shape
+    dev = q.device
+    q = q.double()
+    out = torch.zeros(T, Hq, D, dtype=torch.float64, device=dev)
+    lse = torch.full((T, Hq), -math.inf, dtype=torch.float64, device=dev)
+    bound, lse_bound = torch.zeros_like(out), torch.zeros_like(lse)
+    for r, n in enumerate(lens):
+        new = cu[r + 1] - cu[r]
+        if new <= 0:
+            continue
+        end = min(max(n, 0), len(table[r]) * B)
+        pos = torch.arange(n - new, n, device=dev)
+        if end == 0:
+            continue
+        ids = table[r][: -(-end // B)]
+        keep = [0 <= i < P for i in ids]
+        at = torch.tensor([i if ok else 0 for i, ok in zip(ids, keep)], device=dev)
+        ok = torch.tensor(keep, device=dev).repeat_interleave(B)[:end]
+        seen = (torch.arange(end, device=dev) <= pos[:, None]) & ok
+        for h in range(Hkv):
+            ks = k_scale[at, h].double().repeat_interleave(B)[:end, None]
+            vs = v_scale[at, h].double().repeat_interleave(B)[:end, None]
+            kk, vv = k[at, h].reshape(-1, D)[:end] * ks, v[at, h].reshape(-1, D)[:end] * vs
+            spoilt = (seen.double() @ torch.isnan(vv).double()) > 0
+            vv = torch.nan_to_num(vv, nan=0.0)
+            top_v = torch.nan_to_num(vs[:, 0], nan=0.0) * code_max
+            for g in range(Hq // Hkv):
+                j, rows = h * (Hq // Hkv) + g, slice(cu[r], cu[r + 1])
+                qq = q[rows, j]
+                s = (qq @ kk.T * scale).masked_fill(~seen, -math.inf)
+                live = seen.any(1)
+                top = s.amax(1, keepdim=True)
+                p = torch.where(seen, (s - torch.where(live[:, None], top, 0.0)).exp(), 0.0)
+                l = p.sum(1, keepdim=True)
+                l1 = torch.where(live[:, None], l, 1.0)
+                o = torch.where(spoilt, math.nan, p @ vv / l1)
+                delta = ((qq.abs() @ kk.abs().T * abs(scale)) * (D + 8) * 2.0 ** -24).masked_fill(~seen, 0).amax(1, keepdim=True) \
+                    + 2.0 ** -19
+                a = p @ vv.abs() / l1
+                bound[rows, j] = (2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * delta) * a
+                                  + end * 2.0 ** -31 * (p * top_v / l1).amax(1, keepdim=True) + 2.0 ** -134)
+                out[rows, j] = o
+                lse[rows, j] = torch.where(live, (top + l.log())[:, 0], -math.inf)
+                lse_bound[rows, j] = delta[:, 0] * 2 + 2.0 ** -22 * lse[rows, j].abs().clamp(max=1e6) + end * 2.0 ** -24
+    return out, lse, bound, lse_bound
+
+
+def check_attention(out, lse, want):
+    """NaN exactly where the definition has it, the rest within its bound."""
+    o, l, bound, lse_bound = want
+    out, lse = out.double(), lse.double()
+    nan = torch.isnan(o)
+    assert torch.equal(torch.isnan(out), nan)
+    err = (out - o).abs()[~nan]
+    assert (err <= bound[~nan]).all(), f"worst {float((err - bound[~nan]).max()):.3g} over the bound"
+    assert torch.equal(torch.isnan(lse), torch.isnan(l))
+    assert torch.equal(torch.isinf(lse) & (lse < 0), torch.isinf(l))
+    assert (out[torch.isinf(l)] == 0).all()
+    plain = torch.isfinite(l)
+    assert ((lse - l).abs()[plain] <= lse_bound[plain]).all()

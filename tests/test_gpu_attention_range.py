@@ -1,0 +1,85 @@
+"""paged_attention where values lie far apart, are NaN, or lengths leave the
+table: against the definition in 64 bits, in which a row depends on the tokens
+that it sees and on nothing else."""
+import random
+
+import pytest
+import torch
+
+import w8a8_int8_quantized_i8_gb300 as i8
+from tests import _serving as ref
+
+pytestmark = pytest.mark.gpu
+
+# one token a request (a row or two a kv head, and 16 rows), and chunks on tcgen05
+FORMS = [pytest.param(1, 2, 2, 64, id="step64"), pytest.param(1, 8, 2, 128, id="step128"),
+         pytest.param(4, 8, 2, 128, id="rows16"), pytest.param(1, 4, 1, 256, id="step256"),
+         pytest.param(120, 2, 2, 64, id="chunk64"), pytest.param(130, 4, 2, 128, id="chunk128")]
+
+
+class Case:
+    """Requests over a shuffled pool, values of any kind set by the test."""
+
+    def __init__(self, lens, news, block, Hq, Hkv, D, fmt, seed, width=None):
+        g, rng = torch.Generator().manual_seed(seed), random.Random(seed)
+        need = [-(-n // block) for n in lens]
+        P, ids = sum(need) + 2, list(range(sum(need) + 2))
+        rng.shuffle(ids)
+        self.table = [[ids.pop() for _ in range(n)] + [-1] * (max(need) - n) for n in need]
+        if width is not None:
+            self.table = [row[:width] for row in self.table]
+        self.lens, self.fmt, self.block = lens, fmt, block
+        self.cu = [0]
+        for n in news:
+            self.cu.append(self.cu[-1] + n)
+        self.q = torch.randn(self.cu[-1], Hq, D, generator=g).bfloat16()
+        self.limit = int(ref.LIMIT[fmt])
+        x = torch.randn(2, P, Hkv, block, D, generator=g) * self.limit / 5
+        x = x.clamp(-self.limit, self.limit)
+        self.codes = [c.round().to(torch.int8) if fmt == "int8" else c.to(torch.float8_e4m3fn) for c in x]
+        self.scales = [torch.full((P, Hkv), 0.02 * 127 / self.limit) for _ in range(2)]
+
+    def bits(self, side):
+        return self.codes[side].view(torch.uint8)
+
+    def run(self, status=0, **kw):
+        cache = i8.QuantKVCache(*(c.view(torch.uint8).cuda().view(c.dtype) for c in self.codes),
+                                *(s.cuda() for s in self.scales))
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        r = i8.paged_attention(self.q.cuda(), cache, i32(self.table), i32(self.lens), i32(self.cu), want_lse=True, **kw)
+        if status:
+            with pytest.raises(i8.I8Error) as e:
+                i8.sync_check()
+            assert e.value.status == status
+        else:
+            i8.sync_check()
+        return r
+
+    def want(self, scale=None):
+        D = self.q.shape[2]
+        k, v = (c.view(torch.uint8).cuda().view(c.dtype).float().double() for c in self.codes)
+        return ref.attention_definition(self.q.cuda(), k, v, self.scales[0].cuda(), self.scales[1].cuda(), self.table,
+                                        self.lens, self.cu, D ** -0.5 if scale is None else scale, float(self.limit))
+
+    def check(self, status=0, **kw):
+        ref.check_attention(*self.run(status), self.want(**kw))
+
+
+# ------------------------------------------------------------------ lengths past the table
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_sequence_longer_than_its_table(new, Hq, Hkv, D):
+    """The tokens past the table are absent, the others stay where they are: the
+    rows' positions are the sequence's, and sync_check says that it was cut."""
+    lens = [400, 333, 500]
+    c = Case(lens, [min(new, 100)] * 3, 16, Hq, Hkv, D, "int8", 1, width=21)   # 336 tokens of 400 and 500
+    c.check(status=7)
+
+
+def test_table_that_ran_out_of_width():
+    """What build_block_tables gives where the width runs out: the rows whose
+    own tokens have a block see exactly what they would in a wide table."""
+    c = Case([200], [150], 16, 4, 2, 128, "int8", 2)
+    want, _, bound, _ = c.want()
+    c.table = [c.table[0][:8]]                           # 128 tokens: the rows of positions 50..127
+    cut, _ = c.run(status=7)
+    assert ((cut.double() - want).abs() <= bound)[:78].all()

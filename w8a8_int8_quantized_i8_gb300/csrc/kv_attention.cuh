@@ -195,7 +195,9 @@ __device__ __forceinline__ int64_t attn_scan(int64_t v, int64_t& total, int64_t*
 
 // What a CTA needs to know of a request.
 struct AttnRequest {
-  int q0, fresh, len;
+  int q0, fresh;
+  int pos0;        // position of its first new token
+  int len;         // its tokens that the table has room for
   int tiles;       // row tiles
   int per_item;    // units of an item
   int64_t units;
@@ -206,13 +208,14 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   AttnRequest a;
   a.q0 = p.cu_new[r];
   const int64_t fresh = static_cast<int64_t>(p.cu_new[r + 1]) - a.q0;
-  a.len = max(0, p.seq_lens[r]);
+  const int len = max(0, p.seq_lens[r]);
   const bool bad = a.q0 < 0 || a.q0 + fresh > p.tokens || fresh > p.max_new;
   a.fresh = bad || fresh < 0 ? 0 : static_cast<int>(fresh);
-  if (bad || a.len > static_cast<int64_t>(p.width) * p.block) {
-    atomicOr(&g_status, 1u << 7);
-    a.len = min(a.len, p.width * p.block);
-  }
+  // the tokens past the table are absent; the others, and the rows, stay where
+  // they are
+  a.pos0 = len - a.fresh;
+  a.len = min(len, p.width * p.block);
+  if (bad || a.len < len) atomicOr(&g_status, 1u << 7);
   a.tiles = static_cast<int>((static_cast<int64_t>(a.fresh) * (p.q_heads / p.kv_heads) + ROWS - 1) / ROWS);
   a.per_item = max(1, (a.len + UNIT - 1) / UNIT);  // one even where there is nothing to see
   a.units = static_cast<int64_t>(a.per_item) * a.tiles * p.kv_heads;
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
 
   // A segment: the part of an item in this share.
   struct Segment {
-    int q0, fresh, len, rows;  // of the request
+    int q0, pos0, len, rows;   // of the request
     int head, row0;
     int first, last, per_item; // units of the item
     int64_t item_u;            // the item's first unit
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
     }
     const int64_t item = (u - base) / rq.per_item;
     sg.q0 = rq.q0;
-    sg.fresh = rq.fresh;
+    sg.pos0 = rq.pos0;
     sg.len = rq.len;
     sg.rows = rq.fresh * group;
     sg.per_item = rq.per_item;
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
     sg.head = static_cast<int>(item / rq.tiles);
     sg.row0 = static_cast<int>(item - static_cast<int64_t>(sg.head) * rq.tiles) * ROWS;
     const int newest = (min(sg.row0 + ROWS, sg.rows) - 1) / group;  // new token of the tile's last row
-    const int most = min(max(sg.len - sg.fresh + newest + 1, 0), sg.len);
+    const int most = min(max(sg.pos0 + newest + 1, 0), sg.len);
     feed_begin<D>(p, feed, &k_map, &v_map, p.table + req * p.ld_table, sg.head, sg.first * UNIT,
                   min(most, sg.last * UNIT), ring, bars, warp, lane);
     u = sg.item_u + sg.last;
@@ -663,7 +666,6 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
   for (; u < u_end;) {
     Segment sg;
     begin_segment(sg);                   // its first keys come while q is read
-    const int pos0 = sg.len - sg.fresh;  // position of the request's first new token
 
     // q fragments (column n of a tile is row g) and what the lane's two columns
     // of S^T need: their factor and the first position that they do not see
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
       }
       // row g's exponent and limit go to the lanes whose columns 2c, 2c + 1 it is
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * p.scale_log2;
-      const int lim = real ? min(max(pos0 + i + 1, 0), sg.len) : 0;
+      const int lim = real ? min(max(sg.pos0 + i + 1, 0), sg.len) : 0;
 #pragma unroll
       for (int i2 = 0; i2 < 2; ++i2) {
         rowfac[n][i2] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i2) * 4);

@@ -83,7 +83,7 @@ struct PrefillScales {   // of the 16-token granules of a tile, and its place
 // The part of an item in a CTA's share, written down by the warp that copies:
 // the softmax threads have no registers to spare for finding it themselves.
 struct PrefillSegment {
-  int q0, fresh, len;      // of the request
+  int q0, fresh, pos0, len;  // of the request
   int head, row0;
   int first, last, n;      // its units, of the item's n
   int64_t item_u;          // the item's first unit
@@ -102,7 +102,7 @@ struct PrefillCursor {
 // The tokens that a row tile sees.
 __device__ __forceinline__ int prefill_end(const AttnRequest& rq, int group, int tile) {
   const int last = min((tile + 1) * kPreRows, rq.fresh * group) - 1;
-  return min(max(rq.len - rq.fresh + last / group + 1, 0), rq.len);
+  return min(max(rq.pos0 + last / group + 1, 0), rq.len);
 }
 // Units of a row tile: one even where it sees nothing.
 __device__ __forceinline__ int prefill_units(const AttnRequest& rq, int group, int tile) {
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&q_full));
       }
       const int limit =
-          real ? min(max(sg.len - sg.fresh + i + 1, 0), sg.len) : 0x7FFFFFFF;
+          real ? min(max(sg.pos0 + i + 1, 0), sg.len) : 0x7FFFFFFF;
       float R = -INFINITY, l = 0.0f, Lr = 0.0f;
 #pragma unroll 1
       for (int j = first; j < last; ++j, ++jt) {
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           ++seg;
           if (lane == 0)
             segs[seg & (kPreSegments - 1)] = {
-                cur.rq.q0, cur.rq.fresh, cur.rq.len, cur.head, cur.tile * kPreRows, j,
+                cur.rq.q0, cur.rq.fresh, cur.rq.pos0, cur.rq.len, cur.head, cur.tile * kPreRows, j,
                 static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u)), cur.n, cur.item_u};
         }
         if (lv == -1000.0f) lv = ref - 60.0f;  // a block of zeros: its weight does not matter
