@@ -83,3 +83,55 @@ def test_table_that_ran_out_of_width():
     c.table = [c.table[0][:8]]                           # 128 tokens: the rows of positions 50..127
     cut, _ = c.run(status=7)
     assert ((cut.double() - want).abs() <= bound)[:78].all()
+
+
+# ------------------------------------------------------------------ V's scales far apart
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("far", [1e-18, 1e-30, 3e-36, 1e-37, 1e-41])
+@pytest.mark.parametrize("order", ["small_first", "large_first", "between"])
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_values_far_apart(new, Hq, Hkv, D, order, far, fmt):
+    """Blocks whose values differ by up to 10^41: the sum of exponentials counts
+    all of them."""
+    c = Case([400, 40 + new], [new, new], 16, Hq, Hkv, D, fmt, 3)
+    for row in c.table:
+        ids = [b for b in row if b >= 0]
+        small = {"small_first": ids[: len(ids) // 2], "large_first": ids[len(ids) // 2:], "between": ids[1::2]}[order]
+        for b in small:
+            c.scales[1][b] *= far
+    c.check()
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+@pytest.mark.parametrize("loud", [0, 1])
+def test_the_attended_block_is_the_quiet_one(new, Hq, Hkv, D, loud):
+    """All of a row's weight lies on tokens whose values are 10^36 times smaller
+    than the others': the row's result is those values."""
+    c = Case([160 + new], [new], 16, Hq, Hkv, D, "int8", 4)
+    ids = [b for b in c.table[0] if b >= 0][: 10]
+    c.q = c.q.abs()
+    for i, b in enumerate(ids):
+        quiet = (i >= 5) == bool(loud)
+        c.codes[0][b] = 120 if quiet else -120
+        if quiet:
+            c.scales[1][b] *= 1e-36
+    for b in c.table[0][10:]:
+        c.codes[0][b] = -120
+    c.scales[0][:] = 0.5
+    c.check()
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_blocks_of_zeros_everywhere(new, Hq, Hkv, D):
+    """Values that are all zero, in some blocks and in every block of a
+    request: 0, and the sum of exponentials of all tokens."""
+    c = Case([150 + new, 90 + new], [new, new], 16, Hq, Hkv, D, "int8", 5)
+    for i, b in enumerate(c.table[0]):
+        if i % 3 != 1:
+            c.scales[1][b] = 0.0
+            c.codes[1][b] = 0
+    for b in c.table[1]:
+        if b >= 0:
+            c.scales[1][b] = 0.0
+            c.codes[1][b] = 0
+    c.check()

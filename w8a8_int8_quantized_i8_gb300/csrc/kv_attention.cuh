@@ -19,8 +19,14 @@
 //   * P is rounded to fp16 (11 bits) for the second product, as 2^(10 + s - R)
 //     with s = log2(e) S + log2 sv, the log of a term's weight in O, and R its
 //     running maximum in the row: at most 2^10, and what lies 2^-35 below the
-//     maximum vanishes.  The sum of exponentials adds P / sv, in fp32.  (A
-//     block of zeros counts with the block before it for sv.)
+//     maximum vanishes;
+//   * the sum of exponentials counts every token, however small its block's
+//     values are next to others'.  While log2 sv stays within 40 of that of
+//     the first block, Lr, it adds P / sv, as 2^(10 + log2(e) S + Lr - R).  From
+//     the first block on that is further off, or all zeros, it has a maximum X
+//     of its own, that of log2(e) S alone, and adds 2^(log2(e) S - X) instead.
+//     Either is l * 2^X, with X = R - 10 - Lr in the first form, and where parts
+//     meet it is its logarithm L = X + log2 l: O * 2^(R - 10 - L) is the result.
 //
 // The products run transposed: S^T = K q^T and O^T = V^T P^T, so that the
 // tokens and the head dimension fill the 16-row side of the warp MMA
@@ -109,6 +115,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A running maximum as a reference for exponents: where nothing has been seen
+// it is -inf, and any finite number will do (2^(-inf - 0) = 0).
+__device__ __forceinline__ float exp_ref(float m) { return m > -INFINITY ? m : 0.0f; }
 
 // Four codes of a word as two fp16 pairs, (0, 1) and (2, 3).
 template <bool E4M3>
@@ -154,7 +163,9 @@ template <int D, int NT>
 struct AttnState {
   float o[D / 16][NT][4];  // O^T: rows d, columns 8 * nt + 2c + {0, 1}
   float m[NT][2];          // running maximum R of those columns
-  float l[NT][2];          // this lane's share of the sum of 2^(10 + log2(e) S - R)
+  float l[NT][2];          // this lane's share of the sum of 2^(log2(e) S - X)
+  float x[NT][2];          // X: the second form's maximum of this lane's scores
+  float ref;               // Lr
 };
 
 // A warp's feed: where its copies of a segment of keys stand.
@@ -223,13 +234,23 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   return a;
 }
 
-// D / 16 contiguous head dimensions of one row, times inv, to bf16.
+// log2 of a sum l * 2^x; -inf where nothing was seen.
+__device__ __forceinline__ float attn_log(float x, float l) {
+  return l == 0.0f ? -INFINITY : x + __log2f(l);
+}
+// What O is multiplied by, twice, for the result: its exponent's range is more
+// than fp32's.  A row that sees nothing gives 0.
+__device__ __forceinline__ float attn_factor(float o_ref, float L) {
+  return L == -INFINITY ? 0.0f : ex2(0.5f * (o_ref - L));
+}
+
+// D / 16 contiguous head dimensions of one row, times f * f, to bf16.
 template <int D>
-__device__ __forceinline__ void attn_store_row(uint16_t* out, const float (&o)[D / 16], float inv) {
+__device__ __forceinline__ void attn_store_row(uint16_t* out, const float (&o)[D / 16], float f) {
   uint32_t w[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * i] * f * f, o[2 * i + 1] * f * f);
     w[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
   if constexpr (D == 64) {
@@ -254,16 +275,14 @@ __device__ __forceinline__ int attn_own_row(int t) { return 2 * (t & 3) + ((t >>
 
 template <int D>
 __device__ __forceinline__ void attn_write(const AttnArgs& p, int q0, int r, int head, int t,
-                                           const float (&o)[D / 16], float m, float l) {
+                                           const float (&o)[D / 16], float m, float L) {
   const int group = p.q_heads / p.kv_heads;
   const int i = r / group, hq = head * group + r - i * group;
-  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;  // a row that sees nothing gives 0
   const int d = attn_own_dim<D>(t);
   const int64_t token = static_cast<int64_t>(q0) + i;
-  attn_store_row<D>(p.out + token * p.ldo_token + hq * p.ldo_head + d, o, inv);
-  if (p.lse && d == 0)
-    p.lse[token * p.q_heads + hq] =
-        l > 0.0f ? (m + (log2f(l) - 10.0f)) * 0.69314718055994531f : -INFINITY;
+  attn_store_row<D>(p.out + token * p.ldo_token + hq * p.ldo_head + d, o,
+                    attn_factor(exp_ref(m) - 10.0f, L));
+  if (p.lse && d == 0) p.lse[token * p.q_heads + hq] = L * 0.69314718055994531f;
 }
 
 __device__ __forceinline__ uint4 lds_16(uint32_t a) {
@@ -382,10 +401,12 @@ __device__ __forceinline__ void feed_begin(const AttnArgs& p, AttnFeed<D>& f, co
   }
 }
 
-// A row tile of a request's rows against the segment that the feed has begun.
+// A row tile of a request's rows against the segment that the feed has begun,
+// from its tile at t0 on, which is in stage `slot`, to the end, or, without
+// FAR, to the first tile whose values are far from the first one's.
 // `ring` and `bars`: the shared-memory addresses of the warp's stages and of
 // the barriers on which their copies count; `parity`: a bit for each stage.
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool FAR>
 __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, const void* k_map,
                                              const void* v_map,
                                              const uint32_t (&qf)[NT][D / 16][2],
@@ -393,7 +414,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
                                              const int (&limit)[NT][2], int all_seen,
                                              uint32_t ring, uint32_t bars, uint32_t& parity,
                                              volatile int* abort_flag, int lane,
-                                             AttnState<D, NT>& st) {
+                                             AttnState<D, NT>& st, int& t0, int& slot) {
   using Tile = AttnTile<D>;
   constexpr int H = Tile::HALVES;
   constexpr int S = Tile::STAGES;
@@ -401,21 +422,28 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
   constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // the same of V (8 bytes at D = 64)
   constexpr int VB = D / 8 < 16 ? D / 8 : 16;    // contiguous bytes of V a lane takes
   const int g = lane >> 2, c = lane & 3;
-  int slot = 0;
-  float last_sv = 0x1p-60f;    // of the last block that is not all zeros
 #pragma unroll 1
-  for (int t0 = f.t_first; t0 < f.end; t0 += Tile::UNIT) {
-    if (!mbar_wait(bars + 8 * slot, (parity >> slot) & 1u, abort_flag)) break;
-    parity ^= 1u << slot;
-    float sk[H], lv[H], back[H];  // log2 sv and 1 / sv
+  for (; t0 < f.end; t0 += Tile::UNIT) {
+    float sk[H], lv[H], back[H];  // lv: log2 sv, back: 2^(Lr - lv)
     bool gone[H];                 // no such block: its tokens are left out
+    bool far = false;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       sk[h] = f.ksc[0][h];
       gone[h] = isnan(sk[h]);
-      if (f.vsc[0][h] > 0.0f) last_sv = f.vsc[0][h];
-      lv[h] = __log2f(last_sv);
-      back[h] = __fdividef(1.0f, last_sv);
+      lv[h] = gone[h] ? st.ref : __log2f(f.vsc[0][h]);  // -inf for a block of zeros
+      if (!FAR && h == 0 && t0 == f.t_first && lv[0] > -INFINITY) st.ref = lv[0];
+      far = far || !(fabsf(lv[h] - st.ref) <= 40.0f);
+      back[h] = ex2(st.ref - lv[h]);
+    }
+    if (!FAR && __builtin_expect(__any_sync(0xFFFFFFFFu, far), 0)) break;
+    if (!mbar_wait(bars + 8 * slot, (parity >> slot) & 1u, abort_flag)) {
+      t0 = f.end;
+      break;
+    }
+    parity ^= 1u << slot;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
 #pragma unroll
       for (int i = 0; i + 2 < S; ++i) {
         f.ksc[i][h] = f.ksc[i + 1][h];
@@ -492,11 +520,27 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
       for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[h][n][i] = fmaf(s[h][n][i], sk[h] * rowfac[n][i & 1], lv[h]);
+          s[h][n][i] = fmaf(s[h][n][i], sk[h] * rowfac[n][i & 1], FAR ? 0.0f : lv[h]);
           if (masked && (gone[h] || t0 + 16 * h + g + 8 * (i >> 1) >= limit[n][i & 1]))
             s[h][n][i] = -INFINITY;
           top[i & 1] = fmaxf(top[i & 1], s[h][n][i]);
         }
+      if constexpr (FAR) {  // (s without lv)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = fmaxf(st.x[n][i], top[i]);
+          st.l[n][i] *= ex2(st.x[n][i] - exp_ref(x));
+          st.x[n][i] = x;
+          top[i] = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            st.l[n][i] += ex2(s[h][n][i] - exp_ref(x)) + ex2(s[h][n][i + 2] - exp_ref(x));
+            s[h][n][i] += lv[h];
+            s[h][n][i + 2] += lv[h];
+            top[i] = fmaxf(top[i], fmaxf(s[h][n][i], s[h][n][i + 2]));
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = top[i];
@@ -505,10 +549,9 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
         const float m = fmaxf(st.m[n][i], x);
         moved = moved || m != st.m[n][i];
-        // a row that has seen nothing yet keeps m = -inf: its factor is 0
-        alpha[n][i] = m > -INFINITY ? ex2(st.m[n][i] - m) : 0.0f;
+        alpha[n][i] = ex2(st.m[n][i] - exp_ref(m));
         st.m[n][i] = m;
-        st.l[n][i] *= alpha[n][i];
+        if constexpr (!FAR) st.l[n][i] *= alpha[n][i];
       }
     }
     if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -528,10 +571,8 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float m = st.m[n][i & 1];
-          // (where the row has seen nothing, s and m are -inf both: 0, not NaN)
-          e[i] = s[h][n][i] > -INFINITY ? ex2(s[h][n][i] - m + 10.0f) : 0.0f;
-          st.l[n][i & 1] = fmaf(e[i], back[h], st.l[n][i & 1]);
+          e[i] = ex2(s[h][n][i] + (10.0f - exp_ref(st.m[n][i & 1])));
+          if constexpr (!FAR) st.l[n][i & 1] = fmaf(e[i], back[h], st.l[n][i & 1]);
         }
         b[n][0] = transpose_8x8(pack_f16x2(e[0], e[1]));
         b[n][1] = transpose_8x8(pack_f16x2(e[2], e[3]));
@@ -580,7 +621,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
   __shared__ float sm_o[kAttnWarps * kAttnMeet * NT * 4 * 32];  // where the warps' parts meet
   __shared__ __align__(8) uint64_t sm_bars[kAttnWarps][S];
   __shared__ int abort_flag;
-  __shared__ float sm_m[kAttnWarps][ROWS], sm_l[kAttnWarps][ROWS];
+  __shared__ float sm_m[kAttnWarps][ROWS], sm_l[kAttnWarps][ROWS];  // R and L
   __shared__ int64_t sm_scan[kAttnWarps];
   __shared__ int64_t sm_base;
   __shared__ int sm_req;
@@ -713,6 +754,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
     least = __reduce_min_sync(0xFFFFFFFFu, least);
 
     AttnState<D, NT> st;
+    st.ref = 0.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       st.m[n][0] = st.m[n][1] = -INFINITY;
@@ -722,8 +764,29 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.o[j][n][i] = 0.0f;
     }
-    attend_tiles<D, E4M3, NT>(p, feed, &k_map, &v_map, qf, rowfac, limit, least, ring, bars, parity,
-                              &abort_flag, lane, st);
+    int t0 = feed.t_first, at = 0;  // (the ring begins each segment at its first stage)
+    attend_tiles<D, E4M3, NT, false>(p, feed, &k_map, &v_map, qf, rowfac, limit, least, ring, bars,
+                                     parity, &abort_flag, lane, st, t0, at);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) st.x[n][i] = st.m[n][i] - 10.0f - st.ref;
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, t0 < feed.end), 0)) {
+      attend_tiles<D, E4M3, NT, true>(p, feed, &k_map, &v_map, qf, rowfac, limit, least, ring, bars,
+                                      parity, &abort_flag, lane, st, t0, at);
+      // the lanes' sums on one X, that of the row
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = st.x[n][i];
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+          st.l[n][i] *= ex2(st.x[n][i] - exp_ref(x));
+          st.x[n][i] = x;
+        }
+    }
     // ---- the four warps' parts meet
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -735,7 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
         if (g == 0) {
           sm_m[warp][8 * n + 2 * c + i] = st.m[n][i];
-          sm_l[warp][8 * n + 2 * c + i] = l;
+          sm_l[warp][8 * n + 2 * c + i] = attn_log(st.x[n][i], l);
         }
       }
     const bool whole = sg.first == 0 && sg.last == sg.per_item;
@@ -769,7 +832,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
         for (int k = 0; k < kAttnMeet; ++k) o[n][part * kAttnMeet + k] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) {
-          const float f = sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f;
+          const float f = ex2(sm_m[w][row] - exp_ref(m));
 #pragma unroll
           for (int k = 0; k < kAttnMeet; ++k) {
             const int x = static_cast<int>(threadIdx.x >> 6) * (kAttnMeet / 2) + (k >> 1);
@@ -784,14 +847,17 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = 8 * n + attn_own_row(threadIdx.x);
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, most = -INFINITY, l = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, sm_m[w][row]);
+      for (int w = 0; w < kAttnWarps; ++w) {
+        m = fmaxf(m, sm_m[w][row]);
+        most = fmaxf(most, sm_l[w][row]);
+      }
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w)
-        l = fmaf(sm_m[w][row] > -INFINITY ? ex2(sm_m[w][row] - m) : 0.0f, sm_l[w][row], l);
+      for (int w = 0; w < kAttnWarps; ++w) l += ex2(sm_l[w][row] - exp_ref(most));
+      const float L = attn_log(most, l);
       if (whole) {
-        if (sg.row0 + row < sg.rows) attn_write<D>(p, sg.q0, sg.row0 + row, sg.head, threadIdx.x, o[n], m, l);
+        if (sg.row0 + row < sg.rows) attn_write<D>(p, sg.q0, sg.row0 + row, sg.head, threadIdx.x, o[n], m, L);
       } else {
         float* to = piece + (n * kAttnThreads + threadIdx.x) * (D / 16);
 #pragma unroll
@@ -799,7 +865,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
           *reinterpret_cast<float4*>(to + k) = make_float4(o[n][k], o[n][k + 1], o[n][k + 2], o[n][k + 3]);
         if (attn_own_dim<D>(threadIdx.x) == 0) {
           piece[ROWS * D + 2 * row] = m;
-          piece[ROWS * D + 2 * row + 1] = l;
+          piece[ROWS * D + 2 * row + 1] = L;
         }
       }
     }
@@ -823,7 +889,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads* kJoinGroups) kv_attention_join_kernel(const AttnArgs p) {
   constexpr int ROWS = 8 * NT;
   constexpr int PIECE = ROWS * (D + 2);
-  __shared__ float sm_m[kJoinGroups][8], sm_l[kJoinGroups][8];
+  __shared__ float sm_m[kJoinGroups][8], sm_x[kJoinGroups][8], sm_l[kJoinGroups][8];
   __shared__ float sm_o[kJoinGroups - 1][D / 16][kAttnThreads];
   const int w0 = blockIdx.x, n = blockIdx.y;
   const int t = threadIdx.x % kAttnThreads, grp = threadIdx.x / kAttnThreads;
@@ -834,22 +900,22 @@ __global__ void __launch_bounds__(kAttnThreads* kJoinGroups) kv_attention_join_k
   const int q0 = p.cut[2 * w0 + 1].x;
   const int pieces = cut.x - w0 + 1;
   const int row = attn_own_row(t);
-  float m = -INFINITY, l = 0.0f, o[D / 16];
+  float m = -INFINITY, xm = -INFINITY, l = 0.0f, o[D / 16];
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) o[k] = 0.0f;
 #pragma unroll 2
   for (int i = grp; i < pieces; i += kJoinGroups) {
     const float* piece = p.pieces + (i == 0 ? 2 * static_cast<int64_t>(w0) + 1 : 2 * (static_cast<int64_t>(w0) + i)) * PIECE;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece + ROWS * D) + 8 * n + row);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece + ROWS * D) + 8 * n + row);  // R, L
     float4 v[D / 64];
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)
       v[k] = __ldcg(reinterpret_cast<const float4*>(piece + (n * kAttnThreads + t) * (D / 16)) + k);
-    const float top = fmaxf(m, ml.x);
-    const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
-    const float add = ml.x > -INFINITY ? ex2(ml.x - top) : 0.0f;
+    const float top = fmaxf(m, ml.x), most = fmaxf(xm, ml.y);
+    const float keep = ex2(m - exp_ref(top)), add = ex2(ml.x - exp_ref(top));
+    l = l * ex2(xm - exp_ref(most)) + ex2(ml.y - exp_ref(most));
     m = top;
-    l = l * keep + ml.y * add;
+    xm = most;
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
       o[4 * k] = o[4 * k] * keep + v[k].x * add;
@@ -860,6 +926,7 @@ __global__ void __launch_bounds__(kAttnThreads* kJoinGroups) kv_attention_join_k
   }
   if (attn_own_dim<D>(t) == 0) {
     sm_m[grp][row] = m;
+    sm_x[grp][row] = xm;
     sm_l[grp][row] = l;
   }
   if (grp > 0) {
@@ -868,18 +935,21 @@ __global__ void __launch_bounds__(kAttnThreads* kJoinGroups) kv_attention_join_k
   }
   __syncthreads();
   if (grp > 0) return;
-  float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kJoinGroups; ++i) top = fmaxf(top, sm_m[i][row]);
+  float top = -INFINITY, most = -INFINITY, sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kJoinGroups; ++i) {
-    const float f = sm_m[i][row] > -INFINITY ? ex2(sm_m[i][row] - top) : 0.0f;
-    sum = fmaf(f, sm_l[i][row], sum);
+    top = fmaxf(top, sm_m[i][row]);
+    most = fmaxf(most, sm_x[i][row]);
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinGroups; ++i) {
+    const float f = ex2(sm_m[i][row] - exp_ref(top));
+    sum = fmaf(ex2(sm_x[i][row] - exp_ref(most)), sm_l[i][row], sum);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) o[k] = i == 0 ? o[k] * f : fmaf(f, sm_o[i > 0 ? i - 1 : 0][k][t], o[k]);
   }
   const int r = cut.z + 8 * n + row;
-  if (r < cut.w) attn_write<D>(p, q0, r, cut.y, t, o, top, sum);
+  if (r < cut.w) attn_write<D>(p, q0, r, cut.y, t, o, top, attn_log(most, sum));
 }
 
 }  // namespace i8

@@ -17,7 +17,9 @@
 // grows by more than 8 (2^8 in weight), so that O in TMEM is rarely rescaled,
 // and P, held in fp16 as 2^(6 + s + log2 sv - R), stays below 2^14.  The sum of
 // exponentials is kept in fp32 beside it, each 16 tokens' sum of P times
-// 2^(Lr - log2 sv), Lr a fixed reference.
+// 2^(Lr - log2 sv), Lr a segment's fixed reference; from the first tile on that
+// holds a log2 sv further than 40 from Lr, or a block of zeros, it has a maximum X
+// of its own, as in kv_attention.cuh.
 //
 // Bound by a row tile's chain: S, softmax (about 2400 cycles and the barriers
 // around it), P, O.  TMEM is full, so a tile has one S buffer and its next S
@@ -44,6 +46,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kv_attention.cuh"
 #include "ptx.cuh"
@@ -74,8 +77,10 @@ struct PrefillSmem {
 struct PrefillScales {   // of the 16-token granules of a tile, and its place
   float k[kPreGranules];
   float lv[kPreGranules];     // log2 of V's
-  float back[kPreGranules];   // 2^(Lr - lv)
+  float back[kPreGranules];   // 2^(Lr - lv), or 0 where `far`
   float ref;                  // Lr
+  int far;                    // the segment's lv has left Lr's neighbourhood
+  int there;                  // a bit for each granule that holds tokens
   int ends;                   // it is a segment's last
   int strange;                // places in it may hold codes that are no token's
 };
@@ -428,9 +433,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       const int limit =
           real ? min(max(sg.pos0 + i + 1, 0), sg.len) : 0x7FFFFFFF;
-      float R = -INFINITY, l = 0.0f, Lr = 0.0f;
+      float R = -INFINITY, l = 0.0f, Lr = 0.0f, X = -INFINITY;
+      int j = first;
+      // the segment's tiles; without FAR, up to the first one that is far (two
+      // loops, so that the usual one pays nothing for the other)
+      auto go_over = [&](auto kind) {
+      constexpr bool FAR = decltype(kind)::value;
 #pragma unroll 1
-      for (int j = first; j < last; ++j, ++jt) {
+      for (; j < last; ++j, ++jt) {
         ok = ok && mbar_wait(smem_u32(&sc_full[jt & 3]), (jt >> 2) & 1, &abort_flag) &&
              mbar_wait(smem_u32(&s_full[t]), jt & 1, &abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -440,14 +450,36 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         tc_fence_after();
         const PrefillScales& z = sc[jt & 3];
-        if (j == first) Lr = z.ref;
+        if (!FAR && j == first) Lr = z.ref;
         const int seen = limit - j * kPreTokens - 64 * half;  // columns below this are seen
-        const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
+        const bool masked = __any_sync(0xFFFFFFFFu, seen < 64 || (!FAR && z.far));
+        if constexpr (FAR) {
+          // this thread's exponentials by themselves: their maximum, their sum
+          float x = X, sum = 0.0f;
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            const int gr = 4 * half + (g & 3);
+            const int lim = (z.there >> gr) & 1 ? seen - 16 * (g & 3) : 0;
+            const float f = z.k[gr] * rowfac;
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_at + 16 * (g & 3), v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float y = k < lim ? __uint_as_float(v[k]) * f : -INFINITY;
+              if (g < 4) x = fmaxf(x, y);
+              else sum += ex2(y - exp_ref(x));
+            }
+          }
+          l = fmaf(l, ex2(X - exp_ref(x)), sum);
+          X = x;
+        }
         uint32_t s[2][32];
         tmem_ld_32x32b_x32(s_at, s[0]);
         tmem_ld_32x32b_x32(s_at + 32, s[1]);
         tmem_wait_ld(s[0]);
         tmem_wait_ld(s[1]);
+        if (!FAR && masked && z.far) return;
         float top = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -478,9 +510,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         top = fmaxf(top, sm_top[t][half ^ 1][r]);
         float alpha = 1.0f;
         if (top > R + 8.0f) {  // (-inf + 8 is -inf)
-          alpha = R > -INFINITY ? ex2(R - top) : 0.0f;
+          alpha = ex2(R - top);
           R = top;
-          l *= alpha;
+          if (!FAR) l *= alpha;
         }
         if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && j > first) {
           // S of this tile was committed after the last product into O, so O
@@ -495,7 +527,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             tmem_st_32x32b_x16(o_at + 16 * q, o);
           }
         }
-        const float ref = (R > -INFINITY ? R : 0.0f) - 6.0f;
+        const float ref = exp_ref(R) - 6.0f;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t pk[16];
@@ -531,8 +563,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
       }
+      };
+      go_over(std::false_type{});
+      X = R - 6.0f - Lr;  // l is the sum of 2^(s - X)
+      if (j < last) go_over(std::true_type{});
       // ---- out: each thread its half of the head dimensions
-      sm_sum[t][half][r] = l;
+      sm_sum[t][half][r] = attn_log(X, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sum_full[t]));
       ok = ok && mbar_wait(smem_u32(&sum_full[t]), seg & 1, &abort_flag) &&
@@ -540,11 +576,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
         tc_fence_after();
-        l = (l + sm_sum[t][half ^ 1][r]) * ex2(-Lr);  // the sum of 2^(6 + s - R)
+        const float l0 = sm_sum[t][0][r], l1 = sm_sum[t][1][r], most = fmaxf(l0, l1);
+        const float L = attn_log(most, ex2(l0 - exp_ref(most)) + ex2(l1 - exp_ref(most)));
         const int hq = sg.head * group + (real ? row - i * group : 0);
         const int64_t token = static_cast<int64_t>(sg.q0) + i;
         const bool whole = first == 0 && last == sg.n;
-        const float inv = whole ? (l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f) : 1.0f;
+        const float fac = attn_factor(exp_ref(R) - 6.0f, L);
         uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + half * (D / 2);
         // a piece of an item begun earlier goes to the first slot, of one that
         // goes on to the second
@@ -561,8 +598,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               uint32_t y[4];
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
-                const float lo = l > 0.0f ? __uint_as_float(o[k + 2 * m]) * inv : 0.0f;
-                const float hi = l > 0.0f ? __uint_as_float(o[k + 2 * m + 1]) * inv : 0.0f;
+                const float lo = __uint_as_float(o[k + 2 * m]) * fac * fac;
+                const float hi = __uint_as_float(o[k + 2 * m + 1]) * fac * fac;
                 const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
                 y[m] = *reinterpret_cast<const uint32_t*>(&v);
               }
@@ -577,10 +614,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (half == 0) {
           if (!whole) {
             piece[kPreRows * D + 2 * (t * 128 + r)] = R;
-            piece[kPreRows * D + 2 * (t * 128 + r) + 1] = l;
+            piece[kPreRows * D + 2 * (t * 128 + r) + 1] = L;
           } else if (real && p.lse) {
-            p.lse[token * p.q_heads + hq] =
-                l > 0.0f ? (R - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            p.lse[token * p.q_heads + hq] = L * 0.69314718055994531f;
           }
         }
         if (!whole && first == 0 && threadIdx.x == 0) {
@@ -601,7 +637,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       first_item(cur);
       int item = 0, jt = 0, seg = -1;
       float ref = 0.0f;
-      bool ok = true;
+      bool far = false, ok = true;
 #pragma unroll 1
       for (int64_t u = u_begin; u < u_end && ok; ++u, ++jt) {
         prefill_seek(p, cur, u);
@@ -610,7 +646,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int32_t* table = p.table + cur.req * p.ld_table;
         const bool begins = u == u_begin || j == 0, ends = u + 1 == u_end || j + 1 == cur.n;
         // scales, a lane a granule
-        float sk = 0.0f, lv = -INFINITY;
+        float sk = 0.0f, lv = -INFINITY;  // (-inf: no tokens, or a block of zeros)
+        bool there = false;
         if (lane < kPreGranules) {
           const int tk = j * kPreTokens + 16 * lane;
           if (tk < end) {
@@ -618,7 +655,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (blk >= 0 && blk < p.blocks) {
               sk = __ldg(p.k_scale + blk * p.kv_heads + cur.head);
               const float sv = __ldg(p.v_scale + blk * p.kv_heads + cur.head);
-              lv = sv > 0.0f ? log2f(sv) : -1000.0f;
+              lv = log2f(sv);
+              there = true;
             } else {
               atomicOr(&g_status, 1u << 7);
             }
@@ -629,25 +667,28 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
           x = __shfl_sync(0xFFFFFFFFu, x, 0);
-          ref = x > -500.0f ? x : 0.0f;
+          ref = x > -INFINITY ? x : 0.0f;
+          far = false;
           ++seg;
           if (lane == 0)
             segs[seg & (kPreSegments - 1)] = {
                 cur.rq.q0, cur.rq.fresh, cur.rq.pos0, cur.rq.len, cur.head, cur.tile * kPreRows, j,
                 static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u)), cur.n, cur.item_u};
         }
-        if (lv == -1000.0f) lv = ref - 60.0f;  // a block of zeros: its weight does not matter
-        const bool gap = __any_sync(0xFFFFFFFFu, lane < kPreGranules && lv == -INFINITY);
+        const unsigned held = __ballot_sync(0xFFFFFFFFu, there);
+        far = far || __any_sync(0xFFFFFFFFu, there && !(fabsf(lv - ref) <= 40.0f));
         PrefillScales& z = sc[jt & 3];
         if (lane < kPreGranules) {
           z.k[lane] = sk;
           z.lv[lane] = lv;
-          z.back[lane] = lv > -INFINITY ? ex2(ref - lv) : 0.0f;
+          z.back[lane] = !there || far ? 0.0f : ex2(ref - lv);
         }
         if (lane == 0) {
           z.ref = ref;
           z.ends = ends;
-          z.strange = gap || (j + 1) * kPreTokens > end;
+          z.far = far;
+          z.there = static_cast<int>(held);
+          z.strange = held != (1u << kPreGranules) - 1u || (j + 1) * kPreTokens > end;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sc_full[jt & 3]));
@@ -826,18 +867,18 @@ __global__ void __launch_bounds__(32 * kPreJoinRows) kv_prefill_join_kernel(cons
   if (cut.x < 0 || r >= cut.w) return;
   const int q0 = p.cut[2 * w0 + 1].x;
   const int pieces = cut.x - w0 + 1;
-  float m = -INFINITY, l = 0.0f, o[V];
+  float m = -INFINITY, xm = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.0f;
   // two pieces at a time, both on their way before either is used (most items
   // are cut once)
 #pragma unroll 1
   for (int i = 0; i < pieces; i += 2) {
-    float2 ml[2];
+    float2 ml[2];  // R, L
     float v[2][V];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      ml[x] = make_float2(-INFINITY, 0.0f);
+      ml[x] = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
       for (int k = 0; k < V; ++k) v[x][k] = 0.0f;
       if (i + x < pieces) {
@@ -855,11 +896,11 @@ __global__ void __launch_bounds__(32 * kPreJoinRows) kv_prefill_join_kernel(cons
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const float top = fmaxf(m, ml[x].x);
-      const float keep = m > -INFINITY ? ex2(m - top) : 0.0f;
-      const float add = ml[x].x > -INFINITY ? ex2(ml[x].x - top) : 0.0f;
+      const float top = fmaxf(m, ml[x].x), most = fmaxf(xm, ml[x].y);
+      const float keep = ex2(m - exp_ref(top)), add = ex2(ml[x].x - exp_ref(top));
+      l = l * ex2(xm - exp_ref(most)) + ex2(ml[x].y - exp_ref(most));
       m = top;
-      l = l * keep + ml[x].y * add;
+      xm = most;
 #pragma unroll
       for (int k = 0; k < V; ++k) o[k] = o[k] * keep + v[x][k] * add;
     }
@@ -867,19 +908,17 @@ __global__ void __launch_bounds__(32 * kPreJoinRows) kv_prefill_join_kernel(cons
   const int group = p.q_heads / p.kv_heads;
   const int i = r / group, hq = cut.y * group + r - i * group;
   const int64_t token = static_cast<int64_t>(q0) + i;
-  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+  const float L = attn_log(xm, l), fac = attn_factor(exp_ref(m) - 6.0f, L);
   uint16_t* to = p.out + token * p.ldo_token + hq * p.ldo_head + lane * V;
   uint32_t y[V / 2];
 #pragma unroll
   for (int k = 0; k < V / 2; ++k) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k] * fac * fac, o[2 * k + 1] * fac * fac);
     y[k] = *reinterpret_cast<const uint32_t*>(&b);
   }
   if constexpr (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
   else *reinterpret_cast<uint32_t*>(to) = y[0];
-  if (p.lse && lane == 0)
-    p.lse[token * p.q_heads + hq] =
-        l > 0.0f ? (m - 6.0f + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (p.lse && lane == 0) p.lse[token * p.q_heads + hq] = L * 0.69314718055994531f;
 }
 
 }  // namespace i8
