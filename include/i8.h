@@ -348,7 +348,10 @@ i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_
  * tokens; each sees the positions up to its own.  A row that sees nothing
  * (a request whose seq_len is less than its count of new tokens) gives 0, and
  * -inf in lse.  Tokens of a sequence that have no block (an id out of range,
- * or a place past the table's width) are absent, and reported.
+ * or a place past the table's width) are absent, and reported.  A row depends
+ * on its q and on the tokens that it sees: a NaN there, or a scale that is not
+ * finite, makes it NaN (a NaN code of a value: that head dimension); the other
+ * rows, and what no row sees, may hold anything.
  *   q, out [tokens, q_heads, head_dim] bf16, element strides between tokens
  *   and heads (% 8 == 0); lse [tokens, q_heads] fp32 or NULL: the natural log
  *   of the sum of exponentials

@@ -135,3 +135,76 @@ def test_blocks_of_zeros_everywhere(new, Hq, Hkv, D):
             c.scales[1][b] = 0.0
             c.codes[1][b] = 0
     c.check()
+
+
+# ------------------------------------------------------------------ NaN
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_nan_in_a_row_of_q(new, Hq, Hkv, D, fmt):
+    """The row's result is NaN; no other row's is; a row that sees nothing gives
+    0 and -inf all the same."""
+    c = Case([300, 64, 2], [new, new, new], 16, Hq, Hkv, D, fmt, 6)
+    for t in (0, new, 2 * new + new // 2):
+        c.q[t, Hq - 1, D // 2] = float("nan")
+    c.q[2 * new, 0, 3] = float("nan")
+    c.check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_nan_scales(new, Hq, Hkv, D, side, fmt):
+    """A block with a NaN scale spoils the rows that see one of its tokens."""
+    c = Case([300, 80 + new, 16 * 7], [new, new, min(new, 112)], 16, Hq, Hkv, D, fmt, 7)
+    c.scales[side][c.table[0][3], Hkv - 1] = float("nan")
+    c.scales[side][c.table[1][(80 + new - 1) // 16], 0] = float("nan")     # the last block
+    c.check()
+
+
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_nan_codes(new, Hq, Hkv, D, side):
+    """NaN codes of E4M3 in tokens: rows that see the token are NaN (a value's
+    in its head dimension), the rows before it are not; places past the end and
+    of blocks that are missing may hold anything."""
+    c = Case([300, 80 + new, 250 + new], [new, new, new], 16, Hq, Hkv, D, "e4m3", 8)
+    bits = c.bits(side)
+    bits[c.table[0][2], Hkv - 1, 5, 7] = 0x7F                              # an old token
+    last = 80 + new - 1
+    bits[c.table[1][last // 16], 0, last % 16, D - 1] = 0xFF               # the newest token
+    if new > 2:
+        t = 250 + new // 2                                                 # a new token in the middle
+        bits[c.table[2][t // 16], 0, t % 16, 1] = 0x7F
+        bits[c.table[2][(t + 3) // 16], Hkv - 1, (t + 3) % 16, D // 2] = 0x7F
+    for r, n in enumerate(c.lens):                                         # no token's places
+        if n % 16:
+            c.codes[0].view(torch.uint8)[c.table[r][n // 16], :, n % 16:] = 0x7F
+            c.codes[1].view(torch.uint8)[c.table[r][n // 16], :, n % 16:] = 0xFF
+    c.check()
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_nan_codes_and_missing_blocks(new, Hq, Hkv, D):
+    c = Case([300, 260], [new, new], 16, Hq, Hkv, D, "e4m3", 9)
+    c.bits(1)[c.table[0][1], 0, 3, 2] = 0x7F
+    c.bits(0)[c.table[1][0], 0, 3, 2] = 0x7F
+    c.table[0][4], c.table[0][5], c.table[1][9] = -1, 10 ** 6, -5
+    c.check(status=7)
+
+
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_infinite_scales_do_not_vanish(new, Hq, Hkv, D, side):
+    """A block with an infinite scale: rows that see it are not finite, the
+    others' are those of the definition."""
+    c = Case([300, 80 + new], [new, new], 16, Hq, Hkv, D, "int8", 10)
+    c.scales[side][c.table[0][3], Hkv - 1] = float("inf")
+    out, lse = c.run()
+    group = Hq // Hkv
+    assert not torch.isfinite(out[:new, (Hkv - 1) * group:].float()).any()
+    c.scales[side][c.table[0][3], Hkv - 1] = 1.0
+    o, l, bound, lse_bound = c.want()
+    rest = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    rest[:new, (Hkv - 1) * group:] = False
+    assert ((out.double() - o).abs() <= bound)[rest].all()
+    assert ((lse.double() - l).abs() <= lse_bound)[rest].all()

@@ -27,6 +27,10 @@
 //     of its own, that of log2(e) S alone, and adds 2^(log2(e) S - X) instead.
 //     Either is l * 2^X, with X = R - 10 - Lr in the first form, and where parts
 //     meet it is its logarithm L = X + log2 l: O * 2^(R - 10 - L) is the result.
+//   * a row depends on the tokens that it sees and on nothing else.  NaN in its q,
+//     in a scale or in a key makes it NaN, a NaN code of a value its head
+//     dimension; infinite scales count as NaN.  Tokens that it does not see are
+//     left out by their place, whatever they hold.
 //
 // The products run transposed: S^T = K q^T and O^T = V^T P^T, so that the
 // tokens and the head dimension fill the 16-row side of the warp MMA
@@ -132,11 +136,12 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
-// E4M3 NaN codes, which places that hold no token may contain, as zeros (the
-// product's 0 * NaN would spread).
-__device__ __forceinline__ uint32_t without_nan_codes(uint32_t w) {
-  return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+// The bytes of a word that are E4M3's NaN codes, as a mask.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
+// An infinite scale as NaN (an infinity less an infinity).
+__device__ __forceinline__ float scale_value(float s) { return s + (s - s); }
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -179,7 +184,8 @@ struct AttnFeed {
   int t_first, end;         // the warp's first token of the segment, the segment's end
   int t_look, col, off;     // the next tile to look up: token, column of the table, offset in the block
   int next_id[H], next_off[H];  // looked up, not yet copied
-  float ksc[S][H], vsc[S][H];   // block scales of the tiles in the ring; K's is NaN for a missing block
+  float ksc[S][H], vsc[S][H];   // block scales of the tiles in the ring
+  uint32_t have[S];             // a bit for each half whose block exists
 };
 
 // Adds the calls' values up over the CTA: returns the exclusive sum before
@@ -369,11 +375,13 @@ __device__ __forceinline__ void feed_issue(const AttnArgs& p, AttnFeed<D>& f, co
         }
       }
   }
+  f.have[into] = 0;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t row = static_cast<int64_t>(f.next_id[h]) * p.kv_heads + f.head;
-    f.ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : NAN;
+    f.ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : 0.0f;
     f.vsc[into][h] = there[h] ? __ldg(p.v_scale + row) : 0.0f;
+    f.have[into] |= there[h] ? 1u << h : 0u;
   }
 }
 
@@ -429,8 +437,8 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
     bool far = false;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      sk[h] = f.ksc[0][h];
-      gone[h] = isnan(sk[h]);
+      sk[h] = scale_value(f.ksc[0][h]);
+      gone[h] = !((f.have[0] >> h) & 1u);
       lv[h] = gone[h] ? st.ref : __log2f(f.vsc[0][h]);  // -inf for a block of zeros
       if (!FAR && h == 0 && t0 == f.t_first && lv[0] > -INFINITY) st.ref = lv[0];
       far = far || !(fabsf(lv[h] - st.ref) <= 40.0f);
@@ -443,9 +451,10 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
     }
     parity ^= 1u << slot;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
+    for (int i = 0; i + 2 < S; ++i) {
+      f.have[i] = f.have[i + 1];
 #pragma unroll
-      for (int i = 0; i + 2 < S; ++i) {
+      for (int h = 0; h < H; ++h) {
         f.ksc[i][h] = f.ksc[i + 1][h];
         f.vsc[i][h] = f.vsc[i + 1][h];
       }
@@ -535,8 +544,9 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             st.l[n][i] += ex2(s[h][n][i] - exp_ref(x)) + ex2(s[h][n][i + 2] - exp_ref(x));
-            s[h][n][i] += lv[h];
-            s[h][n][i + 2] += lv[h];
+            // (left out is left out, whatever lv is)
+            s[h][n][i] = s[h][n][i] == -INFINITY ? -INFINITY : s[h][n][i] + lv[h];
+            s[h][n][i + 2] = s[h][n][i + 2] == -INFINITY ? -INFINITY : s[h][n][i + 2] + lv[h];
             top[i] = fmaxf(top[i], fmaxf(s[h][n][i], s[h][n][i + 2]));
           }
         }
@@ -578,10 +588,49 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
         b[n][1] = transpose_8x8(pack_f16x2(e[2], e[3]));
       }
       if (E4M3 && masked) {
+        // 0 * NaN is NaN: the codes of tokens that not every row sees go in as
+        // zeros, and a product of "is NaN" and "is seen" says where they show
+        uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) vr[h][i][j] = without_nan_codes(vr[h][i][j]);
+          for (int j = 0; j < D / 32; ++j) bad |= nan_codes(vr[h][i][j]);
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, bad != 0), 0)) {
+          uint32_t one[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int tk = t0 + 16 * h + g + 8 * x;
+              one[n][x] = transpose_8x8(pack_f16x2(!gone[h] && tk < limit[n][0] ? 1.0f : 0.0f,
+                                                   !gone[h] && tk < limit[n][1] ? 1.0f : 0.0f));
+            }
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t w[4], f[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i] = nan_codes(vr[h][i][j]);
+              vr[h][i][j] &= ~w[i];
+              w[i] &= 0x38383838u;  // 1.0
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              codes_to_f16<E4M3>(__byte_perm(w[2 * i], w[2 * i + 1], 0x5140), f[i][0], f[i][1]);
+              codes_to_f16<E4M3>(__byte_perm(w[2 * i], w[2 * i + 1], 0x7362), f[i][2], f[i][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_16816(count, f[0][2 * i], f[0][2 * i + 1], f[1][2 * i], f[1][2 * i + 1], one[n][0], one[n][1]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if (count[x] != 0.0f) st.o[2 * j + i][n][x] = NAN;
+              }
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // word j of the V rows: 4 head dimensions, 2 MMAs

@@ -82,7 +82,9 @@ struct PrefillScales {   // of the 16-token granules of a tile, and its place
   int far;                    // the segment's lv has left Lr's neighbourhood
   int there;                  // a bit for each granule that holds tokens
   int ends;                   // it is a segment's last
-  int strange;                // places in it may hold codes that are no token's
+  int at;                     // its first token
+  int tokens;                 // tokens that some row of the item sees
+  int strange;                // there are places that not every row sees
 };
 
 // The part of an item in a CTA's share, written down by the warp that copies:
@@ -92,6 +94,7 @@ struct PrefillSegment {
   int head, row0;
   int first, last, n;      // its units, of the item's n
   int64_t item_u;          // the item's first unit
+  int nan;                 // NaN codes were taken out of its values
 };
 constexpr int kPreSegments = 8;  // stages of them: the copies run at most three tiles ahead
 
@@ -275,6 +278,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       o_full, drained;
   __shared__ PrefillScales sc[kPreScales];
   __shared__ PrefillSegment segs[kPreSegments];
+  // the first token with a NaN code, of those taken out, by head dimension
+  __shared__ int first_nan[E4M3 ? kPreSegments : 1][E4M3 ? D : 1];
   __shared__ float sm_top[2][2][128], sm_sum[2][2][128];  // [tile][half of the keys][row]
   __shared__ int64_t sm_scan[kAttnWarps], sm_base;
   __shared__ int sm_req;
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(smem_u32(&sum_full[i]), kPreSoftWarps / 2);
     }
     mbar_init(smem_u32(&q_full), kPreSoftWarps);
-    mbar_init(smem_u32(&o_full), 1);
+    mbar_init(smem_u32(&o_full), 2);
     mbar_init(smem_u32(&drained), 1);
     tma_prefetch_desc(&k_map);
     tma_prefetch_desc(&v_map);
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             float s0, s1;
             f2_split(f2_add(sum[0], sum[1]), s0, s1);
-            l = fmaf(s0 + s1, z.back[gr], l);
+            if constexpr (!FAR) l = fmaf(s0 + s1, z.back[gr], l);
           }
           tmem_st_32x32b_x16(p_at + 16 * q, pk);
         }
@@ -592,6 +597,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           uint32_t o[16];
           tmem_ld_32x32b_x16(o_at + 16 * q, o);
           tmem_wait_ld(o);
+          if (E4M3 && sg.nan) {
+            const int* at = first_nan[seg & (kPreSegments - 1)] + half * (D / 2) + 16 * q;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (limit > at[k]) o[k] = 0x7FFFFFFFu;  // the row sees it
+          }
           if (whole && real) {
 #pragma unroll
             for (int k = 0; k < 16; k += 8) {
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (tk < end) {
             const int64_t blk = __ldg(table + tk / p.block);  // end lies within the table's width
             if (blk >= 0 && blk < p.blocks) {
-              sk = __ldg(p.k_scale + blk * p.kv_heads + cur.head);
+              sk = scale_value(__ldg(p.k_scale + blk * p.kv_heads + cur.head));
               const float sv = __ldg(p.v_scale + blk * p.kv_heads + cur.head);
               lv = log2f(sv);
               there = true;
@@ -673,7 +684,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (lane == 0)
             segs[seg & (kPreSegments - 1)] = {
                 cur.rq.q0, cur.rq.fresh, cur.rq.pos0, cur.rq.len, cur.head, cur.tile * kPreRows, j,
-                static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u)), cur.n, cur.item_u};
+                static_cast<int>(min(static_cast<int64_t>(cur.n), u_end - cur.item_u)), cur.n, cur.item_u, 0};
+          if constexpr (E4M3)
+            for (int d = lane; d < D; d += 32) first_nan[seg & (kPreSegments - 1)][d] = 0x7FFFFFFF;
         }
         const unsigned held = __ballot_sync(0xFFFFFFFFu, there);
         far = far || __any_sync(0xFFFFFFFFu, there && !(fabsf(lv - ref) <= 40.0f));
@@ -688,7 +701,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           z.ends = ends;
           z.far = far;
           z.there = static_cast<int>(held);
-          z.strange = held != (1u << kPreGranules) - 1u || (j + 1) * kPreTokens > end;
+          z.at = j * kPreTokens;
+          z.tokens = min(end - j * kPreTokens, kPreTokens);
+          const int least = cur.rq.pos0 + cur.tile * kPreRows / group + 1;  // what the first row sees
+          z.strange = held != (1u << kPreGranules) - 1u || (j + 1) * kPreTokens > min(least, end);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sc_full[jt & 3]));
@@ -777,7 +793,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (!ok) break;
         if (ends) {
+          // (the commit says that O is complete, the arrival passes on what the
+          // converting warps wrote down)
           mma_commit_warp(smem_u32(&o_full));
+          if (lane == 0) mbar_arrive(smem_u32(&o_full));
           ++seg;
         } else {
           mma_commit_warp(smem_u32(&kv_empty[next_slot]));
@@ -791,6 +810,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     } else {
       // ================================================================= conversion
       const int cw = warp - kPreSoftWarps - 2;
+      int seg = 0;
       bool ok = true;
 #pragma unroll 1
       for (int item = 0; item < 2 * tiles && ok; ++item) {
@@ -801,8 +821,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (!ok) break;
         const uint32_t from = base + Sm::CODES + slot * Sm::RAW;
         const uint32_t to = base + Sm::KV + slot * Sm::TILE;
-        // places that hold no token may hold NaN codes
-        const bool strange = E4M3 && sc[(item >> 1) & 3].strange != 0;
+        // Places that hold no token may hold NaN codes, and 0 * NaN is NaN: what
+        // is not there goes in as zeros, and so do the NaN codes of V where not
+        // every row sees its token; those of tokens are written down.
+        const PrefillScales& z = sc[(item >> 1) & 3];
+        const bool strange = E4M3 && z.strange != 0;
+        const int there = z.there, tokens = z.tokens, at = z.at;
         // 8 rows a step (16 at 64 head dimensions).  Eight neighbouring lanes
         // read 128 bytes on different banks and write eight different chunks
         // of the swizzle: at 128 head dimensions the lanes of the row's second
@@ -820,9 +844,24 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               r = r0 + 8 * pass + (lane >> 2);
             }
             uint4 w = lds_16(from + r * D + c * 16);
-            if (strange)
-              w = make_uint4(without_nan_codes(w.x), without_nan_codes(w.y), without_nan_codes(w.z),
-                             without_nan_codes(w.w));
+            if (strange) {
+              if (!((there >> (r >> 4)) & 1)) {
+                w = make_uint4(0u, 0u, 0u, 0u);
+              } else if (item & 1) {
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                if ((nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3])) != 0) {
+                  w = make_uint4(x[0] & ~nan_codes(x[0]), x[1] & ~nan_codes(x[1]), x[2] & ~nan_codes(x[2]),
+                                 x[3] & ~nan_codes(x[3]));
+                  if (r < tokens) {
+                    segs[seg & (kPreSegments - 1)].nan = 1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      if ((nan_codes(x[i >> 2]) >> (8 * (i & 3))) & 1u)
+                        atomicMin(&first_nan[seg & (kPreSegments - 1)][c * 16 + i], at + r);
+                  }
+                }
+              }
+            }
             uint32_t h[8];
             codes_to_f16<E4M3>(w.x, h[0], h[1]);
             codes_to_f16<E4M3>(w.y, h[2], h[3]);
@@ -834,6 +873,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             sts_16(row + (((at + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
           }
         }
+        if (E4M3 && (item & 1) && z.ends) ++seg;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
