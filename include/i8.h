@@ -335,7 +335,9 @@ typedef struct {
  *   s = max(older tokens' scale, max|new| / L);
  *   where s grew, the older codes become round_half_even(code * (s_old / s));
  *   the new ones are round_half_even(x / s).
- * A block that is begun at offset 0 starts over with max|new| / L.          */
+ * A block that is begun at offset 0 starts over with max|new| / L.  A NaN among
+ * the new ones makes s NaN (the new codes are 0, the older ones stay), and so
+ * every value of that block and head until it is begun again.               */
 i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_head,
                              const void* v_bf16, int64_t ldv_token, int64_t ldv_head,
                              const int64_t* slots, int64_t tokens, const i8_kv_cache* cache,

@@ -126,3 +126,42 @@ def test_slots_out_of_range_are_reported():
         written = {s for i, s in enumerate(slots) if 0 <= s < 48 and slots != [4, 3, 0]} | ({4} if slots == [4, 3, 0] else set())
         rows = cache.k.cpu().reshape(48, 64).ne(0).any(1).nonzero()[:, 0].tolist()
         assert set(rows) == written
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_nan_shows_in_the_scale(fmt):
+    """A NaN among a block's new tokens makes that block's scale of that head
+    NaN, and it stays so until the block is begun again; nothing else differs
+    from the same step without it, and attention over it is NaN."""
+    g = torch.Generator().manual_seed(13)
+    heads, block, D = 2, 16, 64
+    x = torch.randn(40, heads, D, generator=g).bfloat16()
+    bad = x.clone()
+    bad[20, 1, 9] = float("nan")                          # block 1, head 1
+    bad[39, 0, 0] = float("-nan")                         # block 2, head 0, with older tokens before it
+    caches = []
+    for k in (x, bad):
+        cache = i8.QuantKVCache.empty(3, heads, block, D, fmt)
+        for lo, hi in ((0, 36), (36, 40)):
+            i8.kv_cache_append(k[lo:hi].cuda(), x[lo:hi].cuda(), torch.arange(lo, hi, device="cuda"), cache)
+        caches.append(cache)
+    i8.sync_check()
+    good, spoilt = caches
+    nan = torch.zeros(3, heads, dtype=torch.bool)
+    nan[1, 1] = nan[2, 0] = True
+    assert torch.equal(torch.isnan(spoilt.k_scale).cpu(), nan)
+    assert torch.equal(spoilt.k_scale.cpu()[~nan], good.k_scale.cpu()[~nan])
+    assert torch.equal(spoilt.k.view(torch.uint8).cpu()[~nan], good.k.view(torch.uint8).cpu()[~nan])
+    assert torch.equal(spoilt.v.view(torch.uint8), good.v.view(torch.uint8)) and torch.equal(spoilt.v_scale, good.v_scale)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn(2, heads, D, generator=g).bfloat16().cuda()
+    o = i8.paged_attention(q, spoilt, i32([[0, 1, 2], [0, 1, 2]]), i32([40, 10]), i32([0, 1, 2]), max_new=1)
+    i8.sync_check()
+    assert torch.isnan(o[0]).all() and torch.isfinite(o[1]).all()
+    # more tokens do not hide it, a new beginning does
+    i8.kv_cache_append(x[:2].cuda(), x[:2].cuda(), torch.tensor([40, 41], device="cuda"), spoilt)
+    i8.sync_check()
+    assert torch.isnan(spoilt.k_scale[2, 0])
+    i8.kv_cache_append(x[:2].cuda(), x[:2].cuda(), torch.tensor([32, 33], device="cuda"), spoilt)
+    i8.sync_check()
+    assert torch.isfinite(spoilt.k_scale[2]).all()

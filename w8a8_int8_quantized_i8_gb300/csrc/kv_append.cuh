@@ -10,7 +10,9 @@
 //   m     = max |x| over the run's tokens
 //   s_new = max(o > 0 ? s_old : 0, m / L)
 //   older codes:  q' = rne(q * fl(s_old / s_new))   where s_new > s_old
-//   new codes:    q  = rne(fl(x / s_new))           (0 where s_new is 0)
+//   new codes:    q  = rne(fl(x / s_new))           (0 where s_new is 0 or NaN)
+// where a NaN wins a maximum: it makes the block's scale NaN until the block is
+// begun again.
 // A block whose scale does not grow keeps its codes, so appending a token
 // costs that token only, except when it is the loudest of its block yet.
 //
@@ -85,6 +87,19 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
   e4m3x2_to_f32(w >> 16, c, d);
   return e4m3x2(__fmul_rn(a, ratio), __fmul_rn(b, ratio)) |
          (e4m3x2(__fmul_rn(c, ratio), __fmul_rn(d, ratio)) << 16);
+}
+
+// Lane-wise max of |a| and |b| over bf16 pairs, as absmax_bf16x2, but a NaN wins:
+// it has to show in the block's scale, since an int8 code cannot hold it.
+__device__ __forceinline__ uint32_t loudest_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 struct AppendRun {
@@ -172,20 +187,20 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   }
 #pragma unroll
   for (int q = 0; q < kAppendKeep; ++q) {
-    amax2 = absmax_bf16x2(amax2, keep[q].x);
-    amax2 = absmax_bf16x2(amax2, keep[q].y);
-    amax2 = absmax_bf16x2(amax2, keep[q].z);
-    amax2 = absmax_bf16x2(amax2, keep[q].w);
+    amax2 = loudest_bf16x2(amax2, keep[q].x);
+    amax2 = loudest_bf16x2(amax2, keep[q].y);
+    amax2 = loudest_bf16x2(amax2, keep[q].z);
+    amax2 = loudest_bf16x2(amax2, keep[q].w);
   }
 #pragma unroll 4
   for (int i = me + kAppendKeep * threads; i < n; i += threads) {
     const int t = i >> vs, c = i - (t << vs);
     if (gaps && slots[t] < 0) continue;
     const uint4 v = *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8);
-    amax2 = absmax_bf16x2(amax2, v.x);
-    amax2 = absmax_bf16x2(amax2, v.y);
-    amax2 = absmax_bf16x2(amax2, v.z);
-    amax2 = absmax_bf16x2(amax2, v.w);
+    amax2 = loudest_bf16x2(amax2, v.x);
+    amax2 = loudest_bf16x2(amax2, v.y);
+    amax2 = loudest_bf16x2(amax2, v.z);
+    amax2 = loudest_bf16x2(amax2, v.w);
   }
   amax2 &= 0x7FFF7FFFu;
   uint32_t abits = __reduce_max_sync(0xFFFFFFFFu, max(amax2 & 0xFFFFu, amax2 >> 16));
@@ -200,7 +215,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
     __syncwarp();
   }
   const float s_run = __fdiv_rn(__uint_as_float(abits << 16), E4M3 ? 448.0f : 127.0f);
-  const float s = fmaxf(s_old, s_run);
+  const float s = max_or_nan(s_old, s_run);
   if (me == 0) *sp = s;  // every thread has read s_old before the barrier above
   if (s > s_old && off > 0) {
     const float ratio = __fdiv_rn(s_old, s);
@@ -224,7 +239,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
       to = (static_cast<int>(slots[t] - s0) << vs) + i - (t << vs);
     }
     uint2 w = make_uint2(0u, 0u);
-    if (s != 0.0f) {
+    if (s > 0.0f) {
       if constexpr (E4M3) {
         const float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
                             bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
