@@ -274,7 +274,8 @@ i8_status i8_gelu_quant_act_pertoken(const void* x_bf16, int64_t M, int64_t K,
  * h and y are fp32 inside; the only other rounding is h's to bf16 where it is
  * stored.  In detail t = h * weight (fp32), s_t = max|t| / L, q =
  * round_half_even(t / s_t) (IEEE fp32 steps) and s_a = s_t / sqrt(...): the
- * codes do not depend on the order of the sum.
+ * codes do not depend on the order of the sum.  A row whose squares leave
+ * fp32's range is multiplied by a power of two before, and s_a by its inverse.
  *   x, residual [M,K] bf16 (row strides ldx, ldr, % 8 == 0), weight [K] bf16,
  *   q [M,K] codes and s_a [M] as in i8_layernorm_quant_act_pertoken,
  *   h [M,K] bf16 or NULL (row stride ldh, % 8 == 0); h may be residual or x

@@ -115,3 +115,32 @@ def test_empty():
     q, s, h = i8.add_rmsnorm_quant_act_pertoken(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
                                                 torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
     assert q.shape == (0, 64) and s.shape == (0,) and h.shape == (0, 64)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "f16codes"])
+@pytest.mark.parametrize("K", [64, 3072, 32768])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_squares_outside_of_fp32(K, eps, fmt):
+    """Rows whose squares (not the row or its norm) leave fp32: the result is
+    the formula's.  Codes within half a step of y / s_a (E4M3: half a step of
+    the code, or of the smallest one), s_a within 2^-19 of max|y| / L: the
+    reduction's 2^-20 and the fp32 steps after it.  A scale below fp32's normal
+    range is off by half its spacing, 2^-150."""
+    g = torch.Generator().manual_seed(K)
+    mags = torch.tensor([1e25, 3e37, 1.9e19, 1e19, 1e-12, 1e-23, 1e-30, 1e-38, 1e-40])
+    x = (torch.randn(len(mags), K, generator=g).clamp(-8, 8) * mags[:, None]).bfloat16()
+    x[0, 1:] *= 1e-12                                     # one element far above the others
+    res = (torch.randn(len(mags), K, generator=g).clamp(-8, 8) * mags[:, None] * 0.5).bfloat16()
+    w = (1 + 0.2 * torch.randn(K, generator=g)).bfloat16()
+    q, s, h = i8.add_rmsnorm_quant_act_pertoken(x.cuda(), res.cuda(), w.cuda(), eps=eps, fmt=fmt)
+    i8.sync_check()
+    hh = x.double() + res.double()
+    y = hh * w.double() / (hh.square().mean(1, keepdim=True) + eps).sqrt()
+    limit = ref.LIMIT[fmt]
+    want = y.abs().amax(1) / limit
+    got = s.cpu().double()
+    assert ((got - want).abs() <= 2.0 ** -19 * want + 2.0 ** -149).all()
+    codes, ratio = _values(q), y / want[:, None]
+    step = 0.5 if fmt != "e4m3" else (2.0 ** -4 * ratio.abs()).clamp(min=2.0 ** -10)
+    assert ((codes - ratio).abs() <= step + 2.0 ** -18 * limit).all()
+    assert torch.equal(h.cpu().view(torch.int16), (x.float() + res.float()).bfloat16().view(torch.int16))

@@ -13,6 +13,12 @@
 // the norm uses the unrounded sum), and the row is never rounded to bf16
 // between the norm and the quantizer: one rounding, to the 8-bit code.
 //
+// The squares of a row leave fp32's range long before the row or its norm does.
+// A vector of 8 whose squares do not fit well is put aside: its h is stored
+// later (it may lie where x or r does).  A row whose sum of squares is infinite
+// or below 2^-60 is then read again and done times 2^-80 or 2^80, which its scale
+// undoes; the vectors not put aside do not count beside the others.
+//
 // Bound by HBM: 2 + 2 bytes read and 2 + 1 written an element.  A row a CTA, as
 // in the quantizer: small CTAs spread evenly, each element is read once and
 // stays in registers.  16384 x 3072, E4M3: 58.6 us, 6.0 TB/s (89 % of the
@@ -70,9 +76,110 @@ __device__ __forceinline__ uint2 quant_f32x8_e4m3(const float (&t)[8], float s, 
                     e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
 }
 
+// A row by its CTA of G warps, as kept by add_rmsnorm_quant_kernel.
+struct NormRow {
+  const uint16_t *x, *res, *weight;
+  uint16_t* h;
+  int8_t* q;
+  float* scale;
+  float eps;
+  int K, G, V, first;  // first: the lane's first element of V vectors 256 elements apart
+  uint32_t aside;      // those whose h is not stored yet
+  float* red_s;
+  uint32_t* red_m;
+};
+
+// The unrounded h of the lane's vector i, times f, and the same times the gain.
+__device__ __forceinline__ void norm_again(const NormRow& a, int i, float f, float (&h)[8], float (&t)[8]) {
+  const int e = a.first + i * 256;
+  const bool kept = a.h == nullptr || ((a.aside >> i) & 1u);  // x and r are still there
+  const uint4 c = *reinterpret_cast<const uint4*>((kept ? a.x : a.h) + e);
+  uint4 d = make_uint4(0u, 0u, 0u, 0u), g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  if (kept && a.res) d = *reinterpret_cast<const uint4*>(a.res + e);
+  if (a.weight) g = *reinterpret_cast<const uint4*>(a.weight + e);
+  const uint32_t x[4] = {c.x, c.y, c.z, c.w}, r[4] = {d.x, d.y, d.z, d.w}, w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[2 * j] = __fmul_rn(__fadd_rn(bf16_lo(x[j]), bf16_lo(r[j])), f);
+    h[2 * j + 1] = __fmul_rn(__fadd_rn(bf16_hi(x[j]), bf16_hi(r[j])), f);
+    t[2 * j] = __fmul_rn(h[2 * j], bf16_lo(w[j]));
+    t[2 * j + 1] = __fmul_rn(h[2 * j + 1], bf16_hi(w[j]));
+  }
+}
+// Stores the h of the vectors put aside.
+__device__ __forceinline__ void norm_store_aside(const NormRow& a) {
+  float h[8], t[8];
+#pragma unroll 1
+  for (int i = 0; i < a.V; ++i)
+    if ((a.aside >> i) & 1u) {
+      norm_again(a, i, 1.0f, h, t);
+      *reinterpret_cast<uint4*>(a.h + a.first + i * 256) =
+          make_uint4(pack_bf16x2_rn(h[0], h[1]), pack_bf16x2_rn(h[2], h[3]), pack_bf16x2_rn(h[4], h[5]),
+                     pack_bf16x2_rn(h[6], h[7]));
+    }
+}
+// A row whose sum of squares is out of range (the whole CTA calls).
+template <int FMT>
+__device__ __forceinline__ void norm_far_row(const NormRow& a, bool large) {
+  const float f = large ? 0x1p-80f : 0x1p80f;
+  float h[8], t[8], ss = 0.0f;
+  uint32_t amax = 0;
+#pragma unroll 1
+  for (int i = 0; i < a.V && a.first + i * 256 < a.K; ++i) {
+    norm_again(a, i, f, h, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ss = fmaf(h[j], h[j], ss);
+      amax = max(amax, __float_as_uint(fabsf(t[j])));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+  if (a.G > 1) {
+    __syncthreads();  // the first sums have been read
+    if ((threadIdx.x & 31) == 0) {
+      a.red_s[threadIdx.x >> 5] = ss;
+      a.red_m[threadIdx.x >> 5] = amax;
+    }
+    __syncthreads();
+    ss = 0.0f;
+    amax = 0;
+    for (int j = 0; j < a.G; ++j) {
+      ss += a.red_s[j];
+      amax = max(amax, a.red_m[j]);
+    }
+  }
+  const float s = __fdiv_rn(__uint_as_float(amax), FMT == kQuantE4M3 ? 448.0f : 127.0f);
+  if (threadIdx.x == 0) {
+    // s / f over sqrt(mean / f^2 + eps); where eps * f^2 overflows the mean is
+    // nothing beside eps
+    const float mean = __fdiv_rn(ss, static_cast<float>(a.K)), e = __fmul_rn(__fmul_rn(a.eps, f), f);
+    const float rstd = e < INFINITY ? __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, e)))
+                                    : __fdiv_rn(0x1p-80f, __fsqrt_rn(a.eps));
+    *a.scale = s == 0.0f ? 0.0f : __fmul_rn(s, rstd);
+  }
+  const bool fast = s >= 0x1p-126f;
+  const float r = __frcp_rn(s);
+#pragma unroll 1
+  for (int i = 0; i < a.V && a.first + i * 256 < a.K; ++i) {
+    norm_again(a, i, f, h, t);
+    uint2 c = make_uint2(0u, 0u);
+    if (s != 0.0f) {
+      if constexpr (FMT == kQuantE4M3) c = quant_f32x8_e4m3(t, s, r, fast);
+      else c = quant_f32x8(t, s, r, fast);
+    }
+    store_codes8<FMT>(a.q, a.first + i * 256, c);
+  }
+}
+
+// Registers a thread: what the usual row needs.  The far row's code would take
+// more and cost CTAs (16384 x 3072, E4M3: 62 us, and 67 without the limit).
+constexpr int norm_registers(int V) { return V <= 4 ? 64 : V == 6 ? 80 : 104; }
+
 // One row per CTA of G warps, V 16-byte vectors a lane in registers.
 template <int V, int FMT>
-__global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(
+__global__ void __maxnreg__(norm_registers(V)) add_rmsnorm_quant_kernel(
     const uint16_t* __restrict__ x, int K, int64_t ldx, const uint16_t* __restrict__ res,
     int64_t ldr, const uint16_t* __restrict__ weight, float eps, int8_t* __restrict__ q,
     int64_t ldq, float* __restrict__ scale, uint16_t* __restrict__ h_out, int64_t ldh, int G) {
@@ -102,6 +209,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(
 
   float t[V][8];
   float ss = 0.0f;
+  uint32_t aside = 0;  // the vectors put aside
   uint32_t amax = 0;  // bit patterns of |t| order like the values; a NaN wins
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -112,18 +220,22 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(
     if (weight && e < K) g = __ldg(reinterpret_cast<const uint4*>(weight + e));
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
     uint32_t o[4];
+    float sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float h0 = __fadd_rn(bf16_lo(a[j]), bf16_lo(b[j]));
       const float h1 = __fadd_rn(bf16_hi(a[j]), bf16_hi(b[j]));
-      ss = fmaf(h0, h0, ss);
-      ss = fmaf(h1, h1, ss);
+      sq = fmaf(h0, h0, sq);
+      sq = fmaf(h1, h1, sq);
       t[i][2 * j] = __fmul_rn(h0, bf16_lo(w[j]));
       t[i][2 * j + 1] = __fmul_rn(h1, bf16_hi(w[j]));
       amax = max(amax, max(__float_as_uint(fabsf(t[i][2 * j])), __float_as_uint(fabsf(t[i][2 * j + 1]))));
       o[j] = pack_bf16x2_rn(h0, h1);
     }
-    if (h_out && e < K)
+    ss += sq;
+    const bool wanted = h_out && e < K, fits = sq >= 0x1p-40f && sq <= 0x1p64f;
+    aside |= wanted && !fits ? 1u << i : 0u;
+    if (wanted && fits)
       *reinterpret_cast<uint4*>(h_out + row * ldh + e) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 #pragma unroll
@@ -142,26 +254,35 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(
       amax = max(amax, red_m[j]);
     }
   }
-  const float s = __fdiv_rn(__uint_as_float(amax), FMT == kQuantE4M3 ? 448.0f : 127.0f);
-  if (threadIdx.x == 0) {
-    const float mean = __fdiv_rn(ss, static_cast<float>(K));
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
-    scale[row] = amax == 0 ? 0.0f : __fmul_rn(s, rstd);
-  }
-  int8_t* qr = q + row * ldq * (FMT == kQuantF16 ? 2 : 1);
-  const bool fast = s >= 0x1p-126f;
-  const float r = __frcp_rn(s);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = slice0 + (i * 32 + lane) * 8;
-    if (e < K) {
-      uint2 c = make_uint2(0u, 0u);
-      if (amax != 0) {
-        if constexpr (FMT == kQuantE4M3) c = quant_f32x8_e4m3(t[i], s, r, fast);
-        else c = quant_f32x8(t[i], s, r, fast);
-      }
-      store_codes8<FMT>(qr, e, c);
+  const bool in_range = ss >= 0x1p-60f && ss < INFINITY;  // the same in the whole CTA
+  if (__builtin_expect(in_range, 1)) {
+    const float s = __fdiv_rn(__uint_as_float(amax), FMT == kQuantE4M3 ? 448.0f : 127.0f);
+    if (threadIdx.x == 0) {
+      const float mean = __fdiv_rn(ss, static_cast<float>(K));
+      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
+      scale[row] = amax == 0 ? 0.0f : __fmul_rn(s, rstd);
     }
+    int8_t* qr = q + row * ldq * (FMT == kQuantF16 ? 2 : 1);
+    const bool fast = s >= 0x1p-126f;
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = slice0 + (i * 32 + lane) * 8;
+      if (e < K) {
+        uint2 c = make_uint2(0u, 0u);
+        if (amax != 0) {
+          if constexpr (FMT == kQuantE4M3) c = quant_f32x8_e4m3(t[i], s, r, fast);
+          else c = quant_f32x8(t[i], s, r, fast);
+        }
+        store_codes8<FMT>(qr, e, c);
+      }
+    }
+  }
+  if (__builtin_expect(!in_range || aside != 0, 0)) {
+    const NormRow far{xr, rr, weight, h_out ? h_out + row * ldh : nullptr, q + row * ldq * (FMT == kQuantF16 ? 2 : 1),
+                      scale + row, eps, K, G, V, slice0 + lane * 8, aside, red_s, red_m};
+    if (!in_range) norm_far_row<FMT>(far, !(ss < 1.0f));
+    norm_store_aside(far);
   }
 }
 
