@@ -180,9 +180,8 @@ constexpr int norm_registers(int V) { return V <= 4 ? 64 : V == 6 ? 80 : 104; }
 // One row per CTA of G warps, V 16-byte vectors a lane in registers.
 template <int V, int FMT>
 __global__ void __maxnreg__(norm_registers(V)) add_rmsnorm_quant_kernel(
-    const uint16_t* __restrict__ x, int K, int64_t ldx, const uint16_t* __restrict__ res,
-    int64_t ldr, const uint16_t* __restrict__ weight, float eps, int8_t* __restrict__ q,
-    int64_t ldq, float* __restrict__ scale, uint16_t* __restrict__ h_out, int64_t ldh, int G) {
+    const uint16_t* x, int K, int64_t ldx, const uint16_t* res, int64_t ldr, const uint16_t* weight,
+    float eps, int8_t* q, int64_t ldq, float* scale, uint16_t* h_out, int64_t ldh, int G) {
   __shared__ float red_s[16];
   __shared__ uint32_t red_m[16];
   const int warp = threadIdx.x >> 5;
@@ -198,8 +197,9 @@ __global__ void __maxnreg__(norm_registers(V)) add_rmsnorm_quant_kernel(
   for (int i = 0; i < V; ++i) {
     const int e = slice0 + (i * 32 + lane) * 8;
     v[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
-    // the residual may be updated in place (h_out == res), so its loads are
-    // ordinary ones; each thread reads the elements that it writes
+    // h_out may be res or x, and the kernel before may have written any of them
+    // while this one lived: ordinary loads, of pointers that promise nothing;
+    // each thread reads the elements that it writes, before it writes any
     if (e < K) {
       v[i] = *reinterpret_cast<const uint4*>(xr + e);
       if (rr) u[i] = *reinterpret_cast<const uint4*>(rr + e);
@@ -217,6 +217,7 @@ __global__ void __maxnreg__(norm_registers(V)) add_rmsnorm_quant_kernel(
     const uint32_t a[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     const uint32_t b[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
     uint4 g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);  // ones
+    // (the gains are a model's: no kernel that this one may overlap writes them)
     if (weight && e < K) g = __ldg(reinterpret_cast<const uint4*>(weight + e));
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
     uint32_t o[4];
