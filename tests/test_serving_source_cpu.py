@@ -23,7 +23,8 @@ def _code(name):
     return " ".join(text.split())
 
 
-@pytest.mark.parametrize("name", ["rmsnorm.cuh", "block_tables.cuh", "kv_append.cuh"])
+@pytest.mark.parametrize("name", ["rmsnorm.cuh", "block_tables.cuh", "kv_append.cuh", "kv_attention.cuh",
+                                  "kv_prefill.cuh"])
 def test_loads_are_ordinary(name):
     """The norm's gains, a model's parameters, are the exception."""
     src = _code(name).replace("g = __ldg(reinterpret_cast<const uint4*>(weight + e));", "")

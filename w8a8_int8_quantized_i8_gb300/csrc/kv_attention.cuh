@@ -32,6 +32,9 @@
 //     dimension; infinite scales count as NaN.  Tokens that it does not see are
 //     left out by their place, whatever they hold.
 //
+// Blocks, scales and q are read by ordinary loads: the kernels that write them
+// may still run when this one begins (it waits for them, but lives meanwhile).
+//
 // The products run transposed: S^T = K q^T and O^T = V^T P^T, so that the
 // tokens and the head dimension fill the 16-row side of the warp MMA
 // (m16n8k16) and the few query rows its 8-wide side.  The order of the head
@@ -327,7 +330,7 @@ __device__ __forceinline__ void feed_look_up(const AttnArgs& p, AttnFeed<D>& f) 
   for (int h = 0; h < Tile::HALVES; ++h) {
     const bool wraps = f.off + 16 * h >= p.block;
     f.next_off[h] = wraps ? f.off + 16 * h - p.block : f.off + 16 * h;
-    f.next_id[h] = f.t_look + 16 * h < f.end ? __ldg(f.table + (wraps ? f.col + 1 : f.col)) : -1;
+    f.next_id[h] = f.t_look + 16 * h < f.end ? f.table[wraps ? f.col + 1 : f.col] : -1;
   }
   f.t_look += Tile::UNIT;
   f.col += p.unit_cols;
@@ -379,8 +382,8 @@ __device__ __forceinline__ void feed_issue(const AttnArgs& p, AttnFeed<D>& f, co
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t row = static_cast<int64_t>(f.next_id[h]) * p.kv_heads + f.head;
-    f.ksc[into][h] = there[h] ? __ldg(p.k_scale + row) : 0.0f;
-    f.vsc[into][h] = there[h] ? __ldg(p.v_scale + row) : 0.0f;
+    f.ksc[into][h] = there[h] ? p.k_scale[row] : 0.0f;
+    f.vsc[into][h] = there[h] ? p.v_scale[row] : 0.0f;
     f.have[into] |= there[h] ? 1u << h : 0u;
   }
 }
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_ctas<D, NT>()))
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         const int d = attn_k_dim<D>(j >> 2, c) + (j & 3) * 4;  // step j = 4 * chunk + word
-        w[j] = real ? __ldg(reinterpret_cast<const uint2*>(qp + d)) : make_uint2(0u, 0u);
+        w[j] = real ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
         const uint32_t a = (w[j].x & 0x7FFF7FFFu), b = (w[j].y & 0x7FFF7FFFu);
         amax = max(amax, max(max(a & 0xFFFFu, a >> 16), max(b & 0xFFFFu, b >> 16)));
       }

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         uint32_t amax = 0;
 #pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 w = real ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint32_t to = base + Sm::Q + t * Sm::TILE + r * 128;
 #pragma unroll 4
         for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
-          const uint4 w = real ? __ldg(qp + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 w = real ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
           uint32_t y[4];
 #pragma unroll
@@ -662,10 +662,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (lane < kPreGranules) {
           const int tk = j * kPreTokens + 16 * lane;
           if (tk < end) {
-            const int64_t blk = __ldg(table + tk / p.block);  // end lies within the table's width
+            const int64_t blk = table[tk / p.block];  // end lies within the table's width
             if (blk >= 0 && blk < p.blocks) {
-              sk = scale_value(__ldg(p.k_scale + blk * p.kv_heads + cur.head));
-              const float sv = __ldg(p.v_scale + blk * p.kv_heads + cur.head);
+              sk = scale_value(p.k_scale[blk * p.kv_heads + cur.head]);
+              const float sv = p.v_scale[blk * p.kv_heads + cur.head];
               lv = log2f(sv);
               there = true;
             } else {
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (lane < boxes && tb < end) {
           const int col = tb / p.block;
           off = tb - col * p.block;
-          blk = __ldg(table + col);
+          blk = table[col];
           if (blk >= p.blocks) blk = -1;
         }
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, blk >= 0)) * p.box_rows * D;
