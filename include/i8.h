@@ -302,8 +302,10 @@ i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x_bf16, int64_t M, int64
  *   counts [3]             tokens; entries of free_blocks in use after the
  *                          step; tokens that got no block because the free
  *                          list or the table's width ran out
- * Negative lengths count as 0.  requests <= 16384, block_size <= 1024; the
- * tables, free list and outputs do not overlap (taken and counts neither).  */
+ * Negative lengths count as 0.  requests <= 16384, block_size <= 1024.  No
+ * output, the tables among them, shares memory with an input or another output
+ * (I8_ERR_INVALID_ARG): a program that keeps lengths or `taken` from step to step
+ * copies seq_lens and counts[1] over them after the call.                    */
 i8_status i8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens,
                                 int64_t requests, int32_t* block_tables, int64_t width,
                                 int64_t ld_table, const int32_t* free_blocks, int64_t n_free,

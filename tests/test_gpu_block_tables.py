@@ -94,3 +94,30 @@ def test_most_requests_and_graph():
     want = ref.tables_reference([10, 0, 33], [7, 2, 0], [[1, -1, -1], [-1, -1, -1], [2, 3, 4]], list(range(50, 60)), 0, 16, 8)
     assert [table.tolist(), out.cu_new.tolist(), out.seq_lens.tolist(), out.slots.tolist(), out.positions.tolist(),
             out.counts.tolist()] == list(want)
+
+
+def test_operands_between_the_table_s_rows():
+    """Vectors in the gaps of a row-strided table share no memory with it."""
+    R, width, ld = 3, 2, 16
+    buf = torch.full((R, ld), -9, dtype=torch.int32, device="cuda")
+    table, context, new, free = buf[:, :width], buf[0, 2:5], buf[1, 2:5], buf[2, 2:8]
+    context.copy_(torch.tensor([0, 5, 17]))
+    new.copy_(torch.tensor([1, 1, 3]))
+    free.copy_(torch.tensor([11, 12, 13, 14, 15, 16]))
+    table.copy_(torch.tensor([[-7, -7], [3, -7], [4, 5]]))
+    plan = i8.build_block_tables(context, new, table, free, 16, 5)
+    i8.sync_check()
+    want = ref.tables_reference([0, 5, 17], [1, 1, 3], [[-7, -7], [3, -7], [4, 5]], [11, 12, 13, 14, 15, 16], 0, 16, 5)
+    assert table.tolist() == want[0] and plan.slots.tolist() == want[3] and plan.counts.tolist() == want[5]
+
+
+def test_kept_in_place_is_refused():
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = i8.BlockPlan.empty(2, 4)
+    table, free = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.arange(6, dtype=torch.int32, device="cuda")
+    plan.seq_lens.copy_(i32([1, 2]))
+    plan.counts.copy_(i32([0, 0, 0]))
+    for args, kw in (((plan.seq_lens, i32([1, 1])), {}), ((i32([1, 2]), i32([1, 1])), {"taken": plan.counts[1:2]})):
+        with pytest.raises(i8.I8Error) as e:
+            i8.build_block_tables(*args, table, free, 16, 4, out=plan, **kw)
+        assert e.value.status == 1

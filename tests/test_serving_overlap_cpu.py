@@ -1,0 +1,51 @@
+"""build_block_tables refuses operands that share memory, on the host: every CTA
+reads the inputs for itself, so an output in their place is a race.  (Only
+refusals here: the addresses are no memory.)"""
+import ctypes
+
+import pytest
+
+from w8a8_int8_quantized_i8_gb300 import binding
+
+R, WIDTH, LD, FREE, T = 6, 4, 10, 20, 32
+SIZES = dict(context=4 * R, new=4 * R, table=4 * (LD * (R - 1) + WIDTH), free=4 * FREE, taken=4, cu=4 * (R + 1),
+             lens=4 * R, slots=8 * T, positions=4 * T, counts=12)
+INPUTS, OUTPUTS = ("context", "new", "free", "taken"), ("table", "cu", "lens", "slots", "positions", "counts")
+BASE = {name: 0x100000 + 0x1000 * i for i, name in enumerate(SIZES)}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load()
+
+
+def _call(lib, **at):
+    a = {name: ctypes.c_void_p(v) for name, v in {**BASE, **at}.items()}
+    return lib.i8_build_block_tables(a["context"], a["new"], R, a["table"], WIDTH, LD, a["free"], FREE, a["taken"], 16, T,
+                                     a["cu"], a["lens"], a["slots"], a["positions"], a["counts"], None)
+
+
+@pytest.mark.parametrize("out", OUTPUTS)
+@pytest.mark.parametrize("other", INPUTS + OUTPUTS)
+def test_shared_memory_is_refused(lib, out, other):
+    """The same address, the other's last bytes, and the other's end over the
+    beginning of this one."""
+    if out == other:
+        pytest.skip("an operand is itself")
+    grain = 8 if out == "slots" or other == "slots" else 4
+    last = -(-SIZES[other] // grain) * grain - grain
+    for shift in (0, last, -(-(-SIZES[out] // grain) * grain - grain)):
+        assert _call(lib, **{out: BASE[other] + shift}) == 1, shift
+
+
+def test_step_kept_in_place_is_refused(lib):
+    """Last step's seq_lens as this step's context_lens, its counts[1] as taken,
+    with the same outputs again."""
+    assert _call(lib, context=BASE["lens"]) == 1
+    assert _call(lib, taken=BASE["counts"] + 4) == 1
+
+
+def test_every_row_of_the_table_counts(lib):
+    for row in range(R):
+        for col in (0, WIDTH - 1):
+            assert _call(lib, taken=BASE["table"] + 4 * (row * LD + col)) == 1

@@ -84,6 +84,26 @@ cudaError_t launch_norm_v(const NormArgs& a, int fmt, cudaStream_t st) {
   return go(add_rmsnorm_quant_kernel<V, kQuantInt8>);
 }
 
+// ----------------------------------------------------------------- overlap
+// Memory of an operand: `rows` rows of `bytes`, `stride` bytes apart.
+struct Extent {
+  const void* base;
+  int64_t bytes;
+  int64_t rows = 1;
+  int64_t stride = 0;
+};
+
+// Whether rows of `t` and the one row of `v` share a byte.
+bool overlap(const Extent& t, const Extent& v) {
+  if (!t.base || !v.base || t.bytes <= 0 || t.rows <= 0 || v.bytes <= 0) return false;
+  const int64_t lo = static_cast<int64_t>(reinterpret_cast<uintptr_t>(v.base) - reinterpret_cast<uintptr_t>(t.base));
+  const int64_t hi = lo + v.bytes;  // from t's base on
+  if (hi <= 0) return false;
+  // the first row that ends behind lo
+  const int64_t row = lo < t.bytes ? 0 : t.rows == 1 ? 1 : (lo - t.bytes) / t.stride + 1;
+  return row < t.rows && row * t.stride < hi;
+}
+
 // ----------------------------------------------------------------- cache checks
 i8_status check_cache(const i8_kv_cache* c) {
   if (!c || c->blocks < 0 || c->block_size <= 0 || c->kv_heads <= 0 || c->head_dim <= 0)
@@ -341,6 +361,22 @@ i8_status i8_build_block_tables(const int32_t* context_lens, const int32_t* new_
       !aligned4(free_blocks) || !aligned4(taken) || !aligned4(cu_new) || !aligned4(seq_lens) ||
       !aligned8(slots) || !aligned4(positions) || !aligned4(counts))
     return I8_ERR_ALIGNMENT;
+  // every CTA reads the inputs for itself while others write
+  const int64_t word = sizeof(int32_t);
+  const Extent table{block_tables, width * word, requests, ld_table * word};
+  const Extent in[] = {{context_lens, requests * word}, {new_lens, requests * word}, {taken, word},
+                       {free_blocks, n_free * word}};
+  const Extent out[] = {{cu_new, (requests + 1) * word}, {seq_lens, requests * word}, {slots, max_tokens * 2 * word},
+                        {positions, max_tokens * word}, {counts, 3 * word}};
+  for (const Extent& v : in)
+    if (overlap(table, v)) return I8_ERR_INVALID_ARG;
+  for (const Extent& v : out) {
+    if (overlap(table, v)) return I8_ERR_INVALID_ARG;
+    for (const Extent& u : in)
+      if (overlap(u, v)) return I8_ERR_INVALID_ARG;
+    for (const Extent& u : out)
+      if (&u != &v && overlap(u, v)) return I8_ERR_INVALID_ARG;
+  }
   TableArgs a{context_lens, new_lens, block_tables, free_blocks, taken, cu_new, seq_lens, slots,
               positions, counts, ld_table, n_free, max_tokens, static_cast<int32_t>(requests),
               static_cast<int32_t>(width), static_cast<int32_t>(block_size), -1};

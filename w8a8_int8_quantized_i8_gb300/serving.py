@@ -236,7 +236,9 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, block
     lengths (int32 [R] each); ``block_tables`` (int32 [R, width], row-strided
     views allowed) gets the blocks that the new tokens need, from
     ``free_blocks`` (int32) in request order, beginning at entry ``taken``
-    (int32 [1]; None: 0).  See i8_build_block_tables for the outputs."""
+    (int32 [1]; None: 0).  See i8_build_block_tables for the outputs; they and
+    the tables share no memory with the inputs (lengths that are kept from step
+    to step are copied over afterwards, as decoder.Requests does)."""
     index = _device_index(context_lens, "context_lens")
     if context_lens.dim() != 1:
         raise ValueError("context_lens must be 1-D")
