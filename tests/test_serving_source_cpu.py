@@ -30,3 +30,33 @@ def test_loads_are_ordinary(name):
     src = _code(name).replace("g = __ldg(reinterpret_cast<const uint4*>(weight + e));", "")
     for promise in ("__ldg", "ld.global.nc", "ld_stream_v4", "__restrict__"):
         assert promise not in src, (name, promise)
+
+
+SOURCES = ["rmsnorm.cuh", "block_tables.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prefill.cuh"]
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_every_wait_is_bounded_and_nothing_traps(name):
+    src = _code(name)
+    for word in ("mbar_try_wait", "for (;;)", "do {", "__trap", "trap;"):
+        assert word not in src, (name, word)
+    assert not re.search(r"\bwhile\s*\((?!off|a\.box)", src), name
+    assert not re.search(r"(?<!static_)\bassert\(", src), name
+
+
+def test_what_is_on_its_way_ends_before_the_cta_does():
+    """A CTA that gives up waits, bounded, for its own copies and products: a copy
+    that lands later writes another CTA's shared memory.  Whichever role gave up,
+    the copying and the issuing warp of the chunks' kernel drain after the last
+    barrier; a warp of the few-row kernel drains its ring where it gives up."""
+    few, many = _code("kv_attention.cuh"), _code("kv_prefill.cuh")
+    m = re.search(r"if \(!mbar_wait\(bars \+ 8 \* slot, \(parity >> slot\) & 1u, abort_flag\)\) \{(.*?)break; \}", few)
+    assert m and "for (int i = 0; i < S - 1; ++i, t0 += Tile::UNIT)" in m.group(1)
+    assert "mbar_wait_bounded(bars + 8 * at, (parity >> at) & 1u, kDrainLimitNs);" in m.group(1)
+    end = many[many.index("copied = item;"):]
+    m = re.search(r"__syncthreads\(\); if \(abort_flag\) \{(.*?)\} pdl_trigger\(\);", end)
+    assert m, "the drain does not follow the last barrier"
+    assert "at = max(0, copied - kPreSlots); at < copied;" in m.group(1)
+    assert "mbar_wait_bounded(smem_u32(&raw_full[at % kPreSlots]), (at / kPreSlots) & 1, kDrainLimitNs);" in m.group(1)
+    assert "mma_commit_warp(smem_u32(&drained)); mbar_wait_bounded(smem_u32(&drained), 0, kDrainLimitNs);" in m.group(1)
+    assert "tmem_dealloc(tmem, 512);" in end[m.end():]

@@ -90,6 +90,7 @@ struct AttnTile {
   static constexpr int STAGE = 2 * SIDE;
   static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row in one TMA box
 };
+constexpr unsigned long long kDrainLimitNs = 1000000000ull;  // of a wait on the way out
 constexpr int kAttnMeet = 4;    // m-tiles of O^T a warp's parts meet by at a time
 constexpr int kJoinGroups = 4;  // groups of kAttnThreads that share an item's pieces in the join
 
@@ -449,6 +450,13 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs& p, AttnFeed<D>& f, 
     }
     if (!FAR && __builtin_expect(__any_sync(0xFFFFFFFFu, far), 0)) break;
     if (!mbar_wait(bars + 8 * slot, (parity >> slot) & 1u, abort_flag)) {
+      // given up: what is on its way lands (bounded) while the CTA is there
+#pragma unroll 1
+      for (int i = 0; i < S - 1; ++i, t0 += Tile::UNIT)
+        if (t0 < f.end) {
+          const int at = (slot + i) % S;
+          mbar_wait_bounded(bars + 8 * at, (parity >> at) & 1u, kDrainLimitNs);
+        }
       t0 = f.end;
       break;
     }

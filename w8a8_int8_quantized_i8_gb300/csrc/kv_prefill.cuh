@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     prefill_seek(p, c, u_begin);
   };
 
+  int copied = 0;  // tiles of K or V whose copies the copying warp has begun
   if (warp < kPreSoftWarps) {
     // =================================================================== softmax
     regs_inc<96>();
@@ -734,12 +735,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         static_cast<int>(blk) * p.kv_heads + cur.head);
         }
       }
-      if (!ok) {  // let the copies in flight land (bounded) before the CTA ends
-        for (int back_i = 1; back_i <= kPreSlots && item - back_i >= 0; ++back_i) {
-          const int at = item - back_i;
-          mbar_wait_bounded(smem_u32(&raw_full[at % kPreSlots]), (at / kPreSlots) & 1, 1000000ull);
-        }
-      }
+      copied = item;
     } else if (warp == kPreSoftWarps + 1) {
       // ================================================================= products
       constexpr uint32_t kIdS = idesc_f16_f32(128, kPreTokens);
@@ -802,10 +798,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           mma_commit_warp(smem_u32(&kv_empty[next_slot]));
         }
         begins = ends;
-      }
-      if (!ok) {  // the products in flight end (bounded) before TMEM is freed
-        mma_commit_warp(smem_u32(&drained));
-        mbar_wait_bounded(smem_u32(&drained), 0, 1000000000ull);
       }
     } else {
       // ================================================================= conversion
@@ -884,6 +876,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
   }
   __syncthreads();
+  if (abort_flag) {
+    // given up, whoever did: what is on its way ends (bounded) before shared
+    // memory and TMEM go
+    if (warp == kPreSoftWarps) {
+      for (int at = max(0, copied - kPreSlots); at < copied; ++at)
+        mbar_wait_bounded(smem_u32(&raw_full[at % kPreSlots]), (at / kPreSlots) & 1, kDrainLimitNs);
+    } else if (warp == kPreSoftWarps + 1) {
+      mma_commit_warp(smem_u32(&drained));
+      mbar_wait_bounded(smem_u32(&drained), 0, kDrainLimitNs);
+    }
+  }
   pdl_trigger();
   if (warp == kPreSoftWarps + 1) {
     tc_fence_after();
