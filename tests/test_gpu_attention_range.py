@@ -208,3 +208,14 @@ def test_infinite_scales_do_not_vanish(new, Hq, Hkv, D, side):
     rest[:new, (Hkv - 1) * group:] = False
     assert ((out.double() - o).abs() <= bound)[rest].all()
     assert ((lse.double() - l).abs() <= lse_bound)[rest].all()
+
+
+# ------------------------------------------------------------------ many requests, and what is left out
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_offsets_that_go_back_are_reported(new, Hq, Hkv, D):
+    c = Case([150, 140], [new, new], 16, Hq, Hkv, D, "int8", 13)
+    c.cu = [2 * new, 0, new]                             # the first request has a negative count
+    out = torch.full((2 * new, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.lens = [150, 0]                                    # and the second sees nothing
+    c.run(status=7, out=out, max_new=new)
+    assert (out[:new] == 0).all() and (out[new:] == 7).all()

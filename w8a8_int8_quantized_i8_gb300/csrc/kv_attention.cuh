@@ -230,8 +230,8 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   a.q0 = p.cu_new[r];
   const int64_t fresh = static_cast<int64_t>(p.cu_new[r + 1]) - a.q0;
   const int len = max(0, p.seq_lens[r]);
-  const bool bad = a.q0 < 0 || a.q0 + fresh > p.tokens || fresh > p.max_new;
-  a.fresh = bad || fresh < 0 ? 0 : static_cast<int>(fresh);
+  const bool bad = a.q0 < 0 || fresh < 0 || a.q0 + fresh > p.tokens || fresh > p.max_new;
+  a.fresh = bad ? 0 : static_cast<int>(fresh);
   // the tokens past the table are absent; the others, and the rows, stay where
   // they are
   a.pos0 = len - a.fresh;
