@@ -358,8 +358,8 @@ i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_
  * finite, makes it NaN (a NaN code of a value: that head dimension); the other
  * rows, and what no row sees, may hold anything.
  *   q, out [tokens, q_heads, head_dim] bf16, element strides between tokens
- *   and heads (% 8 == 0); lse [tokens, q_heads] fp32 or NULL: the natural log
- *   of the sum of exponentials
+ *   and heads (% 8 == 0; out's rows share no element); lse [tokens, q_heads]
+ *   fp32 or NULL: the natural log of the sum of exponentials
  *   max_new: no request brings more new tokens than this (one that does is left
  *   out and reported)
  *   ws / ws_bytes: 16-byte aligned, at least

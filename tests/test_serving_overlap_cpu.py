@@ -49,3 +49,28 @@ def test_every_row_of_the_table_counts(lib):
     for row in range(R):
         for col in (0, WIDTH - 1):
             assert _call(lib, taken=BASE["table"] + 4 * (row * LD + col)) == 1
+
+
+def _attention(lib, T, Hq, ot, oh, D=64):
+    ok = ctypes.c_void_p(0x10000)
+    info = binding.KVCacheInfo(0x10000, 0x10000, 0x10000, 0x10000, 4, 16, 1, D, 0)
+    # (max_new 0: nothing is queued where the strides are fine)
+    return lib.i8_paged_attention(ok, Hq * D, D, T, Hq, ctypes.byref(info), ok, 4, 4, ok, ok, 2, 0, 0.1, ok, ot, oh, None,
+                                  ok, 1 << 30, None)
+
+
+def test_out_whose_rows_share_elements_is_refused(lib):
+    """Every pair of strides, counted out on the host."""
+    D = 64
+    seen = {0: 0, 1: 0}
+    for T in (1, 2, 3, 5):
+        for Hq in (1, 2, 3, 4):
+            for ot in range(0, 9 * D, 24):
+                for oh in (0, 8, 56, 64, 72, 128, 136, 192, 200, 320):
+                    starts = [t * ot + h * oh for t in range(T) for h in range(Hq)]
+                    starts.sort()
+                    shared = any(b - a < D for a, b in zip(starts, starts[1:]))
+                    got = _attention(lib, T, Hq, ot, oh)
+                    assert got == int(shared), (T, Hq, ot, oh)
+                    seen[got] += 1
+    assert min(seen.values()) > 100

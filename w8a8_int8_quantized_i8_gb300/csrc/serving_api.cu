@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "../../include/i8.h"
@@ -102,6 +103,19 @@ bool overlap(const Extent& t, const Extent& v) {
   // the first row that ends behind lo
   const int64_t row = lo < t.bytes ? 0 : t.rows == 1 ? 1 : (lo - t.bytes) / t.stride + 1;
   return row < t.rows && row * t.stride < hi;
+}
+
+// Whether rows [tokens, heads] of `dim` elements, these strides apart, share an
+// element.
+bool rows_overlap(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+  if ((tokens > 1 && token < dim) || (heads > 1 && head < dim)) return true;
+  if (tokens <= 1 || heads <= 1) return false;
+  if (token >= head * (heads - 1) + dim || head >= token * (tokens - 1) + dim) return false;
+  // neither inside the other: the tokens nearest to each head's offset
+  for (int64_t h = 1; h < heads; ++h)
+    for (int64_t t = h * head / token; t <= h * head / token + 1 && t < tokens; ++t)
+      if (std::abs(h * head - t * token) < dim) return true;
+  return false;
 }
 
 // ----------------------------------------------------------------- cache checks
@@ -471,6 +485,7 @@ i8_status i8_paged_attention(const void* q, int64_t ldq_token, int64_t ldq_head,
       ldo_token % 8 != 0 || ldo_head % 8 != 0 || !aligned4(block_tables) || !aligned4(seq_lens) ||
       !aligned4(cu_new) || !aligned4(lse))
     return I8_ERR_ALIGNMENT;
+  if (rows_overlap(tokens, ldo_token, q_heads, ldo_head, cache->head_dim)) return I8_ERR_INVALID_ARG;
   if (tokens == 0 || requests == 0 || max_new == 0) return I8_OK;
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
