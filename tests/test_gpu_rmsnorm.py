@@ -144,3 +144,23 @@ def test_squares_outside_of_fp32(K, eps, fmt):
     step = 0.5 if fmt != "e4m3" else (2.0 ** -4 * ratio.abs()).clamp(min=2.0 ** -10)
     assert ((codes - ratio).abs() <= step + 2.0 ** -18 * limit).all()
     assert torch.equal(h.cpu().view(torch.int16), (x.float() + res.float()).bfloat16().view(torch.int16))
+
+
+def test_h_between_the_rows_of_the_inputs():
+    """h in the columns beside x, in place of the residual, and over a single
+    row with another stride: nothing of it lies over another row."""
+    g = torch.Generator().manual_seed(12)
+    both = torch.randn(9, 2 * 128, generator=g).bfloat16()
+    res = torch.randn(9, 128, generator=g).bfloat16()
+    d = both.cuda()
+    r = i8.add_rmsnorm_quant_act_pertoken(d[:, :128], res.cuda(), residual_out=d[:, 128:])
+    i8.sync_check()
+    _compare(r, both[:, :128], res, None, 1e-6, "int8")
+    assert torch.equal(d[:, :128].cpu(), both[:, :128])
+    one = both[:1].cuda()
+    r = i8.add_rmsnorm_quant_act_pertoken(one[:, :128], res[:1].cuda(), residual_out=one[:, :128])
+    i8.sync_check()
+    _compare(r, both[:1, :128], res[:1], None, 1e-6, "int8")
+    with pytest.raises(i8.I8Error) as e:
+        i8.add_rmsnorm_quant_act_pertoken(d[:8, :128], res[:8].cuda(), residual_out=d[1:, :128])
+    assert e.value.status == 1

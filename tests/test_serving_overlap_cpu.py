@@ -74,3 +74,29 @@ def test_out_whose_rows_share_elements_is_refused(lib):
                     assert got == int(shared), (T, Hq, ot, oh)
                     seen[got] += 1
     assert min(seen.values()) > 100
+
+
+def test_h_over_other_rows_of_the_inputs_is_refused(lib):
+    """h beside x and the residual, counted out on the host by rows; refused
+    exactly where row i of h shares memory with row j != i of an input."""
+    K, far = 64, 1 << 30
+    x0 = 0x100000
+
+    def call(at, M, ldx, ldh, which):
+        x, r = (x0, far) if which == "x" else (far, x0)
+        return lib.i8_add_rmsnorm_quant_act_pertoken(ctypes.c_void_p(x), M, K, ldx if which == "x" else K, ctypes.c_void_p(r),
+                                                     ldx if which == "r" else K, None, 1e-6, 0, ctypes.c_void_p(2 * far), K,
+                                                     ctypes.c_void_p(3 * far), ctypes.c_void_p(at), ldh, None)
+
+    refused = 0
+    for M in (2, 3, 5):
+        for ldx in (64, 72, 136, 200):
+            for ldh in (64, 72, 136, 200):
+                for shift in range(-6 * 200, 6 * 200, 40):
+                    cross = any(abs(shift + i * ldh - j * ldx) < K for i in range(M) for j in range(M) if i != j)
+                    if not cross:
+                        continue                    # (it would be queued)
+                    refused += 1
+                    for which in "xr":
+                        assert call(x0 + 2 * shift - (2 * shift) % 16, M, ldx, ldh, which) == 1, (M, ldx, ldh, shift)
+    assert refused > 500

@@ -105,6 +105,27 @@ bool overlap(const Extent& t, const Extent& v) {
   return row < t.rows && row * t.stride < hi;
 }
 
+// Whether a row of `a` shares a byte with another row of `b` (both of as many
+// rows): a row may lie where the other's same row does.
+bool rows_cross(const Extent& a, const Extent& b) {
+  if (!a.base || !b.base || a.rows <= 1) return false;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base));
+  if (d >= (a.rows - 1) * a.stride + a.bytes || d + (b.rows - 1) * b.stride + b.bytes <= 0) return false;
+  if (a.stride != b.stride) {
+    for (int64_t i = 0; i < b.rows; ++i) {
+      const Extent row{static_cast<const char*>(b.base) + i * b.stride, b.bytes};
+      const Extent before{a.base, a.bytes, i, a.stride};
+      const Extent after{static_cast<const char*>(a.base) + (i + 1) * a.stride, a.bytes, a.rows - i - 1, a.stride};
+      if (overlap(before, row) || overlap(after, row)) return true;
+    }
+    return false;
+  }
+  // row i + k of a begins d - k * stride before row i of b
+  const int64_t k = d >= 0 ? d / a.stride : -((-d + a.stride - 1) / a.stride), r = d - k * a.stride;
+  return (k != 0 && std::abs(k) < a.rows && r < a.bytes) ||
+         (k + 1 != 0 && std::abs(k + 1) < a.rows && a.stride - r < b.bytes);
+}
+
 // Whether rows [tokens, heads] of `dim` elements, these strides apart, share an
 // element.
 bool rows_overlap(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
@@ -337,6 +358,10 @@ i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x, int64_t M, int64_t K,
       ldq % (fmt == kQuantF16 ? 8 : 16) != 0 || !aligned16(residual) ||
       (residual && ldr % 8 != 0) || !aligned16(weight) || !aligned16(h) || (h && ldh % 8 != 0))
     return I8_ERR_ALIGNMENT;
+  // a row's CTA writes its h when others have not read theirs
+  const Extent to{h, K * 2, M, ldh * 2};
+  if (rows_cross(to, {x, K * 2, M, ldx * 2}) || rows_cross(to, {residual, K * 2, M, ldr * 2}))
+    return I8_ERR_INVALID_ARG;
   if (M == 0) return I8_OK;
   const int vecs = static_cast<int>(K / 8);
   int G = 1;
