@@ -60,3 +60,12 @@ def test_what_is_on_its_way_ends_before_the_cta_does():
     assert "mbar_wait_bounded(smem_u32(&raw_full[at % kPreSlots]), (at / kPreSlots) & 1, kDrainLimitNs);" in m.group(1)
     assert "mma_commit_warp(smem_u32(&drained)); mbar_wait_bounded(smem_u32(&drained), 0, kDrainLimitNs);" in m.group(1)
     assert "tmem_dealloc(tmem, 512);" in end[m.end():]
+
+
+def test_a_run_s_vectors_are_counted_in_64_bits():
+    """Skipped tokens count into a run's span: 2^26 of them are 2^31 vectors of a
+    256-wide head, so the loops over them count in 64 bits."""
+    src = _code("kv_append.cuh")
+    assert "const int64_t n = static_cast<int64_t>(run.span) << vs;" in src
+    assert not re.search(r"for \(int i = me \+ kAppendKeep \* threads; i < n;", src)
+    assert len(re.findall(r"for \(int64_t i = me \+ kAppendKeep \* threads; i < n;", src)) == 2

@@ -176,7 +176,8 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   const float s_old = off > 0 ? *sp : 0.0f;
 
   uint32_t amax2 = 0;
-  const int n = run.span << vs;
+  // (a run with many skipped tokens may span more vectors than 32 bits count)
+  const int64_t n = static_cast<int64_t>(run.span) << vs;
   uint4 keep[kAppendKeep];
 #pragma unroll
   for (int q = 0; q < kAppendKeep; ++q) {
@@ -193,8 +194,8 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
     amax2 = loudest_bf16x2(amax2, keep[q].w);
   }
 #pragma unroll 4
-  for (int i = me + kAppendKeep * threads; i < n; i += threads) {
-    const int t = i >> vs, c = i - (t << vs);
+  for (int64_t i = me + kAppendKeep * threads; i < n; i += threads) {
+    const int t = static_cast<int>(i >> vs), c = static_cast<int>(i) & ((1 << vs) - 1);
     if (gaps && slots[t] < 0) continue;
     const uint4 v = *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8);
     amax2 = loudest_bf16x2(amax2, v.x);
@@ -231,12 +232,12 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
   const float r = __frcp_rn(s);
   const unsigned long long rr = f2(r, r);
   uint2* out = reinterpret_cast<uint2*>(dst + (off << p.dim_shift));
-  auto code = [&](int i, const uint4& v) {
-    const int t = i >> vs;
-    int to = i;
+  auto code = [&](int64_t i, const uint4& v) {
+    const int t = static_cast<int>(i >> vs);
+    int to = static_cast<int>(i);
     if (gaps) {
       if (slots[t] < 0) return;
-      to = (static_cast<int>(slots[t] - s0) << vs) + i - (t << vs);
+      to = (static_cast<int>(slots[t] - s0) << vs) + (static_cast<int>(i) & ((1 << vs) - 1));
     }
     uint2 w = make_uint2(0u, 0u);
     if (s > 0.0f) {
@@ -253,8 +254,8 @@ __device__ __forceinline__ void append_run(const AppendArgs& p, const AppendSide
 #pragma unroll
   for (int q = 0; q < kAppendKeep; ++q)
     if (me + q * threads < n) code(me + q * threads, keep[q]);
-  for (int i = me + kAppendKeep * threads; i < n; i += threads) {
-    const int t = i >> vs, c = i - (t << vs);
+  for (int64_t i = me + kAppendKeep * threads; i < n; i += threads) {
+    const int t = static_cast<int>(i >> vs), c = static_cast<int>(i) & ((1 << vs) - 1);
     if (gaps && slots[t] < 0) continue;
     code(i, *reinterpret_cast<const uint4*>(src + t * a.ld_token + c * 8));
   }
