@@ -165,3 +165,20 @@ def test_nan_shows_in_the_scale(fmt):
     i8.kv_cache_append(x[:2].cuda(), x[:2].cuda(), torch.tensor([32, 33], device="cuda"), spoilt)
     i8.sync_check()
     assert torch.isfinite(spoilt.k_scale[2]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("gap", [31, 32, 255, 256, 257, 5000, 100000])
+def test_long_stretches_of_skipped_tokens(gap, fmt):
+    """Skipped tokens before, inside and between runs: a run goes on behind them,
+    and what begins behind them begins a run."""
+    slots = [-1] * gap + [35, 36] + [-1] * gap + [37, 0] + [-1] * gap + [1, 2, 64] + [-1] * gap
+    g = torch.Generator().manual_seed(gap)
+    T, heads, D = len(slots), 1, 64
+    (kc, ks), (vc, vs) = _pool(5, heads, 16, D, fmt, g), _pool(5, heads, 16, D, fmt, g)
+    rows = torch.randn(T, heads, D, generator=g).bfloat16()
+    cache = i8.QuantKVCache(kc.view(torch.uint8).cuda().view(kc.dtype), vc.view(torch.uint8).cuda().view(vc.dtype),
+                            ks.cuda(), vs.cuda())
+    i8.kv_cache_append(rows.cuda(), rows.cuda(), torch.tensor(slots, dtype=torch.int64, device="cuda"), cache)
+    i8.sync_check()
+    _check((rows, rows), {"k": (kc, ks), "v": (vc, vs)}, slots, cache, fmt)

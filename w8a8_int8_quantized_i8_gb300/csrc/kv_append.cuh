@@ -138,6 +138,22 @@ __device__ __forceinline__ int64_t next_token(const AppendSlots& slots, int64_t 
   return T;
 }
 
+// The slot of the last token before t that is not skipped, or -1 (the whole
+// warp calls).
+__device__ __forceinline__ int64_t slot_before(const AppendSlots& slots, int64_t t, int lane) {
+  for (; t > 0; t -= 256) {
+    int back = 256;
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+      const int64_t u = t - 1 - (32 * j + lane);
+      if (u >= 0 && slots[u] >= 0) back = 32 * j + lane;
+    }
+    back = __reduce_min_sync(0xFFFFFFFFu, back);
+    if (back < 256) return slots[t - 1 - back];
+  }
+  return -1;
+}
+
 // Extends a run from its first token to its last (the whole warp calls).
 // Every round finds tokens of the run or ends, so there are at most `most`.
 __device__ __forceinline__ void run_extent(const AppendSlots& slots, int64_t T, AppendRun& r,
@@ -286,11 +302,18 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     bool starts = false;
     int64_t s = -1, blk = 0;
     if (lane < p.window && t < p.tokens) s = near[lane + 1];
+    // the slot of the last token before it that is not skipped: a lane's of the
+    // window, or for the first one what lies before the window
+    int64_t before = near[lane];
+    if (__any_sync(0xFFFFFFFFu, s >= 0 && before < 0)) {
+      const unsigned held = __ballot_sync(0xFFFFFFFFu, s >= 0);
+      const unsigned earlier = held & ((1u << lane) - 1u);
+      const int64_t inside = __shfl_sync(0xFFFFFFFFu, s, earlier ? 31 - __clz(earlier) : 0);
+      const int64_t outside = slot_before(slots, w0, lane);
+      before = earlier ? inside : outside;
+    }
     if (s >= 0) {
       blk = s / p.block;
-      int64_t before = near[lane];  // the slot of the last token before it that is not skipped
-      if (before < 0)
-        for (int64_t u = t - 2; u >= 0 && before < 0; --u) before = slots[u];
       starts = true;
       if (before >= 0 && before >= blk * p.block && before < (blk + 1) * p.block) {
         starts = false;  // inside a run
