@@ -211,6 +211,48 @@ def test_infinite_scales_do_not_vanish(new, Hq, Hkv, D, side):
 
 
 # ------------------------------------------------------------------ many requests, and what is left out
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("R", [129, 300, 1000])
+def test_many_requests(R, D):
+    """Ragged batches of more requests than a CTA has threads for, some empty:
+    every thread walks over several of them."""
+    rng = random.Random(R)
+    lens = [rng.choice([0, 1, 5, 16, 17, 40]) for _ in range(R)]
+    news = [min(n, rng.choice([0, 1, 1, 1, 2])) for n in lens]
+    Case(lens, news, 16, 4, 2, D, "int8", 11).check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("R", [129, 300, 1000])
+def test_many_requests_a_few_with_many_rows(R, D):
+    rng = random.Random(R + 1)
+    lens = [rng.choice([0, 1, 16, 17, 30]) for _ in range(R)]
+    news = [min(n, rng.choice([0, 1, 1])) for n in lens]
+    for at in (0, R // 3, R // 2, R - 1):
+        lens[at], news[at] = 70 + at % 50, 60 + at % 7
+    Case(lens, news, 16, 4, 2, D, "int8", 12).check()
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+def test_left_out_requests_are_not_written(new, Hq, Hkv, D):
+    """Offsets past q or before it: that request's rows keep what was there, its
+    neighbour's are right."""
+    c = Case([150, 140], [new, new], 16, Hq, Hkv, D, "int8", 13)
+    want = c.want()
+    for cu, kept in (([0, new, 2 * new + 1], 0), ([-1, new, 2 * new], 1)):
+        good = Case([150, 140], [new, new], 16, Hq, Hkv, D, "int8", 13)
+        good.cu = cu
+        out = torch.full((2 * new, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        good.run(status=7, out=out, max_new=new)
+        rows = [slice(0, new), slice(new, 2 * new)]
+        for r in range(2):
+            if r == kept:
+                err = (out[rows[r]].double() - want[0][rows[r]]).abs()
+                assert (err <= want[2][rows[r]]).all()
+            else:
+                assert (out[rows[r]] == 7).all()
+
+
 @pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
 def test_offsets_that_go_back_are_reported(new, Hq, Hkv, D):
     c = Case([150, 140], [new, new], 16, Hq, Hkv, D, "int8", 13)
@@ -219,3 +261,12 @@ def test_offsets_that_go_back_are_reported(new, Hq, Hkv, D):
     c.lens = [150, 0]                                    # and the second sees nothing
     c.run(status=7, out=out, max_new=new)
     assert (out[:new] == 0).all() and (out[new:] == 7).all()
+
+
+def test_repeats_itself_exactly():
+    for new, Hq, Hkv, D in ((1, 8, 2, 128), (4, 8, 2, 128), (130, 4, 2, 128)):
+        c = Case([3000, 700, 150], [new] * 3, 16, Hq, Hkv, D, "int8", 14)
+        a, la = c.run()
+        for _ in range(4):
+            b, lb = c.run()
+            assert torch.equal(a, b) and torch.equal(la, lb)
