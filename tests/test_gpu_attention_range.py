@@ -103,6 +103,18 @@ def test_values_far_apart(new, Hq, Hkv, D, order, far, fmt):
 
 
 @pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
+@pytest.mark.parametrize("exponent", [20, 39, 40, 41, 80])
+def test_values_on_both_sides_of_the_first_block(new, Hq, Hkv, D, exponent):
+    """The first block's values between those of the others, around the distance
+    (2^40) at which the sum changes its form."""
+    c = Case([400, 40 + new], [new, new], 16, Hq, Hkv, D, "int8", 15)
+    for row in c.table:
+        for i, b in enumerate(b for b in row if b >= 0):
+            c.scales[1][b] *= (1.0, 2.0 ** exponent, 2.0 ** -exponent, 1.0)[i % 4]
+    c.check()
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", FORMS)
 @pytest.mark.parametrize("loud", [0, 1])
 def test_the_attended_block_is_the_quiet_one(new, Hq, Hkv, D, loud):
     """All of a row's weight lies on tokens whose values are 10^36 times smaller
@@ -261,6 +273,14 @@ def test_offsets_that_go_back_are_reported(new, Hq, Hkv, D):
     c.lens = [150, 0]                                    # and the second sees nothing
     c.run(status=7, out=out, max_new=new)
     assert (out[:new] == 0).all() and (out[new:] == 7).all()
+
+
+def test_workspace_of_another_type_is_refused():
+    c = Case([40], [1], 16, 2, 1, 64, "int8", 16)
+    for bad, error in ((1 << 20, TypeError), (torch.empty(1 << 20, dtype=torch.uint8), ValueError),
+                       (torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0], ValueError)):
+        with pytest.raises(error):
+            c.run(workspace=bad)
 
 
 def test_repeats_itself_exactly():

@@ -325,6 +325,8 @@ def paged_attention(q: torch.Tensor, cache: QuantKVCache, block_tables: torch.Te
     if workspace is None:
         need = _attention_workspace(Hq, info.kv_heads, D, info.fmt, max_new, index)
         workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{index}")
     _call("i8_paged_attention", index, qp, qt, qh, T, Hq, ctypes.byref(info), table, width, ld, lens, cu, R,
