@@ -333,7 +333,8 @@ typedef struct {
  *   and between heads (% 8 == 0), head_dim contiguous
  *   slots [tokens] int64 as i8_build_block_tables writes them; negative: the
  *   token is skipped.  A block's tokens come in order, with none of another
- *   block between them.
+ *   block between them: one out of order is not written, and reported; a block
+ *   that comes twice is not found, and its codes and scale are undefined then.
  * A block's new tokens start at some offset; the tokens before it are older
  * ones.  Per block and head, with L = 127 or 448:
  *   s = max(older tokens' scale, max|new| / L);
@@ -362,7 +363,8 @@ i8_status i8_kv_cache_append(const void* k_bf16, int64_t ldk_token, int64_t ldk_
  *   and heads (% 8 == 0; out's rows share no element); lse [tokens, q_heads]
  *   fp32 or NULL: the natural log of the sum of exponentials
  *   max_new: no request brings more new tokens than this (one that does is left
- *   out and reported)
+ *   out and reported; 0: nothing is queued).  It chooses the kernels and the
+ *   row tile, so a bound that is far too large costs time
  *   ws / ws_bytes: 16-byte aligned, at least
  *   i8_paged_attention_workspace_bytes(); calls that may overlap in time do
  *   not share one

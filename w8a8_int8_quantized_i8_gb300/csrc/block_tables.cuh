@@ -14,8 +14,8 @@
 // launch without a grid-wide wait: every CTA scans all requests by itself (two
 // loads a request, from L2) into shared memory, then writes its share of the
 // tokens and of the tables.  A fresh block is taken from the free list, not
-// from the table that another CTA may still be writing.  5.3 us for 64 decoding
-// requests, 7.2 us for 2048 requests with 104236 tokens (1.3 MB); one scan over
+// from the table that another CTA may still be writing.  5.1 us for 64 decoding
+// requests, 7.0 us for 2048 requests with 104236 tokens (1.3 MB); one scan over
 // consecutive requests a thread instead of one a 512 requests took 2 us off the
 // latter, shifts instead of 64-bit divisions 1 us off the former.
 #pragma once

@@ -25,7 +25,7 @@
 // need go to shared memory first, in one load a thread.
 //
 // Bound by latency (slots, rows, maximum, codes): 128 tokens of 8 heads of 128
-// take 4.6 us; 4767 tokens of prompts (29 MB) 16.1 us, in two waves of CTAs.
+// take 4.6 us; 4767 tokens of prompts (29 MB) 15.7 us, in two waves of CTAs.
 // 8 vectors a thread with 6 CTAs an SM, or 256 threads, measured no faster.
 #pragma once
 #include <cuda_bf16.h>

@@ -60,15 +60,16 @@
 namespace i8 {
 
 // Bound by HBM: 64 requests up to 8192 tokens, 32 query and 8 kv heads of 128,
-// int8: 91.7 us, 5.3 TB/s (78 % of the measured copy rate); one request of
-// 131071 tokens, E4M3: 50.7 us (78 %).  About 8 us of either are the start and
-// the join.  Two stages and three CTAs an SM beat three and two (95 against 108
-// us), TMA the lanes' own cp.async (95 against 122).
+// int8: 96.7 us, 5.0 TB/s (75 % of the measured copy rate); 64 of 4096 each: 90.0
+// us (89 %); one request of 131071 tokens, E4M3: 53.6 us (75 %).  About 8 us of
+// each are the start and the join.  Two stages and three CTAs an SM beat three
+// and two (95 against 108 us), TMA the lanes' own cp.async (95 against 122).
+// The two forms of the sum cost 4 % against one that goes by V alone (92 us).
 //
 // How the work is split.  An item is a request's row tile (8 * NT rows) of one
-// kv head; its tokens come in units of 4 warps' tiles.  The units of all items, request
-// after request, are one line that the resident CTAs cut into equal shares, so
-// ragged lengths balance and one long context fills the GPU.  Nobody but the
+// kv head; its tokens come in units of 4 warps' tiles.  The units of all items,
+// request after request, are one line that the resident CTAs cut into equal
+// shares, so ragged lengths balance and one long context fills the GPU.  Nobody but the
 // device knows the lengths: every CTA adds up the requests' units by itself
 // (two loads a request).  A CTA that covers an item whole writes its rows; the
 // pieces of an item that is cut go to the workspace (two slots a CTA: an item

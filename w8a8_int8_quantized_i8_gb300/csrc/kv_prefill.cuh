@@ -27,7 +27,7 @@
 // tile of keys, of which the products take 2950 (2048 at the nominal rate: S
 // reads both operands from shared memory, which the conversion uses too).  Four
 // requests, 5357 new tokens, contexts to 8000, 32 query and 8 kv heads of 128:
-// 556 us, 46 % of the measured bf16 rate (warp MMA: 4224 us).  Two softmax
+// 560 us, 46 % of the measured bf16 rate (warp MMA: 4224 us).  Two softmax
 // threads a row against one: 510 against 543 us; 8 converting warps against 6:
 // 528 against 510.
 //

@@ -21,8 +21,8 @@
 //
 // Bound by HBM: 2 + 2 bytes read and 2 + 1 written an element.  A row a CTA, as
 // in the quantizer: small CTAs spread evenly, each element is read once and
-// stays in registers.  16384 x 3072, E4M3: 58.6 us, 6.0 TB/s (89 % of the
-// measured copy rate); one row of 3072: 2.9 us, a launch.
+// stays in registers.  16384 x 3072, E4M3: 60.1 us, 5.9 TB/s (88 % of the
+// measured copy rate); one row of 3072: 2.7 us, a launch.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -174,7 +174,7 @@ __device__ __forceinline__ void norm_far_row(const NormRow& a, bool large) {
 }
 
 // Registers a thread: what the usual row needs.  The far row's code would take
-// more and cost CTAs (16384 x 3072, E4M3: 62 us, and 67 without the limit).
+// more and cost CTAs (16384 x 3072, E4M3: 60 us, and 67 without the limit).
 constexpr int norm_registers(int V) { return V <= 4 ? 64 : V == 6 ? 80 : 104; }
 
 // One row per CTA of G warps, V 16-byte vectors a lane in registers.

@@ -171,8 +171,9 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // The cache's codes [blocks * kv_heads, block, D] in boxes of `rows` tokens by
-// at most 128 bytes, swizzled (the warps' fragments) or as they are.  A third dimension for the block keeps every coordinate
-// below 2^31 however large the cache is.
+// at most 128 bytes, swizzled (the warps' fragments) or as they are.  A third
+// dimension for the block keeps every coordinate below 2^31 however large the
+// cache is.
 i8_status encode_cache(CUtensorMap* map, const void* base, const i8_kv_cache& c, int rows,
                        bool swizzle) {
   static std::mutex mu;
@@ -236,9 +237,12 @@ size_t attention_ws(int workers) {
 
 // Rows of a request and kv head from which the tcgen05 kernel takes it.  It
 // always pays for 256 rows; the warp kernel reads and converts the keys again
-// for every 16.  us by the warp kernel / by tcgen05, 8 requests of 4096 tokens
-// and 8 kv heads of 128: 64 rows 39 / 58, 96 rows 85 / 63, 128 rows 64 / 59, 256
-// rows 117 / 66; one request of 32768: 64 rows 57 / 57, 128 rows 101 / 59.
+// for every 16.  us by the warp kernel / by tcgen05, requests of one length:
+//                                    32 rows   64 rows   96 rows   128 rows   256
+//   8 of 4096, 8 kv heads of 128     37 / 67   60 / 67   88 / 69   110 / 70   207 / 82
+//   8 of 4096, 8 kv heads of 64      27 / 53   42 / 53   58 / 54    76 / 55   140 / 60
+//   1 of 32768, 8 kv heads of 128    34 / 58   58 / 61   80 / 62   103 / 63   192 / 69
+//   64 of 1024, 2 kv heads of 128    26 / 51   41 / 52   56 / 54    71 / 56   128 / 66
 constexpr int kPrefillRows = 96;
 
 template <int D>

@@ -270,8 +270,9 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                     cache: QuantKVCache) -> QuantKVCache:
     """Quantizes the step's keys and values, bf16 [T, kv_heads, head_dim] each
     (views of the fused projection's output allowed), into their slots
-    (int64 [T], as build_block_tables gives them; negative: skipped).  A block
-    whose tokens get louder is re-coded with its new scale."""
+    (int64 [T], as build_block_tables gives them; negative: skipped; a block's
+    tokens in order and together).  A block whose tokens get louder is re-coded
+    with its new scale; a NaN makes the scale of its block and head NaN."""
     index = _device_index(k, "k")
     info = _cache(cache, index)
     T = k.shape[0] if k.dim() else 0
@@ -291,11 +292,14 @@ def paged_attention(q: torch.Tensor, cache: QuantKVCache, block_tables: torch.Te
     over the cache, which holds them already.  Request r's tokens are rows
     cu_new[r]..cu_new[r+1] of q and the last of its seq_lens[r] tokens; its
     blocks are row r of ``block_tables``.  ``max_new`` bounds the new tokens of
-    a request (None: T); scale defaults to head_dim ** -0.5.
+    a request and chooses the kernels by it (None: T, which costs a batch of
+    single tokens a third more: 90 -> 119 us for 64 requests of 4096 tokens);
+    scale defaults to head_dim ** -0.5.
 
     Returns out [T, q_heads, head_dim] bf16, and with ``want_lse`` also the
     natural log of the sum of exponentials, fp32 [T, q_heads] (-inf for a row
-    that sees nothing, whose output is 0).  Rows of no request are not written."""
+    that sees nothing, whose output is 0).  Rows of no request are not written.
+    NaN shows in the rows that see it, and in no others."""
     index = _device_index(q, "q")
     info = _cache(cache, index)
     if q.dim() != 3:
