@@ -329,17 +329,25 @@ def _nearest(x, mantissa_bits, least, most):
     return torch.sign(x) * ((size / step).round() * step).clamp(max=most)
 
 
+def _power_above(x):
+    """The exponent of the smallest power of two that is at least x (log2 alone may be off in its last digit)."""
+    k = torch.floor(torch.log2(x)) - 1
+    for _ in range(3):
+        k = torch.where(torch.exp2(k) < x, k + 1, k)
+    return k
+
+
 def _exact_values(t, fmt):
     """What rows in 64 bits stand for once they are held in the format."""
     size = t.abs()
     if fmt == "nvfp4":
         most = size.amax(1, keepdim=True)
-        row = torch.where(most > 0, torch.exp2(torch.ceil(torch.log2(most / 2688)).clamp(min=-126)), 1.0)
+        row = torch.where(most > 0, torch.exp2(_power_above(most / 2688).clamp(min=-126)), 1.0)
         top = (size / row).reshape(t.shape[0], -1, 16).amax(2).repeat_interleave(16, 1)
         scale = _nearest(top / 6, 3, -6, 448.0) * row
     else:
         top = size.reshape(t.shape[0], -1, 32).amax(2).repeat_interleave(32, 1)
-        scale = torch.exp2(torch.ceil(torch.log2(top / 6)).clamp(min=-127))
+        scale = torch.exp2(_power_above(top / 6).clamp(min=-127))
     full = torch.where(scale > 0, scale, 1.0)
     return torch.where(scale > 0, _nearest(t / full, 1, 0, 6.0) * scale, 0.0)
 
