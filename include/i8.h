@@ -379,6 +379,100 @@ i8_status i8_paged_attention(const void* q_bf16, int64_t ldq_token, int64_t ldq_
                              int64_t ldo_head, float* lse, void* ws, size_t ws_bytes,
                              i8_stream_t stream);
 
+/* ------------------------------------------------------------------ rotation
+ * The root-mean-square norm of each query and key head with a gain (NULL: no
+ * norm), and the rotation of its first rotary_dim elements by the token's
+ * position, in one pass:
+ *   y = x * weight / sqrt(mean(x^2) + eps)        over the head's elements
+ *   (y[a], y[b]) -> (y[a] cos t - y[b] sin t, y[b] cos t + y[a] sin t)
+ * for the pairs i = 0 .. rotary_dim / 2 - 1, with (a, b) = (i, i + rotary_dim / 2)
+ * or, interleaved, (2 i, 2 i + 1), and t = position * inv_freq[i].  fp32 inside
+ * (t to 2^-24 turns up to position 2^20), one rounding to bf16.
+ *   q, k [tokens, heads, head_dim] bf16: element strides between tokens and
+ *   between heads (% 8 == 0), head_dim contiguous, % 8 == 0, <= 512
+ *   rotary_dim % 16 == 0 (0: the norm alone)
+ *   positions [axes, tokens] int32 (ld_positions apart), any sign
+ *   sections [axes] HOST pointer: how many pairs each axis turns, in order;
+ *   their sum is rotary_dim / 2.  axes 1 .. 4
+ *   q_weight, k_weight [head_dim] bf16 or NULL; inv_freq [rotary_dim / 2] fp32
+ *   q_out, k_out: as q and k; each is its input with the same strides (in place)
+ *   or shares no memory with any operand (I8_ERR_INVALID_ARG; operands of
+ *   interleaved memory are told apart where their token strides are the same)
+ * q_heads or kv_heads may be 0.                                             */
+i8_status i8_heads_rmsnorm_rotate(const void* q_bf16, int64_t ldq_token, int64_t ldq_head, int64_t q_heads,
+                                  const void* k_bf16, int64_t ldk_token, int64_t ldk_head, int64_t kv_heads,
+                                  int64_t tokens, int64_t head_dim, const void* q_weight_bf16,
+                                  const void* k_weight_bf16, float eps, const int32_t* positions,
+                                  int64_t ld_positions, int64_t axes, const int32_t* sections,
+                                  const float* inv_freq, int64_t rotary_dim, int interleaved, void* q_out,
+                                  int64_t ldqo_token, int64_t ldqo_head, void* k_out, int64_t ldko_token,
+                                  int64_t ldko_head, i8_stream_t stream);
+
+/* ------------------------------------------------------------------ 4 bits
+ * The 4-bit route: both operands of a linear layer in microscaled 4-bit floating
+ * point, on the tensor core's block-scaled products.  (No counterpart on the
+ * pages.)  Codes are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
+ * to a byte, the even element in the low half.
+ *   I8_FP4_NV16  value = code * S * s: S in E4M3 for each 16 elements of a row,
+ *                s = 2^k of the row.  s is the smallest power of two (>= 2^-126)
+ *                with max|row| <= 6 * 448 * s (0 for a row of zeros), S =
+ *                E4M3(max|block| / s / 6), code = E2M1(x / s / S)
+ *   I8_FP4_MX32  value = code * S: S = 2^E for each 32 elements, the smallest
+ *                (E >= -127) with max|block| <= 6 * S, held as E + 127; code =
+ *                E2M1(x / S).  No scale of the row
+ * rounded to nearest, ties to even, saturating at 6.  A NaN or an infinity makes
+ * its row (NV16) or its block (MX32) NaN.
+ * Block scales are held in tiles of 128 rows by 256 elements, a tile's rows of
+ * tiles one behind the other: [ceil(rows / 128)][ceil(K / 256)][P][32][4][4]
+ * bytes, P = 4 (NV16) or 2 (MX32); the scale of row r and block b is at
+ * [r / 128][b / (4 P)][b / 4 % P][r % 32][r / 32 % 4][b % 4].  Those past K are 0;
+ * those past the rows may hold anything.
+ * K % 32 == 0, K <= 131072; rows < 2^31.                                    */
+typedef enum { I8_FP4_NV16 = 0, I8_FP4_MX32 = 1 } i8_fp4_format;
+typedef struct {
+  const void* codes;        /* [rows, K / 2] bytes, contiguous, 16-byte aligned */
+  const void* block_scales; /* i8_fp4_block_scale_bytes(), 16-byte aligned */
+  const float* row_scales;  /* [rows], or NULL: ones */
+  int64_t rows;
+  int64_t K;
+  int32_t fmt;              /* i8_fp4_format */
+} i8_fp4_rows;
+
+/* Bytes of the block scales of so many rows (0 for sizes that are refused). */
+size_t i8_fp4_block_scale_bytes(int64_t rows, int64_t K, int fmt);
+
+/* Quantizes rows: a layer's tokens, or its weights (offline).
+ *   x [rows, K] bf16 (row stride ldx, % 8 == 0); row_scales [rows] fp32 (NV16; not
+ *   touched for MX32).  No output shares memory with another operand.        */
+i8_status i8_quant_rows_fp4(const void* x_bf16, int64_t rows, int64_t K, int64_t ldx, int fmt, void* codes,
+                            void* block_scales, float* row_scales, i8_stream_t stream);
+
+/* i8_add_rmsnorm_quant_act_pertoken with a 4-bit output: h = x + residual, t = h *
+ * weight (fp32 steps), codes and block scales of t as above, and row_scales [M] =
+ * (s of the row, 1 for MX32) / sqrt(mean(h^2) + eps); a row of zeros keeps s.
+ * Arguments as there, but K as above.                                       */
+i8_status i8_add_rmsnorm_quant_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* residual_bf16,
+                                   int64_t ldr, const void* weight_bf16, float eps, int fmt, void* codes,
+                                   void* block_scales, float* row_scales, void* h_bf16, int64_t ldh,
+                                   i8_stream_t stream);
+
+/* y[m,n] = bf16(acc * s_a[m] * s_w[n] + bias[n]), acc the fp32 sum over k of the
+ * products of code * block scale, s_a and s_w the rows' scales; fp32 steps.
+ *   a [M, K] tokens, w [N, K] weights of the same format; N % 8 == 0
+ *   bias [N] bf16 or NULL, 16-byte aligned; y [M,N] bf16 (ldy >= N, % 8 == 0),
+ *   which shares no memory with the operands
+ * The order of the sum is fixed for a shape: repeated calls give the same bits. */
+i8_status i8_gemm_fp4_bias_bf16(const i8_fp4_rows* a, const i8_fp4_rows* w, const void* bias_bf16, void* y,
+                                int64_t ldy, i8_stream_t stream);
+
+/* The first half of a gated feed-forward block, both projections in one kernel:
+ *   y = bf16(act(g) * u), g and u as y above (unrounded fp32) for the weights
+ *   gate and up [N, K]; act(g) = g / (1 + exp(-g)) or the erf form of GELU.   */
+typedef enum { I8_GATE_SILU = 0, I8_GATE_GELU = 1 } i8_gate;
+i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, const i8_fp4_rows* up,
+                                 const void* gate_bias_bf16, const void* up_bias_bf16, int activation, void* y,
+                                 int64_t ldy, i8_stream_t stream);
+
 /* i8_gemm_dequant_bias_bf16 for callers that cannot allocate device memory
  * at call time -- for example a plugin running inside another runtime that
  * offers no workspace hook, an application whose device memory is all owned

@@ -53,6 +53,13 @@ class KVCacheInfo(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
+class FP4RowsInfo(ctypes.Structure):
+    """i8_fp4_rows of include/i8.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("block_scales", ctypes.c_void_p),
+                ("row_scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("fmt", ctypes.c_int32)]
+
+
 class I8Error(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {STATUS.get(status, status)}")
@@ -82,6 +89,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib = ctypes.CDLL(path)
         i64, vp, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
         st = ctypes.c_int
+        rows4 = ctypes.POINTER(FP4RowsInfo)
         sigs = {
             "i8_status_string": ([st], ctypes.c_char_p),
             "i8_version": ([], ctypes.c_char_p),
@@ -120,6 +128,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "i8_paged_attention": ([vp, i64, i64, i64, i64, ctypes.POINTER(KVCacheInfo), vp, i64,
                                     i64, vp, vp, i64, i64, ctypes.c_float, vp, i64, i64, vp, vp,
                                     sz, vp], st),
+            "i8_heads_rmsnorm_rotate": ([vp, i64, i64, i64, vp, i64, i64, i64, i64, i64, vp, vp,
+                                         ctypes.c_float, vp, i64, i64, ctypes.POINTER(ctypes.c_int32),
+                                         vp, i64, ctypes.c_int, vp, i64, i64, vp, i64, i64, vp], st),
+            "i8_fp4_block_scale_bytes": ([i64, i64, ctypes.c_int], sz),
+            "i8_quant_rows_fp4": ([vp, i64, i64, i64, ctypes.c_int, vp, vp, vp, vp], st),
+            "i8_add_rmsnorm_quant_fp4": ([vp, i64, i64, i64, vp, i64, vp, ctypes.c_float, ctypes.c_int,
+                                          vp, vp, vp, vp, i64, vp], st),
+            "i8_gemm_fp4_bias_bf16": ([rows4, rows4, vp, vp, i64, vp], st),
+            "i8_gemm_fp4_gated_bf16": ([rows4, rows4, rows4, vp, vp, ctypes.c_int, vp, i64, vp], st),
             "i8_sync_check": ([vp], st),
             "i8_selftest_timeout": ([ctypes.c_int, vp], st),
             "i8_plan_query": ([i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,

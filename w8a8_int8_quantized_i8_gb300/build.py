@@ -2,9 +2,9 @@
 and beside it libi8probe.so, a measurement helper for the benchmark (the
 legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path).
 
-libi8.so is two translation units (the linear layer, the serving operators),
-the probe one; one ``-gencode`` target (sm_103a), no cmake; all three compile
-in parallel.  The outputs are git-ignored and rebuilt whenever a source is
+libi8.so is three translation units (the linear layer, the serving operators,
+the 4-bit route), the probe one; one ``-gencode`` target (sm_103a), no cmake;
+all four compile in parallel.  The outputs are git-ignored and rebuilt whenever a source is
 newer than them.
 """
 from __future__ import annotations
@@ -18,7 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libi8.so")
-UNITS = [os.path.join(CSRC, "i8_api.cu"), os.path.join(CSRC, "serving_api.cu")]
+UNITS = [os.path.join(CSRC, name) for name in ("i8_api.cu", "serving_api.cu", "fp4_api.cu")]
 PROBE_LIB = os.path.join(PKG, "libi8probe.so")
 PROBE_SRC = os.path.join(CSRC, "engine_probe.cu")
 

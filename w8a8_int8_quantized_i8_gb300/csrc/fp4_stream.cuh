@@ -1,0 +1,273 @@
+// fp4_stream.cuh -- the 4-bit product for few tokens: the weights stream through
+// the tensor core, tokens are the narrow operand.
+//
+//   D[channel, token] = sum_k w[channel, k] * x[token, k]
+//
+// A CTA takes 128 channels (of both weights, gated), NT tokens and a share of K.
+// The tensor core's M dimension is the channels', so NT can be as small as 16: one
+// token costs 16 columns and not 128 rows.  (A tile of tokens begins where a tile
+// of their scales does: NT < 128 takes all tokens at once.)  Warp 0 fetches tiles of 256 elements
+// by TMA (codes, 128-byte swizzle) and bulk copies (scales) into a ring, warp 1
+// copies scales to tensor memory and issues products, and all four warps read
+// the 128 lanes of D.
+//
+// Channels alone do not fill the GPU at few tokens (4096 are 32 CTAs), so K is
+// split over the CTAs of a cluster.  They meet in distributed shared memory: each
+// CTA writes its partial sums of every token to the CTA that finishes this token,
+// which adds them in the order of the splits (the same bits every time).  No
+// workspace, no second launch.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "fp4_mma.cuh"
+
+namespace i8 {
+
+template <bool MX, int NT, bool GATED>
+struct Fp4StreamCfg {
+  static constexpr int WEIGHTS = GATED ? 2 : 1;
+  static constexpr int SCALES = fp4_tile_bytes(MX ? 32 : 16);
+  static constexpr int PARTS = SCALES / 512;
+  static constexpr int OFF_T = WEIGHTS * 16384;
+  static constexpr int OFF_WS = OFF_T + NT * 128;
+  static constexpr int OFF_TS = OFF_WS + WEIGHTS * SCALES;
+  static constexpr int STAGE = OFF_TS + SCALES;
+  static constexpr uint32_t TX = WEIGHTS * (16384 + SCALES) + NT * 128 + SCALES;
+  static constexpr int STAGES = 208 * 1024 / STAGE > 8 ? 8 : 208 * 1024 / STAGE;
+  static constexpr int THREADS = 128;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  // tensor memory: D, the weights' scales, the tokens'
+  static constexpr int COL_WS = WEIGHTS * NT;
+  static constexpr int COL_TS = COL_WS + WEIGHTS * 4 * PARTS;
+  static constexpr int COLS_USED = COL_TS + 4 * PARTS;
+  static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
+  static_assert(COLS_USED <= 512 && STAGE % 1024 == 0 && NT % 16 == 0 && NT <= 128);
+  // 8 splits' partial sums of a CTA's tokens fit the ring
+  static_assert(8 * WEIGHTS * ((NT + 7) / 8) * 512 <= STAGES * STAGE);
+};
+
+// One CTA's rows of y: channel n (this thread's), tokens m0 .. m0 + count - 1, with
+// their products in value(c).  Neighbouring lanes exchange halves so that a lane
+// stores two channels of one token.
+template <int NT>
+__device__ __forceinline__ void fp4_store_pair(const Fp4GemmArgs& p, int m, int n, float v0, float v1, int limit) {
+  // v0: token m, v1: token m + 1, both of channel n
+  const bool odd = n & 1;
+  const float give = odd ? v0 : v1;
+  const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+  const uint32_t pair = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
+  const int at = odd ? m + 1 : m;
+  if (at < limit && n < p.N) *reinterpret_cast<uint32_t*>(p.y + at * p.ldy + (n & ~1)) = pair;
+}
+
+template <bool MX, int NT, bool GATED>
+__global__ void __launch_bounds__(128, 1)
+    fp4_stream_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
+                      const __grid_constant__ CUtensorMap tm_t, const Fp4GemmArgs p) {
+  using Cfg = Fp4StreamCfg<MX, NT, GATED>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[Cfg::STAGES];
+  __shared__ __align__(8) uint64_t empty[Cfg::STAGES];
+  __shared__ __align__(8) uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  __shared__ float token_scale[NT];
+  volatile int* abort_flag = &abort_word;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % p.splits, n_tile = static_cast<int>(blockIdx.x) / p.splits;
+  const int n0 = n_tile * 128, m0 = static_cast<int>(blockIdx.y) * NT;
+  const int kb0 = rank * p.deep_per_split, kb1 = min(p.deep, kb0 + p.deep_per_split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(&done), 1);
+    abort_word = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), Cfg::COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w0);
+    if constexpr (GATED) tma_prefetch_desc(&tm_w1);
+    tma_prefetch_desc(&tm_t);
+    // the weights on their way into L2 while the kernel before drains
+    for (int kb = kb0; kb < min(kb1, kb0 + Cfg::STAGES); ++kb) {
+      tma_prefetch_l2_2d(&tm_w0, kb * 128, n0);
+      if constexpr (GATED) tma_prefetch_l2_2d(&tm_w1, kb * 128, n0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0 && lane == 0) {
+    bool ok = true;
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    const int64_t tile = Cfg::SCALES;
+    const uint8_t* ws0 = p.w[0].scales + static_cast<int64_t>(n_tile) * p.deep * tile;
+    const uint8_t* ws1 = GATED ? p.w[1].scales + static_cast<int64_t>(n_tile) * p.deep * tile : nullptr;
+    const uint8_t* ts = p.scales + static_cast<int64_t>(m0 >> 7) * p.deep * tile;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t bar = smem_u32(&full[s]), st = ring + static_cast<uint32_t>(s * Cfg::STAGE);
+      if (!(ok = mbar_wait(smem_u32(&empty[s]), ph ^ 1u, abort_flag))) break;
+      mbar_arrive_expect_tx(bar, Cfg::TX);
+      tma_load_2d(st, &tm_w0, bar, kb * 128, n0);
+      if constexpr (GATED) tma_load_2d(st + 16384, &tm_w1, bar, kb * 128, n0);
+      tma_load_2d(st + Cfg::OFF_T, &tm_t, bar, kb * 128, m0);
+      bulk_load(st + Cfg::OFF_WS, ws0 + kb * tile, Cfg::SCALES, bar);
+      if constexpr (GATED) bulk_load(st + Cfg::OFF_WS + Cfg::SCALES, ws1 + kb * tile, Cfg::SCALES, bar);
+      bulk_load(st + Cfg::OFF_TS, ts + kb * tile, Cfg::SCALES, bar);
+      ++issued;
+      if (++s == Cfg::STAGES) s = 0, ph ^= 1u;
+    }
+    // a CTA that gives up ends after its own copies
+    if (!ok)
+      for (int i = max(0, issued - Cfg::STAGES); i < issued; ++i)
+        mbar_wait_bounded(smem_u32(&full[i % Cfg::STAGES]), (i / Cfg::STAGES) & 1, 100000000ull);
+  } else if (warp == 1 && lane == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t st = ring + static_cast<uint32_t>(s * Cfg::STAGE);
+      const uint64_t bd = smem_desc_sw128(st + Cfg::OFF_T);
+#pragma unroll
+      for (int j = 0; j < Cfg::PARTS; ++j) {
+#pragma unroll
+        for (int w = 0; w < Cfg::WEIGHTS; ++w)
+          copy_scales<1>(tmem + Cfg::COL_WS + (w * Cfg::PARTS + j) * 4,
+                         smem_desc_scales(st + Cfg::OFF_WS + w * Cfg::SCALES + j * 512));
+        copy_scales<1>(tmem + Cfg::COL_TS + j * 4, smem_desc_scales(st + Cfg::OFF_TS + j * 512));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // 64 elements, 32 bytes along the swizzled row
+        const int part = MX ? j / 2 : j;
+        const uint32_t idesc = MX && (j & 1) ? fp4_idesc<MX>(128, NT, 2) : fp4_idesc<MX>(128, NT, 0);
+#pragma unroll
+        for (int w = 0; w < Cfg::WEIGHTS; ++w)
+          mma_fp4<MX, 1>(tmem + w * NT, smem_desc_sw128(st + w * 16384) + 2u * j, bd + 2u * j, idesc,
+                         tmem + Cfg::COL_WS + (w * Cfg::PARTS + part) * 4, tmem + Cfg::COL_TS + part * 4,
+                         kb > kb0 || j > 0 ? 1u : 0u);
+      }
+      mma_commit(smem_u32(&empty[s]));
+      if (++s == Cfg::STAGES) s = 0, ph ^= 1u;
+    }
+    mma_commit(smem_u32(&done));
+    mbar_wait_bounded(smem_u32(&done), 0u, 100000000ull);
+  } else if (warp >= 2) {
+    for (int i = threadIdx.x - 64; i < NT; i += 64)
+      token_scale[i] = m0 + i < p.M ? (p.row_scales ? p.row_scales[m0 + i] : 1.0f) : 0.0f;
+  }
+  __syncwarp();
+  mbar_wait(smem_u32(&done), 0u, abort_flag);
+  __syncthreads();  // token_scale; the abort flag's last word
+  tc_fence_after();
+  const bool ok = *abort_flag == 0;
+  const int n = n0 + static_cast<int>(threadIdx.x);
+  float sw[Cfg::WEIGHTS], b[Cfg::WEIGHTS];
+#pragma unroll
+  for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+    sw[w] = n < p.N && p.w[w].row_scales ? p.w[w].row_scales[n] : 1.0f;
+    b[w] = n < p.N && p.w[w].bias ? __uint_as_float(static_cast<uint32_t>(p.w[w].bias[n]) << 16) : 0.0f;
+  }
+  auto finish = [&](const float* acc, int c) {
+    const float sa = token_scale[c];
+    const float v = fp4_dequant(acc[0], sa, sw[0], b[0]);
+    if constexpr (GATED) return fp4_gate(v, fp4_dequant(acc[1], sa, sw[1], b[1]), p.activation);
+    return v;
+  };
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  if (p.splits == 1) {
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < NT && m0 + c < p.M; c += 16) {
+        uint32_t r[Cfg::WEIGHTS][16];
+#pragma unroll
+        for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float v[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float acc[2];
+#pragma unroll
+            for (int w = 0; w < Cfg::WEIGHTS; ++w) acc[w] = __uint_as_float(r[w][i + k]);
+            v[k] = finish(acc, c + i + k);
+          }
+          fp4_store_pair<NT>(p, m0 + c + i, n, v[0], v[1], p.M);
+        }
+      }
+    }
+  } else {
+    // token c of the tile is finished by CTA c / each
+    const int each = (min(NT, p.M - m0) + p.splits - 1) / p.splits;
+    cluster_sync_all();  // the rings are free: every CTA's products have ended
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < NT && m0 + c < p.M; c += 16) {
+        uint32_t r[Cfg::WEIGHTS][16];
+#pragma unroll
+        for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int owner = (c + i) / each, slot = (c + i) - owner * each;
+          if (owner < p.splits && m0 + c + i < p.M) {
+#pragma unroll
+            for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+              const uint32_t to = mapa_shared(
+                  ring + static_cast<uint32_t>(((rank * Cfg::WEIGHTS + w) * each + slot) * 512 + threadIdx.x * 4), owner);
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(r[w][i]) : "memory");
+            }
+          }
+        }
+      }
+    }
+    cluster_sync_all();
+    const int mine = min(each, min(NT, p.M - m0) - rank * each);
+    if (ok)
+#pragma unroll 1
+      for (int c = 0; c < mine; c += 2) {
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (c + k < mine) {
+            float acc[2] = {0.0f, 0.0f};
+            for (int q = 0; q < p.splits; ++q)
+#pragma unroll
+              for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+                float part;
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(part)
+                             : "r"(ring + static_cast<uint32_t>(((q * Cfg::WEIGHTS + w) * each + c + k) * 512 + threadIdx.x * 4)));
+                acc[w] = q == 0 ? part : __fadd_rn(acc[w], part);
+              }
+            v[k] = finish(acc, rank * each + c + k);
+          }
+        fp4_store_pair<NT>(p, m0 + rank * each + c, n, v[0], v[1], m0 + rank * each + mine);
+      }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::COLS);
+  }
+}
+
+}  // namespace i8

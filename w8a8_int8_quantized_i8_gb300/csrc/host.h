@@ -1,4 +1,4 @@
-// host.h -- what the library's two translation units share on the host: the
+// host.h -- what the library's translation units share on the host: the
 // process-wide options, the NVTX scope of an ABI call, small argument checks
 // and the dependent launch.
 #pragma once
@@ -68,7 +68,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 // Reads and clears the status word of the current device that the serving
 // operators' kernels record into (each translation unit has a word of its
-// own; serving_api.cu defines this).
+// own; serving_api.cu defines this), and the 4-bit route's (fp4_api.cu).
 cudaError_t take_serving_status(unsigned int* word);
+cudaError_t take_fp4_status(unsigned int* word);
 
 }  // namespace i8

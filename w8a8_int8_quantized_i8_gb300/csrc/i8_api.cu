@@ -1522,9 +1522,9 @@ i8_status i8_sync_check(i8_stream_t stream) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return I8_ERR_CUDA;
   }
-  unsigned int serving = 0;
-  if (take_serving_status(&serving) != cudaSuccess) return I8_ERR_CUDA;
-  word |= serving;
+  unsigned int serving = 0, fp4 = 0;
+  if (take_serving_status(&serving) != cudaSuccess || take_fp4_status(&fp4) != cudaSuccess) return I8_ERR_CUDA;
+  word |= serving | fp4;
   if (word & (1u << I8_ERR_DEVICE_TIMEOUT)) return I8_ERR_DEVICE_TIMEOUT;
   if (word & (1u << I8_ERR_DEVICE_DATA)) return I8_ERR_DEVICE_DATA;
   return word == 0 ? I8_OK : I8_ERR_CUDA;

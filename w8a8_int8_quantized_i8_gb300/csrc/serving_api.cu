@@ -15,6 +15,7 @@
 #include "kv_append.cuh"
 #include "kv_attention.cuh"
 #include "kv_prefill.cuh"
+#include "overlap.h"
 #include "ptx.cuh"
 #include "rmsnorm.cuh"
 
@@ -83,60 +84,6 @@ cudaError_t launch_norm_v(const NormArgs& a, int fmt, cudaStream_t st) {
   if (fmt == kQuantE4M3) return go(add_rmsnorm_quant_kernel<V, kQuantE4M3>);
   if (fmt == kQuantF16) return go(add_rmsnorm_quant_kernel<V, kQuantF16>);
   return go(add_rmsnorm_quant_kernel<V, kQuantInt8>);
-}
-
-// ----------------------------------------------------------------- overlap
-// Memory of an operand: `rows` rows of `bytes`, `stride` bytes apart.
-struct Extent {
-  const void* base;
-  int64_t bytes;
-  int64_t rows = 1;
-  int64_t stride = 0;
-};
-
-// Whether rows of `t` and the one row of `v` share a byte.
-bool overlap(const Extent& t, const Extent& v) {
-  if (!t.base || !v.base || t.bytes <= 0 || t.rows <= 0 || v.bytes <= 0) return false;
-  const int64_t lo = static_cast<int64_t>(reinterpret_cast<uintptr_t>(v.base) - reinterpret_cast<uintptr_t>(t.base));
-  const int64_t hi = lo + v.bytes;  // from t's base on
-  if (hi <= 0) return false;
-  // the first row that ends behind lo
-  const int64_t row = lo < t.bytes ? 0 : t.rows == 1 ? 1 : (lo - t.bytes) / t.stride + 1;
-  return row < t.rows && row * t.stride < hi;
-}
-
-// Whether a row of `a` shares a byte with another row of `b` (both of as many
-// rows): a row may lie where the other's same row does.
-bool rows_cross(const Extent& a, const Extent& b) {
-  if (!a.base || !b.base || a.rows <= 1) return false;
-  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base));
-  if (d >= (a.rows - 1) * a.stride + a.bytes || d + (b.rows - 1) * b.stride + b.bytes <= 0) return false;
-  if (a.stride != b.stride) {
-    for (int64_t i = 0; i < b.rows; ++i) {
-      const Extent row{static_cast<const char*>(b.base) + i * b.stride, b.bytes};
-      const Extent before{a.base, a.bytes, i, a.stride};
-      const Extent after{static_cast<const char*>(a.base) + (i + 1) * a.stride, a.bytes, a.rows - i - 1, a.stride};
-      if (overlap(before, row) || overlap(after, row)) return true;
-    }
-    return false;
-  }
-  // row i + k of a begins d - k * stride before row i of b
-  const int64_t k = d >= 0 ? d / a.stride : -((-d + a.stride - 1) / a.stride), r = d - k * a.stride;
-  return (k != 0 && std::abs(k) < a.rows && r < a.bytes) ||
-         (k + 1 != 0 && std::abs(k + 1) < a.rows && a.stride - r < b.bytes);
-}
-
-// Whether rows [tokens, heads] of `dim` elements, these strides apart, share an
-// element.
-bool rows_overlap(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
-  if ((tokens > 1 && token < dim) || (heads > 1 && head < dim)) return true;
-  if (tokens <= 1 || heads <= 1) return false;
-  if (token >= head * (heads - 1) + dim || head >= token * (tokens - 1) + dim) return false;
-  // neither inside the other: the tokens nearest to each head's offset
-  for (int64_t h = 1; h < heads; ++h)
-    for (int64_t t = h * head / token; t <= h * head / token + 1 && t < tokens; ++t)
-      if (std::abs(h * head - t * token) < dim) return true;
-  return false;
 }
 
 // ----------------------------------------------------------------- cache checks
