@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/i8.h"
+#include "fp4_pair.cuh"
 #include "fp4_quant.cuh"
 #include "fp4_stream.cuh"
 #include "heads_rotate.cuh"
@@ -98,31 +99,95 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+i8_status encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  static std::mutex mu;
+  static EncodeTiledFn fn = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!fn) {
+      void* p = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+          q != cudaDriverEntryPointSuccess || !p)
+        return I8_ERR_CUDA;
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+    }
+  }
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(map, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? I8_OK
+             : I8_ERR_CUDA;
+}
+
 // The codes [rows, K / 2 bytes] in boxes of `box` rows by 128 bytes, swizzled;
 // zeros outside.
 i8_status encode_codes(CUtensorMap* map, const i8_fp4_rows& r, int box) {
-  static std::mutex mu;
-  static EncodeTiledFn encode = nullptr;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    if (!encode) {
-      void* fn = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-          q != cudaDriverEntryPointSuccess || !fn)
-        return I8_ERR_CUDA;
-      encode = reinterpret_cast<EncodeTiledFn>(fn);
-    }
-  }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(r.K / 2), static_cast<cuuint64_t>(r.rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(r.K / 2)};
   const cuuint32_t size[2] = {128, static_cast<cuuint32_t>(box)};
-  const cuuint32_t elem[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(r.codes), dims, strides, size, elem,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? I8_OK
-             : I8_ERR_CUDA;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, r.codes, dims, strides, size, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The block scales, a tile of 128 rows by 256 elements a row of 8-byte words.
+i8_status encode_scales(CUtensorMap* map, const i8_fp4_rows& r) {
+  const cuuint64_t words = fp4_tile_bytes(r.fmt == I8_FP4_MX32 ? 32 : 16) / 8;
+  const cuuint64_t dims[2] = {words, static_cast<cuuint64_t>((r.rows + 127) / 128) * fp4_deep(r.K)};
+  const cuuint64_t strides[1] = {words * 8};
+  const cuuint32_t size[2] = {static_cast<cuuint32_t>(words), 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, r.block_scales, dims, strides, size, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// CTA pairs of a kernel that are resident at once.
+template <auto KERN>
+i8_status resident_pairs(int dev, int sms, int threads, size_t smem, int* pairs) {
+  static int cached[kMaxDevices] = {};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cached[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess || n < 1) return I8_ERR_CUDA;
+    cached[dev] = n;
+  }
+  *pairs = cached[dev];
+  return I8_OK;
+}
+
+template <bool MX, bool GATED>
+i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
+                      cudaStream_t st) {
+  using Cfg = Fp4PairCfg<MX, GATED>;
+  constexpr auto kern = fp4_pair_kernel<MX, GATED>;
+  int pairs;
+  if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
+  if (i8_status e = resident_pairs<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, &pairs)) return e;
+  CUtensorMap a, as, b[2], bs[2], y;
+  if (i8_status e = encode_codes(&a, t, 128)) return e;
+  if (i8_status e = encode_scales(&as, t)) return e;
+  for (int k = 0; k < (GATED ? 2 : 1); ++k) {
+    if (i8_status e = encode_codes(&b[k], *w[k], 128)) return e;
+    if (i8_status e = encode_scales(&bs[k], *w[k])) return e;
+  }
+  if (!GATED) b[1] = b[0], bs[1] = bs[0];
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.ldy) * 2, static_cast<cuuint64_t>(p.ldy) * 2 * p.M};
+  const cuuint32_t box[3] = {64, 32, 1};
+  if (i8_status e = encode(&y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return e;
+  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + Cfg::TILE_N - 1) / Cfg::TILE_N);
+  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
+  return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], y, p));
 }
 
 template <bool MX, int NT, bool GATED>
@@ -180,6 +245,8 @@ i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows
   if (p.M <= 16) return launch_stream<MX, 16, GATED>(p, t, w, dev, sms, st);
   if (p.M <= 32) return launch_stream<MX, 32, GATED>(p, t, w, dev, sms, st);
   if (p.M <= 64) return launch_stream<MX, 64, GATED>(p, t, w, dev, sms, st);
+  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
+  if (p.M > 128 && tiles >= sms / 4) return launch_pair<MX, GATED>(p, t, w, dev, sms, st);
   return launch_stream<MX, 128, GATED>(p, t, w, dev, sms, st);
 }
 
@@ -194,7 +261,7 @@ i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows
   if (a->K != w0->K || a->fmt != w0->fmt) return I8_ERR_INVALID_ARG;
   if (ldy < w0->rows || (a->rows > 0 && w0->rows > 0 && !y)) return I8_ERR_INVALID_ARG;
   if (!aligned16(y) || ldy % 8 != 0 || !aligned16(b0) || !aligned16(b1)) return I8_ERR_ALIGNMENT;
-  if (w0->rows % 8 != 0 || (a->rows + 127) / 128 > 65535) return I8_ERR_UNSUPPORTED;
+  if (w0->rows % 8 != 0 || (a->rows + 127) / 128 > 65535 || w0->rows > INT32_MAX - 256) return I8_ERR_UNSUPPORTED;
   if (a->rows == 0 || w0->rows == 0) return I8_OK;
   // other CTAs read the tokens and the weights while one writes its rows of y
   const Extent out{y, w0->rows * 2, a->rows, ldy * 2};

@@ -146,17 +146,6 @@ struct GemmCfg {
   static_assert(STAGE8 % 1024 == 0 && STAGE16 % 1024 == 0, "stage alignment");
 };
 
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void advance(int n) {
-    if (++s == n) {
-      s = 0;
-      ph ^= 1u;
-    }
-  }
-};
-
 struct TileCoord {
   int mb, nb, ks, kb0, kb1;
 };
@@ -169,20 +158,6 @@ __device__ __forceinline__ TileCoord decode_tile(const GemmParams& p, int tile) 
   t.kb0 = t.ks * p.kb_per_split;
   t.kb1 = min(t.kb0 + p.kb_per_split, p.total_kb);
   return t;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
 }
 
 // s8x4_to_f16x4 (four int8 codes -> four fp16 values) lives in quant.cuh.
