@@ -56,7 +56,10 @@ i8_status allow_smem(int dev, size_t bytes) {
   static std::mutex mu;
   std::lock_guard<std::mutex> lk(mu);
   if (done[dev]) return I8_OK;
-  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+  // (and all of the SM's: two CTAs that fit are meant to share it)
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess ||
+      cudaFuncSetAttribute(KERN, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess)
     return I8_ERR_CUDA;
   done[dev] = true;
   return I8_OK;
@@ -139,30 +142,50 @@ i8_status encode_scales(CUtensorMap* map, const i8_fp4_rows& r) {
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, r.block_scales, dims, strides, size, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// CTA pairs of a kernel that are resident at once.
+// Clusters of lo .. hi of a kernel's CTAs that are resident at once: out[size].
 template <auto KERN>
-i8_status resident_pairs(int dev, int sms, int threads, size_t smem, int* pairs) {
-  static int cached[kMaxDevices] = {};
+i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, int hi, int (&out)[kFp4MaxSplits + 1]) {
+  static int cached[kMaxDevices][kFp4MaxSplits + 1] = {};
   static std::mutex mu;
   std::lock_guard<std::mutex> lk(mu);
-  if (cached[dev] == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess || n < 1) return I8_ERR_CUDA;
-    cached[dev] = n;
+  if (cached[dev][lo] == 0) {
+    for (int size = lo; size <= hi; ++size) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(size * sms));
+      cfg.blockDim = dim3(static_cast<unsigned>(threads));
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = static_cast<unsigned>(size);
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess) n = 0;
+      cached[dev][size] = n;
+    }
+    cudaGetLastError();
+    if (cached[dev][lo] < 1) return I8_ERR_CUDA;
   }
-  *pairs = cached[dev];
+  std::copy(cached[dev], cached[dev] + kFp4MaxSplits + 1, out);
   return I8_OK;
+}
+
+// K splits of the streaming kernel: the fewest tiles of K in a row, counting what
+// a CTA costs besides.
+int stream_splits(int tiles, int deep, int most, const int (&clusters)[kFp4MaxSplits + 1]) {
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= most && s <= deep; ++s) {
+    const int each = (deep + s - 1) / s;
+    if (clusters[s] < 1 || (deep + each - 1) / each != s) continue;  // no room, or a CTA without work
+    if (g_opt.force_splits > 0 && s == std::min({g_opt.force_splits, most, deep})) return s;
+    const int waves = (tiles + clusters[s] - 1) / clusters[s];
+    const double cost = waves * (each + 6.0) + (s > 1 ? 2.0 : 0.0);
+    if (s == 1 || cost < least) best = s, least = cost;
+  }
+  return best;
 }
 
 template <bool MX, bool GATED>
@@ -170,9 +193,9 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
                       cudaStream_t st) {
   using Cfg = Fp4PairCfg<MX, GATED>;
   constexpr auto kern = fp4_pair_kernel<MX, GATED>;
-  int pairs;
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
-  if (i8_status e = resident_pairs<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, &pairs)) return e;
+  int clusters[kFp4MaxSplits + 1];
+  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 2, 2, clusters)) return e;
   CUtensorMap a, as, b[2], bs[2], y;
   if (i8_status e = encode_codes(&a, t, 128)) return e;
   if (i8_status e = encode_scales(&as, t)) return e;
@@ -186,7 +209,7 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   const cuuint32_t box[3] = {64, 32, 1};
   if (i8_status e = encode(&y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return e;
   const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + Cfg::TILE_N - 1) / Cfg::TILE_N);
-  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
+  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters[2])));
   return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], y, p));
 }
 
@@ -204,17 +227,10 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
     m1 = m0;
   }
   if (i8_status e = encode_codes(&mt, t, NT)) return e;
-  // K splits: the fewest tiles of K in a row, counting what a CTA costs besides
+  int clusters[kFp4MaxSplits + 1];
+  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 1, Cfg::MAX_SPLITS, clusters)) return e;
   const int tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 8 && s <= p.deep; ++s) {
-    const int each = (p.deep + s - 1) / s;
-    if (s > 1 && (p.deep + each - 1) / each != s) continue;  // a CTA without work
-    const int waves = (tiles * s + sms - 1) / sms;
-    const double cost = waves * (each + 6.0) + (s > 1 ? 2.0 : 0.0);
-    if (s == 1 || cost < least) best = s, least = cost;
-  }
+  const int best = stream_splits(tiles, p.deep, Cfg::MAX_SPLITS, clusters);
   p.splits = best;
   p.deep_per_split = (p.deep + best - 1) / best;
   cudaLaunchConfig_t cfg = {};

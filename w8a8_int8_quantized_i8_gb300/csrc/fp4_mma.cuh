@@ -78,6 +78,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "memory");
 }
 
+// The halves of cluster_sync_all (whole warps call).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 16 bytes into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster_v4(uint32_t to, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 enum Fp4Activation : int { kFp4Silu = 0, kFp4Gelu = 1 };
 
 // act(g) * u in fp32.  silu(g) = g / (1 + exp(-g)): exp(-g) = infinity gives 0.

@@ -169,16 +169,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED
           tc_fence_after();
           const uint32_t st = ring + static_cast<uint32_t>(r.s * Cfg::STAGE);
           const uint64_t ad = smem_desc_sw128(st), bd = smem_desc_sw128(st + Cfg::OFF_B);
-#pragma unroll
-          for (int j = 0; j < Cfg::PARTS; ++j) {
+          auto scales = [&](int j) {  // those of a part
             copy_scales<2>(tmem + Cfg::COL_AS + j * 4, smem_desc_scales(st + Cfg::OFF_AS + j * 512));
             copy_scales<2>(tmem + Cfg::COL_BS + j * 8, smem_desc_scales(st + Cfg::OFF_BS + j * 512));
             copy_scales<2>(tmem + Cfg::COL_BS + j * 8 + 4,
                            smem_desc_scales(st + Cfg::OFF_BS + Cfg::SCALES + j * 512));
-          }
+          };
+          scales(0);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // 64 elements, 32 bytes along the swizzled row
             const int part = MX ? j / 2 : j;
+            if (MX ? j == 0 : j < 3) scales(part + 1);  // while the product before runs
             const uint32_t idesc = MX && (j & 1) ? fp4_idesc<MX>(256, 256, 2) : fp4_idesc<MX>(256, 256, 0);
             mma_fp4<MX, 2>(d, ad + 2u * j, bd + 2u * j, idesc, tmem + Cfg::COL_AS + part * 4,
                            tmem + Cfg::COL_BS + part * 8, kb > 0 || j > 0 ? 1u : 0u);

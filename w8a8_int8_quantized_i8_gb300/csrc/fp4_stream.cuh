@@ -14,8 +14,8 @@
 // Channels alone do not fill the GPU at few tokens (4096 are 32 CTAs), so K is
 // split over the CTAs of a cluster.  They meet in distributed shared memory: each
 // CTA writes its partial sums of every token to the CTA that finishes this token,
-// which adds them in the order of the splits (the same bits every time).  No
-// workspace, no second launch.
+// four tokens of a channel in 16 bytes, which adds them in the order of the splits
+// (the same bits every time).  No workspace, no second launch.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -25,6 +25,19 @@
 #include "fp4_mma.cuh"
 
 namespace i8 {
+
+constexpr int kFp4MaxSplits = 8;
+
+// The most tokens, rounded up to 4 for each split, that the CTAs of up to `most`
+// splits finish together.
+constexpr int fp4_red_tokens(int tokens, int most) {
+  int n = 0;
+  for (int s = 1; s <= most; ++s) {
+    const int all = s * (((tokens + s - 1) / s + 3) / 4 * 4);
+    n = all > n ? all : n;
+  }
+  return n;
+}
 
 template <bool MX, int NT, bool GATED>
 struct Fp4StreamCfg {
@@ -36,17 +49,29 @@ struct Fp4StreamCfg {
   static constexpr int OFF_TS = OFF_WS + WEIGHTS * SCALES;
   static constexpr int STAGE = OFF_TS + SCALES;
   static constexpr uint32_t TX = WEIGHTS * (16384 + SCALES) + NT * 128 + SCALES;
-  static constexpr int STAGES = 208 * 1024 / STAGE > 8 ? 8 : 208 * 1024 / STAGE;
+  // the splits' partial sums, 512 bytes for each token and weight: a region of
+  // their own for the fewest tokens, which saves a barrier of the cluster, else
+  // the ring
+  static constexpr int MAX_SPLITS = GATED ? kFp4MaxSplits / 2 : kFp4MaxSplits;
+  static constexpr int RED = fp4_red_tokens(NT, MAX_SPLITS) * WEIGHTS * 512;
+  static constexpr int RED_OWN = NT == 16 ? RED : 0;
+  // two CTAs an SM, so that one's fetches run while the other meets its cluster
+  // (and the next kernel begins); 128 tokens of two weights want half the GPU's
+  // tensor memory and more, and get an SM to themselves
+  static constexpr int ROOM = GATED && NT == 128 ? 222 * 1024 : 112 * 1024;
+  static constexpr int STAGES = (ROOM - RED_OWN - 1024) / STAGE > 8 ? 8 : (ROOM - RED_OWN - 1024) / STAGE;
   static constexpr int THREADS = 128;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int OFF_RED = RED_OWN ? STAGES * STAGE : 0;
+  static constexpr int SMEM = STAGES * STAGE + RED_OWN + 1024;
   // tensor memory: D, the weights' scales, the tokens'
   static constexpr int COL_WS = WEIGHTS * NT;
   static constexpr int COL_TS = COL_WS + WEIGHTS * 4 * PARTS;
   static constexpr int COLS_USED = COL_TS + 4 * PARTS;
   static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
   static_assert(COLS_USED <= 512 && STAGE % 1024 == 0 && NT % 16 == 0 && NT <= 128);
-  // 8 splits' partial sums of a CTA's tokens fit the ring
-  static_assert(8 * WEIGHTS * ((NT + 7) / 8) * 512 <= STAGES * STAGE);
+  // co-resident CTAs never wait for one another's tensor memory
+  static_assert(STAGES >= 2 && (COLS <= 256 || SMEM > 120 * 1024));
+  static_assert(RED_OWN != 0 || RED <= STAGES * STAGE);
 };
 
 // One CTA's rows of y: channel n (this thread's), tokens m0 .. m0 + count - 1, with
@@ -107,10 +132,19 @@ __global__ void __launch_bounds__(128, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // (every CTA of the cluster is there before another writes to it)
+  if (Cfg::RED_OWN && p.splits > 1) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
   pdl_trigger();
+  const int n = n0 + static_cast<int>(threadIdx.x);
+  float sw[Cfg::WEIGHTS], b[Cfg::WEIGHTS];
+#pragma unroll
+  for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+    sw[w] = n < p.N && p.w[w].row_scales ? p.w[w].row_scales[n] : 1.0f;
+    b[w] = n < p.N && p.w[w].bias ? __uint_as_float(static_cast<uint32_t>(p.w[w].bias[n]) << 16) : 0.0f;
+  }
 
   if (warp == 0 && lane == 0) {
     bool ok = true;
@@ -145,17 +179,18 @@ __global__ void __launch_bounds__(128, 1)
       tc_fence_after();
       const uint32_t st = ring + static_cast<uint32_t>(s * Cfg::STAGE);
       const uint64_t bd = smem_desc_sw128(st + Cfg::OFF_T);
-#pragma unroll
-      for (int j = 0; j < Cfg::PARTS; ++j) {
+      auto scales = [&](int j) {  // those of a part
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w)
           copy_scales<1>(tmem + Cfg::COL_WS + (w * Cfg::PARTS + j) * 4,
                          smem_desc_scales(st + Cfg::OFF_WS + w * Cfg::SCALES + j * 512));
         copy_scales<1>(tmem + Cfg::COL_TS + j * 4, smem_desc_scales(st + Cfg::OFF_TS + j * 512));
-      }
+      };
+      scales(0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // 64 elements, 32 bytes along the swizzled row
         const int part = MX ? j / 2 : j;
+        if (MX ? j == 0 : j < 3) scales(part + 1);  // while the product before runs
         const uint32_t idesc = MX && (j & 1) ? fp4_idesc<MX>(128, NT, 2) : fp4_idesc<MX>(128, NT, 0);
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w)
@@ -177,13 +212,6 @@ __global__ void __launch_bounds__(128, 1)
   __syncthreads();  // token_scale; the abort flag's last word
   tc_fence_after();
   const bool ok = *abort_flag == 0;
-  const int n = n0 + static_cast<int>(threadIdx.x);
-  float sw[Cfg::WEIGHTS], b[Cfg::WEIGHTS];
-#pragma unroll
-  for (int w = 0; w < Cfg::WEIGHTS; ++w) {
-    sw[w] = n < p.N && p.w[w].row_scales ? p.w[w].row_scales[n] : 1.0f;
-    b[w] = n < p.N && p.w[w].bias ? __uint_as_float(static_cast<uint32_t>(p.w[w].bias[n]) << 16) : 0.0f;
-  }
   auto finish = [&](const float* acc, int c) {
     const float sa = token_scale[c];
     const float v = fp4_dequant(acc[0], sa, sw[0], b[0]);
@@ -214,53 +242,54 @@ __global__ void __launch_bounds__(128, 1)
       }
     }
   } else {
-    // token c of the tile is finished by CTA c / each
-    const int each = (min(NT, p.M - m0) + p.splits - 1) / p.splits;
-    cluster_sync_all();  // the rings are free: every CTA's products have ended
+    // token c of the tile is finished by CTA c / each; in its shared memory
+    // [split][weight][each / 4][128 channels][4 tokens]
+    const int count = min(NT, p.M - m0), each = ((count + p.splits - 1) / p.splits + 3) & ~3;
+    const uint32_t red = ring + Cfg::OFF_RED;
+    if constexpr (Cfg::RED_OWN != 0) cluster_wait();
+    else cluster_sync_all();  // the rings are free: every CTA's products have ended
     if (ok) {
+      int owner = 0, slot = 0;
 #pragma unroll 1
-      for (int c = 0; c < NT && m0 + c < p.M; c += 16) {
+      for (int c = 0; c < count; c += 16) {
         uint32_t r[Cfg::WEIGHTS][16];
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int owner = (c + i) / each, slot = (c + i) - owner * each;
-          if (owner < p.splits && m0 + c + i < p.M) {
+        for (int i = 0; i < 16; i += 4) {
+          if (c + i < count) {
+            const uint32_t to = mapa_shared(red, owner);
 #pragma unroll
-            for (int w = 0; w < Cfg::WEIGHTS; ++w) {
-              const uint32_t to = mapa_shared(
-                  ring + static_cast<uint32_t>(((rank * Cfg::WEIGHTS + w) * each + slot) * 512 + threadIdx.x * 4), owner);
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(r[w][i]) : "memory");
-            }
+            for (int w = 0; w < Cfg::WEIGHTS; ++w)
+              st_cluster_v4(to + static_cast<uint32_t>((rank * Cfg::WEIGHTS + w) * each + slot) * 512u + threadIdx.x * 16u,
+                            make_uint4(r[w][i], r[w][i + 1], r[w][i + 2], r[w][i + 3]));
+            if ((slot += 4) == each) slot = 0, ++owner;
           }
         }
       }
     }
     cluster_sync_all();
-    const int mine = min(each, min(NT, p.M - m0) - rank * each);
-    if (ok)
-#pragma unroll 1
-      for (int c = 0; c < mine; c += 2) {
-        float v[2] = {0.0f, 0.0f};
+    const int first = rank * each, mine = min(each, count - first);
+    if (ok) {
+#pragma unroll 2
+      for (int c = 0; c < mine; c += 4) {
+        float acc[4][2] = {};
+        for (int q = 0; q < p.splits; ++q)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (c + k < mine) {
-            float acc[2] = {0.0f, 0.0f};
-            for (int q = 0; q < p.splits; ++q)
+          for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+            const uint4 u = lds128(red + static_cast<uint32_t>((q * Cfg::WEIGHTS + w) * each + c) * 512u + threadIdx.x * 16u);
+            const uint32_t part[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int w = 0; w < Cfg::WEIGHTS; ++w) {
-                float part;
-                asm volatile("ld.shared.f32 %0, [%1];"
-                             : "=f"(part)
-                             : "r"(ring + static_cast<uint32_t>(((q * Cfg::WEIGHTS + w) * each + c + k) * 512 + threadIdx.x * 4)));
-                acc[w] = q == 0 ? part : __fadd_rn(acc[w], part);
-              }
-            v[k] = finish(acc, rank * each + c + k);
+            for (int k = 0; k < 4; ++k) acc[k][w] = __fadd_rn(acc[k][w], __uint_as_float(part[k]));
           }
-        fp4_store_pair<NT>(p, m0 + rank * each + c, n, v[0], v[1], m0 + rank * each + mine);
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = finish(acc[k], min(first + c + k, NT - 1));
+        fp4_store_pair<NT>(p, m0 + first + c, n, v[0], v[1], p.M);
+        fp4_store_pair<NT>(p, m0 + first + c + 2, n, v[2], v[3], p.M);
       }
+    }
   }
   tc_fence_before();
   __syncthreads();
