@@ -20,30 +20,43 @@ __device__ constexpr uint32_t fp4_idesc(int M, int N, int byte) {
          (MX ? 1u << 23 : 0u) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(byte) << 29);
 }
 
+// One lane of a converged warp: 1 in it, 0 in the others.  The issuing warp stays
+// converged and its operands are the same in all lanes, so they reach the tensor
+// core's instructions without a detour; one lane's predicate issues them.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t q;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(q));
+  return q;
+}
+
 // D (+)= A * B^T of 64 elements, the operands scaled by blocks of 16 or 32.
+#define I8_MMA_FP4(form)                                                                                \
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"          \
+               "@q tcgen05.mma." form " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(leader)                \
+               : "memory")
 template <bool MX, int CTAS>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                        uint32_t accumulate) {
-  if constexpr (MX && CTAS == 1)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-                 : "memory");
-  else if constexpr (MX)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-                 : "memory");
-  else if constexpr (CTAS == 1)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-                 : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-                 : "memory");
+__device__ __forceinline__ void mma_fp4(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (MX && CTAS == 1) I8_MMA_FP4("cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
+  else if constexpr (MX) I8_MMA_FP4("cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
+  else if constexpr (CTAS == 1) I8_MMA_FP4("cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else I8_MMA_FP4("cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X");
+}
+#undef I8_MMA_FP4
+
+// mma_commit and mma_commit_pair by the elected lane.
+__device__ __forceinline__ void commit_elected(uint32_t leader, uint32_t bar) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+               "r"(leader)
+               : "memory");
+}
+__device__ __forceinline__ void commit_pair_elected(uint32_t leader, uint32_t bar, uint16_t cta_mask) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+               "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+                   "r"(bar), "h"(cta_mask), "r"(leader)
+               : "memory");
 }
 
 // Matrix descriptor of a 512-byte part of block scales: 32 rows of 16 bytes, no
@@ -56,9 +69,15 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
 // A part of block scales into four columns of tensor memory, the same for each
 // quarter of the lanes.  Ordered with this thread's products before and behind it.
 template <int CTAS>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  if constexpr (CTAS == 1) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-  else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t leader, uint32_t tmem, uint64_t desc) {
+  if constexpr (CTAS == 1)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc), "r"(leader)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc), "r"(leader)
+                 : "memory");
 }
 
 // Bulk copy of `bytes` (a multiple of 16) from global memory, counted on `bar`.

@@ -155,24 +155,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED
     }
   } else if (warp == 1) {
     regs_dec<Cfg::REG_LO>();
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t leader = elect_one();
       Ring r;
       bool ok = true;
       int t = 0;
       for (int i = pair; ok && i < tiles; i += pairs, ++t) {
         // the columns that this buffer shares with the one before have been read
-        if (t > 0 && !(ok = mbar_wait_cluster(accfree, (t - 1) & 1, abort_flag))) break;
+        if (t > 0 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(accfree, (t - 1) & 1, abort_flag)))) break;
         tc_fence_after();
         const uint32_t d = tmem + (t & 1 ? Cfg::COL_D1 : 0);
         for (int kb = 0; kb < p.deep; ++kb) {
-          if (!(ok = mbar_wait_cluster(full(r.s), r.ph, abort_flag))) break;
+          if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(full(r.s), r.ph, abort_flag)))) break;
           tc_fence_after();
           const uint32_t st = ring + static_cast<uint32_t>(r.s * Cfg::STAGE);
           const uint64_t ad = smem_desc_sw128(st), bd = smem_desc_sw128(st + Cfg::OFF_B);
           auto scales = [&](int j) {  // those of a part
-            copy_scales<2>(tmem + Cfg::COL_AS + j * 4, smem_desc_scales(st + Cfg::OFF_AS + j * 512));
-            copy_scales<2>(tmem + Cfg::COL_BS + j * 8, smem_desc_scales(st + Cfg::OFF_BS + j * 512));
-            copy_scales<2>(tmem + Cfg::COL_BS + j * 8 + 4,
+            copy_scales<2>(leader, tmem + Cfg::COL_AS + j * 4, smem_desc_scales(st + Cfg::OFF_AS + j * 512));
+            copy_scales<2>(leader, tmem + Cfg::COL_BS + j * 8, smem_desc_scales(st + Cfg::OFF_BS + j * 512));
+            copy_scales<2>(leader, tmem + Cfg::COL_BS + j * 8 + 4,
                            smem_desc_scales(st + Cfg::OFF_BS + Cfg::SCALES + j * 512));
           };
           scales(0);
@@ -181,15 +182,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED
             const int part = MX ? j / 2 : j;
             if (MX ? j == 0 : j < 3) scales(part + 1);  // while the product before runs
             const uint32_t idesc = MX && (j & 1) ? fp4_idesc<MX>(256, 256, 2) : fp4_idesc<MX>(256, 256, 0);
-            mma_fp4<MX, 2>(d, ad + 2u * j, bd + 2u * j, idesc, tmem + Cfg::COL_AS + part * 4,
+            mma_fp4<MX, 2>(leader, d, ad + 2u * j, bd + 2u * j, idesc, tmem + Cfg::COL_AS + part * 4,
                            tmem + Cfg::COL_BS + part * 8, kb > 0 || j > 0 ? 1u : 0u);
           }
-          mma_commit_pair(empty(r.s), 0x3);
+          commit_pair_elected(leader, empty(r.s), 0x3);
           r.advance(Cfg::STAGES);
         }
-        if (ok) mma_commit_pair(accfull(t & 1), 0x3);
+        if (ok) commit_pair_elected(leader, accfull(t & 1), 0x3);
       }
-      mma_commit_pair(done, 0x1);
+      commit_pair_elected(leader, done, 0x1);
       mbar_wait_bounded(done, 0u, 100000000ull);
     }
   } else if (warp >= Cfg::EPI_WARP0) {

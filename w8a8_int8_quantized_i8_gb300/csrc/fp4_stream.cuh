@@ -171,20 +171,21 @@ __global__ void __launch_bounds__(128, 1)
     if (!ok)
       for (int i = max(0, issued - Cfg::STAGES); i < issued; ++i)
         mbar_wait_bounded(smem_u32(&full[i % Cfg::STAGES]), (i / Cfg::STAGES) & 1, 100000000ull);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
+    const uint32_t leader = elect_one();
     int s = 0;
     uint32_t ph = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag)) break;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&full[s]), ph, abort_flag))) break;
       tc_fence_after();
       const uint32_t st = ring + static_cast<uint32_t>(s * Cfg::STAGE);
       const uint64_t bd = smem_desc_sw128(st + Cfg::OFF_T);
       auto scales = [&](int j) {  // those of a part
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w)
-          copy_scales<1>(tmem + Cfg::COL_WS + (w * Cfg::PARTS + j) * 4,
+          copy_scales<1>(leader, tmem + Cfg::COL_WS + (w * Cfg::PARTS + j) * 4,
                          smem_desc_scales(st + Cfg::OFF_WS + w * Cfg::SCALES + j * 512));
-        copy_scales<1>(tmem + Cfg::COL_TS + j * 4, smem_desc_scales(st + Cfg::OFF_TS + j * 512));
+        copy_scales<1>(leader, tmem + Cfg::COL_TS + j * 4, smem_desc_scales(st + Cfg::OFF_TS + j * 512));
       };
       scales(0);
 #pragma unroll
@@ -194,14 +195,14 @@ __global__ void __launch_bounds__(128, 1)
         const uint32_t idesc = MX && (j & 1) ? fp4_idesc<MX>(128, NT, 2) : fp4_idesc<MX>(128, NT, 0);
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w)
-          mma_fp4<MX, 1>(tmem + w * NT, smem_desc_sw128(st + w * 16384) + 2u * j, bd + 2u * j, idesc,
+          mma_fp4<MX, 1>(leader, tmem + w * NT, smem_desc_sw128(st + w * 16384) + 2u * j, bd + 2u * j, idesc,
                          tmem + Cfg::COL_WS + (w * Cfg::PARTS + part) * 4, tmem + Cfg::COL_TS + part * 4,
                          kb > kb0 || j > 0 ? 1u : 0u);
       }
-      mma_commit(smem_u32(&empty[s]));
+      commit_elected(leader, smem_u32(&empty[s]));
       if (++s == Cfg::STAGES) s = 0, ph ^= 1u;
     }
-    mma_commit(smem_u32(&done));
+    commit_elected(leader, smem_u32(&done));
     mbar_wait_bounded(smem_u32(&done), 0u, 100000000ull);
   } else if (warp >= 2) {
     for (int i = threadIdx.x - 64; i < NT; i += 64)
