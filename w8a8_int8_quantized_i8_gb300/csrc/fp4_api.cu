@@ -143,12 +143,17 @@ i8_status encode_scales(CUtensorMap* map, const i8_fp4_rows& r) {
 }
 
 // Clusters of lo .. hi of a kernel's CTAs that are resident at once: out[size].
+// (The runtime counts clusters with one CTA an SM; where several fit, so do as many
+// times the clusters.)
 template <auto KERN>
 i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, int hi, int (&out)[kFp4MaxSplits + 1]) {
   static int cached[kMaxDevices][kFp4MaxSplits + 1] = {};
   static std::mutex mu;
   std::lock_guard<std::mutex> lk(mu);
   if (cached[dev][lo] == 0) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem) != cudaSuccess || per_sm < 1)
+      return I8_ERR_CUDA;
     for (int size = lo; size <= hi; ++size) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(size * sms));
@@ -163,7 +168,7 @@ i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, 
       cfg.numAttrs = 1;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess) n = 0;
-      cached[dev][size] = n;
+      cached[dev][size] = n * size <= sms ? n * per_sm : n;
     }
     cudaGetLastError();
     if (cached[dev][lo] < 1) return I8_ERR_CUDA;
@@ -172,9 +177,14 @@ i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, 
   return I8_OK;
 }
 
-// K splits of the streaming kernel: the fewest tiles of K in a row, counting what
-// a CTA costs besides.
-int stream_splits(int tiles, int deep, int most, const int (&clusters)[kFp4MaxSplits + 1]) {
+// K splits of the streaming kernel, by a model in tiles of K (0.2 us each): a CTA
+// costs 10 besides its own, two on an SM slow each other down by 0.3, and CTAs that
+// meet pay for the tokens they exchange.  us measured (NV16) at 1, 2, 4, 8 splits:
+//   1 token by 4096 x 11008   13.7  9.1  6.3  5.5
+//   1 by 6144 x 4096           6.6  5.4  4.9  7.6 (two waves)
+//   61 by 2080 x 5120          8.4  7.9  6.4  7.0 (seven splits)
+//   128 by 4096 x 4096         8.4  9.5  8.6  13.4 (two waves)
+int stream_splits(int tiles, int tokens, int deep, int most, int sms, const int (&clusters)[kFp4MaxSplits + 1]) {
   int best = 1;
   double least = 0;
   for (int s = 1; s <= most && s <= deep; ++s) {
@@ -182,7 +192,8 @@ int stream_splits(int tiles, int deep, int most, const int (&clusters)[kFp4MaxSp
     if (clusters[s] < 1 || (deep + each - 1) / each != s) continue;  // no room, or a CTA without work
     if (g_opt.force_splits > 0 && s == std::min({g_opt.force_splits, most, deep})) return s;
     const int waves = (tiles + clusters[s] - 1) / clusters[s];
-    const double cost = waves * (each + 6.0) + (s > 1 ? 2.0 : 0.0);
+    const double shared = static_cast<int64_t>(tiles) * s > sms ? 1.3 : 1.0;
+    const double cost = waves * (each * shared + 10.0) + (s > 1 ? 2.0 + 0.085 * tokens : 0.0);
     if (s == 1 || cost < least) best = s, least = cost;
   }
   return best;
@@ -230,7 +241,7 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
   int clusters[kFp4MaxSplits + 1];
   if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 1, Cfg::MAX_SPLITS, clusters)) return e;
   const int tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
-  const int best = stream_splits(tiles, p.deep, Cfg::MAX_SPLITS, clusters);
+  const int best = stream_splits(tiles, NT, p.deep, Cfg::MAX_SPLITS, sms, clusters);
   p.splits = best;
   p.deep_per_split = (p.deep + best - 1) / best;
   cudaLaunchConfig_t cfg = {};

@@ -28,14 +28,13 @@ namespace i8 {
 
 constexpr int kFp4MaxSplits = 8;
 
-// The most tokens, rounded up to 4 for each split, that the CTAs of up to `most`
-// splits finish together.
+// Tokens that one of `splits` CTAs finishes: fours.
+__host__ __device__ constexpr int fp4_each(int tokens, int splits) { return ((tokens + splits - 1) / splits + 3) / 4 * 4; }
+
+// The most sums of tokens that a CTA gets from up to `most` splits.
 constexpr int fp4_red_tokens(int tokens, int most) {
   int n = 0;
-  for (int s = 1; s <= most; ++s) {
-    const int all = s * (((tokens + s - 1) / s + 3) / 4 * 4);
-    n = all > n ? all : n;
-  }
+  for (int s = 2; s <= most; ++s) n = s * fp4_each(tokens, s) > n ? s * fp4_each(tokens, s) : n;
   return n;
 }
 
@@ -49,8 +48,8 @@ struct Fp4StreamCfg {
   static constexpr int OFF_TS = OFF_WS + WEIGHTS * SCALES;
   static constexpr int STAGE = OFF_TS + SCALES;
   static constexpr uint32_t TX = WEIGHTS * (16384 + SCALES) + NT * 128 + SCALES;
-  // the splits' partial sums, 512 bytes for each token and weight: a region of
-  // their own for the fewest tokens, which saves a barrier of the cluster, else
+  // the sums to be finished, 512 bytes for each split, weight and token: a region
+  // of their own for the fewest tokens, which saves a barrier of the cluster, else
   // the ring
   static constexpr int MAX_SPLITS = GATED ? kFp4MaxSplits / 2 : kFp4MaxSplits;
   static constexpr int RED = fp4_red_tokens(NT, MAX_SPLITS) * WEIGHTS * 512;
@@ -73,20 +72,6 @@ struct Fp4StreamCfg {
   static_assert(STAGES >= 2 && (COLS <= 256 || SMEM > 120 * 1024));
   static_assert(RED_OWN != 0 || RED <= STAGES * STAGE);
 };
-
-// One CTA's rows of y: channel n (this thread's), tokens m0 .. m0 + count - 1, with
-// their products in value(c).  Neighbouring lanes exchange halves so that a lane
-// stores two channels of one token.
-template <int NT>
-__device__ __forceinline__ void fp4_store_pair(const Fp4GemmArgs& p, int m, int n, float v0, float v1, int limit) {
-  // v0: token m, v1: token m + 1, both of channel n
-  const bool odd = n & 1;
-  const float give = odd ? v0 : v1;
-  const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-  const uint32_t pair = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
-  const int at = odd ? m + 1 : m;
-  if (at < limit && n < p.N) *reinterpret_cast<uint32_t*>(p.y + at * p.ldy + (n & ~1)) = pair;
-}
 
 template <bool MX, int NT, bool GATED>
 __global__ void __launch_bounds__(128, 1)
@@ -138,6 +123,7 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t tmem = tmem_slot;
   pdl_wait();
   pdl_trigger();
+  // this thread's channel
   const int n = n0 + static_cast<int>(threadIdx.x);
   float sw[Cfg::WEIGHTS], b[Cfg::WEIGHTS];
 #pragma unroll
@@ -213,45 +199,62 @@ __global__ void __launch_bounds__(128, 1)
   __syncthreads();  // token_scale; the abort flag's last word
   tc_fence_after();
   const bool ok = *abort_flag == 0;
-  auto finish = [&](const float* acc, int c) {
-    const float sa = token_scale[c];
-    const float v = fp4_dequant(acc[0], sa, sw[0], b[0]);
-    if constexpr (GATED) return fp4_gate(v, fp4_dequant(acc[1], sa, sw[1], b[1]), p.activation);
-    return v;
-  };
+  const int count = min(NT, p.M - m0);
   const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  // Finishes tokens c .. c + 3 of the tile (those below `end`) from the sums of this
+  // thread's channel; four lanes exchange them so that each stores four channels
+  // of one token.
+  auto finish = [&](int c, int end, const float (&acc)[Cfg::WEIGHTS][4]) {
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float sa = token_scale[min(c + k, NT - 1)];
+      v[k] = fp4_dequant(acc[0][k], sa, sw[0], b[0]);
+      if constexpr (GATED) v[k] = fp4_gate(v[k], fp4_dequant(acc[1][k], sa, sw[1], b[1]), p.activation);
+    }
+    const uint32_t p01 = pack_bf16x2_rn(v[0], v[1]), p23 = pack_bf16x2_rn(v[2], v[3]);
+    // with the odd or even neighbour: two tokens, of a pair of channels each
+    const bool odd = lane & 1, high = lane & 2;
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? p01 : p23, 1);
+    const uint32_t lo = odd ? got : p01, hi = odd ? p23 : got;  // the even and the odd channel's tokens
+    const uint32_t t0 = __byte_perm(lo, hi, 0x5410), t1 = __byte_perm(lo, hi, 0x7632);
+    // with the other pair: one token of four channels
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, high ? t0 : t1, 2);
+    const int at = c + (odd ? 2 : 0) + (high ? 1 : 0);
+    if (at < end && n < p.N)
+      *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(m0 + at) * p.ldy + (n & ~3)) =
+          high ? make_uint2(other, t1) : make_uint2(t0, other);
+  };
   if (p.splits == 1) {
-    if (ok) {
-#pragma unroll 1
-      for (int c = 0; c < NT && m0 + c < p.M; c += 16) {
+    if (ok)
+#pragma unroll 2
+      for (int c = 0; c < count; c += 16) {
         uint32_t r[Cfg::WEIGHTS][16];
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float v[2];
+        for (int i = 0; i < 16; i += 4) {
+          float acc[Cfg::WEIGHTS][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float acc[2];
+          for (int w = 0; w < Cfg::WEIGHTS; ++w)
 #pragma unroll
-            for (int w = 0; w < Cfg::WEIGHTS; ++w) acc[w] = __uint_as_float(r[w][i + k]);
-            v[k] = finish(acc, c + i + k);
-          }
-          fp4_store_pair<NT>(p, m0 + c + i, n, v[0], v[1], p.M);
+            for (int k = 0; k < 4; ++k) acc[w][k] = __uint_as_float(r[w][i + k]);
+          finish(c + i, count, acc);
         }
       }
-    }
   } else {
-    // token c of the tile is finished by CTA c / each; in its shared memory
+    // token c of the tile is finished by CTA c / each; in its shared memory lie
     // [split][weight][each / 4][128 channels][4 tokens]
-    const int count = min(NT, p.M - m0), each = ((count + p.splits - 1) / p.splits + 3) & ~3;
+    const int each = fp4_each(count, p.splits);
     const uint32_t red = ring + Cfg::OFF_RED;
     if constexpr (Cfg::RED_OWN != 0) cluster_wait();
     else cluster_sync_all();  // the rings are free: every CTA's products have ended
     if (ok) {
+      const uint32_t at = static_cast<uint32_t>(rank * Cfg::WEIGHTS * each) * 512u + threadIdx.x * 16u;
       int owner = 0, slot = 0;
-#pragma unroll 1
+      uint32_t to = mapa_shared(red, 0) + at;
+#pragma unroll 2
       for (int c = 0; c < count; c += 16) {
         uint32_t r[Cfg::WEIGHTS][16];
 #pragma unroll
@@ -260,35 +263,40 @@ __global__ void __launch_bounds__(128, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           if (c + i < count) {
-            const uint32_t to = mapa_shared(red, owner);
+            if (slot == each) {
+              slot = 0;
+              to = mapa_shared(red, ++owner) + at;
+            }
 #pragma unroll
             for (int w = 0; w < Cfg::WEIGHTS; ++w)
-              st_cluster_v4(to + static_cast<uint32_t>((rank * Cfg::WEIGHTS + w) * each + slot) * 512u + threadIdx.x * 16u,
+              st_cluster_v4(to + static_cast<uint32_t>(w * each + slot) * 512u,
                             make_uint4(r[w][i], r[w][i + 1], r[w][i + 2], r[w][i + 3]));
-            if ((slot += 4) == each) slot = 0, ++owner;
+            slot += 4;
           }
         }
       }
     }
     cluster_sync_all();
-    const int first = rank * each, mine = min(each, count - first);
     if (ok) {
-#pragma unroll 2
-      for (int c = 0; c < mine; c += 4) {
-        float acc[4][2] = {};
-        for (int q = 0; q < p.splits; ++q)
+      const int first = rank * each, end = min(count, first + each);
+#pragma unroll 4
+      for (int c = first; c < end; c += 4) {
+        float acc[Cfg::WEIGHTS][4];
 #pragma unroll
-          for (int w = 0; w < Cfg::WEIGHTS; ++w) {
-            const uint4 u = lds128(red + static_cast<uint32_t>((q * Cfg::WEIGHTS + w) * each + c) * 512u + threadIdx.x * 16u);
-            const uint32_t part[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[k][w] = __fadd_rn(acc[k][w], __uint_as_float(part[k]));
+        for (int w = 0; w < Cfg::WEIGHTS; ++w) {
+          const uint32_t at = red + static_cast<uint32_t>(w * each + c - first) * 512u + threadIdx.x * 16u;
+          uint4 u = lds128(at);
+          acc[w][0] = __uint_as_float(u.x), acc[w][1] = __uint_as_float(u.y);
+          acc[w][2] = __uint_as_float(u.z), acc[w][3] = __uint_as_float(u.w);
+          for (int q = 1; q < p.splits; ++q) {
+            u = lds128(at + static_cast<uint32_t>(q * Cfg::WEIGHTS * each) * 512u);
+            acc[w][0] = __fadd_rn(acc[w][0], __uint_as_float(u.x));
+            acc[w][1] = __fadd_rn(acc[w][1], __uint_as_float(u.y));
+            acc[w][2] = __fadd_rn(acc[w][2], __uint_as_float(u.z));
+            acc[w][3] = __fadd_rn(acc[w][3], __uint_as_float(u.w));
           }
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = finish(acc[k], min(first + c + k, NT - 1));
-        fp4_store_pair<NT>(p, m0 + first + c, n, v[0], v[1], p.M);
-        fp4_store_pair<NT>(p, m0 + first + c + 2, n, v[2], v[3], p.M);
+        }
+        finish(c, end, acc);
       }
     }
   }
