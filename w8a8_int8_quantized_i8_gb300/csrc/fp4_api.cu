@@ -199,11 +199,12 @@ int stream_splits(int tiles, int tokens, int deep, int most, int sms, const int 
   return best;
 }
 
-template <bool MX, bool GATED>
+template <bool MX, int ACT>
 i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                       cudaStream_t st) {
+  constexpr bool GATED = ACT != kFp4Plain;
   using Cfg = Fp4PairCfg<MX, GATED>;
-  constexpr auto kern = fp4_pair_kernel<MX, GATED>;
+  constexpr auto kern = fp4_pair_kernel<MX, ACT>;
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
   int clusters[kFp4MaxSplits + 1];
   if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 2, 2, clusters)) return e;
@@ -224,11 +225,12 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], y, p));
 }
 
-template <bool MX, int NT, bool GATED>
+template <bool MX, int NT, int ACT>
 i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                         cudaStream_t st) {
+  constexpr bool GATED = ACT != kFp4Plain;
   using Cfg = Fp4StreamCfg<MX, NT, GATED>;
-  constexpr auto kern = fp4_stream_kernel<MX, NT, GATED>;
+  constexpr auto kern = fp4_stream_kernel<MX, NT, ACT>;
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
   CUtensorMap m0, m1, mt;
   if (i8_status e = encode_codes(&m0, *w[0], 128)) return e;
@@ -266,15 +268,23 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, m0, m1, mt, p));
 }
 
-template <bool MX, bool GATED>
+template <bool MX, int ACT>
 i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                          cudaStream_t st) {
-  if (p.M <= 16) return launch_stream<MX, 16, GATED>(p, t, w, dev, sms, st);
-  if (p.M <= 32) return launch_stream<MX, 32, GATED>(p, t, w, dev, sms, st);
-  if (p.M <= 64) return launch_stream<MX, 64, GATED>(p, t, w, dev, sms, st);
+  constexpr bool GATED = ACT != kFp4Plain;
+  if (p.M <= 16) return launch_stream<MX, 16, ACT>(p, t, w, dev, sms, st);
+  if (p.M <= 32) return launch_stream<MX, 32, ACT>(p, t, w, dev, sms, st);
+  if (p.M <= 64) return launch_stream<MX, 64, ACT>(p, t, w, dev, sms, st);
   const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-  if (p.M > 128 && tiles >= sms / 4) return launch_pair<MX, GATED>(p, t, w, dev, sms, st);
-  return launch_stream<MX, 128, GATED>(p, t, w, dev, sms, st);
+  if (p.M > 128 && tiles >= sms / 4) return launch_pair<MX, ACT>(p, t, w, dev, sms, st);
+  return launch_stream<MX, 128, ACT>(p, t, w, dev, sms, st);
+}
+
+template <int ACT>
+i8_status launch_format(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
+                        cudaStream_t st) {
+  return t.fmt == I8_FP4_MX32 ? launch_product<true, ACT>(p, t, w, dev, sms, st)
+                              : launch_product<false, ACT>(p, t, w, dev, sms, st);
 }
 
 i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows* w1, const void* b0, const void* b1,
@@ -313,14 +323,13 @@ i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows
   p.N = static_cast<int>(w0->rows);
   p.K = static_cast<int>(a->K);
   p.deep = fp4_deep(a->K);
-  p.activation = activation;
   int dev, sms;
   if (i8_status e = current_device(&dev)) return e;
   if (i8_status e = device_sms(dev, &sms)) return e;
   const i8_fp4_rows* const w[2] = {w0, w1};
-  if (a->fmt == I8_FP4_MX32)
-    return w1 ? launch_product<true, true>(p, *a, w, dev, sms, st) : launch_product<true, false>(p, *a, w, dev, sms, st);
-  return w1 ? launch_product<false, true>(p, *a, w, dev, sms, st) : launch_product<false, false>(p, *a, w, dev, sms, st);
+  if (!w1) return launch_format<kFp4Plain>(p, *a, w, dev, sms, st);
+  return activation == I8_GATE_SILU ? launch_format<kFp4Silu>(p, *a, w, dev, sms, st)
+                                    : launch_format<kFp4Gelu>(p, *a, w, dev, sms, st);
 }
 
 // ----------------------------------------------------------------- heads

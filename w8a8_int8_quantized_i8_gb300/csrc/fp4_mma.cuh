@@ -108,12 +108,14 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t to, uint4 v) {
                : "memory");
 }
 
-enum Fp4Activation : int { kFp4Silu = 0, kFp4Gelu = 1 };
+// What a product's epilogue does: nothing more, or act(g) * u.
+enum Fp4Epilogue : int { kFp4Plain = 0, kFp4Silu = 1, kFp4Gelu = 2 };
 
 // act(g) * u in fp32.  silu(g) = g / (1 + exp(-g)): exp(-g) = infinity gives 0.
-__device__ __forceinline__ float fp4_gate(float g, float u, int activation) {
-  const float act = activation == kFp4Silu ? __fdividef(g, 1.0f + __expf(-g)) : gelu_erf(g);
-  return act * u;
+template <int ACT>
+__device__ __forceinline__ float fp4_gate(float g, float u) {
+  if constexpr (ACT == kFp4Silu) return __fdividef(g, 1.0f + __expf(-g)) * u;
+  else return gelu_erf(g) * u;
 }
 
 struct Fp4Weight {
@@ -131,7 +133,6 @@ struct Fp4GemmArgs {
   int M, N;                 // tokens, channels
   int K, deep;              // elements, tiles of 256 of them
   int splits, deep_per_split;
-  int activation;
 };
 
 // acc * s_a * s_w + bias.

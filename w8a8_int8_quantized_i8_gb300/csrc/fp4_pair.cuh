@@ -56,13 +56,24 @@ struct Fp4PairCfg {
   static_assert(SMEM <= 232448 - 512, "shared memory, with the barriers");
 };
 
-template <bool MX, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED>::THREADS, 1)
+// Eight sums of a row times their scales, plus the biases (shared memory).
+__device__ __forceinline__ void fp4_dequant8(const uint32_t* acc, float sa, uint32_t scl, uint32_t bias, float (&v)[8]) {
+  const uint4 s0 = lds128(scl), s1 = lds128(scl + 16), bb = lds128(bias);
+  const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w}, b[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    v[k] = fp4_dequant(__uint_as_float(acc[k]), sa, __uint_as_float(s[k]), k & 1 ? bf16_hi(b[k / 2]) : bf16_lo(b[k / 2]));
+}
+
+template <bool MX, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
                     const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_as,
                     const __grid_constant__ CUtensorMap tm_bs0, const __grid_constant__ CUtensorMap tm_bs1,
                     const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ Fp4GemmArgs p) {
+  constexpr bool GATED = ACT != kFp4Plain;
   using Cfg = Fp4PairCfg<MX, GATED>;
+  static_assert(Cfg::THREADS == 384);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_[Cfg::STAGES];
   __shared__ __align__(8) uint64_t empty_[Cfg::STAGES];
@@ -206,14 +217,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED
       const int m_base = mb * 256 + static_cast<int>(rank) * 128 + quarter * 32;
       // this tile's channel scales and biases, where the tile before has not its
       // own: column 32 * ew + lane of the 256
-      float* scl = reinterpret_cast<float*>(smem_raw + (ring - raw) + Cfg::OFF_SCL) + (t & 1) * 256;
-      uint16_t* bias = reinterpret_cast<uint16_t*>(smem_raw + (ring - raw) + Cfg::OFF_BIAS) + (t & 1) * 256;
+      const uint32_t scl = ring + Cfg::OFF_SCL + (t & 1) * 1024u, bias = ring + Cfg::OFF_BIAS + (t & 1) * 512u;
       {
         const int c = ew * 32 + lane;
         const Fp4Weight& w = GATED && c >= 128 ? p.w[1] : p.w[0];
         const int n = GATED ? nb * 128 + (c & 127) : nb * 256 + c;
-        scl[c] = n < p.N && w.row_scales ? w.row_scales[n] : 1.0f;
-        bias[c] = n < p.N && w.bias ? w.bias[n] : static_cast<uint16_t>(0);
+        const float s = n < p.N && w.row_scales ? w.row_scales[n] : 1.0f;
+        const uint16_t b = n < p.N && w.bias ? w.bias[n] : static_cast<uint16_t>(0);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(scl + 4u * c), "f"(s) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(bias + 2u * c), "h"(b) : "memory");
       }
       const float sa = m_base + lane < p.M && p.row_scales ? p.row_scales[m_base + lane] : 1.0f;
       __syncwarp();
@@ -264,22 +276,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Fp4PairCfg<MX, GATED
         const int c0 = half * (GATED ? 64 : 128) + g * 64;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t o[4];
+          float v[8], u[8];
+          fp4_dequant8(&acc[g * 64 + c * 8], sa, scl + 4 * (c0 + c * 8), bias + 2 * (c0 + c * 8), v);
+          if constexpr (GATED) {
+            fp4_dequant8(&acc[64 + c * 8], sa, scl + 4 * (128 + c0 + c * 8), bias + 2 * (128 + c0 + c * 8), u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = c * 8 + k * 2 + e;
-              auto value = [&](int a, int ch) {
-                return fp4_dequant(__uint_as_float(acc[a]), sa, scl[ch], __uint_as_float(static_cast<uint32_t>(bias[ch]) << 16));
-              };
-              v[e] = value(g * 64 + j, c0 + j);
-              if constexpr (GATED) v[e] = fp4_gate(v[e], value(64 + j, 128 + c0 + j), p.activation);
-            }
-            o[k] = pack_bf16x2_rn(v[0], v[1]);
+            for (int k = 0; k < 8; ++k) v[k] = fp4_gate<ACT>(v[k], u[k]);
           }
-          sts128(row + ((static_cast<uint32_t>(c) ^ x) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(row + ((static_cast<uint32_t>(c) ^ x) << 4),
+                 make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                            pack_bf16x2_rn(v[6], v[7])));
         }
         fence_proxy_async_smem();
         __syncwarp();

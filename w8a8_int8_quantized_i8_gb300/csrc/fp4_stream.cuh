@@ -8,8 +8,8 @@
 // token costs 16 columns and not 128 rows.  (A tile of tokens begins where a tile
 // of their scales does: NT < 128 takes all tokens at once.)  Warp 0 fetches tiles of 256 elements
 // by TMA (codes, 128-byte swizzle) and bulk copies (scales) into a ring, warp 1
-// copies scales to tensor memory and issues products, and all four warps read
-// the 128 lanes of D.
+// copies scales to tensor memory and issues products, and all warps read D, 32
+// lanes and all of the tokens or half of them each.
 //
 // Channels alone do not fill the GPU at few tokens (4096 are 32 CTAs), so K is
 // split over the CTAs of a cluster.  They meet in distributed shared memory: each
@@ -59,7 +59,9 @@ struct Fp4StreamCfg {
   // tensor memory and more, and get an SM to themselves
   static constexpr int ROOM = GATED && NT == 128 ? 222 * 1024 : 112 * 1024;
   static constexpr int STAGES = (ROOM - RED_OWN - 1024) / STAGE > 8 ? 8 : (ROOM - RED_OWN - 1024) / STAGE;
-  static constexpr int THREADS = 128;
+  // two warps for each 32 channels where there are tokens for both
+  static constexpr int GROUPS = NT >= 64 ? 2 : 1;
+  static constexpr int THREADS = 128 * GROUPS;
   static constexpr int OFF_RED = RED_OWN ? STAGES * STAGE : 0;
   static constexpr int SMEM = STAGES * STAGE + RED_OWN + 1024;
   // tensor memory: D, the weights' scales, the tokens'
@@ -73,10 +75,11 @@ struct Fp4StreamCfg {
   static_assert(RED_OWN != 0 || RED <= STAGES * STAGE);
 };
 
-template <bool MX, int NT, bool GATED>
-__global__ void __launch_bounds__(128, 1)
+template <bool MX, int NT, int ACT>
+__global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
     fp4_stream_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
                       const __grid_constant__ CUtensorMap tm_t, const Fp4GemmArgs p) {
+  constexpr bool GATED = ACT != kFp4Plain;
   using Cfg = Fp4StreamCfg<MX, NT, GATED>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[Cfg::STAGES];
@@ -123,8 +126,9 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t tmem = tmem_slot;
   pdl_wait();
   pdl_trigger();
-  // this thread's channel
-  const int n = n0 + static_cast<int>(threadIdx.x);
+  // this thread's channel and its half of the tokens
+  const int channel = threadIdx.x & 127, group = threadIdx.x >> 7;
+  const int n = n0 + channel;
   float sw[Cfg::WEIGHTS], b[Cfg::WEIGHTS];
 #pragma unroll
   for (int w = 0; w < Cfg::WEIGHTS; ++w) {
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(128, 1)
     commit_elected(leader, smem_u32(&done));
     mbar_wait_bounded(smem_u32(&done), 0u, 100000000ull);
   } else if (warp >= 2) {
-    for (int i = threadIdx.x - 64; i < NT; i += 64)
+    for (int i = threadIdx.x - 64; i < NT; i += Cfg::THREADS - 64)
       token_scale[i] = m0 + i < p.M ? (p.row_scales ? p.row_scales[m0 + i] : 1.0f) : 0.0f;
   }
   __syncwarp();
@@ -200,7 +204,8 @@ __global__ void __launch_bounds__(128, 1)
   tc_fence_after();
   const bool ok = *abort_flag == 0;
   const int count = min(NT, p.M - m0);
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const int c0 = group * (NT / Cfg::GROUPS), c1 = min(count, c0 + NT / Cfg::GROUPS);  // the columns that it reads
   // Finishes tokens c .. c + 3 of the tile (those below `end`) from the sums of this
   // thread's channel; four lanes exchange them so that each stores four channels
   // of one token.
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(128, 1)
     for (int k = 0; k < 4; ++k) {
       const float sa = token_scale[min(c + k, NT - 1)];
       v[k] = fp4_dequant(acc[0][k], sa, sw[0], b[0]);
-      if constexpr (GATED) v[k] = fp4_gate(v[k], fp4_dequant(acc[1][k], sa, sw[1], b[1]), p.activation);
+      if constexpr (GATED) v[k] = fp4_gate<ACT>(v[k], fp4_dequant(acc[1][k], sa, sw[1], b[1]));
     }
     const uint32_t p01 = pack_bf16x2_rn(v[0], v[1]), p23 = pack_bf16x2_rn(v[2], v[3]);
     // with the odd or even neighbour: two tokens, of a pair of channels each
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(128, 1)
   if (p.splits == 1) {
     if (ok)
 #pragma unroll 2
-      for (int c = 0; c < count; c += 16) {
+      for (int c = c0; c < c1; c += 16) {
         uint32_t r[Cfg::WEIGHTS][16];
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
@@ -251,18 +256,18 @@ __global__ void __launch_bounds__(128, 1)
     if constexpr (Cfg::RED_OWN != 0) cluster_wait();
     else cluster_sync_all();  // the rings are free: every CTA's products have ended
     if (ok) {
-      const uint32_t at = static_cast<uint32_t>(rank * Cfg::WEIGHTS * each) * 512u + threadIdx.x * 16u;
-      int owner = 0, slot = 0;
-      uint32_t to = mapa_shared(red, 0) + at;
+      const uint32_t at = static_cast<uint32_t>(rank * Cfg::WEIGHTS * each) * 512u + channel * 16u;
+      int owner = c0 / each, slot = c0 - owner * each;
+      uint32_t to = mapa_shared(red, min(owner, p.splits - 1)) + at;
 #pragma unroll 2
-      for (int c = 0; c < count; c += 16) {
+      for (int c = c0; c < c1; c += 16) {
         uint32_t r[Cfg::WEIGHTS][16];
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w) tmem_ld_32x32b_x16(lanes + w * NT + c, r[w]);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          if (c + i < count) {
+          if (c + i < c1) {
             if (slot == each) {
               slot = 0;
               to = mapa_shared(red, ++owner) + at;
@@ -280,11 +285,11 @@ __global__ void __launch_bounds__(128, 1)
     if (ok) {
       const int first = rank * each, end = min(count, first + each);
 #pragma unroll 4
-      for (int c = first; c < end; c += 4) {
+      for (int c = first + 4 * group; c < end; c += 4 * Cfg::GROUPS) {
         float acc[Cfg::WEIGHTS][4];
 #pragma unroll
         for (int w = 0; w < Cfg::WEIGHTS; ++w) {
-          const uint32_t at = red + static_cast<uint32_t>(w * each + c - first) * 512u + threadIdx.x * 16u;
+          const uint32_t at = red + static_cast<uint32_t>(w * each + c - first) * 512u + channel * 16u;
           uint4 u = lds128(at);
           acc[w][0] = __uint_as_float(u.x), acc[w][1] = __uint_as_float(u.y);
           acc[w][2] = __uint_as_float(u.z), acc[w][3] = __uint_as_float(u.w);
