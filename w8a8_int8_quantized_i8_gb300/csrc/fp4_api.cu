@@ -78,15 +78,18 @@ i8_status fp4_sizes(int64_t rows, int64_t K, int fmt) {
 template <bool MX, bool NORM>
 cudaError_t launch_quant(Fp4QuantArgs& a, int64_t rows, cudaStream_t st) {
   const int vecs = a.deep;  // runs of 256 elements
-  const dim3 grid(static_cast<unsigned>(rows));
+  a.rows = rows;
   auto go = [&](auto kern, int V) {
     a.G = V > 0 ? (vecs + V - 1) / V : 16;
-    return launch_pdl(kern, grid, dim3(32 * a.G), 0, st, a);
+    a.R = V > 0 ? std::max(1, 4 / a.G) : 1;  // (long rows: one)
+    return launch_pdl(kern, dim3(static_cast<unsigned>((rows + a.R - 1) / a.R)), dim3(32, a.G, a.R), 0, st, a);
   };
-  if (vecs <= 8) return go(fp4_quant_kernel<1, MX, NORM>, 1);
-  if (vecs <= 32) return go(fp4_quant_kernel<2, MX, NORM>, 2);
-  if (vecs <= 64) return go(fp4_quant_kernel<4, MX, NORM>, 4);
-  return go(fp4_quant_kernel<0, MX, NORM>, 0);
+  // few rows: a warp for each 256 elements; many: fewer warps with more in hand
+  const int64_t most = rows <= 1024 ? 1 : vecs <= 8 ? 2 : 4;
+  if (vecs > 128) return go(fp4_quant_kernel<0, MX, NORM>, 0);
+  if (vecs <= 32 && most == 1) return go(fp4_quant_kernel<1, MX, NORM>, 1);
+  if (vecs <= 64 && most <= 2) return go(fp4_quant_kernel<2, MX, NORM>, 2);
+  return go(fp4_quant_kernel<4, MX, NORM>, 4);
 }
 
 // ----------------------------------------------------------------- products
@@ -208,7 +211,7 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
   int clusters[kFp4MaxSplits + 1];
   if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 2, 2, clusters)) return e;
-  CUtensorMap a, as, b[2], bs[2], y;
+  CUtensorMap a, as, b[2], bs[2];
   if (i8_status e = encode_codes(&a, t, 128)) return e;
   if (i8_status e = encode_scales(&as, t)) return e;
   for (int k = 0; k < (GATED ? 2 : 1); ++k) {
@@ -216,13 +219,9 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
     if (i8_status e = encode_scales(&bs[k], *w[k])) return e;
   }
   if (!GATED) b[1] = b[0], bs[1] = bs[0];
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), 1};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.ldy) * 2, static_cast<cuuint64_t>(p.ldy) * 2 * p.M};
-  const cuuint32_t box[3] = {64, 32, 1};
-  if (i8_status e = encode(&y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return e;
   const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + Cfg::TILE_N - 1) / Cfg::TILE_N);
   const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters[2])));
-  return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], y, p));
+  return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], p));
 }
 
 template <bool MX, int NT, int ACT>
@@ -268,6 +267,20 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, m0, m1, mt, p));
 }
 
+// Whether pairs beat the streaming kernel at 128 tokens, both in us by a model of
+// their waves.  Measured, stream / pair (NV16):
+//   512 tokens by 4096 x 4096     8.9 / 10.8      gated, 128 by 11008 x 4096   11.5 / 17.7
+//   1024 by 4096 x 4096          11.6 / 11.3      256                          21.1 / 18.4
+//   2048 by 4096 x 4096          21.5 / 18.1      512 by 5640 x 2048           15.4 / 13.9
+bool pair_is_faster(int M, int N, int deep, bool gated, int sms) {
+  const int64_t ctas = static_cast<int64_t>((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t tiles = static_cast<int64_t>((M + 255) / 256) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  const int64_t room = gated ? sms : 2 * static_cast<int64_t>(sms);
+  const double stream = ctas <= sms && !gated ? 4.4 + 0.28 * deep : 1.5 + (ctas + room - 1) / room * (3.4 + 0.42 * deep);
+  const double pair = 4.9 + (tiles + sms / 2 - 1) / (sms / 2) * std::max(0.4 * deep, 2.0);
+  return pair < stream;
+}
+
 template <bool MX, int ACT>
 i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                          cudaStream_t st) {
@@ -275,8 +288,7 @@ i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows
   if (p.M <= 16) return launch_stream<MX, 16, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 32) return launch_stream<MX, 32, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 64) return launch_stream<MX, 64, ACT>(p, t, w, dev, sms, st);
-  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-  if (p.M > 128 && tiles >= sms / 4) return launch_pair<MX, ACT>(p, t, w, dev, sms, st);
+  if (p.M > 128 && pair_is_faster(p.M, p.N, p.deep, GATED, sms)) return launch_pair<MX, ACT>(p, t, w, dev, sms, st);
   return launch_stream<MX, 128, ACT>(p, t, w, dev, sms, st);
 }
 

@@ -82,10 +82,25 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
   return d;
 }
 
+// About 1 / x.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The codes of 8 elements of one block and the block's scale byte.  top: bits of
-// the block's largest magnitude; inverse: 1 / s of the row (NV16).
+// the block's largest magnitude; s and inverse: the row's scale and 1 / s (NV16;
+// between 2^-100 and 2^100, where everything below is a normal number).
+//
+// Quotients t / d come from a = t * y, y about 1 / d, and one correction by the
+// residual a * d - t, which an fma gives exactly (P. Markstein, 1990): the result is
+// the exact quotient rounded once but for 2^-40 of an ulp, so it meets a midpoint
+// of E2M1 or E4M3 where the quotient does, and only there.  With these signs -0
+// stays -0.  (In pairs, f32x2, it took 8 % longer.)
 template <bool MX>
-__device__ __forceinline__ uint32_t fp4_codes8(const float (&t)[8], uint32_t top, float inverse, uint32_t* scale) {
+__device__ __forceinline__ uint32_t fp4_codes8(const float (&t)[8], uint32_t top, float s, float inverse,
+                                               uint32_t* scale) {
   float q[8];
   if constexpr (MX) {
     const uint32_t byte = mx32_scale(top);
@@ -95,17 +110,14 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float (&t)[8], uint32_t top
     *scale = byte;
     return e2m1x8(q);
   } else {
-    const uint32_t code = e4m3_of(__fdiv_rn(__fmul_rn(__uint_as_float(top), inverse), 6.0f));
-    const float S = e4m3_value(code), y = __frcp_rn(S);
+    constexpr float kSixth = 1.0f / 6.0f;
+    const float u = __fmul_rn(__uint_as_float(top), inverse), v = __fmul_rn(u, kSixth);
+    const uint32_t code = e4m3_of(__fmaf_rn(__fmaf_rn(v, 6.0f, -u), -kSixth, v));
+    const float S = e4m3_value(code), y = __fmul_rn(rcp_approx(S), inverse), d = __fmul_rn(S, s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // the IEEE quotient of u and S from the rounded reciprocal of S and one
-      // correction (P. Markstein, 1990: exact where, as here, nothing leaves the
-      // range of normal numbers; quotients that small round to 0 either way).  With
-      // these signs -0 stays -0
-      const float u = __fmul_rn(t[i], inverse);
-      const float a = __fmul_rn(u, y);
-      q[i] = __fmaf_rn(__fmaf_rn(a, S, -u), -y, a);
+      const float a = __fmul_rn(t[i], y);
+      q[i] = __fmaf_rn(__fmaf_rn(a, d, -t[i]), -y, a);
     }
     *scale = code;
     return code == 0 ? 0u : e2m1x8(q);

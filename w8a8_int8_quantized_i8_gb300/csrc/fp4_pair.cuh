@@ -9,7 +9,9 @@
 // on CTA 0's barrier.  One thread of CTA 0 copies the scales to both CTAs' tensor
 // memory and issues four M = 256, N = 256 products a stage.  Eight epilogue warps
 // a CTA drain its 128 x 256 sums into registers, hand the buffer back, scale, add
-// the bias (or gate), and store through swizzled staging by TMA.
+// the bias (or gate), and turn 32 rows by 64 columns at a time round in shared
+// memory to store four rows of 128 bytes at once (TMA stores made them wait for
+// the buffer, 32 bytes from each lane are 32 lines an instruction).
 //
 // Tensor memory: 512 columns hold two buffers of 256 only without the scales' 48
 // (NV16).  The second buffer therefore begins at column 208: while the epilogue
@@ -44,7 +46,7 @@ struct Fp4PairCfg {
   static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, THREADS = 384;
   static constexpr int REG_LO = 136, REG_HI = 176;
   static_assert(128 * REG_LO + 256 * REG_HI <= THREADS * ((65536 / THREADS) & ~7));
-  static constexpr int OFF_EPI = STAGES * STAGE;
+  static constexpr int OFF_EPI = STAGES * STAGE;  // 4 KB for each epilogue warp
   // the tile's channel scales (fp32) and biases (bf16), two tiles' worth
   static constexpr int OFF_SCL = OFF_EPI + EPI_WARPS * 4096;
   static constexpr int OFF_BIAS = OFF_SCL + 2 * 256 * 4;
@@ -70,7 +72,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
                     const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_as,
                     const __grid_constant__ CUtensorMap tm_bs0, const __grid_constant__ CUtensorMap tm_bs1,
-                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ Fp4GemmArgs p) {
+                    const __grid_constant__ Fp4GemmArgs p) {
   constexpr bool GATED = ACT != kFp4Plain;
   using Cfg = Fp4PairCfg<MX, GATED>;
   static_assert(Cfg::THREADS == 384);
@@ -120,7 +122,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     tma_prefetch_desc(&tm_as);
     tma_prefetch_desc(&tm_bs0);
     if (GATED) tma_prefetch_desc(&tm_bs1);
-    tma_prefetch_desc(&tm_y);
   }
   tc_fence_before();
   __syncthreads();
@@ -204,32 +205,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       commit_pair_elected(leader, done, 0x1);
       mbar_wait_bounded(done, 0u, 100000000ull);
     }
-  } else if (warp >= Cfg::EPI_WARP0) {
+  } else if (warp < Cfg::EPI_WARP0) {
+    regs_dec<Cfg::REG_LO>();
+  } else {
     regs_inc<Cfg::REG_HI>();
     const int ew = warp - Cfg::EPI_WARP0, quarter = warp & 3, half = ew >> 2;
     const uint32_t staging = ring + Cfg::OFF_EPI + static_cast<uint32_t>(ew) * 4096u;
     const uint32_t free0 = mapa_shared(accfree, 0);
     bool ok = true;
     int t = 0;
+    // the scales and bias of a tile that this lane fetches, a tile ahead: of its
+    // token, and of column 32 * ew + lane of the tile's 256
+    float sa, s;
+    uint16_t bb;
+    auto fetch = [&](int i) {
+      int mb, nb;
+      tile_of(min(i, tiles - 1), mb, nb);
+      const int m = mb * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane, c = ew * 32 + lane;
+      const Fp4Weight& w = GATED && c >= 128 ? p.w[1] : p.w[0];
+      const int n = GATED ? nb * 128 + (c & 127) : nb * 256 + c;
+      sa = m < p.M && p.row_scales ? p.row_scales[m] : 1.0f;
+      s = n < p.N && w.row_scales ? w.row_scales[n] : 1.0f;
+      bb = n < p.N && w.bias ? w.bias[n] : static_cast<uint16_t>(0);
+    };
+    fetch(pair);
     for (int i = pair; ok && i < tiles; i += pairs, ++t) {
       int mb, nb;
       tile_of(i, mb, nb);
       const int m_base = mb * 256 + static_cast<int>(rank) * 128 + quarter * 32;
-      // this tile's channel scales and biases, where the tile before has not its
-      // own: column 32 * ew + lane of the 256
+      // the tile's channel scales and biases, where the tile before has not its own
       const uint32_t scl = ring + Cfg::OFF_SCL + (t & 1) * 1024u, bias = ring + Cfg::OFF_BIAS + (t & 1) * 512u;
-      {
-        const int c = ew * 32 + lane;
-        const Fp4Weight& w = GATED && c >= 128 ? p.w[1] : p.w[0];
-        const int n = GATED ? nb * 128 + (c & 127) : nb * 256 + c;
-        const float s = n < p.N && w.row_scales ? w.row_scales[n] : 1.0f;
-        const uint16_t b = n < p.N && w.bias ? w.bias[n] : static_cast<uint16_t>(0);
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(scl + 4u * c), "f"(s) : "memory");
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(bias + 2u * c), "h"(b) : "memory");
-      }
-      const float sa = m_base + lane < p.M && p.row_scales ? p.row_scales[m_base + lane] : 1.0f;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(scl + 4u * (ew * 32 + lane)), "f"(s) : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(bias + 2u * (ew * 32 + lane)), "h"(bb) : "memory");
+      const float sa_now = sa;
       __syncwarp();
       if (lane == 0) mbar_arrive(chfull);
+      fetch(i + pairs);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(chfull, t & 1, abort_flag)) &&
            __all_sync(0xFFFFFFFFu, mbar_wait(accfull(t & 1), (t >> 1) & 1, abort_flag));
       if (!ok) break;
@@ -270,16 +281,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       tc_fence_before();
       const uint32_t row = staging + static_cast<uint32_t>(lane) * 128u, x = static_cast<uint32_t>(lane & 7);
 #pragma unroll
-      for (int g = 0; g < (GATED ? 1 : 2); ++g) {  // 64 columns of y: a staging buffer
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
+      for (int g = 0; g < (GATED ? 1 : 2); ++g) {  // 64 columns of y
         const int c0 = half * (GATED ? 64 : 128) + g * 64;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           float v[8], u[8];
-          fp4_dequant8(&acc[g * 64 + c * 8], sa, scl + 4 * (c0 + c * 8), bias + 2 * (c0 + c * 8), v);
+          fp4_dequant8(&acc[g * 64 + c * 8], sa_now, scl + 4u * (c0 + c * 8), bias + 2u * (c0 + c * 8), v);
           if constexpr (GATED) {
-            fp4_dequant8(&acc[64 + c * 8], sa, scl + 4 * (128 + c0 + c * 8), bias + 2 * (128 + c0 + c * 8), u);
+            fp4_dequant8(&acc[64 + c * 8], sa_now, scl + 4u * (128 + c0 + c * 8), bias + 2u * (128 + c0 + c * 8), u);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = fp4_gate<ACT>(v[k], u[k]);
           }
@@ -287,18 +296,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                  make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
                             pack_bf16x2_rn(v[6], v[7])));
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tm_y, staging, nb * Cfg::TILE_N + c0, m_base, 0);
-          bulk_commit_group();
+        // four rows of 128 bytes at a time
+        const int n = nb * Cfg::TILE_N + c0 + (lane & 7) * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = k * 4 + (lane >> 3);
+          const uint4 v = lds128(staging + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>((lane & 7) ^ (r & 7)) << 4));
+          if (m_base + r < p.M && n < p.N) *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(m_base + r) * p.ldy + n) = v;
         }
+        __syncwarp();
       }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
-  } else {
-    regs_dec<Cfg::REG_LO>();
   }
 
   __syncwarp();

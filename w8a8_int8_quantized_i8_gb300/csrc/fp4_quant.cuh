@@ -7,7 +7,7 @@
 // order in which the squares are summed.
 //
 // Bound by HBM: 2 bytes read (4 with a residual) and 0.56 written an element (and
-// 2 of h).  A row a CTA of G warps; a lane holds V vectors of 8 elements, 256
+// 2 of h).  A row is G warps, a CTA R rows (several where they are short); a lane holds V vectors of 8 elements, 256
 // elements apart, so every element is read once.  A block is two (NV16) or four
 // (MX32) neighbouring lanes: its largest magnitude takes one or two exchanges.
 // Rows that the registers cannot hold (V = 0) are read twice, the second time
@@ -23,45 +23,92 @@
 
 namespace i8 {
 
+// Lane-wise larger magnitude of bf16 pairs; a NaN wins; the signs are to be masked
+// off.
+__device__ __forceinline__ uint32_t absmax_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 struct Fp4QuantArgs {
   const uint16_t *x, *res, *weight;
   uint16_t* h;
   uint8_t *codes, *scales;
   float* row_scales;
   int64_t ldx, ldr, ldh;
-  int K, deep, G;  // deep: tiles of 256 elements to a row
+  int64_t rows;
+  int K, deep, G, R;  // deep: tiles of 256 elements to a row
   float eps;
 };
 
-// Elements e .. e + 7 of the row: t, and with the norm h and its squares' sums (as
+// Eight elements of a row that a lane holds: without the norm as they are, with it
+// t (fp32) and h.
+template <bool NORM>
+struct Fp4Held {
+  uint4 x;
+  __device__ __forceinline__ void widen(float (&t)[8]) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[2 * j] = bf16_lo(w[j]), t[2 * j + 1] = bf16_hi(w[j]);
+  }
+  // bits of the largest magnitude, which order like the values; a NaN wins
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = absmax_nan_bf16x2(absmax_nan_bf16x2(x.x, x.y), absmax_nan_bf16x2(x.z, x.w)) & 0x7FFF7FFFu;
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+};
+template <>
+struct Fp4Held<true> {
+  float t[8];
+  uint32_t h[4];
+  __device__ __forceinline__ void widen(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = t[j];
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(fabsf(t[j])));
+    return m;
+  }
+};
+
+// Elements e .. e + 7 of the row, and with the norm the sums of h's squares (as
 // they are, and of h * 2^-80 and h * 2^80 for rows whose squares leave fp32's
 // range).  Ordinary loads, of pointers that promise nothing: h may lie where x or
 // the residual does, and a kernel that this one overlaps may have written them.
 template <bool NORM>
-__device__ __forceinline__ void fp4_load8(const Fp4QuantArgs& a, int64_t row, int e, float (&t)[8], uint32_t (&o)[4],
-                                          float (&ss)[3]) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u), u = v, g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  if (e < a.K) {
-    v = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + e);
-    if (NORM && a.res) u = *reinterpret_cast<const uint4*>(a.res + row * a.ldr + e);
-    if (NORM && a.weight) g = *reinterpret_cast<const uint4*>(a.weight + e);
-  }
-  const uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4] = {u.x, u.y, u.z, u.w}, w[4] = {g.x, g.y, g.z, g.w};
+__device__ __forceinline__ void fp4_load8(const Fp4QuantArgs& a, int64_t row, int e, Fp4Held<NORM>& held, float (&ss)[3]) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (e < a.K) v = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + e);
+  if constexpr (!NORM) {
+    held.x = v;
+  } else {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u), g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (e < a.K) {
+      if (a.res) u = *reinterpret_cast<const uint4*>(a.res + row * a.ldr + e);
+      if (a.weight) g = *reinterpret_cast<const uint4*>(a.weight + e);
+    }
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4] = {u.x, u.y, u.z, u.w}, w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    t[2 * j] = bf16_lo(x[j]);
-    t[2 * j + 1] = bf16_hi(x[j]);
-    if constexpr (NORM) {
-      const float h0 = __fadd_rn(t[2 * j], bf16_lo(r[j])), h1 = __fadd_rn(t[2 * j + 1], bf16_hi(r[j]));
+    for (int j = 0; j < 4; ++j) {
+      const float h0 = __fadd_rn(bf16_lo(x[j]), bf16_lo(r[j])), h1 = __fadd_rn(bf16_hi(x[j]), bf16_hi(r[j]));
       const float s0 = h0 * 0x1p-80f, s1 = h1 * 0x1p-80f, l0 = h0 * 0x1p80f, l1 = h1 * 0x1p80f;
       ss[0] = fmaf(h0, h0, fmaf(h1, h1, ss[0]));
       ss[1] = fmaf(s0, s0, fmaf(s1, s1, ss[1]));
       ss[2] = fmaf(l0, l0, fmaf(l1, l1, ss[2]));
-      t[2 * j] = __fmul_rn(h0, bf16_lo(w[j]));
-      t[2 * j + 1] = __fmul_rn(h1, bf16_hi(w[j]));
-      o[j] = pack_bf16x2_rn(h0, h1);
+      held.t[2 * j] = __fmul_rn(h0, bf16_lo(w[j]));
+      held.t[2 * j + 1] = __fmul_rn(h1, bf16_hi(w[j]));
+      held.h[j] = pack_bf16x2_rn(h0, h1);
     }
   }
+}
+template <bool NORM>
+__device__ __forceinline__ void fp4_store_h(const Fp4QuantArgs& a, int64_t row, int e, const Fp4Held<NORM>& held) {
+  if constexpr (NORM)
+    if (a.h && e < a.K)
+      *reinterpret_cast<uint4*>(a.h + row * a.ldh + e) = make_uint4(held.h[0], held.h[1], held.h[2], held.h[3]);
 }
 
 // 1 / sqrt(mean(h^2) + eps) from the three sums.
@@ -77,26 +124,34 @@ __device__ __forceinline__ float fp4_rstd(const float (&ss)[3], int K, float eps
 }
 
 // The codes and scales of the warp's 256 elements from `first` on, of which this
-// lane holds 8 (the whole warp calls).
-template <bool MX>
-__device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, int64_t row, int first, int lane,
-                                             const float (&t)[8], float inverse) {
-  uint32_t top = 0;  // bit patterns of magnitudes order like them; a NaN wins
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(t[i])));
+// lane holds 8 with the largest magnitude `top` (the whole warp calls).  codes and
+// scales: the row's, the latter where its tiles' first part has it.
+template <bool MX, bool NORM>
+__device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, uint8_t* codes, uint8_t* scales, int first, int lane,
+                                             const Fp4Held<NORM>& held, uint32_t top, float s, float inverse) {
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   if constexpr (MX) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  uint32_t s;
-  const uint32_t c = fp4_codes8<MX>(t, top, inverse, &s);
+  float t[8];
+  held.widen(t);
+  if constexpr (!MX) {
+    if (s == 0.0f) {  // not for the fast quotients: times a power of two before
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = __fmul_rn(t[i], inverse);
+      top = __float_as_uint(__fmul_rn(__uint_as_float(top), inverse));
+      s = inverse = 1.0f;
+    }
+  }
+  uint32_t scale;
+  const uint32_t c = fp4_codes8<MX>(t, top, s, inverse, &scale);
   const int e = first + lane * 8;
-  if (e < a.K) *reinterpret_cast<uint32_t*>(a.codes + row * (a.K / 2) + e / 2) = c;
-  // the scales of four blocks make a word
+  if (e < a.K) *reinterpret_cast<uint32_t*>(codes + e / 2) = c;
+  // the scales of four blocks make a word; those past K are 0
   constexpr int LB = MX ? 4 : 2;  // lanes of a block
-  s = e < a.K ? s << (8 * (lane / LB % 4)) : 0u;
-  s |= __shfl_xor_sync(0xFFFFFFFFu, s, LB);
-  s |= __shfl_xor_sync(0xFFFFFFFFu, s, 2 * LB);
-  if (lane % (4 * LB) == 0 && e < a.deep * kFp4TileK)
-    *reinterpret_cast<uint32_t*>(a.scales + fp4_scale_at(row, e / (8 * LB), a.deep, 8 * LB)) = s;
+  scale = e < a.K ? scale << (8 * (lane / LB % 4)) : 0u;
+  scale |= __shfl_xor_sync(0xFFFFFFFFu, scale, LB);
+  scale |= __shfl_xor_sync(0xFFFFFFFFu, scale, 2 * LB);
+  if (lane % (4 * LB) == 0)
+    *reinterpret_cast<uint32_t*>(scales + (first >> 8) * fp4_tile_bytes(8 * LB) + lane / (4 * LB) * 512) = scale;
 }
 
 template <int V, bool MX, bool NORM>
@@ -104,49 +159,37 @@ __global__ void __launch_bounds__(V == 0 ? 512 : 1024) fp4_quant_kernel(const Fp
   __shared__ float red_s[3][32];
   __shared__ uint32_t red_m[32];
   constexpr int H = V > 0 ? V : 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
+  // (block: lanes, a row's warps, rows)
+  const int lane = threadIdx.x, warp = threadIdx.y, local = threadIdx.z;
+  // (a row behind the last one is the last one, read but not written)
+  const bool mine = static_cast<int64_t>(blockIdx.x) * a.R + local < a.rows;
+  const int64_t row = min(static_cast<int64_t>(blockIdx.x) * a.R + local, a.rows - 1);
   const int span = H * 256;  // a warp's elements, and in a long row its next ones
   const int step = a.G * span, end = a.deep * kFp4TileK;
 
   pdl_wait();  // the rows may be the previous kernel's output
-  float t[H][8];
-  uint32_t o[4];
+  Fp4Held<NORM> held[H];
+  uint32_t top[H];
   float ss[3] = {0.0f, 0.0f, 0.0f};
   uint32_t amax = 0;
   if constexpr (V > 0) {
-    uint32_t hold[NORM ? H : 1][4];
+#pragma unroll
+    for (int i = 0; i < H; ++i) fp4_load8<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i], ss);
+    pdl_trigger();
+    // (each thread has read the elements that it writes)
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      const int e = warp * span + i * 256 + lane * 8;
-      fp4_load8<NORM>(a, row, e, t[i], o, ss);
-      if constexpr (NORM) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hold[i][j] = o[j];
-      }
+      if (mine) fp4_store_h<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
+      top[i] = held[i].top();
+      amax = max(amax, top[i]);
     }
-    pdl_trigger();
-    // each thread has read the elements that it writes
-    if constexpr (NORM) {
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const int e = warp * span + i * 256 + lane * 8;
-        if (a.h && e < a.K)
-          *reinterpret_cast<uint4*>(a.h + row * a.ldh + e) = make_uint4(hold[i][0], hold[i][1], hold[i][2], hold[i][3]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < H; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(fabsf(t[i][j])));
   } else {
     for (int first = warp * span; first < end; first += step) {
-      fp4_load8<NORM>(a, row, first + lane * 8, t[0], o, ss);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(fabsf(t[0][j])));
+      fp4_load8<NORM>(a, row, first + lane * 8, held[0], ss);
+      amax = max(amax, held[0].top());
     }
   }
-  float inverse = 1.0f;
+  float s = 1.0f, inverse = 1.0f;
   if (!MX || NORM) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     if constexpr (NORM) {
@@ -157,45 +200,45 @@ __global__ void __launch_bounds__(V == 0 ? 512 : 1024) fp4_quant_kernel(const Fp
     }
     if (a.G > 1) {
       if (lane == 0) {
-        red_m[warp] = amax;
+        red_m[local * a.G + warp] = amax;
         if constexpr (NORM) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) red_s[k][warp] = ss[k];
+          for (int k = 0; k < 3; ++k) red_s[k][local * a.G + warp] = ss[k];
         }
       }
       __syncthreads();
       amax = 0;
       ss[0] = ss[1] = ss[2] = 0.0f;
       for (int j = 0; j < a.G; ++j) {
-        amax = max(amax, red_m[j]);
+        amax = max(amax, red_m[local * a.G + j]);
         if constexpr (NORM) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) ss[k] += red_s[k][j];
+          for (int k = 0; k < 3; ++k) ss[k] += red_s[k][local * a.G + j];
         }
       }
     }
     const int k = nv16_row_exponent(amax);
-    if constexpr (!MX) inverse = pow2f(-k);
-    if (threadIdx.x == 0) {
-      float s = MX ? 1.0f : amax == 0 ? 0.0f : pow2f(min(k, 127));
-      if (NORM && amax != 0) s = __fmul_rn(s, fp4_rstd(ss, a.K, a.eps));
-      if (!MX && amax >= 0x7F800000u) s = __uint_as_float(0x7FC00000u);  // infinity or NaN in the row
-      a.row_scales[row] = s;
+    if (!MX) inverse = pow2f(-k), s = abs(k) <= 100 ? pow2f(k) : 0.0f;
+    if (mine && warp == 0 && lane == 0) {
+      float scale = MX ? 1.0f : amax == 0 ? 0.0f : pow2f(k);
+      if (NORM && amax != 0) scale = __fmul_rn(scale, fp4_rstd(ss, a.K, a.eps));
+      if (!MX && amax >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);  // infinity or NaN in the row
+      a.row_scales[row] = scale;
     }
   }
+  uint8_t* codes = a.codes + row * (a.K / 2);
+  uint8_t* scales = a.scales + fp4_scale_at(row, 0, a.deep, MX ? 32 : 16);
   if constexpr (V > 0) {
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       const int first = warp * span + i * 256;
-      if (first < end) fp4_store256<MX>(a, row, first, lane, t[i], inverse);
+      if (mine && first < end) fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[i], top[i], s, inverse);
     }
   } else {
     for (int first = warp * span; first < end; first += step) {
-      fp4_load8<NORM>(a, row, first + lane * 8, t[0], o, ss);
-      const int e = first + lane * 8;
-      if (NORM && a.h && e < a.K)
-        *reinterpret_cast<uint4*>(a.h + row * a.ldh + e) = make_uint4(o[0], o[1], o[2], o[3]);
-      fp4_store256<MX>(a, row, first, lane, t[0], inverse);
+      fp4_load8<NORM>(a, row, first + lane * 8, held[0], ss);
+      fp4_store_h<NORM>(a, row, first + lane * 8, held[0]);
+      fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[0], held[0].top(), s, inverse);
     }
     pdl_trigger();
   }
