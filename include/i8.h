@@ -473,6 +473,18 @@ i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, 
                                  const void* gate_bias_bf16, const void* up_bias_bf16, int activation, void* y,
                                  int64_t ldy, i8_stream_t stream);
 
+/* The whole layer: quantizes x [M, K] bf16 (row stride ldx, % 8 == 0) in the weights'
+ * format into the workspace, then the product, or the gated one.  y may be x (the
+ * product reads the workspace).
+ *   ws / ws_bytes: 16-byte aligned, at least i8_linear_fp4_workspace_bytes(M, K,
+ *   fmt); calls that may overlap in time do not share one                    */
+size_t i8_linear_fp4_workspace_bytes(int64_t M, int64_t K, int fmt);
+i8_status i8_linear_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const i8_fp4_rows* w,
+                        const void* bias_bf16, void* y, int64_t ldy, void* ws, size_t ws_bytes, i8_stream_t stream);
+i8_status i8_gated_linear_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const i8_fp4_rows* gate,
+                              const i8_fp4_rows* up, const void* gate_bias_bf16, const void* up_bias_bf16,
+                              int activation, void* y, int64_t ldy, void* ws, size_t ws_bytes, i8_stream_t stream);
+
 /* i8_gemm_dequant_bias_bf16 for callers that cannot allocate device memory
  * at call time -- for example a plugin running inside another runtime that
  * offers no workspace hook, an application whose device memory is all owned

@@ -24,13 +24,13 @@ from .serving import (BlockPlan, QuantKVCache, add_rmsnorm_quant_act_pertoken, b
                       heads_rmsnorm_rotate, kv_cache_append, paged_attention,
                       paged_attention_workspace_bytes)
 from .fp4 import (FP4Rows, add_rmsnorm_quant_fp4, gated_linear_fp4, gemm_fp4_bias_bf16,
-                  gemm_fp4_gated_bf16, linear_fp4, quant_rows_fp4)
+                  gemm_fp4_gated_bf16, linear_fp4, linear_fp4_workspace_bytes, quant_rows_fp4)
 
 __all__ = [
     "BlockPlan", "QuantKVCache", "add_rmsnorm_quant_act_pertoken", "build_block_tables",
     "kv_cache_append", "paged_attention", "paged_attention_workspace_bytes", "heads_rmsnorm_rotate",
     "FP4Rows", "add_rmsnorm_quant_fp4", "gated_linear_fp4", "gemm_fp4_bias_bf16", "gemm_fp4_gated_bf16",
-    "linear_fp4", "quant_rows_fp4",
+    "linear_fp4", "linear_fp4_workspace_bytes", "quant_rows_fp4",
     "I8Error", "e4m3_workspace_bytes", "f16codes_workspace_bytes", "gelu_quant_act_pertoken",
     "gemm_dequant_bias_bf16_f16codes", "gemm_int32_f16codes", "get_option", "linear_f16codes",
     "quant_act_pertoken_f16codes", "gemm_dequant_bias_bf16", "gemm_e4m3_dequant_bias_bf16",

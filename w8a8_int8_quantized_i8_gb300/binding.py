@@ -137,6 +137,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                           vp, vp, vp, vp, i64, vp], st),
             "i8_gemm_fp4_bias_bf16": ([rows4, rows4, vp, vp, i64, vp], st),
             "i8_gemm_fp4_gated_bf16": ([rows4, rows4, rows4, vp, vp, ctypes.c_int, vp, i64, vp], st),
+            "i8_linear_fp4_workspace_bytes": ([i64, i64, ctypes.c_int], sz),
+            "i8_linear_fp4": ([vp, i64, i64, i64, rows4, vp, vp, i64, vp, sz, vp], st),
+            "i8_gated_linear_fp4": ([vp, i64, i64, i64, rows4, rows4, vp, vp, ctypes.c_int, vp, i64, vp, sz,
+                                     vp], st),
             "i8_sync_check": ([vp], st),
             "i8_selftest_timeout": ([ctypes.c_int, vp], st),
             "i8_plan_query": ([i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,

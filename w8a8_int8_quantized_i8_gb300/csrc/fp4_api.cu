@@ -299,8 +299,12 @@ i8_status launch_format(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
                               : launch_product<false, ACT>(p, t, w, dev, sms, st);
 }
 
-i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows* w1, const void* b0, const void* b1,
-                  int activation, void* y, int64_t ldy, cudaStream_t st) {
+int64_t scale_bytes(const i8_fp4_rows* r) {
+  return static_cast<int64_t>(i8_fp4_block_scale_bytes(r->rows, r->K, r->fmt));
+}
+
+i8_status check_product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows* w1, const void* b0,
+                        const void* b1, const void* y, int64_t ldy) {
   if (i8_status e = check_rows(a)) return e;
   if (i8_status e = check_rows(w0)) return e;
   if (w1) {
@@ -311,19 +315,19 @@ i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows
   if (ldy < w0->rows || (a->rows > 0 && w0->rows > 0 && !y)) return I8_ERR_INVALID_ARG;
   if (!aligned16(y) || ldy % 8 != 0 || !aligned16(b0) || !aligned16(b1)) return I8_ERR_ALIGNMENT;
   if (w0->rows % 8 != 0 || (a->rows + 127) / 128 > 65535 || w0->rows > INT32_MAX - 256) return I8_ERR_UNSUPPORTED;
-  if (a->rows == 0 || w0->rows == 0) return I8_OK;
   // other CTAs read the tokens and the weights while one writes its rows of y
   const Extent out{y, w0->rows * 2, a->rows, ldy * 2};
-  auto scale_bytes = [](const i8_fp4_rows* r) {
-    return static_cast<int64_t>(i8_fp4_block_scale_bytes(r->rows, r->K, r->fmt));
-  };
-  for (const i8_fp4_rows* r : {a, w0, w1}) {
-    if (!r) continue;
-    if (overlap(out, {r->codes, r->rows * (r->K / 2)}) || overlap(out, {r->block_scales, scale_bytes(r)}) ||
-        overlap(out, {r->row_scales, r->rows * 4}))
+  for (const i8_fp4_rows* r : {a, w0, w1})
+    if (r && (overlap(out, {r->codes, r->rows * (r->K / 2)}) || overlap(out, {r->block_scales, scale_bytes(r)}) ||
+              overlap(out, {r->row_scales, r->rows * 4})))
       return I8_ERR_INVALID_ARG;
-  }
-  if (overlap(out, {b0, w0->rows * 2}) || overlap(out, {b1, w0->rows * 2})) return I8_ERR_INVALID_ARG;
+  return overlap(out, {b0, w0->rows * 2}) || overlap(out, {b1, w0->rows * 2}) ? I8_ERR_INVALID_ARG : I8_OK;
+}
+
+i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows* w1, const void* b0, const void* b1,
+                  int activation, void* y, int64_t ldy, cudaStream_t st) {
+  if (i8_status e = check_product(a, w0, w1, b0, b1, y, ldy)) return e;
+  if (a->rows == 0 || w0->rows == 0) return I8_OK;
   Fp4GemmArgs p{};
   p.w[0] = {static_cast<const uint8_t*>(w0->block_scales), w0->row_scales, static_cast<const uint16_t*>(b0)};
   if (w1) p.w[1] = {static_cast<const uint8_t*>(w1->block_scales), w1->row_scales, static_cast<const uint16_t*>(b1)};
@@ -342,6 +346,42 @@ i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows
   if (!w1) return launch_format<kFp4Plain>(p, *a, w, dev, sms, st);
   return activation == I8_GATE_SILU ? launch_format<kFp4Silu>(p, *a, w, dev, sms, st)
                                     : launch_format<kFp4Gelu>(p, *a, w, dev, sms, st);
+}
+
+// The tokens' rows in a workspace: codes, block scales, row scales.
+struct TokenRows {
+  i8_fp4_rows rows;
+  size_t bytes;
+  TokenRows(void* ws, int64_t M, int64_t K, int fmt) {
+    const size_t codes = static_cast<size_t>(M) * (K / 2), scales = i8_fp4_block_scale_bytes(M, K, fmt);
+    char* at = static_cast<char*>(ws);
+    rows = {at, at + codes, fmt == I8_FP4_NV16 ? reinterpret_cast<float*>(at + codes + scales) : nullptr, M, K, fmt};
+    bytes = codes + scales + (fmt == I8_FP4_NV16 ? static_cast<size_t>(M) * 4 : 0);
+  }
+};
+
+i8_status linear(const void* x, int64_t M, int64_t K, int64_t ldx, const i8_fp4_rows* w0, const i8_fp4_rows* w1,
+                 const void* b0, const void* b1, int activation, void* y, int64_t ldy, void* ws, size_t ws_bytes,
+                 i8_stream_t stream) {
+  if (i8_status e = check_rows(w0)) return e;
+  if (K != w0->K) return I8_ERR_INVALID_ARG;
+  if (i8_status e = fp4_sizes(M, K, w0->fmt)) return e;
+  const TokenRows t(ws, M, K, w0->fmt);
+  if (t.bytes > 0 && (!ws || ws_bytes < t.bytes)) return I8_ERR_WORKSPACE;
+  if (!aligned16(ws)) return I8_ERR_ALIGNMENT;
+  // what the product would refuse is refused before the tokens are written
+  if (i8_status e = check_product(&t.rows, w0, w1, b0, b1, y, ldy)) return e;
+  for (const i8_fp4_rows* r : {w0, w1})
+    if (r && (overlap({ws, static_cast<int64_t>(t.bytes)}, {r->codes, r->rows * (r->K / 2)}) ||
+              overlap({ws, static_cast<int64_t>(t.bytes)}, {r->block_scales, scale_bytes(r)}) ||
+              overlap({ws, static_cast<int64_t>(t.bytes)}, {r->row_scales, r->rows * 4})))
+      return I8_ERR_INVALID_ARG;
+  for (const void* b : {b0, b1})
+    if (overlap({ws, static_cast<int64_t>(t.bytes)}, {b, w0->rows * 2})) return I8_ERR_INVALID_ARG;
+  if (i8_status e = i8_quant_rows_fp4(x, M, K, ldx, w0->fmt, const_cast<void*>(t.rows.codes),
+                                      const_cast<void*>(t.rows.block_scales), const_cast<float*>(t.rows.row_scales), stream))
+    return e;
+  return product(&t.rows, w0, w1, b0, b1, activation, y, ldy, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ----------------------------------------------------------------- heads
@@ -464,6 +504,25 @@ i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, 
   return product(a, gate, up, gate_bias, up_bias, activation, y, ldy, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t i8_linear_fp4_workspace_bytes(int64_t M, int64_t K, int fmt) {
+  I8_NVTX();
+  return fp4_sizes(M, K, fmt) == I8_OK ? TokenRows(nullptr, M, K, fmt).bytes : 0;
+}
+
+i8_status i8_linear_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, const i8_fp4_rows* w, const void* bias, void* y,
+                        int64_t ldy, void* ws, size_t ws_bytes, i8_stream_t stream) {
+  I8_NVTX();
+  return linear(x, M, K, ldx, w, nullptr, bias, nullptr, 0, y, ldy, ws, ws_bytes, stream);
+}
+
+i8_status i8_gated_linear_fp4(const void* x, int64_t M, int64_t K, int64_t ldx, const i8_fp4_rows* gate,
+                              const i8_fp4_rows* up, const void* gate_bias, const void* up_bias, int activation, void* y,
+                              int64_t ldy, void* ws, size_t ws_bytes, i8_stream_t stream) {
+  I8_NVTX();
+  if (!up || (activation != I8_GATE_SILU && activation != I8_GATE_GELU)) return I8_ERR_INVALID_ARG;
+  return linear(x, M, K, ldx, gate, up, gate_bias, up_bias, activation, y, ldy, ws, ws_bytes, stream);
+}
+
 i8_status i8_heads_rmsnorm_rotate(const void* q, int64_t ldq_token, int64_t ldq_head, int64_t q_heads, const void* k,
                                   int64_t ldk_token, int64_t ldk_head, int64_t kv_heads, int64_t tokens,
                                   int64_t head_dim, const void* q_weight, const void* k_weight, float eps,
@@ -503,8 +562,8 @@ i8_status i8_heads_rmsnorm_rotate(const void* q, int64_t ldq_token, int64_t ldq_
     return a.base == b.base && (a.tokens <= 1 || a.token == b.token) && (a.heads <= 1 || a.head == b.head);
   };
   // in place, or apart from everything that another CTA may still read
-  if (rows_overlap(tokens, ldqo_token, q_heads, ldqo_head, head_dim) ||
-      rows_overlap(tokens, ldko_token, kv_heads, ldko_head, head_dim) || heads_meet(qo, ko) || heads_meet(qo, ki) ||
+  if ((q_heads > 0 && rows_overlap(tokens, ldqo_token, q_heads, ldqo_head, head_dim)) ||
+      (kv_heads > 0 && rows_overlap(tokens, ldko_token, kv_heads, ldko_head, head_dim)) || heads_meet(qo, ko) || heads_meet(qo, ki) ||
       heads_meet(ko, qi) || (heads_meet(qo, qi) && !same(qo, qi)) || (heads_meet(ko, ki) && !same(ko, ki)))
     return I8_ERR_INVALID_ARG;
   for (const HeadRows& r : {qo, ko})
@@ -529,19 +588,22 @@ i8_status i8_heads_rmsnorm_rotate(const void* q, int64_t ldq_token, int64_t ldq_
   p.rotary = static_cast<int>(rotary_dim);
   p.interleaved = interleaved != 0;
   p.eps = eps;
+  p.inv_dim = 1.0f / static_cast<float>(head_dim);
   int end = 0;
   for (int a = 0; a < kRotateMaxAxes; ++a) {
     if (a < axes) end += sections[a];
     p.section_end[a] = a < axes - 1 ? end : INT32_MAX;
   }
   while ((16 << p.lanes_log2) < head_dim) ++p.lanes_log2;
+  p.step_tokens = (kRotateThreads >> p.lanes_log2) / p.heads;
+  p.step_heads = (kRotateThreads >> p.lanes_log2) % p.heads;
   int dev, sms;
   if (i8_status e = current_device(&dev)) return e;
   if (i8_status e = device_sms(dev, &sms)) return e;
   // tokens a CTA: a few rounds of its threads, but a CTA for every SM first
   const int64_t lanes = static_cast<int64_t>(p.heads) << p.lanes_log2;
   p.per_cta = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>({4 * kRotateThreads / lanes, tokens / (4 * static_cast<int64_t>(sms)), 8})));
+      1, std::min<int64_t>({16 * kRotateThreads / lanes, tokens / (4 * static_cast<int64_t>(sms)), 8})));
   const size_t smem = static_cast<size_t>(p.per_cta) * (p.rotary / 2) * sizeof(float2);
   return cuda_status(launch_pdl(heads_rmsnorm_rotate_kernel, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta)),
                                 dim3(kRotateThreads), smem, reinterpret_cast<cudaStream_t>(stream), p));

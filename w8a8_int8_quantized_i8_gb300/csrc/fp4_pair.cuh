@@ -58,13 +58,26 @@ struct Fp4PairCfg {
   static_assert(SMEM <= 232448 - 512, "shared memory, with the barriers");
 };
 
-// Eight sums of a row times their scales, plus the biases (shared memory).
-__device__ __forceinline__ void fp4_dequant8(const uint32_t* acc, float sa, uint32_t scl, uint32_t bias, float (&v)[8]) {
-  const uint4 s0 = lds128(scl), s1 = lds128(scl + 16), bb = lds128(bias);
-  const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w}, b[4] = {bb.x, bb.y, bb.z, bb.w};
+// Eight sums of a row of scale sa (twice) times their channels' scales, plus the
+// biases where there are some (shared memory); in pairs.  (With the next eight's
+// scales on their way it took longer: the registers are full.)
+__device__ __forceinline__ void fp4_dequant8(const uint32_t* acc, unsigned long long sa, uint32_t scl, uint32_t bias,
+                                             bool biased, float (&v)[8]) {
+  const uint4 s0 = lds128(scl), s1 = lds128(scl + 16);
+  const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+  unsigned long long r[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    v[k] = fp4_dequant(__uint_as_float(acc[k]), sa, __uint_as_float(s[k]), k & 1 ? bf16_hi(b[k / 2]) : bf16_lo(b[k / 2]));
+  for (int k = 0; k < 4; ++k)
+    r[k] = f2_mul(f2_mul(f2(__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])), sa),
+                  f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])));
+  if (biased) {
+    const uint4 bb = lds128(bias);
+    const uint32_t b[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = f2_add(r[k], f2(bf16_lo(b[k]), bf16_hi(b[k])));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f2_split(r[k], v[2 * k], v[2 * k + 1]);
 }
 
 template <bool MX, int ACT>
@@ -237,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const uint32_t scl = ring + Cfg::OFF_SCL + (t & 1) * 1024u, bias = ring + Cfg::OFF_BIAS + (t & 1) * 512u;
       asm volatile("st.shared.f32 [%0], %1;" ::"r"(scl + 4u * (ew * 32 + lane)), "f"(s) : "memory");
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(bias + 2u * (ew * 32 + lane)), "h"(bb) : "memory");
-      const float sa_now = sa;
+      const unsigned long long sa_now = f2(sa, sa);
       __syncwarp();
       if (lane == 0) mbar_arrive(chfull);
       fetch(i + pairs);
@@ -286,9 +299,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           float v[8], u[8];
-          fp4_dequant8(&acc[g * 64 + c * 8], sa_now, scl + 4u * (c0 + c * 8), bias + 2u * (c0 + c * 8), v);
+          fp4_dequant8(&acc[g * 64 + c * 8], sa_now, scl + 4u * (c0 + c * 8), bias + 2u * (c0 + c * 8),
+                       p.w[0].bias != nullptr, v);
           if constexpr (GATED) {
-            fp4_dequant8(&acc[64 + c * 8], sa_now, scl + 4u * (128 + c0 + c * 8), bias + 2u * (128 + c0 + c * 8), u);
+            fp4_dequant8(&acc[64 + c * 8], sa_now, scl + 4u * (128 + c0 + c * 8), bias + 2u * (128 + c0 + c * 8),
+                         p.w[1].bias != nullptr, u);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = fp4_gate<ACT>(v[k], u[k]);
           }

@@ -48,8 +48,9 @@ struct RotateArgs {
   int dim, rotary, interleaved;
   int per_cta;                 // tokens
   int lanes_log2;              // lanes of a row
+  int step_tokens, step_heads; // from a thread's row to its next
   int section_end[kRotateMaxAxes];
-  float eps;
+  float eps, inv_dim;
 };
 
 // position * f in turns, without whole ones.
@@ -70,35 +71,17 @@ __device__ __forceinline__ float rotate_turns(int32_t position, float f) {
 struct RotateItem {
   uint4 a, b;
   const RotateHeads* h;
-  int64_t token, head;
-  int local, at_a, at_b;  // local: the CTA's token; at_b = dim where there is no second vector
-  bool valid;
+  int local, head;  // the CTA's token, the head among those of q and k
 };
 
-__device__ __forceinline__ RotateItem rotate_load(const RotateArgs& p, int item, int count, int64_t first) {
-  RotateItem t;
-  const int lane = item & ((1 << p.lanes_log2) - 1), row = item >> p.lanes_log2;
-  t.local = row / p.heads;
-  const int head = row - t.local * p.heads;
-  const int turning = p.rotary >> 4;  // lanes that rotate
-  if (lane >= turning || p.interleaved) {
-    t.at_a = lane * 16;
-    t.at_b = t.at_a + 8;
-  } else {
-    t.at_a = lane * 8;
-    t.at_b = t.at_a + p.rotary / 2;
-  }
-  t.valid = t.local < count && t.at_a < p.dim;
-  t.token = first + t.local;
-  t.h = head < p.q_heads ? &p.q : &p.k;
-  t.head = head < p.q_heads ? head : head - p.q_heads;
+__device__ __forceinline__ void rotate_load(const RotateArgs& p, RotateItem& t, bool valid, int64_t first, int at_a, int at_b) {
+  t.h = t.head < p.q_heads ? &p.q : &p.k;
   t.a = t.b = make_uint4(0u, 0u, 0u, 0u);
-  if (t.valid) {
-    const uint16_t* x = t.h->in + t.token * t.h->in_token + t.head * t.h->in_head;
-    t.a = *reinterpret_cast<const uint4*>(x + t.at_a);
-    if (t.at_b < p.dim) t.b = *reinterpret_cast<const uint4*>(x + t.at_b);
+  if (valid) {
+    const uint16_t* x = t.h->in + (first + t.local) * t.h->in_token + (t.head < p.q_heads ? t.head : t.head - p.q_heads) * t.h->in_head;
+    t.a = *reinterpret_cast<const uint4*>(x + at_a);
+    if (at_b < p.dim) t.b = *reinterpret_cast<const uint4*>(x + at_b);
   }
-  return t;
 }
 
 __device__ __forceinline__ void rotate_widen(const uint4& v, float (&x)[8]) {
@@ -110,13 +93,41 @@ __device__ __forceinline__ void rotate_widen(const uint4& v, float (&x)[8]) {
   }
 }
 
-__global__ void __launch_bounds__(kRotateThreads) heads_rmsnorm_rotate_kernel(const __grid_constant__ RotateArgs p) {
-  extern __shared__ float2 turn[];  // (cos, sin) [tokens of the CTA][rotary / 2]
+// The norm's factor where some row of the warp has squares out of fp32's range: from
+// the sums of others as well (the whole warp calls).
+__device__ __forceinline__ float rotate_far_rstd(const RotateArgs& p, const float (&a)[8], const float (&b)[8], float sum) {
+  float ss[3] = {sum, 0.0f, 0.0f};
+  for (int j = 0; j < 8; ++j) {
+    const float s0 = a[j] * 0x1p-80f, s1 = b[j] * 0x1p-80f, l0 = a[j] * 0x1p80f, l1 = b[j] * 0x1p80f;
+    ss[1] = fmaf(s0, s0, fmaf(s1, s1, ss[1]));
+    ss[2] = fmaf(l0, l0, fmaf(l1, l1, ss[2]));
+  }
+  for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) {
+    ss[1] += __shfl_xor_sync(0xFFFFFFFFu, ss[1], d);
+    ss[2] += __shfl_xor_sync(0xFFFFFFFFu, ss[2], d);
+  }
+  return fp4_rstd(ss, p.dim, p.eps);
+}
+
+__global__ void __launch_bounds__(kRotateThreads, 5) heads_rmsnorm_rotate_kernel(const __grid_constant__ RotateArgs p) {
+  extern __shared__ __align__(16) float2 turn[];  // (cos, sin) [tokens of the CTA][rotary / 2]
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int count = static_cast<int>(min(static_cast<int64_t>(p.per_cta), p.tokens - first));
-  const int half = p.rotary / 2, items = (count * p.heads) << p.lanes_log2;
+  const int half = p.rotary / 2, rows = count * p.heads;
+  const int lane = threadIdx.x & ((1 << p.lanes_log2) - 1), stride = kRotateThreads >> p.lanes_log2;
+  // this lane's elements of every row it works on: pairs 8 lane .. 8 lane + 7, or,
+  // behind the rotated part, two vectors that lie side by side
+  const bool turns = lane < (p.rotary >> 4);
+  const bool split = turns && !p.interleaved;
+  const int at_a = split ? lane * 8 : lane * 16, at_b = split ? at_a + half : at_a + 8;
+  const bool inside = at_a < p.dim;
+
   pdl_wait();
-  RotateItem t = rotate_load(p, threadIdx.x, count, first);
+  int row = threadIdx.x >> p.lanes_log2;
+  RotateItem t;
+  t.local = row / p.heads;
+  t.head = row - t.local * p.heads;
+  rotate_load(p, t, inside && row < rows, first, at_a, at_b);
   for (int i = threadIdx.x; i < count * half; i += kRotateThreads) {
     const int local = i / half, pair = i - local * half;
     int axis = 0;
@@ -128,73 +139,65 @@ __global__ void __launch_bounds__(kRotateThreads) heads_rmsnorm_rotate_kernel(co
   }
   pdl_trigger();
   __syncthreads();
-  for (int item = threadIdx.x; item - static_cast<int>(threadIdx.x) < items; item += kRotateThreads) {
+  for (int base = 0; base < rows; base += stride, row += stride) {  // the same rounds for whole warps
     float a[8], b[8];
     rotate_widen(t.a, a);
     rotate_widen(t.b, b);
-    const RotateItem now = t;
-    if (item - static_cast<int>(threadIdx.x) + kRotateThreads < items) t = rotate_load(p, item + kRotateThreads, count, first);
+    const bool valid = inside && row < rows;
+    const RotateHeads* const h = t.h;
+    const int local = t.local, head = t.head;
+    t.local += p.step_tokens;
+    t.head += p.step_heads;
+    if (t.head >= p.heads) t.head -= p.heads, ++t.local;
+    rotate_load(p, t, inside && row + stride < rows, first, at_a, at_b);
     if (p.q.weight || p.k.weight) {  // (whole warps: rows of q and k share them)
-      float ss[3] = {0.0f, 0.0f, 0.0f};
+      float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(a[j], a[j], fmaf(b[j], b[j], ss[0]));
-      for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) ss[0] += __shfl_xor_sync(0xFFFFFFFFu, ss[0], d);
-      if (__any_sync(0xFFFFFFFFu, now.valid && !(ss[0] >= 0x1p-60f && ss[0] < INFINITY))) {
-        // squares out of fp32's range in some row: the sums of others as well
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s0 = a[j] * 0x1p-80f, s1 = b[j] * 0x1p-80f, l0 = a[j] * 0x1p80f, l1 = b[j] * 0x1p80f;
-          ss[1] = fmaf(s0, s0, fmaf(s1, s1, ss[1]));
-          ss[2] = fmaf(l0, l0, fmaf(l1, l1, ss[2]));
-        }
-        for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) {
-          ss[1] += __shfl_xor_sync(0xFFFFFFFFu, ss[1], d);
-          ss[2] += __shfl_xor_sync(0xFFFFFFFFu, ss[2], d);
-        }
-      }
-      if (now.valid && now.h->weight) {
-        const float r = fp4_rstd(ss, p.dim, p.eps);
+      for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+      for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+      float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+      if (__any_sync(0xFFFFFFFFu, valid && !(ss >= 0x1p-60f && ss < INFINITY))) r = rotate_far_rstd(p, a, b, ss);
+      if (valid && h->weight) {
         float w[8];
-        rotate_widen(*reinterpret_cast<const uint4*>(now.h->weight + now.at_a), w);
+        rotate_widen(*reinterpret_cast<const uint4*>(h->weight + at_a), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
-        if (now.at_b < p.dim) {
-          rotate_widen(*reinterpret_cast<const uint4*>(now.h->weight + now.at_b), w);
+        if (at_b < p.dim) {
+          rotate_widen(*reinterpret_cast<const uint4*>(h->weight + at_b), w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[j] = b[j] * r * w[j];
         }
       }
     }
-    if (!now.valid) continue;
-    const int lane = item & ((1 << p.lanes_log2) - 1);
-    if (lane < (p.rotary >> 4)) {
-      const float2* cs = turn + now.local * half + lane * 8;
-      if (p.interleaved) {
+    if (!valid) continue;
+    if (turns) {
+      const float4* cs = reinterpret_cast<const float4*>(turn + local * half + lane * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = cs[j], v = cs[j + 4];
-          const float a0 = a[2 * j], b0 = b[2 * j];
-          a[2 * j] = a0 * u.x - a[2 * j + 1] * u.y;
-          a[2 * j + 1] = a[2 * j + 1] * u.x + a0 * u.y;
-          b[2 * j] = b0 * v.x - b[2 * j + 1] * v.y;
-          b[2 * j + 1] = b[2 * j + 1] * v.x + b0 * v.y;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 u = cs[j];
-          const float a0 = a[j];
-          a[j] = a0 * u.x - b[j] * u.y;
-          b[j] = b[j] * u.x + a0 * u.y;
+      for (int j = 0; j < 4; ++j) {
+        const float4 u = cs[j];  // pairs 2 j and 2 j + 1 of the lane's eight
+        if (p.interleaved) {
+          float (&z)[8] = j < 2 ? a : b;
+          const int k = 4 * (j & 1);
+          const float z0 = z[k], z2 = z[k + 2];
+          z[k] = z0 * u.x - z[k + 1] * u.y;
+          z[k + 1] = z[k + 1] * u.x + z0 * u.y;
+          z[k + 2] = z2 * u.z - z[k + 3] * u.w;
+          z[k + 3] = z[k + 3] * u.z + z2 * u.w;
+        } else {
+          const float a0 = a[2 * j], a1 = a[2 * j + 1];
+          a[2 * j] = a0 * u.x - b[2 * j] * u.y;
+          b[2 * j] = b[2 * j] * u.x + a0 * u.y;
+          a[2 * j + 1] = a1 * u.z - b[2 * j + 1] * u.w;
+          b[2 * j + 1] = b[2 * j + 1] * u.z + a1 * u.w;
         }
       }
     }
-    uint16_t* y = now.h->out + now.token * now.h->out_token + now.head * now.h->out_head;
-    *reinterpret_cast<uint4*>(y + now.at_a) = make_uint4(pack_bf16x2_rn(a[0], a[1]), pack_bf16x2_rn(a[2], a[3]),
-                                                         pack_bf16x2_rn(a[4], a[5]), pack_bf16x2_rn(a[6], a[7]));
-    if (now.at_b < p.dim)
-      *reinterpret_cast<uint4*>(y + now.at_b) = make_uint4(pack_bf16x2_rn(b[0], b[1]), pack_bf16x2_rn(b[2], b[3]),
-                                                           pack_bf16x2_rn(b[4], b[5]), pack_bf16x2_rn(b[6], b[7]));
+    uint16_t* y = h->out + (first + local) * h->out_token + (head < p.q_heads ? head : head - p.q_heads) * h->out_head;
+    *reinterpret_cast<uint4*>(y + at_a) = make_uint4(pack_bf16x2_rn(a[0], a[1]), pack_bf16x2_rn(a[2], a[3]),
+                                                     pack_bf16x2_rn(a[4], a[5]), pack_bf16x2_rn(a[6], a[7]));
+    if (at_b < p.dim)
+      *reinterpret_cast<uint4*>(y + at_b) = make_uint4(pack_bf16x2_rn(b[0], b[1]), pack_bf16x2_rn(b[2], b[3]),
+                                                       pack_bf16x2_rn(b[4], b[5]), pack_bf16x2_rn(b[6], b[7]));
   }
 }
 

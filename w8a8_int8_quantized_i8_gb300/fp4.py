@@ -18,12 +18,13 @@ captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
 
 from .binding import FP4RowsInfo
-from .serving import _bf16, _call, _device_index, _explain, _f32, _rows, _vector
+from .serving import _bf16, _call, _explain, _f32, _library, _rows, _vector
 
 FORMATS = {"nvfp4": 0, "mxfp4": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1}
@@ -63,44 +64,55 @@ def _format(fmt) -> int:
     return code
 
 
+def _activation(activation) -> int:
+    code = ACTIVATIONS.get(activation) if isinstance(activation, str) else None
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return code
+
+
 def _info(rows, name: str, index: int) -> FP4RowsInfo:
     if not isinstance(rows, FP4Rows):
         raise TypeError(f"{name} must be FP4Rows")
     codes, scales, row = rows
-    if not (isinstance(codes, torch.Tensor) and codes.dtype is _u8 and codes.dim() == 2 and codes.get_device() == index
-            and isinstance(scales, torch.Tensor) and scales.dtype is _u8 and scales.dim() == 3
-            and scales.get_device() == index and index >= 0):
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is _u8 and codes.get_device() == index
+            and isinstance(scales, torch.Tensor) and scales.dtype is _u8 and scales.get_device() == index
+            and index >= 0 and codes.dim() == 2 and scales.dim() == 3):
         _explain(codes, _u8, f"{name}.codes", 2, index)
         _explain(scales, _u8, f"{name}.block_scales", 3, index)
     n, half = codes.shape
-    tiles, deep, size = scales.shape
-    if size not in _TILE or tiles != -(-n // 128) or deep != -(-half // 128):
+    size = scales.shape[2]
+    if size not in _TILE or scales.shape != (-(-n // 128), -(-half // 128), size):
         raise ValueError(f"{name}.block_scales must be [ceil(rows / 128), ceil(K / 256), 2048 or 1024]")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name} must be contiguous")
     return FP4RowsInfo(codes.data_ptr(), scales.data_ptr(),
                        _vector(row, _f32, f"{name}.row_scales", n, index) if row is not None else None, n, 2 * half,
-                       _TILE.index(size))
+                       0 if size == 2048 else 1)
 
 
-def _out_rows(out, rows: int, K: int, code: int, scaled: bool, x) -> tuple[FP4Rows, FP4RowsInfo]:
+def _out_rows(out, rows: int, K: int, code: int, scaled: bool, x, index: int) -> tuple[FP4Rows, FP4RowsInfo]:
     if out is None:
         out = FP4Rows.empty(rows, K, _NAMES[code], x.device, scaled)
-    info = _info(out, "out", x.get_device())
+        codes, scales, row = out
+        return out, FP4RowsInfo(codes.data_ptr(), scales.data_ptr(), row.data_ptr() if scaled else None, rows, K, code)
+    info = _info(out, "out", index)
     if (info.rows, info.K, info.fmt) != (rows, K, code) or scaled != (out.row_scales is not None):
         raise ValueError("out must be FP4Rows.empty of the rows' sizes and format")
     return out, info
 
 
 def _matrix(x, name: str):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise TypeError(f"{name} must be a 2-D bf16 CUDA tensor")
-    index = _device_index(x, name)
+    """(device, rows, K, address, row stride) of bf16 rows to quantize."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is _bf16 and x.dim() == 2 and x.get_device() >= 0):
+        _explain(x, _bf16, name, 2, None if not isinstance(x, torch.Tensor) else x.get_device())
     rows, K = x.shape
+    ld, unit = x.stride()
     if K % 32 or not K:
         raise ValueError(f"{name}'s width must be a multiple of 32")
-    p, ld = _rows(x, _bf16, name, rows, K, index)
-    return index, rows, K, p, ld
+    if unit != 1 or (ld < K and rows > 1):
+        raise ValueError(f"{name} must have unit stride along its rows, which do not overlap")
+    return x.get_device(), rows, K, x.data_ptr(), ld if rows > 1 else K
 
 
 def quant_rows_fp4(x: torch.Tensor, fmt: str = "nvfp4", out: FP4Rows | None = None) -> FP4Rows:
@@ -108,7 +120,7 @@ def quant_rows_fp4(x: torch.Tensor, fmt: str = "nvfp4", out: FP4Rows | None = No
     weights; x may be a row-strided view.  K % 32 == 0."""
     code = _format(fmt)
     index, rows, K, p, ld = _matrix(x, "x")
-    out, o = _out_rows(out, rows, K, code, code == 0, x)
+    out, o = _out_rows(out, rows, K, code, code == 0, x, index)
     _call("i8_quant_rows_fp4", index, p, rows, K, ld, code, o.codes, o.block_scales, o.row_scales)
     return out
 
@@ -133,7 +145,7 @@ def add_rmsnorm_quant_fp4(x: torch.Tensor, residual: torch.Tensor | None = None,
         if residual_out is None:
             residual_out = torch.empty((M, K), dtype=_bf16, device=x.device)
         hp, ldh = _rows(residual_out, _bf16, "residual_out", M, K, index)
-    out, o = _out_rows(out, M, K, code, True, x)
+    out, o = _out_rows(out, M, K, code, True, x, index)
     _call("i8_add_rmsnorm_quant_fp4", index, xp, M, K, ldx, rp, ldr, wp, eps, code, o.codes, o.block_scales,
           o.row_scales, hp, ldh)
     return out if residual is None else (out, residual_out)
@@ -170,9 +182,7 @@ def gemm_fp4_gated_bf16(a: FP4Rows, gate: FP4Rows, up: FP4Rows, gate_bias: torch
     """bf16(act(g) * u) with g and u the products of a with ``gate`` and ``up``
     [N, K] (biases added), both in fp32: the first half of a gated feed-forward
     block in one kernel.  activation: "silu" or "gelu" (erf form)."""
-    code = ACTIVATIONS.get(activation) if isinstance(activation, str) else None
-    if code is None:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    code = _activation(activation)
     index = a.codes.get_device() if isinstance(a, FP4Rows) and isinstance(a.codes, torch.Tensor) else -1
     ai, gi, ui = _info(a, "a", index), _info(gate, "gate", index), _info(up, "up", index)
     if not (ai.K == gi.K == ui.K and ai.fmt == gi.fmt == ui.fmt and gi.rows == ui.rows):
@@ -183,18 +193,53 @@ def gemm_fp4_gated_bf16(a: FP4Rows, gate: FP4Rows, up: FP4Rows, gate_bias: torch
     return out
 
 
-def linear_fp4(x: torch.Tensor, w: FP4Rows, bias: torch.Tensor | None = None,
-               out: torch.Tensor | None = None) -> torch.Tensor:
-    """The whole 4-bit linear layer: quantizes x in w's format, then the product."""
-    if not isinstance(w, FP4Rows):
-        raise TypeError("w must be FP4Rows")
-    return gemm_fp4_bias_bf16(quant_rows_fp4(x, w.fmt), w, bias, out=out)
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(M: int, K: int, code: int) -> int:
+    return _library().i8_linear_fp4_workspace_bytes(M, K, code)
+
+
+def linear_fp4_workspace_bytes(M: int, w: FP4Rows) -> int:
+    """Bytes of workspace that linear_fp4 and gated_linear_fp4 need for M tokens."""
+    return _workspace_bytes(M, w.shape[1], _format(w.fmt))
+
+
+def _linear(x, first, name, out, workspace):
+    """What both layers share: (index, x's address, M, K, row stride, the first
+    weight's info, out, its address and stride, the workspace)."""
+    index, M, K, xp, ldx = _matrix(x, "x")
+    wi = _info(first, name, index)
+    if wi.K != K:
+        raise ValueError(f"x and {name} must have the same K")
+    out, yp, ldy = _output(out, M, wi.rows, x.device, index)
+    if workspace is None:
+        workspace = torch.empty((_workspace_bytes(M, K, wi.fmt),), dtype=_u8, device=x.device)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return index, xp, M, K, ldx, wi, out, yp, ldy, workspace
+
+
+def linear_fp4(x: torch.Tensor, w: FP4Rows, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The whole 4-bit linear layer: quantizes x, bf16 [M, K] (row-strided views
+    allowed), in w's format, then the product."""
+    index, xp, M, K, ldx, wi, out, yp, ldy, ws = _linear(x, w, "w", out, workspace)
+    _call("i8_linear_fp4", index, xp, M, K, ldx, ctypes.byref(wi), _bias(bias, "bias", wi.rows, index), yp, ldy,
+          ws.data_ptr(), ws.numel() * ws.element_size())
+    return out
 
 
 def gated_linear_fp4(x: torch.Tensor, gate: FP4Rows, up: FP4Rows, gate_bias: torch.Tensor | None = None,
                      up_bias: torch.Tensor | None = None, activation: str = "silu",
-                     out: torch.Tensor | None = None) -> torch.Tensor:
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Quantizes x in the weights' format, then gemm_fp4_gated_bf16."""
-    if not isinstance(gate, FP4Rows):
-        raise TypeError("gate must be FP4Rows")
-    return gemm_fp4_gated_bf16(quant_rows_fp4(x, gate.fmt), gate, up, gate_bias, up_bias, activation, out=out)
+    code = _activation(activation)
+    index, xp, M, K, ldx, gi, out, yp, ldy, ws = _linear(x, gate, "gate", out, workspace)
+    ui = _info(up, "up", index)
+    if (ui.K, ui.fmt, ui.rows) != (K, gi.fmt, gi.rows):
+        raise ValueError("gate and up must have the same rows, K and format")
+    _call("i8_gated_linear_fp4", index, xp, M, K, ldx, ctypes.byref(gi), ctypes.byref(ui),
+          _bias(gate_bias, "gate_bias", gi.rows, index), _bias(up_bias, "up_bias", gi.rows, index), code, yp, ldy,
+          ws.data_ptr(), ws.numel() * ws.element_size())
+    return out

@@ -273,10 +273,13 @@ def heads_rmsnorm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tens
     if len(sections) != axes or sum(sections) != half:
         raise ValueError("sections must be one count of pairs an axis, together len(inv_freq)")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=_bf16, device=q.device), torch.empty((T, Hk, D), dtype=_bf16, device=q.device)
-    qo, ko = out
-    qop, qot, qoh = _heads(qo, "out[0]", (T, Hq, D), index)
-    kop, kot, koh = _heads(ko, "out[1]", (T, Hk, D), index)
+        dev = q.device
+        qo, ko = torch.empty((T, Hq, D), dtype=_bf16, device=dev), torch.empty((T, Hk, D), dtype=_bf16, device=dev)
+        qop, qot, kop, kot, qoh, koh = qo.data_ptr(), Hq * D, ko.data_ptr(), Hk * D, D, D
+    else:
+        qo, ko = out
+        qop, qot, qoh = _heads(qo, "out[0]", (T, Hq, D), index)
+        kop, kot, koh = _heads(ko, "out[1]", (T, Hk, D), index)
     _call("i8_heads_rmsnorm_rotate", index, qp, qt, qh, Hq, kp, kt, kh, Hk, T, D,
           _vector(q_weight, _bf16, "q_weight", D, index) if q_weight is not None else None,
           _vector(k_weight, _bf16, "k_weight", D, index) if k_weight is not None else None, eps, pp, ldp, axes,
