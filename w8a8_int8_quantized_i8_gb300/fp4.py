@@ -71,24 +71,28 @@ def _activation(activation) -> int:
     return code
 
 
-def _info(rows, name: str, index: int) -> FP4RowsInfo:
-    if not isinstance(rows, FP4Rows):
+# As in serving.py, the checks are one expression over cheap attributes where all is
+# well: what the host does between two launches runs with cold caches and is what
+# a small call costs.
+
+def _info(rows, name: str, index: int):
+    """(struct, rows, K, format's code) of 4-bit rows on a device."""
+    if type(rows) is not FP4Rows:
         raise TypeError(f"{name} must be FP4Rows")
     codes, scales, row = rows
-    if not (isinstance(codes, torch.Tensor) and codes.dtype is _u8 and codes.get_device() == index
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is _u8 and codes.get_device() == index and codes.dim() == 2
             and isinstance(scales, torch.Tensor) and scales.dtype is _u8 and scales.get_device() == index
-            and index >= 0 and codes.dim() == 2 and scales.dim() == 3):
+            and scales.dim() == 3 and codes.is_contiguous() and scales.is_contiguous() and index >= 0):
         _explain(codes, _u8, f"{name}.codes", 2, index)
         _explain(scales, _u8, f"{name}.block_scales", 3, index)
-    n, half = codes.shape
-    size = scales.shape[2]
-    if size not in _TILE or scales.shape != (-(-n // 128), -(-half // 128), size):
-        raise ValueError(f"{name}.block_scales must be [ceil(rows / 128), ceil(K / 256), 2048 or 1024]")
-    if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name} must be contiguous")
-    return FP4RowsInfo(codes.data_ptr(), scales.data_ptr(),
-                       _vector(row, _f32, f"{name}.row_scales", n, index) if row is not None else None, n, 2 * half,
-                       0 if size == 2048 else 1)
+    n, half = codes.shape
+    tiles, deep, size = scales.shape
+    if size not in _TILE or tiles != (n + 127) // 128 or deep != (half + 127) // 128:
+        raise ValueError(f"{name}.block_scales must be [ceil(rows / 128), ceil(K / 256), 2048 or 1024]")
+    code = 0 if size == 2048 else 1
+    rp = None if row is None else _vector(row, _f32, f"{name}.row_scales", n, index)
+    return FP4RowsInfo(codes.data_ptr(), scales.data_ptr(), rp, n, 2 * half, code), n, 2 * half, code
 
 
 def _out_rows(out, rows: int, K: int, code: int, scaled: bool, x, index: int) -> tuple[FP4Rows, FP4RowsInfo]:
@@ -96,8 +100,8 @@ def _out_rows(out, rows: int, K: int, code: int, scaled: bool, x, index: int) ->
         out = FP4Rows.empty(rows, K, _NAMES[code], x.device, scaled)
         codes, scales, row = out
         return out, FP4RowsInfo(codes.data_ptr(), scales.data_ptr(), row.data_ptr() if scaled else None, rows, K, code)
-    info = _info(out, "out", index)
-    if (info.rows, info.K, info.fmt) != (rows, K, code) or scaled != (out.row_scales is not None):
+    info, *sizes = _info(out, "out", index)
+    if sizes != [rows, K, code] or scaled != (out.row_scales is not None):
         raise ValueError("out must be FP4Rows.empty of the rows' sizes and format")
     return out, info
 
@@ -105,7 +109,7 @@ def _out_rows(out, rows: int, K: int, code: int, scaled: bool, x, index: int) ->
 def _matrix(x, name: str):
     """(device, rows, K, address, row stride) of bf16 rows to quantize."""
     if not (isinstance(x, torch.Tensor) and x.dtype is _bf16 and x.dim() == 2 and x.get_device() >= 0):
-        _explain(x, _bf16, name, 2, None if not isinstance(x, torch.Tensor) else x.get_device())
+        _explain(x, _bf16, name, 2)
     rows, K = x.shape
     ld, unit = x.stride()
     if K % 32 or not K:
@@ -163,16 +167,21 @@ def _bias(bias, name: str, N: int, index: int):
     return _vector(bias, _bf16, name, N, index) if bias is not None else None
 
 
+def _of(a) -> int:
+    return a.codes.get_device() if type(a) is FP4Rows and isinstance(a.codes, torch.Tensor) else -1
+
+
 def gemm_fp4_bias_bf16(a: FP4Rows, w: FP4Rows, bias: torch.Tensor | None = None,
                        out: torch.Tensor | None = None) -> torch.Tensor:
     """bf16(acc * s_a[m] * s_w[n] + bias[n]): tokens a [M, K] by weights w [N, K] of
     the same format, N % 8 == 0."""
-    index = a.codes.get_device() if isinstance(a, FP4Rows) and isinstance(a.codes, torch.Tensor) else -1
-    ai, wi = _info(a, "a", index), _info(w, "w", index)
-    if ai.K != wi.K or ai.fmt != wi.fmt:
+    index = _of(a)
+    ai, M, *kind = _info(a, "a", index)
+    wi, N, *kind_w = _info(w, "w", index)
+    if kind != kind_w:
         raise ValueError("a and w must have the same K and format")
-    out, p, ld = _output(out, ai.rows, wi.rows, a.codes.device, index)
-    _call("i8_gemm_fp4_bias_bf16", index, ctypes.byref(ai), ctypes.byref(wi), _bias(bias, "bias", wi.rows, index), p, ld)
+    out, p, ld = _output(out, M, N, a.codes.device, index)
+    _call("i8_gemm_fp4_bias_bf16", index, ctypes.byref(ai), ctypes.byref(wi), _bias(bias, "bias", N, index), p, ld)
     return out
 
 
@@ -183,13 +192,15 @@ def gemm_fp4_gated_bf16(a: FP4Rows, gate: FP4Rows, up: FP4Rows, gate_bias: torch
     [N, K] (biases added), both in fp32: the first half of a gated feed-forward
     block in one kernel.  activation: "silu" or "gelu" (erf form)."""
     code = _activation(activation)
-    index = a.codes.get_device() if isinstance(a, FP4Rows) and isinstance(a.codes, torch.Tensor) else -1
-    ai, gi, ui = _info(a, "a", index), _info(gate, "gate", index), _info(up, "up", index)
-    if not (ai.K == gi.K == ui.K and ai.fmt == gi.fmt == ui.fmt and gi.rows == ui.rows):
+    index = _of(a)
+    ai, M, *kind = _info(a, "a", index)
+    gi, N, *kind_g = _info(gate, "gate", index)
+    ui, *up_sizes = _info(up, "up", index)
+    if kind != kind_g or up_sizes != [N, *kind]:
         raise ValueError("a, gate and up must have the same K and format, gate and up the same rows")
-    out, p, ld = _output(out, ai.rows, gi.rows, a.codes.device, index)
+    out, p, ld = _output(out, M, N, a.codes.device, index)
     _call("i8_gemm_fp4_gated_bf16", index, ctypes.byref(ai), ctypes.byref(gi), ctypes.byref(ui),
-          _bias(gate_bias, "gate_bias", gi.rows, index), _bias(up_bias, "up_bias", gi.rows, index), code, p, ld)
+          _bias(gate_bias, "gate_bias", N, index), _bias(up_bias, "up_bias", N, index), code, p, ld)
     return out
 
 
@@ -203,30 +214,30 @@ def linear_fp4_workspace_bytes(M: int, w: FP4Rows) -> int:
     return _workspace_bytes(M, w.shape[1], _format(w.fmt))
 
 
-def _linear(x, first, name, out, workspace):
-    """What both layers share: (index, x's address, M, K, row stride, the first
-    weight's info, out, its address and stride, the workspace)."""
-    index, M, K, xp, ldx = _matrix(x, "x")
-    wi = _info(first, name, index)
-    if wi.K != K:
-        raise ValueError(f"x and {name} must have the same K")
-    out, yp, ldy = _output(out, M, wi.rows, x.device, index)
+def _workspace(workspace, M: int, K: int, code: int, device, index: int):
+    """(workspace, its address, its bytes)"""
     if workspace is None:
-        workspace = torch.empty((_workspace_bytes(M, K, wi.fmt),), dtype=_u8, device=x.device)
-    elif not isinstance(workspace, torch.Tensor):
+        size = _workspace_bytes(M, K, code)
+        workspace = torch.empty((size,), dtype=_u8, device=device)
+        return workspace, workspace.data_ptr(), size
+    if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
-    elif workspace.get_device() != index or not workspace.is_contiguous():
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{index}")
-    return index, xp, M, K, ldx, wi, out, yp, ldy, workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def linear_fp4(x: torch.Tensor, w: FP4Rows, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The whole 4-bit linear layer: quantizes x, bf16 [M, K] (row-strided views
     allowed), in w's format, then the product."""
-    index, xp, M, K, ldx, wi, out, yp, ldy, ws = _linear(x, w, "w", out, workspace)
-    _call("i8_linear_fp4", index, xp, M, K, ldx, ctypes.byref(wi), _bias(bias, "bias", wi.rows, index), yp, ldy,
-          ws.data_ptr(), ws.numel() * ws.element_size())
+    index, M, K, xp, ldx = _matrix(x, "x")
+    wi, N, Kw, code = _info(w, "w", index)
+    if Kw != K:
+        raise ValueError("x and w must have the same K")
+    out, yp, ldy = _output(out, M, N, x.device, index)
+    workspace, wp, size = _workspace(workspace, M, K, code, x.device, index)
+    _call("i8_linear_fp4", index, xp, M, K, ldx, ctypes.byref(wi), _bias(bias, "bias", N, index), yp, ldy, wp, size)
     return out
 
 
@@ -234,12 +245,14 @@ def gated_linear_fp4(x: torch.Tensor, gate: FP4Rows, up: FP4Rows, gate_bias: tor
                      up_bias: torch.Tensor | None = None, activation: str = "silu",
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Quantizes x in the weights' format, then gemm_fp4_gated_bf16."""
-    code = _activation(activation)
-    index, xp, M, K, ldx, gi, out, yp, ldy, ws = _linear(x, gate, "gate", out, workspace)
-    ui = _info(up, "up", index)
-    if (ui.K, ui.fmt, ui.rows) != (K, gi.fmt, gi.rows):
-        raise ValueError("gate and up must have the same rows, K and format")
+    act = _activation(activation)
+    index, M, K, xp, ldx = _matrix(x, "x")
+    gi, N, Kw, code = _info(gate, "gate", index)
+    ui, *up_sizes = _info(up, "up", index)
+    if Kw != K or up_sizes != [N, K, code]:
+        raise ValueError("x, gate and up must have the same K, gate and up the same rows and format")
+    out, yp, ldy = _output(out, M, N, x.device, index)
+    workspace, wp, size = _workspace(workspace, M, K, code, x.device, index)
     _call("i8_gated_linear_fp4", index, xp, M, K, ldx, ctypes.byref(gi), ctypes.byref(ui),
-          _bias(gate_bias, "gate_bias", gi.rows, index), _bias(up_bias, "up_bias", gi.rows, index), code, yp, ldy,
-          ws.data_ptr(), ws.numel() * ws.element_size())
+          _bias(gate_bias, "gate_bias", N, index), _bias(up_bias, "up_bias", N, index), act, yp, ldy, wp, size)
     return out
