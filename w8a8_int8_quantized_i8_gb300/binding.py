@@ -9,6 +9,8 @@ fallback: if libi8.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -153,6 +155,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
         if path == _build.LIB:
             _lib = lib
         return lib
+
+
+_calls = None
+
+
+def load_calls():
+    """The extension _calls.so (csrc/torch_calls.cpp), built first if it is stale.
+    Raises on failure; there is no other path."""
+    global _calls
+    if _calls is None:
+        load()
+        with _lock:
+            if _calls is None:
+                from .fp4 import FP4Rows
+                loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_LIB)
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+                loader.exec_module(module)
+                module.types(FP4Rows, I8Error)
+                _calls = module
+    return _calls
 
 
 def _check(status: int, what: str) -> None:

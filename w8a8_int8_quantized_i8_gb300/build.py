@@ -1,10 +1,12 @@
 """Builds libi8.so (the CUDA library behind include/i8.h) in-tree with nvcc,
 and beside it libi8probe.so, a measurement helper for the benchmark (the
-legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path).
+legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path), and _calls.so,
+the CPython extension that hands torch tensors to libi8 where a small call's time
+is the host's (csrc/torch_calls.cpp).
 
 libi8.so is three translation units (the linear layer, the serving operators,
-the 4-bit route), the probe one; one ``-gencode`` target (sm_103a), no cmake;
-all four compile in parallel.  The outputs are git-ignored and rebuilt whenever a source is
+the 4-bit route), the probe and the extension one each; one ``-gencode`` target
+(sm_103a), no cmake; all of them compile in parallel.  The outputs are git-ignored and rebuilt whenever a source is
 newer than them.
 """
 from __future__ import annotations
@@ -13,12 +15,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libi8.so")
 UNITS = [os.path.join(CSRC, name) for name in ("i8_api.cu", "serving_api.cu", "fp4_api.cu")]
+CALLS_LIB = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 PROBE_LIB = os.path.join(PKG, "libi8probe.so")
 PROBE_SRC = os.path.join(CSRC, "engine_probe.cu")
 
@@ -52,12 +57,34 @@ def _stale(lib, sources) -> bool:
     return any(os.path.getmtime(s) > t for s in sources)
 
 
+def _calls_sources():
+    return [CALLS_SRC, os.path.join(ROOT, "include", "i8.h")]
+
+
 def stale() -> bool:
-    return _stale(LIB, _sources()) or _stale(PROBE_LIB, [PROBE_SRC])
+    return _stale(LIB, _sources()) or _stale(PROBE_LIB, [PROBE_SRC]) or _stale(CALLS_LIB, _calls_sources())
+
+
+def _calls_compile(obj: str) -> list[str]:
+    """Compiles the extension against this torch and this Python."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-c", "-o", obj, CALLS_SRC]
+
+
+def _calls_link(out: str, obj: str) -> list[str]:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", out, obj, "-L", PKG, "-l:libi8.so", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libi8.so and libi8probe.so if missing or older than their sources."""
+    """Compile libi8.so, libi8probe.so and _calls.so if missing or older than their sources."""
     targets = []
     if force or _stale(LIB, _sources()):
         targets.append((LIB, UNITS))
@@ -74,6 +101,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objects = [f"{lib}.{os.path.basename(u)}.tmp{os.getpid()}.o" for u in units]
         jobs.append((lib, objects, [start([nvcc(), *NVCC_FLAGS, "-c", "-o", o, u])
                                     for o, u in zip(objects, units)]))
+    calls = None
+    if force or _stale(CALLS_LIB, _calls_sources()):
+        obj = f"{CALLS_LIB}.tmp{os.getpid()}.o"
+        calls = (obj, start(_calls_compile(obj)))
     failed = []
     for lib, objects, procs in jobs:
         ok = all([p.wait() == 0 for p in procs])
@@ -85,8 +116,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for o in objects:
             if os.path.exists(o):
                 os.remove(o)
+    if calls:
+        obj, proc = calls
+        tmp = f"{CALLS_LIB}.tmp{os.getpid()}"
+        if proc.wait() == 0 and not failed and start(_calls_link(tmp, obj)).wait() == 0:
+            os.replace(tmp, CALLS_LIB)
+        else:
+            failed.append(os.path.basename(CALLS_LIB))
+        if os.path.exists(obj):
+            os.remove(obj)
     if failed:
-        raise RuntimeError(f"nvcc failed building {', '.join(failed)}")
+        raise RuntimeError(f"the compiler failed building {', '.join(failed)}")
     return LIB
 
 

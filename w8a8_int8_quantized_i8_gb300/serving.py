@@ -22,11 +22,11 @@ from typing import NamedTuple
 
 import torch
 
-from .binding import _FMT, KVCacheInfo, _check, load
+from .binding import _FMT, KVCacheInfo, _check, load, load_calls
 
 _CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _bf16, _i32, _i64, _f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
-_lib = None
+_lib = _calls = None
 
 
 def _library():
@@ -229,11 +229,6 @@ def add_rmsnorm_quant_act_pertoken(x: torch.Tensor, residual: torch.Tensor | Non
     return q, s, residual_out
 
 
-@functools.lru_cache(maxsize=64)
-def _sections(sections: tuple):
-    return (ctypes.c_int32 * len(sections))(*sections)
-
-
 def heads_rmsnorm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
                          q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
                          eps: float = 1e-6, sections=None, interleaved: bool = False,
@@ -248,43 +243,10 @@ def heads_rmsnorm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tens
     pairs that each axis turns, in order (time, height and width of a patch, say).
     Pairs are (i, i + len(inv_freq)), or, ``interleaved``, (2 i, 2 i + 1).  ``out``:
     two tensors like q and k, or (q, k) themselves: in place.  Returns both."""
-    index = _device_index(q, "q")
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("q and k must be 3-D")
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    qp, qt, qh = _heads(q, "q", (T, Hq, D), index)
-    kp, kt, kh = _heads(k, "k", (T, Hk, D), index)
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-        raise TypeError("inv_freq must be a 1-D fp32 CUDA tensor")
-    half = inv_freq.shape[0]
-    fp = _vector(inv_freq, _f32, "inv_freq", half, index)
-    if not isinstance(positions, torch.Tensor):
-        raise TypeError("positions must be a torch.Tensor")
-    if positions.dim() == 2:
-        axes = positions.shape[0]
-        if sections is None:
-            raise ValueError("positions of several axes need sections")
-        pp, ldp = _rows(positions, _i32, "positions", axes, T, index)
-    else:
-        axes, ldp = 1, T
-        pp = _vector(positions, _i32, "positions", T, index)
-    sections = (half,) if sections is None else tuple(sections)
-    if len(sections) != axes or sum(sections) != half:
-        raise ValueError("sections must be one count of pairs an axis, together len(inv_freq)")
-    if out is None:
-        dev = q.device
-        qo, ko = torch.empty((T, Hq, D), dtype=_bf16, device=dev), torch.empty((T, Hk, D), dtype=_bf16, device=dev)
-        qop, qot, kop, kot, qoh, koh = qo.data_ptr(), Hq * D, ko.data_ptr(), Hk * D, D, D
-    else:
-        qo, ko = out
-        qop, qot, qoh = _heads(qo, "out[0]", (T, Hq, D), index)
-        kop, kot, koh = _heads(ko, "out[1]", (T, Hk, D), index)
-    _call("i8_heads_rmsnorm_rotate", index, qp, qt, qh, Hq, kp, kt, kh, Hk, T, D,
-          _vector(q_weight, _bf16, "q_weight", D, index) if q_weight is not None else None,
-          _vector(k_weight, _bf16, "k_weight", D, index) if k_weight is not None else None, eps, pp, ldp, axes,
-          _sections(sections), fp, 2 * half, int(interleaved), qop, qot, qoh, kop, kot, koh)
-    return qo, ko
+    global _calls
+    if _calls is None:
+        _calls = load_calls()
+    return _calls.rotate(q, k, positions, inv_freq, q_weight, k_weight, eps, sections, interleaved, out)
 
 
 def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
