@@ -84,12 +84,14 @@ cudaError_t launch_quant(Fp4QuantArgs& a, int64_t rows, cudaStream_t st) {
     a.R = V > 0 ? std::max(1, 4 / a.G) : 1;  // (long rows: one)
     return launch_pdl(kern, dim3(static_cast<unsigned>((rows + a.R - 1) / a.R)), dim3(32, a.G, a.R), 0, st, a);
   };
-  // few rows: a warp for each 256 elements; many: fewer warps with more in hand
-  const int64_t most = rows <= 1024 ? 1 : vecs <= 8 ? 2 : 4;
+  // few rows: a warp for each 256 elements; many: fewer warps, with more in hand, to
+  // meet at the row's barrier
+  const int V = rows <= 512 ? 1 : vecs < 8 ? 2 : vecs < (NORM ? 64 : 32) ? 4 : 8;
   if (vecs > 128) return go(fp4_quant_kernel<0, MX, NORM>, 0);
-  if (vecs <= 32 && most == 1) return go(fp4_quant_kernel<1, MX, NORM>, 1);
-  if (vecs <= 64 && most <= 2) return go(fp4_quant_kernel<2, MX, NORM>, 2);
-  return go(fp4_quant_kernel<4, MX, NORM>, 4);
+  if (V == 1 && vecs <= 16) return go(fp4_quant_kernel<1, MX, NORM>, 1);
+  if (V <= 2 && vecs <= 32) return go(fp4_quant_kernel<2, MX, NORM>, 2);
+  if (V <= 4 && vecs <= 64) return go(fp4_quant_kernel<4, MX, NORM>, 4);
+  return go(fp4_quant_kernel<8, MX, NORM>, 8);
 }
 
 // ----------------------------------------------------------------- products
@@ -146,17 +148,25 @@ i8_status encode_scales(CUtensorMap* map, const i8_fp4_rows& r) {
 }
 
 // Clusters of lo .. hi of a kernel's CTAs that are resident at once: out[size].
-// (The runtime counts clusters with one CTA an SM; where several fit, so do as many
-// times the clusters.)
+// (For kernels with tensor memory the runtime counts one CTA an SM.  Two run where
+// their shared memory, registers and tensor memory, `cols` columns each, fit: counted
+// here.)
 template <auto KERN>
-i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, int hi, int (&out)[kFp4MaxSplits + 1]) {
+i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int cols, int lo, int hi,
+                            int (&out)[kFp4MaxSplits + 1]) {
   static int cached[kMaxDevices][kFp4MaxSplits + 1] = {};
   static std::mutex mu;
   std::lock_guard<std::mutex> lk(mu);
   if (cached[dev][lo] == 0) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem) != cudaSuccess || per_sm < 1)
+    cudaFuncAttributes f;
+    int room = 0, reserved = 0, regs = 0;
+    if (cudaFuncGetAttributes(&f, KERN) != cudaSuccess ||
+        cudaDeviceGetAttribute(&room, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&regs, cudaDevAttrMaxRegistersPerMultiprocessor, dev) != cudaSuccess)
       return I8_ERR_CUDA;
+    const size_t block = (smem + f.sharedSizeBytes + reserved + 1023) / 1024 * 1024;
+    const int per_sm = 2 * block <= static_cast<size_t>(room) && 2 * cols <= 512 && 2 * threads * ((f.numRegs + 7) / 8 * 8) <= regs ? 2 : 1;
     for (int size = lo; size <= hi; ++size) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(size * sms));
@@ -182,12 +192,14 @@ i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int lo, 
 
 // K splits of the streaming kernel, by a model in tiles of K (0.2 us each): a CTA
 // costs 10 besides its own, two on an SM slow each other down by 0.3, and CTAs that
-// meet pay for the tokens they exchange.  us measured (NV16) at 1, 2, 4, 8 splits:
-//   1 token by 4096 x 11008   13.7  9.1  6.3  5.5
-//   1 by 6144 x 4096           6.6  5.4  4.9  7.6 (two waves)
-//   61 by 2080 x 5120          8.4  7.9  6.4  7.0 (seven splits)
-//   128 by 4096 x 4096         8.4  9.5  8.6  13.4 (two waves)
-int stream_splits(int tiles, int tokens, int deep, int most, int sms, const int (&clusters)[kFp4MaxSplits + 1]) {
+// meet pay 2 and 0.03 for each other one and each sum of a token that they exchange.
+// us measured (NV16) at 1, 2, 4, 8 splits:
+//   1 token by 4096 x 11008   13.8  9.1  6.3  5.5
+//   1 by 6144 x 4096           6.7  5.4  4.9  7.5 (two waves)
+//   32 by 4096 x 4096          7.0  6.5  5.5  5.7
+//   61 by 2080 x 5120          8.2  7.3  6.0  6.9 (seven splits)
+//   128 by 4096 x 4096         8.0  8.2  7.9  12.1 (two waves)
+int stream_splits(int tiles, int sums, int deep, int most, int sms, const int (&clusters)[kFp4MaxSplits + 1]) {
   int best = 1;
   double least = 0;
   for (int s = 1; s <= most && s <= deep; ++s) {
@@ -196,7 +208,7 @@ int stream_splits(int tiles, int tokens, int deep, int most, int sms, const int 
     if (g_opt.force_splits > 0 && s == std::min({g_opt.force_splits, most, deep})) return s;
     const int waves = (tiles + clusters[s] - 1) / clusters[s];
     const double shared = static_cast<int64_t>(tiles) * s > sms ? 1.3 : 1.0;
-    const double cost = waves * (each * shared + 10.0) + (s > 1 ? 2.0 + 0.085 * tokens : 0.0);
+    const double cost = waves * (each * shared + 10.0) + (s > 1 ? 2.0 + 0.03 * sums * s : 0.0);
     if (s == 1 || cost < least) best = s, least = cost;
   }
   return best;
@@ -210,7 +222,7 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   constexpr auto kern = fp4_pair_kernel<MX, ACT>;
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
   int clusters[kFp4MaxSplits + 1];
-  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 2, 2, clusters)) return e;
+  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 512, 2, 2, clusters)) return e;
   CUtensorMap a, as, b[2], bs[2];
   if (i8_status e = encode_codes(&a, t, 128)) return e;
   if (i8_status e = encode_scales(&as, t)) return e;
@@ -240,9 +252,9 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
   }
   if (i8_status e = encode_codes(&mt, t, NT)) return e;
   int clusters[kFp4MaxSplits + 1];
-  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, 1, Cfg::MAX_SPLITS, clusters)) return e;
+  if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, Cfg::COLS, 1, Cfg::MAX_SPLITS, clusters)) return e;
   const int tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
-  const int best = stream_splits(tiles, NT, p.deep, Cfg::MAX_SPLITS, sms, clusters);
+  const int best = stream_splits(tiles, NT * Cfg::WEIGHTS, p.deep, Cfg::MAX_SPLITS, sms, clusters);
   p.splits = best;
   p.deep_per_split = (p.deep + best - 1) / best;
   cudaLaunchConfig_t cfg = {};

@@ -42,79 +42,117 @@ struct Fp4QuantArgs {
   float eps;
 };
 
-// Eight elements of a row that a lane holds: without the norm as they are, with it
-// t (fp32) and h.
+// Eight elements of a row that a lane holds: as they are, or with the norm h, not
+// rounded (its product with the gain is made again where it is wanted: a register
+// is dearer than a load from L1).
 template <bool NORM>
 struct Fp4Held {
   uint4 x;
-  __device__ __forceinline__ void widen(float (&t)[8]) const {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) t[2 * j] = bf16_lo(w[j]), t[2 * j + 1] = bf16_hi(w[j]);
-  }
-  // bits of the largest magnitude, which order like the values; a NaN wins
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t m = absmax_nan_bf16x2(absmax_nan_bf16x2(x.x, x.y), absmax_nan_bf16x2(x.z, x.w)) & 0x7FFF7FFFu;
-    return max(m << 16, m & 0xFFFF0000u);
-  }
 };
 template <>
 struct Fp4Held<true> {
-  float t[8];
-  uint32_t h[4];
-  __device__ __forceinline__ void widen(float (&o)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = t[j];
-  }
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(fabsf(t[j])));
-    return m;
-  }
+  float h[8];
 };
 
-// Elements e .. e + 7 of the row, and with the norm the sums of h's squares (as
-// they are, and of h * 2^-80 and h * 2^80 for rows whose squares leave fp32's
-// range).  Ordinary loads, of pointers that promise nothing: h may lie where x or
-// the residual does, and a kernel that this one overlaps may have written them.
+// The gains of elements e .. e + 7, bf16.
+__device__ __forceinline__ uint4 fp4_gains(const Fp4QuantArgs& a, int e) {
+  return a.weight && e < a.K ? *reinterpret_cast<const uint4*>(a.weight + e)
+                             : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+}
+
+// Elements e .. e + 7 of the row as they are held.  Ordinary loads, of pointers that
+// promise nothing: h may lie where x or the residual does, and a kernel that this
+// one overlaps may have written them.
 template <bool NORM>
-__device__ __forceinline__ void fp4_load8(const Fp4QuantArgs& a, int64_t row, int e, Fp4Held<NORM>& held, float (&ss)[3]) {
+__device__ __forceinline__ void fp4_load8(const Fp4QuantArgs& a, int64_t row, int e, Fp4Held<NORM>& held) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (e < a.K) v = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + e);
   if constexpr (!NORM) {
     held.x = v;
   } else {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u), g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    if (e < a.K) {
-      if (a.res) u = *reinterpret_cast<const uint4*>(a.res + row * a.ldr + e);
-      if (a.weight) g = *reinterpret_cast<const uint4*>(a.weight + e);
-    }
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4] = {u.x, u.y, u.z, u.w}, w[4] = {g.x, g.y, g.z, g.w};
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (a.res && e < a.K) u = *reinterpret_cast<const uint4*>(a.res + row * a.ldr + e);
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float h0 = __fadd_rn(bf16_lo(x[j]), bf16_lo(r[j])), h1 = __fadd_rn(bf16_hi(x[j]), bf16_hi(r[j]));
-      const float s0 = h0 * 0x1p-80f, s1 = h1 * 0x1p-80f, l0 = h0 * 0x1p80f, l1 = h1 * 0x1p80f;
-      ss[0] = fmaf(h0, h0, fmaf(h1, h1, ss[0]));
-      ss[1] = fmaf(s0, s0, fmaf(s1, s1, ss[1]));
-      ss[2] = fmaf(l0, l0, fmaf(l1, l1, ss[2]));
-      held.t[2 * j] = __fmul_rn(h0, bf16_lo(w[j]));
-      held.t[2 * j + 1] = __fmul_rn(h1, bf16_hi(w[j]));
-      held.h[j] = pack_bf16x2_rn(h0, h1);
+      held.h[2 * j] = __fadd_rn(bf16_lo(x[j]), bf16_lo(r[j]));
+      held.h[2 * j + 1] = __fadd_rn(bf16_hi(x[j]), bf16_hi(r[j]));
     }
   }
 }
+
+// What is quantized: the elements, or t = h * gain.
+template <bool NORM>
+__device__ __forceinline__ void fp4_widen(const Fp4QuantArgs& a, int e, const Fp4Held<NORM>& held, float (&t)[8]) {
+  if constexpr (NORM) {
+    const uint4 g = fp4_gains(a, e);
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      t[2 * j] = __fmul_rn(held.h[2 * j], bf16_lo(w[j]));
+      t[2 * j + 1] = __fmul_rn(held.h[2 * j + 1], bf16_hi(w[j]));
+    }
+  } else {
+    const uint32_t w[4] = {held.x.x, held.x.y, held.x.z, held.x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[2 * j] = bf16_lo(w[j]), t[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+
+// Bits of the largest magnitude of what is quantized, which order like the values
+// (a NaN wins), and with the norm the squares' sum.
+template <bool NORM>
+__device__ __forceinline__ uint32_t fp4_top(const Fp4QuantArgs& a, int e, const Fp4Held<NORM>& held, float& ss) {
+  if constexpr (NORM) {
+    float t[8];
+    fp4_widen<true>(a, e, held, t);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m = max(m, __float_as_uint(fabsf(t[j])));
+      ss = fmaf(held.h[j], held.h[j], ss);
+    }
+    return m;
+  } else {
+    const uint4& x = held.x;
+    const uint32_t m = absmax_nan_bf16x2(absmax_nan_bf16x2(x.x, x.y), absmax_nan_bf16x2(x.z, x.w)) & 0x7FFF7FFFu;
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+}
+
+// The squares' sums of rows whose squares leave fp32's range, of h * 2^-80 and of h *
+// 2^80.
+__device__ __forceinline__ void fp4_far_squares(const Fp4Held<true>& held, float (&ss)[3]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = held.h[j] * 0x1p-80f, l = held.h[j] * 0x1p80f;
+    ss[1] = fmaf(s, s, ss[1]);
+    ss[2] = fmaf(l, l, ss[2]);
+  }
+}
+
 template <bool NORM>
 __device__ __forceinline__ void fp4_store_h(const Fp4QuantArgs& a, int64_t row, int e, const Fp4Held<NORM>& held) {
   if constexpr (NORM)
     if (a.h && e < a.K)
-      *reinterpret_cast<uint4*>(a.h + row * a.ldh + e) = make_uint4(held.h[0], held.h[1], held.h[2], held.h[3]);
+      *reinterpret_cast<uint4*>(a.h + row * a.ldh + e) =
+          make_uint4(pack_bf16x2_rn(held.h[0], held.h[1]), pack_bf16x2_rn(held.h[2], held.h[3]),
+                     pack_bf16x2_rn(held.h[4], held.h[5]), pack_bf16x2_rn(held.h[6], held.h[7]));
 }
 
-// 1 / sqrt(mean(h^2) + eps) from the three sums.
+__device__ __forceinline__ void warp_sum(float& v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+}
+
+// Whether a sum of squares says all there is to say.
+__device__ __forceinline__ bool fp4_in_range(float ss) { return ss >= 0x1p-60f && ss < INFINITY; }
+
+// 1 / sqrt(mean(h^2) + eps) from the sum of squares and, where that is out of
+// range, the two others.
 __device__ __forceinline__ float fp4_rstd(const float (&ss)[3], int K, float eps) {
   const float n = static_cast<float>(K);
-  if (ss[0] >= 0x1p-60f && ss[0] < INFINITY) return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps)));
+  if (fp4_in_range(ss[0])) return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps)));
   // (eps beside squares of 2^64 and more is nothing)
   if (!(ss[0] < 1.0f)) return __fdiv_rn(0x1p-80f, __fsqrt_rn(__fdiv_rn(ss[1], n)));
   // where eps * 2^160 overflows, squares below 2^-60 are nothing beside eps
@@ -132,7 +170,7 @@ __device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, uint8_t* cod
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   if constexpr (MX) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
   float t[8];
-  held.widen(t);
+  fp4_widen<NORM>(a, first + lane * 8, held, t);
   if constexpr (!MX) {
     if (s == 0.0f) {  // not for the fast quotients: times a power of two before
 #pragma unroll
@@ -155,7 +193,7 @@ __device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, uint8_t* cod
 }
 
 template <int V, bool MX, bool NORM>
-__global__ void __launch_bounds__(V == 0 ? 512 : 1024) fp4_quant_kernel(const Fp4QuantArgs a) {
+__global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
   __shared__ float red_s[3][32];
   __shared__ uint32_t red_m[32];
   constexpr int H = V > 0 ? V : 1;
@@ -174,47 +212,68 @@ __global__ void __launch_bounds__(V == 0 ? 512 : 1024) fp4_quant_kernel(const Fp
   uint32_t amax = 0;
   if constexpr (V > 0) {
 #pragma unroll
-    for (int i = 0; i < H; ++i) fp4_load8<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i], ss);
+    for (int i = 0; i < H; ++i) fp4_load8<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
     pdl_trigger();
-    // (each thread has read the elements that it writes)
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      if (mine) fp4_store_h<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
-      top[i] = held[i].top();
+      top[i] = fp4_top<NORM>(a, warp * span + i * 256 + lane * 8, held[i], ss[0]);
       amax = max(amax, top[i]);
     }
   } else {
     for (int first = warp * span; first < end; first += step) {
-      fp4_load8<NORM>(a, row, first + lane * 8, held[0], ss);
-      amax = max(amax, held[0].top());
+      fp4_load8<NORM>(a, row, first + lane * 8, held[0]);
+      amax = max(amax, fp4_top<NORM>(a, first + lane * 8, held[0], ss[0]));
     }
   }
   float s = 1.0f, inverse = 1.0f;
   if (!MX || NORM) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    if constexpr (NORM) {
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) ss[k] += __shfl_xor_sync(0xFFFFFFFFu, ss[k], d);
-    }
+    if constexpr (NORM) warp_sum(ss[0]);
     if (a.G > 1) {
       if (lane == 0) {
         red_m[local * a.G + warp] = amax;
-        if constexpr (NORM) {
-#pragma unroll
-          for (int k = 0; k < 3; ++k) red_s[k][local * a.G + warp] = ss[k];
-        }
+        if constexpr (NORM) red_s[0][local * a.G + warp] = ss[0];
       }
       __syncthreads();
       amax = 0;
-      ss[0] = ss[1] = ss[2] = 0.0f;
+      ss[0] = 0.0f;
       for (int j = 0; j < a.G; ++j) {
         amax = max(amax, red_m[local * a.G + j]);
-        if constexpr (NORM) {
+        if constexpr (NORM) ss[0] += red_s[0][local * a.G + j];
+      }
+    }
+    if constexpr (NORM) {
+      // squares out of fp32's range in a row of the CTA: the others' sums as well
+      if (__syncthreads_or(!fp4_in_range(ss[0]))) {
+        if constexpr (V > 0) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) ss[k] += red_s[k][local * a.G + j];
+          for (int i = 0; i < H; ++i) fp4_far_squares(held[i], ss);
+        } else {
+          for (int first = warp * span; first < end; first += step) {
+            fp4_load8<NORM>(a, row, first + lane * 8, held[0]);  // (h is not stored yet)
+            fp4_far_squares(held[0], ss);
+          }
         }
+        warp_sum(ss[1]);
+        warp_sum(ss[2]);
+        if (a.G > 1) {
+          if (lane == 0) {
+            red_s[1][local * a.G + warp] = ss[1];
+            red_s[2][local * a.G + warp] = ss[2];
+          }
+          __syncthreads();
+          ss[1] = ss[2] = 0.0f;
+          for (int j = 0; j < a.G; ++j) {
+            ss[1] += red_s[1][local * a.G + j];
+            ss[2] += red_s[2][local * a.G + j];
+          }
+        }
+      }
+      // (each thread has read the elements that it writes)
+      if constexpr (V > 0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          if (mine) fp4_store_h<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
       }
     }
     const int k = nv16_row_exponent(amax);
@@ -236,9 +295,11 @@ __global__ void __launch_bounds__(V == 0 ? 512 : 1024) fp4_quant_kernel(const Fp
     }
   } else {
     for (int first = warp * span; first < end; first += step) {
-      fp4_load8<NORM>(a, row, first + lane * 8, held[0], ss);
+      float sum = 0.0f;
+      fp4_load8<NORM>(a, row, first + lane * 8, held[0]);
       fp4_store_h<NORM>(a, row, first + lane * 8, held[0]);
-      fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[0], held[0].top(), s, inverse);
+      fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[0], fp4_top<NORM>(a, first + lane * 8, held[0], sum), s,
+                             inverse);
     }
     pdl_trigger();
   }

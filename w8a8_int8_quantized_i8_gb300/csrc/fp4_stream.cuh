@@ -27,6 +27,7 @@
 namespace i8 {
 
 constexpr int kFp4MaxSplits = 8;
+constexpr int kFp4Prefetch = 6;  // tiles of K
 
 // Tokens that one of `splits` CTAs finishes: fours.
 __host__ __device__ constexpr int fp4_each(int tokens, int splits) { return ((tokens + splits - 1) / splits + 3) / 4 * 4; }
@@ -112,11 +113,16 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
     tma_prefetch_desc(&tm_w0);
     if constexpr (GATED) tma_prefetch_desc(&tm_w1);
     tma_prefetch_desc(&tm_t);
-    // the weights on their way into L2 while the kernel before drains
-    for (int kb = kb0; kb < min(kb1, kb0 + Cfg::STAGES); ++kb) {
+    // this CTA's weights on their way into L2 while the kernel before drains, more of
+    // them than the ring holds: HBM's latency is paid once
+    const int64_t ws0 = (static_cast<int64_t>(n_tile) * p.deep + kb0) * Cfg::SCALES;
+    for (int kb = kb0; kb < min(kb1, kb0 + kFp4Prefetch); ++kb) {
       tma_prefetch_l2_2d(&tm_w0, kb * 128, n0);
       if constexpr (GATED) tma_prefetch_l2_2d(&tm_w1, kb * 128, n0);
     }
+    const uint32_t ahead = static_cast<uint32_t>(min(kb1 - kb0, kFp4Prefetch) * Cfg::SCALES);
+    bulk_prefetch_l2(p.w[0].scales + ws0, ahead);
+    if constexpr (GATED) bulk_prefetch_l2(p.w[1].scales + ws0, ahead);
   }
   tc_fence_before();
   __syncthreads();
