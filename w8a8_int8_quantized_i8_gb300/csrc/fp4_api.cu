@@ -181,8 +181,11 @@ i8_status resident_clusters(int dev, int sms, int threads, size_t smem, int cols
       cfg.numAttrs = 1;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess) n = 0;
-      cached[dev][size] = n * size <= sms ? n * per_sm : n;
+      cached[dev][size] = n;
     }
+    // two an SM: twice as many clusters, or as many as of half the size
+    if (per_sm == 2)
+      for (int size = hi; size >= lo; --size) cached[dev][size] = std::max(2 * cached[dev][size], cached[dev][std::max(lo, (size + 1) / 2)]);
     cudaGetLastError();
     if (cached[dev][lo] < 1) return I8_ERR_CUDA;
   }

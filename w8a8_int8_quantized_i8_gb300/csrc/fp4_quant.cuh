@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
   const int step = a.G * span, end = a.deep * kFp4TileK;
 
   pdl_wait();  // the rows may be the previous kernel's output
+  pdl_trigger();
   Fp4Held<NORM> held[H];
   uint32_t top[H];
   float ss[3] = {0.0f, 0.0f, 0.0f};
@@ -213,7 +214,6 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
   if constexpr (V > 0) {
 #pragma unroll
     for (int i = 0; i < H; ++i) fp4_load8<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
-    pdl_trigger();
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       top[i] = fp4_top<NORM>(a, warp * span + i * 256 + lane * 8, held[i], ss[0]);
@@ -301,7 +301,6 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
       fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[0], fp4_top<NORM>(a, first + lane * 8, held[0], sum), s,
                              inverse);
     }
-    pdl_trigger();
   }
 }
 
