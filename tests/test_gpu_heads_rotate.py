@@ -150,3 +150,18 @@ def test_another_stream_and_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_without_a_norm_what_is_not_finite_stays_in_its_pair(interleaved, bad):
+    _, q, k, positions, inv, sections, _ = _case(6, 9, 4, 2, 128, 64, norm=False)
+    q[3, 2, 5], q[3, 2, 70], q[4, 1, 101] = bad, bad, bad     # one that is rotated, two that are not
+    qo, ko = i8.heads_rmsnorm_rotate(q, k, positions, inv, interleaved=interleaved)
+    where = (~torch.isfinite(qo)).nonzero().tolist()
+    assert where == [[3, 2, 4], [3, 2, 5], [3, 2, 70], [4, 1, 101]] if interleaved else \
+        where == [[3, 2, 5], [3, 2, 37], [3, 2, 70], [4, 1, 101]]
+    assert torch.isfinite(ko).all()
+    keep = torch.ones(9, dtype=torch.bool, device="cuda")
+    keep[3:5] = False
+    _check(qo[keep], q[keep], None, positions[keep], inv, sections, interleaved, 1e-6)

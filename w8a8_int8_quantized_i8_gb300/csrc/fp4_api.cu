@@ -615,11 +615,14 @@ i8_status i8_heads_rmsnorm_rotate(const void* q, int64_t ldq_token, int64_t ldq_
   int dev, sms;
   if (i8_status e = current_device(&dev)) return e;
   if (i8_status e = device_sms(dev, &sms)) return e;
-  // tokens a CTA: a few rounds of its threads, but a CTA for every SM first
+  p.kinds = q_weight || k_weight ? 2 : 1;
+  // tokens a CTA: several rounds of its threads, but CTAs for every SM first
   const int64_t lanes = static_cast<int64_t>(p.heads) << p.lanes_log2;
+  const size_t table = static_cast<size_t>(p.kinds) * ((p.dim + 15) / 16 * 8) * 4 * sizeof(float);
   p.per_cta = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>({16 * kRotateThreads / lanes, tokens / (4 * static_cast<int64_t>(sms)), 8})));
-  const size_t smem = static_cast<size_t>(p.per_cta) * (p.rotary / 2) * sizeof(float2);
+      1, std::min<int64_t>({8 * kRotateThreads / lanes, tokens / (4 * static_cast<int64_t>(sms)), 8,
+                            kRotateTable / static_cast<int64_t>(table)})));
+  const size_t smem = p.per_cta * table;
   return cuda_status(launch_pdl(heads_rmsnorm_rotate_kernel, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta)),
                                 dim3(kRotateThreads), smem, reinterpret_cast<cudaStream_t>(stream), p));
 }

@@ -15,10 +15,13 @@
 // each product as its rounded value (whose whole turns are dropped, exactly) and
 // its rounding error (one fma).  Up to 2^20 the error is below 2^-24 turns.
 //
-// Bound by HBM: 2 bytes read and 2 written an element.  A lane holds 8 pairs, that
-// is two vectors of 16 bytes, in either pairing; a row is up to 32 lanes.  The
-// sines and cosines of a CTA's tokens are made once, in shared memory, for all
-// their heads, while the first rows are on their way.
+// 2 bytes read and 2 written an element.  A lane holds 8 pairs, that is two vectors
+// of 16 bytes, in either pairing; a row is up to 32 lanes.  What bounds it is how
+// many instructions an element takes, so the gains go into the sines and cosines:
+// a CTA makes the four products
+//   y_a = x_a (w_a cos) + x_b (-w_b sin),  y_b = x_a (w_a sin) + x_b (w_b cos)
+// of its tokens once, in shared memory, for all their heads, while the first rows
+// are on their way, and the norm's factor comes last.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -31,6 +34,7 @@
 namespace i8 {
 
 constexpr int kRotateMaxAxes = 4, kRotateThreads = 256;
+constexpr int kRotateTable = 32 * 1024;  // bytes of products a CTA makes, at most, where it takes several tokens
 
 struct RotateHeads {
   const uint16_t* in;
@@ -47,6 +51,7 @@ struct RotateArgs {
   int tokens, q_heads, heads;  // heads: of q and k
   int dim, rotary, interleaved;
   int per_cta;                 // tokens
+  int kinds;                   // tables a token: 2 where q and k have gains of their own
   int lanes_log2;              // lanes of a row
   int step_tokens, step_heads; // from a thread's row to its next
   int section_end[kRotateMaxAxes];
@@ -84,13 +89,40 @@ __device__ __forceinline__ void rotate_load(const RotateArgs& p, RotateItem& t, 
   }
 }
 
-__device__ __forceinline__ void rotate_widen(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// A lane's 16 elements as the firsts and the seconds of 8 pairs, and back.
+__device__ __forceinline__ void rotate_widen(const uint4& v, const uint4& u, bool interleaved, float (&a)[8], float (&b)[8]) {
+  const uint32_t w[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
+  if (interleaved) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = bf16_lo(w[j]);
-    x[2 * j + 1] = bf16_hi(w[j]);
+    for (int j = 0; j < 8; ++j) a[j] = bf16_lo(w[j]), b[j] = bf16_hi(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[2 * j] = bf16_lo(w[j]), a[2 * j + 1] = bf16_hi(w[j]);
+      b[2 * j] = bf16_lo(w[j + 4]), b[2 * j + 1] = bf16_hi(w[j + 4]);
+    }
   }
+}
+__device__ __forceinline__ void rotate_narrow(const float (&a)[8], const float (&b)[8], bool interleaved, uint4& v, uint4& u) {
+  uint32_t w[8];
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2_rn(a[j], b[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = pack_bf16x2_rn(a[2 * j], a[2 * j + 1]);
+      w[j + 4] = pack_bf16x2_rn(b[2 * j], b[2 * j + 1]);
+    }
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  u = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // The norm's factor where some row of the warp has squares out of fp32's range: from
@@ -109,8 +141,11 @@ __device__ __forceinline__ float rotate_far_rstd(const RotateArgs& p, const floa
   return fp4_rstd(ss, p.dim, p.eps);
 }
 
-__global__ void __launch_bounds__(kRotateThreads, 5) heads_rmsnorm_rotate_kernel(const __grid_constant__ RotateArgs p) {
-  extern __shared__ __align__(16) float2 turn[];  // (cos, sin) [tokens of the CTA][rotary / 2]
+__global__ void __launch_bounds__(kRotateThreads, 4) heads_rmsnorm_rotate_kernel(const __grid_constant__ RotateArgs p) {
+  // [tokens of the CTA][kinds][w_a cos, w_a sin, -w_b sin, w_b cos][pairs 0-3 or 4-7 of
+  // a lane][lanes][4]: a row's lanes read side by side.  Lanes behind the rotated part
+  // have their gains there
+  extern __shared__ __align__(16) float turn[];
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int count = static_cast<int>(min(static_cast<int64_t>(p.per_cta), p.tokens - first));
   const int half = p.rotary / 2, rows = count * p.heads;
@@ -128,21 +163,39 @@ __global__ void __launch_bounds__(kRotateThreads, 5) heads_rmsnorm_rotate_kernel
   t.local = row / p.heads;
   t.head = row - t.local * p.heads;
   rotate_load(p, t, inside && row < rows, first, at_a, at_b);
-  for (int i = threadIdx.x; i < count * half; i += kRotateThreads) {
-    const int local = i / half, pair = i - local * half;
-    int axis = 0;
+  const int group = (p.dim + 15) >> 4, pairs = group * 8;
+  for (int i = threadIdx.x; i < count * pairs; i += kRotateThreads) {
+    const int local = i / pairs, pair = i - local * pairs;
+    float s = 0.0f, c = 1.0f;
+    // the elements of the pair
+    int one = 2 * pair, two = one + 1;
+    if (!p.interleaved) {
+      one = pair < half ? pair : (pair >> 3) * 16 + (pair & 7);
+      two = pair < half ? pair + half : one + 8;
+    }
+    if (pair < half) {
+      int axis = 0;
 #pragma unroll
-    for (int a = 0; a < kRotateMaxAxes - 1; ++a) axis += pair >= p.section_end[a] ? 1 : 0;
-    float s, c;
-    sincospif(2.0f * rotate_turns(p.positions[axis * p.ld_pos + first + local], p.inv_freq[pair]), &s, &c);
-    turn[i] = make_float2(c, s);
+      for (int a = 0; a < kRotateMaxAxes - 1; ++a) axis += pair >= p.section_end[a] ? 1 : 0;
+      sincospif(2.0f * rotate_turns(p.positions[axis * p.ld_pos + first + local], p.inv_freq[pair]), &s, &c);
+    }
+    for (int kind = 0; kind < p.kinds; ++kind) {
+      const uint16_t* w = kind == 0 ? p.q.weight : p.k.weight;
+      const float wa = w && one < p.dim ? __uint_as_float(static_cast<uint32_t>(w[one]) << 16) : 1.0f;
+      const float wb = w && two < p.dim ? __uint_as_float(static_cast<uint32_t>(w[two]) << 16) : 1.0f;
+      float* at = turn + (local * p.kinds + kind) * 4 * pairs + ((((pair >> 2) & 1) * group + (pair >> 3)) << 2) + (pair & 3);
+      at[0] = wa * c;
+      at[pairs] = wa * s;
+      at[2 * pairs] = -wb * s;
+      at[3 * pairs] = wb * c;
+    }
   }
   pdl_trigger();
   __syncthreads();
+  const bool norms = p.q.weight || p.k.weight;
   for (int base = 0; base < rows; base += stride, row += stride) {  // the same rounds for whole warps
     float a[8], b[8];
-    rotate_widen(t.a, a);
-    rotate_widen(t.b, b);
+    rotate_widen(t.a, t.b, p.interleaved, a, b);
     const bool valid = inside && row < rows;
     const RotateHeads* const h = t.h;
     const int local = t.local, head = t.head;
@@ -150,54 +203,46 @@ __global__ void __launch_bounds__(kRotateThreads, 5) heads_rmsnorm_rotate_kernel
     t.head += p.step_heads;
     if (t.head >= p.heads) t.head -= p.heads, ++t.local;
     rotate_load(p, t, inside && row + stride < rows, first, at_a, at_b);
-    if (p.q.weight || p.k.weight) {  // (whole warps: rows of q and k share them)
+    float r = 1.0f;
+    if (norms) {  // (whole warps: rows of q and k share them)
       float ss = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
       for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-      float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+      r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
       if (__any_sync(0xFFFFFFFFu, valid && !(ss >= 0x1p-60f && ss < INFINITY))) r = rotate_far_rstd(p, a, b, ss);
-      if (valid && h->weight) {
-        float w[8];
-        rotate_widen(*reinterpret_cast<const uint4*>(h->weight + at_a), w);
+      if (!h->weight) r = 1.0f;
+    }
+    const bool key = head >= p.q_heads;
+    // (lanes without a row's elements stay with the warp, at the first products)
+    const float4* m = reinterpret_cast<const float4*>(turn);
+    if (valid) m += (local * p.kinds + (key ? p.kinds - 1 : 0)) * 8 * group + lane;
+    const unsigned long long rr = f2(r, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
-        if (at_b < p.dim) {
-          rotate_widen(*reinterpret_cast<const uint4*>(h->weight + at_b), w);
+    for (int j = 0; j < 2; ++j) {  // four pairs
+      const float4 ca = m[j * group], sa = m[(2 + j) * group], sb = m[(4 + j) * group], cb = m[(6 + j) * group];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) b[j] = b[j] * r * w[j];
+      for (int e = 0; e < 2; ++e) {
+        const int k = 4 * j + 2 * e;
+        const unsigned long long x = f2(a[k], a[k + 1]), z = f2(b[k], b[k + 1]);
+        unsigned long long u, v;
+        if (turns) {
+          u = f2_fma(x, e ? f2(ca.z, ca.w) : f2(ca.x, ca.y), f2_mul(z, e ? f2(sb.z, sb.w) : f2(sb.x, sb.y)));
+          v = f2_fma(x, e ? f2(sa.z, sa.w) : f2(sa.x, sa.y), f2_mul(z, e ? f2(cb.z, cb.w) : f2(cb.x, cb.y)));
+        } else {  // (0 times what is not finite is not 0)
+          u = f2_mul(x, e ? f2(ca.z, ca.w) : f2(ca.x, ca.y));
+          v = f2_mul(z, e ? f2(cb.z, cb.w) : f2(cb.x, cb.y));
         }
+        f2_split(f2_mul(u, rr), a[k], a[k + 1]);
+        f2_split(f2_mul(v, rr), b[k], b[k + 1]);
       }
     }
     if (!valid) continue;
-    if (turns) {
-      const float4* cs = reinterpret_cast<const float4*>(turn + local * half + lane * 8);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 u = cs[j];  // pairs 2 j and 2 j + 1 of the lane's eight
-        if (p.interleaved) {
-          float (&z)[8] = j < 2 ? a : b;
-          const int k = 4 * (j & 1);
-          const float z0 = z[k], z2 = z[k + 2];
-          z[k] = z0 * u.x - z[k + 1] * u.y;
-          z[k + 1] = z[k + 1] * u.x + z0 * u.y;
-          z[k + 2] = z2 * u.z - z[k + 3] * u.w;
-          z[k + 3] = z[k + 3] * u.z + z2 * u.w;
-        } else {
-          const float a0 = a[2 * j], a1 = a[2 * j + 1];
-          a[2 * j] = a0 * u.x - b[2 * j] * u.y;
-          b[2 * j] = b[2 * j] * u.x + a0 * u.y;
-          a[2 * j + 1] = a1 * u.z - b[2 * j + 1] * u.w;
-          b[2 * j + 1] = b[2 * j + 1] * u.z + a1 * u.w;
-        }
-      }
-    }
-    uint16_t* y = h->out + (first + local) * h->out_token + (head < p.q_heads ? head : head - p.q_heads) * h->out_head;
-    *reinterpret_cast<uint4*>(y + at_a) = make_uint4(pack_bf16x2_rn(a[0], a[1]), pack_bf16x2_rn(a[2], a[3]),
-                                                     pack_bf16x2_rn(a[4], a[5]), pack_bf16x2_rn(a[6], a[7]));
-    if (at_b < p.dim)
-      *reinterpret_cast<uint4*>(y + at_b) = make_uint4(pack_bf16x2_rn(b[0], b[1]), pack_bf16x2_rn(b[2], b[3]),
-                                                       pack_bf16x2_rn(b[4], b[5]), pack_bf16x2_rn(b[6], b[7]));
+    uint4 v, u;
+    rotate_narrow(a, b, p.interleaved, v, u);
+    uint16_t* y = h->out + (first + local) * h->out_token + (key ? head - p.q_heads : head) * h->out_head;
+    *reinterpret_cast<uint4*>(y + at_a) = v;
+    if (at_b < p.dim) *reinterpret_cast<uint4*>(y + at_b) = u;
   }
 }
 
