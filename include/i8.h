@@ -542,7 +542,9 @@ i8_status i8_gemm_dequant_bias_bf16_w16(const int8_t* aq, const float* s_a,
  *   I8_OPT_FORCE_SPLITS K-splits to use for every shape, on every GEMM route
  *                       (int8, fp16-held and E4M3 codes; at most one split
  *                       per K block, and at most 8 on the few-token
- *                       kernel); 0 = the plan's own choice.
+ *                       kernel; the 4-bit route's few-token kernel, at most
+ *                       8, or 4 gated, where they leave no split without
+ *                       work); 0 = the plan's own choice.
  *   I8_OPT_MAX_CTAS     cap on the persistent grid (0 = one CTA per SM).
  *   I8_OPT_TILE_N       GEMM tile width, 128 or 256 (0 = the table).
  *   I8_OPT_CTA_PAIR     GEMM on CTA pairs (256 x 256 tiles per cluster of 2):

@@ -22,6 +22,13 @@
 // values of an output are 128 columns apart in the same lane.
 //
 // Persistent: tiles go round the pairs, the larger operand's blocks slowest.
+//
+// 8192 x 8192 x 4096: 87 us MX32 (6.3 PFLOP/s), 90 us NV16; gated, 4096 tokens by two
+// weights of 12288 x 4096, 141 and 146 us.  The products' own time at the clock that
+// the power limit leaves bounds it: without the weights' loads it takes 79 us, without
+// the copies of scales 87, without the epilogue 81.  Up to K = 2048 a tile's epilogue
+// (2 to 2.5 us: its reads of shared memory queue behind the products') is the longer
+// part.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -139,15 +139,18 @@ NewRows new_rows(PyObject* given, int64_t n, int64_t K, int fmt, bool scaled, in
 // FP4Rows of them: `given`, or a new one.
 PyObject* finish_rows(PyObject* given, const NewRows& r) {
   if (given != Py_None) return Py_NewRef(given);
-  PyObject* const codes = wrap(r.codes);
-  PyObject* const scales = wrap(r.scales);
-  PyObject* const row = r.row.defined() ? wrap(r.row) : Py_NewRef(Py_None);
-  PyObject* const args[3] = {codes, scales, row};
-  PyObject* const made = PyObject_Vectorcall(g_rows_type, args, 3, nullptr);
-  Py_DECREF(codes);
-  Py_DECREF(scales);
-  Py_DECREF(row);
+  // (a tuple's subclass, filled here: its own constructor runs in the interpreter)
+  PyTypeObject* const type = reinterpret_cast<PyTypeObject*>(g_rows_type);
+  PyObject* const made = type->tp_alloc(type, 3);
   if (!made) throw Refusal{nullptr, {}};
+  try {
+    PyTuple_SET_ITEM(made, 0, wrap(r.codes));
+    PyTuple_SET_ITEM(made, 1, wrap(r.scales));
+    PyTuple_SET_ITEM(made, 2, r.row.defined() ? wrap(r.row) : Py_NewRef(Py_None));
+  } catch (...) {
+    Py_DECREF(made);
+    throw;
+  }
   return made;
 }
 
