@@ -475,7 +475,9 @@ i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, 
 
 /* The whole layer: quantizes x [M, K] bf16 (row stride ldx, % 8 == 0) in the weights'
  * format into the workspace, then the product, or the gated one.  y may be x (the
- * product reads the workspace).
+ * product reads the workspace).  A few tokens (up to four) that share no memory with
+ * y are quantized inside the product, to the same codes, and the workspace stays as
+ * it was.
  *   ws / ws_bytes: 16-byte aligned, at least i8_linear_fp4_workspace_bytes(M, K,
  *   fmt); calls that may overlap in time do not share one                    */
 size_t i8_linear_fp4_workspace_bytes(int64_t M, int64_t K, int fmt);

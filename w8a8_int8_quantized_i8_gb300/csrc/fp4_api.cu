@@ -75,6 +75,25 @@ i8_status fp4_sizes(int64_t rows, int64_t K, int fmt) {
   return I8_OK;
 }
 
+i8_status check_quant(const void* x, int64_t rows, int64_t K, int64_t ldx, int fmt, const void* codes,
+                      const void* block_scales, const float* row_scales) {
+  if (i8_status e = fp4_sizes(rows, K, fmt)) return e;
+  if (ldx < K) return I8_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !codes || !block_scales || (fmt == I8_FP4_NV16 && !row_scales))) return I8_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(block_scales) || !aligned4(row_scales) || ldx % 8 != 0)
+    return I8_ERR_ALIGNMENT;
+  const Extent in{x, K * 2, rows, ldx * 2};
+  const Extent out[] = {{codes, rows * (K / 2)},
+                        {block_scales, static_cast<int64_t>(i8_fp4_block_scale_bytes(rows, K, fmt))},
+                        {row_scales, fmt == I8_FP4_NV16 ? rows * 4 : 0}};
+  for (const Extent& u : out) {
+    if (overlap(in, u)) return I8_ERR_INVALID_ARG;
+    for (const Extent& v : out)
+      if (&u != &v && overlap(u, v)) return I8_ERR_INVALID_ARG;
+  }
+  return I8_OK;
+}
+
 template <bool MX, bool NORM>
 cudaError_t launch_quant(Fp4QuantArgs& a, int64_t rows, cudaStream_t st) {
   const int vecs = a.deep;  // runs of 256 elements
@@ -239,12 +258,12 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], p));
 }
 
-template <bool MX, int NT, int ACT>
+template <bool MX, int NT, int ACT, bool FUSED = false>
 i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                         cudaStream_t st) {
   constexpr bool GATED = ACT != kFp4Plain;
-  using Cfg = Fp4StreamCfg<MX, NT, GATED>;
-  constexpr auto kern = fp4_stream_kernel<MX, NT, ACT>;
+  using Cfg = Fp4StreamCfg<MX, NT, GATED, FUSED>;
+  constexpr auto kern = fp4_stream_kernel<MX, NT, ACT, FUSED>;
   if (i8_status e = allow_smem<kern>(dev, Cfg::SMEM)) return e;
   CUtensorMap m0, m1, mt;
   if (i8_status e = encode_codes(&m0, *w[0], 128)) return e;
@@ -253,7 +272,8 @@ i8_status launch_stream(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows*
   } else {
     m1 = m0;
   }
-  if (i8_status e = encode_codes(&mt, t, NT)) return e;
+  if (FUSED) mt = m0;
+  else if (i8_status e = encode_codes(&mt, t, NT)) return e;
   int clusters[kFp4MaxSplits + 1];
   if (i8_status e = resident_clusters<kern>(dev, sms, Cfg::THREADS, Cfg::SMEM, Cfg::COLS, 1, Cfg::MAX_SPLITS, clusters)) return e;
   const int tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
@@ -300,6 +320,7 @@ template <bool MX, int ACT>
 i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* const (&w)[2], int dev, int sms,
                          cudaStream_t st) {
   constexpr bool GATED = ACT != kFp4Plain;
+  if (p.x) return launch_stream<MX, 16, ACT, true>(p, t, w, dev, sms, st);
   if (p.M <= 16) return launch_stream<MX, 16, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 32) return launch_stream<MX, 32, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 64) return launch_stream<MX, 64, ACT>(p, t, w, dev, sms, st);
@@ -339,28 +360,31 @@ i8_status check_product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp
   return overlap(out, {b0, w0->rows * 2}) || overlap(out, {b1, w0->rows * 2}) ? I8_ERR_INVALID_ARG : I8_OK;
 }
 
-i8_status product(const i8_fp4_rows* a, const i8_fp4_rows* w0, const i8_fp4_rows* w1, const void* b0, const void* b1,
-                  int activation, void* y, int64_t ldy, cudaStream_t st) {
-  if (i8_status e = check_product(a, w0, w1, b0, b1, y, ldy)) return e;
-  if (a->rows == 0 || w0->rows == 0) return I8_OK;
+// Of checked operands.  x: null, or the tokens themselves (bf16, ldx apart), read in
+// place of a's codes.
+i8_status product(const i8_fp4_rows& a, const uint16_t* x, int64_t ldx, const i8_fp4_rows* w0, const i8_fp4_rows* w1,
+                  const void* b0, const void* b1, int activation, void* y, int64_t ldy, cudaStream_t st) {
+  if (a.rows == 0 || w0->rows == 0) return I8_OK;
   Fp4GemmArgs p{};
   p.w[0] = {static_cast<const uint8_t*>(w0->block_scales), w0->row_scales, static_cast<const uint16_t*>(b0)};
   if (w1) p.w[1] = {static_cast<const uint8_t*>(w1->block_scales), w1->row_scales, static_cast<const uint16_t*>(b1)};
-  p.scales = static_cast<const uint8_t*>(a->block_scales);
-  p.row_scales = a->row_scales;
+  p.x = x;
+  p.ldx = ldx;
+  p.scales = static_cast<const uint8_t*>(a.block_scales);
+  p.row_scales = a.row_scales;
   p.y = static_cast<uint16_t*>(y);
   p.ldy = ldy;
-  p.M = static_cast<int>(a->rows);
+  p.M = static_cast<int>(a.rows);
   p.N = static_cast<int>(w0->rows);
-  p.K = static_cast<int>(a->K);
-  p.deep = fp4_deep(a->K);
+  p.K = static_cast<int>(a.K);
+  p.deep = fp4_deep(a.K);
   int dev, sms;
   if (i8_status e = current_device(&dev)) return e;
   if (i8_status e = device_sms(dev, &sms)) return e;
   const i8_fp4_rows* const w[2] = {w0, w1};
-  if (!w1) return launch_format<kFp4Plain>(p, *a, w, dev, sms, st);
-  return activation == I8_GATE_SILU ? launch_format<kFp4Silu>(p, *a, w, dev, sms, st)
-                                    : launch_format<kFp4Gelu>(p, *a, w, dev, sms, st);
+  if (!w1) return launch_format<kFp4Plain>(p, a, w, dev, sms, st);
+  return activation == I8_GATE_SILU ? launch_format<kFp4Silu>(p, a, w, dev, sms, st)
+                                    : launch_format<kFp4Gelu>(p, a, w, dev, sms, st);
 }
 
 // The tokens' rows in a workspace: codes, block scales, row scales.
@@ -393,10 +417,17 @@ i8_status linear(const void* x, int64_t M, int64_t K, int64_t ldx, const i8_fp4_
       return I8_ERR_INVALID_ARG;
   for (const void* b : {b0, b1})
     if (overlap({ws, static_cast<int64_t>(t.bytes)}, {b, w0->rows * 2})) return I8_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // the fewest tokens are quantized by the product itself, unless y lies where x does:
+  // other CTAs read x while one writes its channels of y
+  if (M <= fp4_fused_tokens(w0->fmt == I8_FP4_MX32) && !overlap({x, K * 2, M, ldx * 2}, {y, ((M - 1) * ldy + w0->rows) * 2})) {
+    if (i8_status e = check_quant(x, M, K, ldx, w0->fmt, t.rows.codes, t.rows.block_scales, t.rows.row_scales)) return e;
+    return product(t.rows, static_cast<const uint16_t*>(x), ldx, w0, w1, b0, b1, activation, y, ldy, st);
+  }
   if (i8_status e = i8_quant_rows_fp4(x, M, K, ldx, w0->fmt, const_cast<void*>(t.rows.codes),
                                       const_cast<void*>(t.rows.block_scales), const_cast<float*>(t.rows.row_scales), stream))
     return e;
-  return product(&t.rows, w0, w1, b0, b1, activation, y, ldy, reinterpret_cast<cudaStream_t>(stream));
+  return product(t.rows, nullptr, 0, w0, w1, b0, b1, activation, y, ldy, st);
 }
 
 // ----------------------------------------------------------------- heads
@@ -438,21 +469,8 @@ size_t i8_fp4_block_scale_bytes(int64_t rows, int64_t K, int fmt) {
 i8_status i8_quant_rows_fp4(const void* x, int64_t rows, int64_t K, int64_t ldx, int fmt, void* codes,
                             void* block_scales, float* row_scales, i8_stream_t stream) {
   I8_NVTX();
-  if (i8_status e = fp4_sizes(rows, K, fmt)) return e;
-  if (ldx < K) return I8_ERR_INVALID_ARG;
-  if (rows > 0 && (!x || !codes || !block_scales || (fmt == I8_FP4_NV16 && !row_scales))) return I8_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(codes) || !aligned16(block_scales) || !aligned4(row_scales) || ldx % 8 != 0)
-    return I8_ERR_ALIGNMENT;
+  if (i8_status e = check_quant(x, rows, K, ldx, fmt, codes, block_scales, row_scales)) return e;
   if (rows == 0) return I8_OK;
-  const Extent in{x, K * 2, rows, ldx * 2};
-  const Extent out[] = {{codes, rows * (K / 2)},
-                        {block_scales, static_cast<int64_t>(i8_fp4_block_scale_bytes(rows, K, fmt))},
-                        {row_scales, fmt == I8_FP4_NV16 ? rows * 4 : 0}};
-  for (const Extent& u : out) {
-    if (overlap(in, u)) return I8_ERR_INVALID_ARG;
-    for (const Extent& v : out)
-      if (&u != &v && overlap(u, v)) return I8_ERR_INVALID_ARG;
-  }
   Fp4QuantArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.ldx = ldx;
@@ -508,7 +526,8 @@ i8_status i8_add_rmsnorm_quant_fp4(const void* x, int64_t M, int64_t K, int64_t 
 i8_status i8_gemm_fp4_bias_bf16(const i8_fp4_rows* a, const i8_fp4_rows* w, const void* bias, void* y, int64_t ldy,
                                 i8_stream_t stream) {
   I8_NVTX();
-  return product(a, w, nullptr, bias, nullptr, 0, y, ldy, reinterpret_cast<cudaStream_t>(stream));
+  if (i8_status e = check_product(a, w, nullptr, bias, nullptr, y, ldy)) return e;
+  return product(*a, nullptr, 0, w, nullptr, bias, nullptr, 0, y, ldy, reinterpret_cast<cudaStream_t>(stream));
 }
 
 i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, const i8_fp4_rows* up,
@@ -516,7 +535,8 @@ i8_status i8_gemm_fp4_gated_bf16(const i8_fp4_rows* a, const i8_fp4_rows* gate, 
                                  i8_stream_t stream) {
   I8_NVTX();
   if (!up || (activation != I8_GATE_SILU && activation != I8_GATE_GELU)) return I8_ERR_INVALID_ARG;
-  return product(a, gate, up, gate_bias, up_bias, activation, y, ldy, reinterpret_cast<cudaStream_t>(stream));
+  if (i8_status e = check_product(a, gate, up, gate_bias, up_bias, y, ldy)) return e;
+  return product(*a, nullptr, 0, gate, up, gate_bias, up_bias, activation, y, ldy, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t i8_linear_fp4_workspace_bytes(int64_t M, int64_t K, int fmt) {

@@ -128,6 +128,8 @@ struct Fp4GemmArgs {
   Fp4Weight w[2];           // the second of a gated product only
   const uint8_t* scales;    // the tokens'
   const float* row_scales;  // null: ones
+  const uint16_t* x;        // or the tokens themselves, bf16
+  int64_t ldx;
   uint16_t* y;
   int64_t ldy;
   int M, N;                 // tokens, channels

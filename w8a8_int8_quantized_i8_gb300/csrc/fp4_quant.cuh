@@ -166,6 +166,24 @@ __device__ __forceinline__ float fp4_rstd(const float (&ss)[3], int K, float eps
   return __fdiv_rn(0x1p80f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[2], n), e)));
 }
 
+// NV16: a row's scale from the bits of its largest magnitude, and s and 1 / s for its
+// codes; s = 0 where they want a power of two before (fp4_row_scaled).
+__device__ __forceinline__ float fp4_row_scale(uint32_t amax, float& s, float& inverse) {
+  const int k = nv16_row_exponent(amax);
+  inverse = pow2f(-k);
+  s = abs(k) <= 100 ? pow2f(k) : 0.0f;
+  if (amax >= 0x7F800000u) return __uint_as_float(0x7FC00000u);  // infinity or NaN in the row
+  return amax == 0 ? 0.0f : pow2f(k);
+}
+__device__ __forceinline__ void fp4_row_scaled(float (&t)[8], uint32_t& top, float& s, float& inverse) {
+  if (s == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = __fmul_rn(t[i], inverse);
+    top = __float_as_uint(__fmul_rn(__uint_as_float(top), inverse));
+    s = inverse = 1.0f;
+  }
+}
+
 // The codes and scales of the warp's 256 elements from `first` on, of which this
 // lane holds 8 with the largest magnitude `top` (the whole warp calls).  codes and
 // scales: the row's, the latter where its tiles' first part has it.
@@ -176,14 +194,7 @@ __device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, uint8_t* cod
   if constexpr (MX) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
   float t[8];
   fp4_widen<NORM>(a, first + lane * 8, held, t);
-  if constexpr (!MX) {
-    if (s == 0.0f) {  // not for the fast quotients: times a power of two before
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __fmul_rn(t[i], inverse);
-      top = __float_as_uint(__fmul_rn(__uint_as_float(top), inverse));
-      s = inverse = 1.0f;
-    }
-  }
+  if constexpr (!MX) fp4_row_scaled(t, top, s, inverse);
   uint32_t scale;
   const uint32_t c = fp4_codes8<MX>(t, top, s, inverse, &scale);
   const int e = first + lane * 8;
@@ -281,14 +292,9 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
           if (mine) fp4_store_h<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
       }
     }
-    const int k = nv16_row_exponent(amax);
-    if (!MX) inverse = pow2f(-k), s = abs(k) <= 100 ? pow2f(k) : 0.0f;
-    if (mine && warp == 0 && lane == 0) {
-      float scale = MX ? 1.0f : amax == 0 ? 0.0f : pow2f(k);
-      if (NORM && amax != 0) scale = __fmul_rn(scale, fp4_rstd(ss, a.K, a.eps));
-      if (!MX && amax >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);  // infinity or NaN in the row
-      a.row_scales[row] = scale;
-    }
+    float scale = MX ? 1.0f : fp4_row_scale(amax, s, inverse);
+    if (NORM && amax != 0) scale = __fmul_rn(scale, fp4_rstd(ss, a.K, a.eps));
+    if (mine && warp == 0 && lane == 0) a.row_scales[row] = scale;
   }
   uint8_t* codes = a.codes + row * (a.K / 2);
   uint8_t* scales = a.scales + fp4_scale_at(row, 0, a.deep, MX ? 32 : 16);

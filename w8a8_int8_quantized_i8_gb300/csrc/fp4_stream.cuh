@@ -17,11 +17,17 @@
 // four tokens of a channel in 16 bytes, which adds them in the order of the splits
 // (the same bits every time).  No workspace, no second launch.
 //
+// The fewest tokens, still bf16 (FUSED), are quantized here by the two warps without
+// another role, in turns at the stages, while the weights are on their way: no
+// launch of its own, no rows in memory.  What a row's scale needs (NV16) is the row's
+// largest magnitude, which each CTA finds by itself (2 K bytes a token from L2; by
+// the cluster together, with a barrier of it, one token took 2.5 us more).
+//
 // Bound by HBM where the weights come from there, else by a chain of latencies: one
-// token by 6144 x 4096 (NV16, 4 splits) 4.9 us from L2, of them 1 to the first
-// tile, 2 of products, 1 for the cluster's meeting; four tokens by two weights of
-// 11008 x 4096, from HBM, 13.5 us with the quantizer (50 MB, 5.2 TB/s while they
-// stream); 256 tokens by 4096 x 4096 8.2 us.
+// token by 6144 x 4096 (NV16, 4 splits) 4.9 us from L2 behind a quantizer, of them 1
+// to the first tile, 2 of products, 1 for the cluster's meeting, and 4.5 with the
+// quantizing in it; one token by two weights of 11008 x 4096, from HBM, 10.2 us (50
+// MB, 5.0 TB/s); 256 tokens by 4096 x 4096 8.2 us.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -29,11 +35,19 @@
 #include <cstdint>
 
 #include "fp4_mma.cuh"
+#include "fp4_quant.cuh"
 
 namespace i8 {
 
 constexpr int kFp4MaxSplits = 8;
 constexpr int kFp4Prefetch = 6;  // tiles of K
+
+// The most tokens that a CTA quantizes for itself.  us measured, so and with the
+// quantizer's launch, of 1, 2, 3, 4 tokens by 6144 x 4096 from HBM:
+//   MX32  4.8 4.9 4.8 4.8 and 6.5 6.6 6.6 6.6; by 28672 x 8192 20.9 .. 22.6 and 22.6 .. 22.9
+//   NV16  5.3 5.5 and 6.8 6.9; built for four, 5.7 6.3 6.8 7.6: the rows' largest
+//         magnitudes are found before the first product, by two warps
+constexpr int fp4_fused_tokens(bool mx) { return mx ? 4 : 2; }
 
 // Tokens that one of `splits` CTAs finishes: fours.
 __host__ __device__ constexpr int fp4_each(int tokens, int splits) { return ((tokens + splits - 1) / splits + 3) / 4 * 4; }
@@ -45,16 +59,17 @@ constexpr int fp4_red_tokens(int tokens, int most) {
   return n;
 }
 
-template <bool MX, int NT, bool GATED>
+template <bool MX, int NT, bool GATED, bool FUSED = false>
 struct Fp4StreamCfg {
   static constexpr int WEIGHTS = GATED ? 2 : 1;
+  static constexpr int TOKENS = fp4_fused_tokens(MX);  // FUSED
   static constexpr int SCALES = fp4_tile_bytes(MX ? 32 : 16);
   static constexpr int PARTS = SCALES / 512;
   static constexpr int OFF_T = WEIGHTS * 16384;
   static constexpr int OFF_WS = OFF_T + NT * 128;
   static constexpr int OFF_TS = OFF_WS + WEIGHTS * SCALES;
   static constexpr int STAGE = OFF_TS + SCALES;
-  static constexpr uint32_t TX = WEIGHTS * (16384 + SCALES) + NT * 128 + SCALES;
+  static constexpr uint32_t TX = WEIGHTS * (16384 + SCALES) + (FUSED ? 0 : NT * 128 + SCALES);
   // the sums to be finished, 512 bytes for each split, weight and token: a region
   // of their own for the fewest tokens, which saves a barrier of the cluster, else
   // the ring
@@ -80,14 +95,43 @@ struct Fp4StreamCfg {
   // co-resident CTAs never wait for one another's tensor memory
   static_assert(STAGES >= 2 && (COLS <= 256 || SMEM > 120 * 1024));
   static_assert(RED_OWN != 0 || RED <= STAGES * STAGE);
+  static_assert(!FUSED || NT == 16);
 };
 
-template <bool MX, int NT, int ACT>
+// Codes and scales of 256 elements of a token, of which this lane holds 8 (the whole
+// warp calls), where a stage's tile of tokens has them (128-byte swizzle) and its
+// tile of scales.
+template <bool MX>
+__device__ __forceinline__ void fp4_smem256(uint32_t codes, uint32_t scales, int row, int lane, bool inside, const uint4& x,
+                                            float s, float inverse) {
+  const Fp4Held<false> held{x};
+  float unused = 0.0f;
+  const Fp4QuantArgs none{};
+  uint32_t top = fp4_top<false>(none, 0, held, unused);
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  if constexpr (MX) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  float t[8];
+  fp4_widen<false>(none, 0, held, t);
+  if constexpr (!MX) fp4_row_scaled(t, top, s, inverse);
+  uint32_t scale;
+  const uint32_t c = fp4_codes8<MX>(t, top, s, inverse, &scale);
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(codes + row * 128u + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4u),
+               "r"(inside ? c : 0u)
+               : "memory");
+  constexpr int LB = MX ? 4 : 2;  // lanes of a block
+  scale = inside ? scale << (8 * (lane / LB % 4)) : 0u;
+  scale |= __shfl_xor_sync(0xFFFFFFFFu, scale, LB);
+  scale |= __shfl_xor_sync(0xFFFFFFFFu, scale, 2 * LB);
+  if (lane % (4 * LB) == 0)
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(scales + lane / (4 * LB) * 512u + row * 16u), "r"(scale) : "memory");
+}
+
+template <bool MX, int NT, int ACT, bool FUSED>
 __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
     fp4_stream_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
                       const __grid_constant__ CUtensorMap tm_t, const Fp4GemmArgs p) {
   constexpr bool GATED = ACT != kFp4Plain;
-  using Cfg = Fp4StreamCfg<MX, NT, GATED>;
+  using Cfg = Fp4StreamCfg<MX, NT, GATED, FUSED>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[Cfg::STAGES];
   __shared__ __align__(8) uint64_t empty[Cfg::STAGES];
@@ -95,6 +139,7 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ float token_scale[NT];
+  __shared__ uint32_t warp_max[2][FUSED ? Cfg::TOKENS : 1];
   volatile int* abort_flag = &abort_word;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -104,7 +149,7 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), FUSED ? 2 : 1);  // the producer, and a quantizing warp
       mbar_init(smem_u32(&empty[s]), 1);
     }
     mbar_init(smem_u32(&done), 1);
@@ -118,7 +163,7 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_w0);
     if constexpr (GATED) tma_prefetch_desc(&tm_w1);
-    tma_prefetch_desc(&tm_t);
+    if constexpr (!FUSED) tma_prefetch_desc(&tm_t);
     // this CTA's weights on their way into L2 while the kernel before drains, more of
     // them than the ring holds: HBM's latency is paid once
     const int64_t ws0 = (static_cast<int64_t>(n_tile) * p.deep + kb0) * Cfg::SCALES;
@@ -155,17 +200,17 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
     const int64_t tile = Cfg::SCALES;
     const uint8_t* ws0 = p.w[0].scales + static_cast<int64_t>(n_tile) * p.deep * tile;
     const uint8_t* ws1 = GATED ? p.w[1].scales + static_cast<int64_t>(n_tile) * p.deep * tile : nullptr;
-    const uint8_t* ts = p.scales + static_cast<int64_t>(m0 >> 7) * p.deep * tile;
+    const uint8_t* ts = FUSED ? nullptr : p.scales + static_cast<int64_t>(m0 >> 7) * p.deep * tile;
     for (int kb = kb0; kb < kb1; ++kb) {
       const uint32_t bar = smem_u32(&full[s]), st = ring + static_cast<uint32_t>(s * Cfg::STAGE);
       if (!(ok = mbar_wait(smem_u32(&empty[s]), ph ^ 1u, abort_flag))) break;
       mbar_arrive_expect_tx(bar, Cfg::TX);
       tma_load_2d(st, &tm_w0, bar, kb * 128, n0);
       if constexpr (GATED) tma_load_2d(st + 16384, &tm_w1, bar, kb * 128, n0);
-      tma_load_2d(st + Cfg::OFF_T, &tm_t, bar, kb * 128, m0);
+      if constexpr (!FUSED) tma_load_2d(st + Cfg::OFF_T, &tm_t, bar, kb * 128, m0);
       bulk_load(st + Cfg::OFF_WS, ws0 + kb * tile, Cfg::SCALES, bar);
       if constexpr (GATED) bulk_load(st + Cfg::OFF_WS + Cfg::SCALES, ws1 + kb * tile, Cfg::SCALES, bar);
-      bulk_load(st + Cfg::OFF_TS, ts + kb * tile, Cfg::SCALES, bar);
+      if constexpr (!FUSED) bulk_load(st + Cfg::OFF_TS, ts + kb * tile, Cfg::SCALES, bar);
       ++issued;
       if (++s == Cfg::STAGES) s = 0, ph ^= 1u;
     }
@@ -206,6 +251,70 @@ __global__ void __launch_bounds__(NT >= 64 ? 256 : 128, 1)
     }
     commit_elected(leader, smem_u32(&done));
     mbar_wait_bounded(smem_u32(&done), 0u, 100000000ull);
+  } else if (FUSED && warp >= 2) {
+    constexpr int TOKENS = Cfg::TOKENS;
+    const int me = warp - 2;
+    auto load = [&](int row, int kb, int end) {
+      const int e = kb * kFp4TileK + lane * 8;
+      return row < p.M && kb < end && e < p.K ? *reinterpret_cast<const uint4*>(p.x + row * p.ldx + e)
+                                              : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 next[TOKENS];
+#pragma unroll
+    for (int row = 0; row < TOKENS; ++row) next[row] = load(row, kb0 + me, kb1);
+    float s[TOKENS], inverse[TOKENS];
+#pragma unroll
+    for (int row = 0; row < TOKENS; ++row) s[row] = inverse[row] = 1.0f;
+    if constexpr (!MX) {
+      constexpr int BATCH = 8;  // loads of a row in flight
+      uint32_t top[TOKENS] = {};  // pairs of magnitudes, the signs undefined
+      for (int kb = me; kb < p.deep; kb += 2 * BATCH) {
+        uint4 v[TOKENS][BATCH];
+#pragma unroll
+        for (int row = 0; row < TOKENS; ++row)
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) v[row][i] = load(row, kb + 2 * i, p.deep);
+#pragma unroll
+        for (int row = 0; row < TOKENS; ++row)
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i)
+            for (uint32_t x : {v[row][i].x, v[row][i].y, v[row][i].z, v[row][i].w})
+              top[row] = absmax_nan_bf16x2(top[row], x);
+      }
+#pragma unroll
+      for (int row = 0; row < TOKENS; ++row) {
+        const uint32_t m = top[row] & 0x7FFF7FFFu, t = __reduce_max_sync(0xFFFFFFFFu, max(m << 16, m & 0xFFFF0000u));
+        if (lane == 0) warp_max[me][row] = t;
+      }
+      named_bar_sync(1, 64);
+#pragma unroll
+      for (int row = 0; row < TOKENS; ++row) {
+        const float scale = fp4_row_scale(max(warp_max[0][row], warp_max[1][row]), s[row], inverse[row]);
+        if (me == 0 && lane == 0) token_scale[row] = scale;
+      }
+    }
+    if (me == 1 && lane < NT && (MX || lane >= TOKENS)) token_scale[lane] = 1.0f;
+    int stage = me;
+    uint32_t ph = 0;
+    for (int kb = kb0 + me; kb < kb1; kb += 2) {
+      uint4 v[TOKENS];
+#pragma unroll
+      for (int row = 0; row < TOKENS; ++row) {
+        v[row] = next[row];
+        next[row] = load(row, kb + 2, kb1);
+      }
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&empty[stage]), ph ^ 1u, abort_flag))) break;
+      const uint32_t st = ring + static_cast<uint32_t>(stage * Cfg::STAGE);
+#pragma unroll
+      for (int row = 0; row < TOKENS; ++row)
+        if (row < p.M)
+          fp4_smem256<MX>(st + Cfg::OFF_T, st + Cfg::OFF_TS, row, lane, kb * kFp4TileK + lane * 8 < p.K, v[row], s[row],
+                          inverse[row]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&full[stage]));
+      if ((stage += 2) >= Cfg::STAGES) stage -= Cfg::STAGES, ph ^= 1u;
+    }
   } else if (warp >= 2) {
     for (int i = threadIdx.x - 64; i < NT; i += Cfg::THREADS - 64)
       token_scale[i] = m0 + i < p.M ? (p.row_scales ? p.row_scales[m0 + i] : 1.0f) : 0.0f;
