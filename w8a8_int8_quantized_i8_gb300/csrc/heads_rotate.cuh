@@ -126,10 +126,10 @@ __device__ __forceinline__ void rotate_narrow(const float (&a)[8], const float (
   u = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// The norm's factor where some row of the warp has squares out of fp32's range (the
-// whole warp calls).  Such a row's elements are left times 2^80 or 2^-80, which is
-// exact, so that neither its squares nor the factor leave the range; the others stay
-// as they are, and get the factor that the same sums give.
+// The norm's factor of the rows whose squares leave fp32's range (the whole warp
+// calls).  Their elements are left times 2^80 or 2^-80, which is exact, so that
+// neither their squares nor the factor leave the range.  What it returns for the
+// warp's other rows, which stay as they are, is not used: a row's bits are its own.
 __device__ __forceinline__ float rotate_far_rstd(const RotateArgs& p, float sum, float (&a)[8], float (&b)[8]) {
   const float n = static_cast<float>(p.dim);
   const bool small = sum < 0x1p-60f;
@@ -215,8 +215,11 @@ __global__ void __launch_bounds__(kRotateThreads, 4) heads_rmsnorm_rotate_kernel
       for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
       for (int d = 1 << p.lanes_log2 >> 1; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
       r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
-      // (a row without a norm stays as it is)
-      if (__any_sync(0xFFFFFFFFu, valid && h->weight && !fp4_in_range(ss))) r = rotate_far_rstd(p, h->weight ? ss : 1.0f, a, b);
+      const bool far = h->weight && !fp4_in_range(ss);  // (a row without a norm stays as it is)
+      if (__any_sync(0xFFFFFFFFu, valid && far)) {
+        const float f = rotate_far_rstd(p, far ? ss : 1.0f, a, b);
+        if (far) r = f;
+      }
       if (!h->weight) r = 1.0f;
     }
     const bool key = head >= p.q_heads;
