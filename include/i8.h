@@ -280,7 +280,8 @@ i8_status i8_gelu_quant_act_pertoken(const void* x_bf16, int64_t M, int64_t K,
  *   q [M,K] codes and s_a [M] as in i8_layernorm_quant_act_pertoken,
  *   h [M,K] bf16 or NULL (row stride ldh, % 8 == 0); h may be residual or x
  *   (in place, with the same stride; no row of it shares memory with another
- *   row of theirs: I8_ERR_INVALID_ARG).  K % 16 == 0, K <= 32768.             */
+ *   row of theirs, or with its own from another element on:
+ *   I8_ERR_INVALID_ARG).  K % 16 == 0, K <= 32768.                            */
 i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x_bf16, int64_t M, int64_t K,
                                             int64_t ldx, const void* residual_bf16,
                                             int64_t ldr, const void* weight_bf16, float eps,

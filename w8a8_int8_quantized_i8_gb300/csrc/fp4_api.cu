@@ -494,9 +494,12 @@ i8_status i8_add_rmsnorm_quant_fp4(const void* x, int64_t M, int64_t K, int64_t 
       !aligned16(residual) || (residual && ldr % 8 != 0) || !aligned16(weight) || !aligned16(h) || (h && ldh % 8 != 0))
     return I8_ERR_ALIGNMENT;
   if (M == 0) return I8_OK;
-  // a row's CTA writes its h when others have not read theirs
+  // a row's CTA writes its h when others have not read theirs, and a thread the
+  // elements that it has read when others of the row have not read theirs
   const Extent to{h, K * 2, M, ldh * 2}, in{x, K * 2, M, ldx * 2}, other{residual, K * 2, M, ldr * 2}, gain{weight, K * 2};
-  if (rows_cross(to, in) || rows_cross(to, other) || overlap(to, gain)) return I8_ERR_INVALID_ARG;
+  for (const Extent& from : {in, other})
+    if (rows_cross(to, from) || rows_shifted(to, from)) return I8_ERR_INVALID_ARG;
+  if (overlap(to, gain)) return I8_ERR_INVALID_ARG;
   const Extent out[] = {{codes, M * (K / 2)},
                         {block_scales, static_cast<int64_t>(i8_fp4_block_scale_bytes(M, K, fmt))},
                         {row_scales, M * 4}};

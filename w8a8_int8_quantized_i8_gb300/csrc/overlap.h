@@ -1,5 +1,6 @@
 // overlap.h -- whether operands of a call share memory, for the host's checks.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 
@@ -43,6 +44,26 @@ inline bool rows_cross(const Extent& a, const Extent& b) {
   const int64_t k = d >= 0 ? d / a.stride : -((-d + a.stride - 1) / a.stride), r = d - k * a.stride;
   return (k != 0 && std::abs(k) < a.rows && r < a.bytes) ||
          (k + 1 != 0 && std::abs(k + 1) < a.rows && a.stride - r < b.bytes);
+}
+
+// Whether some row of `a` shares bytes with the same row of `b` (both of as many rows)
+// and does not begin where it does.
+inline bool rows_shifted(const Extent& a, const Extent& b) {
+  if (!a.base || !b.base || a.rows <= 0) return false;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.base) - reinterpret_cast<uintptr_t>(a.base));
+  // row i of b begins d + i * drift behind row i of a: the rows i where that is small
+  const int64_t drift = b.stride - a.stride;
+  int64_t first = 0, last = 0;
+  if (a.rows > 1 && drift != 0) {
+    const int64_t middle = -d / drift, around = std::max(a.bytes, b.bytes) / std::abs(drift) + 1;
+    first = std::max<int64_t>(0, middle - around);
+    last = std::min(a.rows - 1, middle + around);
+  }
+  for (int64_t i = first; i <= last; ++i) {
+    const int64_t at = d + i * drift;
+    if (at != 0 && at < a.bytes && -at < b.bytes) return true;
+  }
+  return false;
 }
 
 // Whether rows [tokens, heads] of `dim` elements, these strides apart, share an

@@ -309,10 +309,11 @@ i8_status i8_add_rmsnorm_quant_act_pertoken(const void* x, int64_t M, int64_t K,
       ldq % (fmt == kQuantF16 ? 8 : 16) != 0 || !aligned16(residual) ||
       (residual && ldr % 8 != 0) || !aligned16(weight) || !aligned16(h) || (h && ldh % 8 != 0))
     return I8_ERR_ALIGNMENT;
-  // a row's CTA writes its h when others have not read theirs
+  // a row's CTA writes its h when others have not read theirs, and a thread the
+  // elements that it has read when others of the row have not read theirs
   const Extent to{h, K * 2, M, ldh * 2};
-  if (rows_cross(to, {x, K * 2, M, ldx * 2}) || rows_cross(to, {residual, K * 2, M, ldr * 2}))
-    return I8_ERR_INVALID_ARG;
+  for (const Extent& from : {Extent{x, K * 2, M, ldx * 2}, Extent{residual, K * 2, M, ldr * 2}})
+    if (rows_cross(to, from) || rows_shifted(to, from)) return I8_ERR_INVALID_ARG;
   if (M == 0) return I8_OK;
   const int vecs = static_cast<int>(K / 8);
   int G = 1;
