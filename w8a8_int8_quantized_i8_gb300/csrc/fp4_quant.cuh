@@ -20,6 +20,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "fp4_format.cuh"
@@ -153,17 +154,20 @@ __device__ __forceinline__ void warp_sum(float& v) {
 // Whether a sum of squares says all there is to say.
 __device__ __forceinline__ bool fp4_in_range(float ss) { return ss >= 0x1p-60f && ss < INFINITY; }
 
-// 1 / sqrt(mean(h^2) + eps) from the sum of squares and, where that is out of
-// range, the two others.
-__device__ __forceinline__ float fp4_rstd(const float (&ss)[3], int K, float eps) {
+// scale / sqrt(mean(h^2) + eps) from the sum of squares and, where that is out of
+// range, the two others.  The factor of rows below 2^-128 is no fp32 number (eps = 0):
+// its product with NV16's scale is one again, and MX32 gets the largest there is.
+__device__ __forceinline__ float fp4_normed_scale(float scale, const float (&ss)[3], int K, float eps) {
   const float n = static_cast<float>(K);
-  if (fp4_in_range(ss[0])) return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps)));
+  if (fp4_in_range(ss[0])) return __fmul_rn(scale, __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps))));
   // (eps beside squares of 2^64 and more is nothing)
-  if (!(ss[0] < 1.0f)) return __fdiv_rn(0x1p-80f, __fsqrt_rn(__fdiv_rn(ss[1], n)));
+  if (!(ss[0] < 1.0f)) return __fmul_rn(scale, __fdiv_rn(0x1p-80f, __fsqrt_rn(__fdiv_rn(ss[1], n))));
   // where eps * 2^160 overflows, squares below 2^-60 are nothing beside eps
   const float e = __fmul_rn(__fmul_rn(eps, 0x1p80f), 0x1p80f);
-  if (!(e < INFINITY)) return __fdiv_rn(1.0f, __fsqrt_rn(eps));
-  return __fdiv_rn(0x1p80f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[2], n), e)));
+  if (!(e < INFINITY)) return __fmul_rn(scale, __fdiv_rn(1.0f, __fsqrt_rn(eps)));
+  const float d = __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[2], n), e));
+  const float r = d < 1.0f ? __fmul_rn(__fdiv_rn(scale, d), 0x1p80f) : __fmul_rn(scale, __fdiv_rn(0x1p80f, d));
+  return r == INFINITY ? FLT_MAX : r;
 }
 
 // NV16: a row's scale from the bits of its largest magnitude, and s and 1 / s for its
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
       }
     }
     float scale = MX ? 1.0f : fp4_row_scale(amax, s, inverse);
-    if (NORM && amax != 0) scale = __fmul_rn(scale, fp4_rstd(ss, a.K, a.eps));
+    if (NORM && amax != 0) scale = fp4_normed_scale(scale, ss, a.K, a.eps);
     if (mine && warp == 0 && lane == 0) a.row_scales[row] = scale;
   }
   uint8_t* codes = a.codes + row * (a.K / 2);
