@@ -451,7 +451,9 @@ i8_status i8_quant_rows_fp4(const void* x_bf16, int64_t rows, int64_t K, int64_t
 /* i8_add_rmsnorm_quant_act_pertoken with a 4-bit output: h = x + residual, t = h *
  * weight (fp32 steps), codes and block scales of t as above, and row_scales [M] =
  * (s of the row, 1 for MX32) / sqrt(mean(h^2) + eps), at most fp32's largest number
- * (which rows below 2^-128 reach with eps = 0); a row of zeros keeps s.
+ * (which rows below 2^-128 reach with eps = 0); a row of zeros keeps s.  A row whose
+ * t leaves fp32's range where its h does not is multiplied by 2^-126 before, and its
+ * scale by 2^126.
  * Arguments as there, but K as above.                                       */
 i8_status i8_add_rmsnorm_quant_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, const void* residual_bf16,
                                    int64_t ldr, const void* weight_bf16, float eps, int fmt, void* codes,

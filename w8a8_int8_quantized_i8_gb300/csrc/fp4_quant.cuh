@@ -126,15 +126,24 @@ __device__ __forceinline__ uint32_t fp4_top(const Fp4QuantArgs& a, int e, const 
   }
 }
 
-// The squares' sums of rows whose squares leave fp32's range, of h * 2^-80 and of h *
-// 2^80.
-__device__ __forceinline__ void fp4_far_squares(const Fp4Held<true>& held, float (&ss)[3]) {
+// Of rows whose squares, or whose t, leave fp32's range: the squares' sums of h * 2^-80
+// and of h * 2^80, and the bits of the largest magnitude of t * 2^-126.
+__device__ __forceinline__ void fp4_down(Fp4Held<true>& held) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) held.h[j] = __fmul_rn(held.h[j], 0x1p-126f);
+}
+__device__ __forceinline__ void fp4_far(const Fp4QuantArgs& a, int e, const Fp4Held<true>& held, float (&ss)[3],
+                                        uint32_t& down) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float s = held.h[j] * 0x1p-80f, l = held.h[j] * 0x1p80f;
     ss[1] = fmaf(s, s, ss[1]);
     ss[2] = fmaf(l, l, ss[2]);
   }
+  Fp4Held<true> low = held;
+  float unused = 0.0f;
+  fp4_down(low);
+  down = max(down, fp4_top<true>(a, e, low, unused));
 }
 
 template <bool NORM>
@@ -155,13 +164,20 @@ __device__ __forceinline__ void warp_sum(float& v) {
 __device__ __forceinline__ bool fp4_in_range(float ss) { return ss >= 0x1p-60f && ss < INFINITY; }
 
 // scale / sqrt(mean(h^2) + eps) from the sum of squares and, where that is out of
-// range, the two others.  The factor of rows below 2^-128 is no fp32 number (eps = 0):
+// range, the two others; times 2^126 where `over`, t having been taken times 2^-126
+// (by steps that stay in range).  The factor of rows below 2^-128 is no fp32 number (eps = 0):
 // its product with NV16's scale is one again, and MX32 gets the largest there is.
-__device__ __forceinline__ float fp4_normed_scale(float scale, const float (&ss)[3], int K, float eps) {
+__device__ __forceinline__ float fp4_normed_scale(float scale, const float (&ss)[3], int K, float eps, bool over) {
   const float n = static_cast<float>(K);
-  if (fp4_in_range(ss[0])) return __fmul_rn(scale, __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps))));
+  if (fp4_in_range(ss[0])) {
+    const float r = __fmul_rn(scale, __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], n), eps))));
+    return over ? __fmul_rn(r, 0x1p126f) : r;
+  }
   // (eps beside squares of 2^64 and more is nothing)
-  if (!(ss[0] < 1.0f)) return __fmul_rn(scale, __fdiv_rn(0x1p-80f, __fsqrt_rn(__fdiv_rn(ss[1], n))));
+  if (!(ss[0] < 1.0f)) {
+    const float m = over ? 0x1p23f : 0x1p-40f;  // squared, 2^-80 or 2^-80 * 2^126
+    return __fmul_rn(__fmul_rn(__fmul_rn(scale, m), __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss[1], n)))), m);
+  }
   // where eps * 2^160 overflows, squares below 2^-60 are nothing beside eps
   const float e = __fmul_rn(__fmul_rn(eps, 0x1p80f), 0x1p80f);
   if (!(e < INFINITY)) return __fmul_rn(scale, __fdiv_rn(1.0f, __fsqrt_rn(eps)));
@@ -212,8 +228,14 @@ __device__ __forceinline__ void fp4_store256(const Fp4QuantArgs& a, uint8_t* cod
     *reinterpret_cast<uint32_t*>(scales + (first >> 8) * fp4_tile_bytes(8 * LB) + lane / (4 * LB) * 512) = scale;
 }
 
+// Registers a thread, at most: what the usual row needs.  The rare rows' code would take
+// more and cost CTAs (8192 x 8192 with the norm, NV16: 79 us, and 99 with 86 registers).
+constexpr int fp4_quant_registers(int V, bool mx, bool norm) {
+  return V <= 1 ? (norm && !mx ? 40 : 32) : norm && V == 2 ? 56 : norm && V == 4 ? 80 : V == 8 && mx && !norm ? 64 : 128;
+}
+
 template <int V, bool MX, bool NORM>
-__global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
+__global__ void __maxnreg__(fp4_quant_registers(V, MX, NORM)) fp4_quant_kernel(const Fp4QuantArgs a) {
   __shared__ float red_s[3][32];
   __shared__ uint32_t red_m[32];
   constexpr int H = V > 0 ? V : 1;
@@ -246,6 +268,7 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
     }
   }
   float s = 1.0f, inverse = 1.0f;
+  bool over = false;  // t leaves fp32's range, h does not
   if (!MX || NORM) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     if constexpr (NORM) warp_sum(ss[0]);
@@ -263,41 +286,55 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
       }
     }
     if constexpr (NORM) {
-      // squares out of fp32's range in a row of the CTA: the others' sums as well
-      if (__syncthreads_or(!fp4_in_range(ss[0]))) {
+      // squares or t out of fp32's range in a row of the CTA: the other sums as well
+      if (__syncthreads_or(!fp4_in_range(ss[0]) || amax == 0x7F800000u)) {
+        uint32_t down = 0;
         if constexpr (V > 0) {
 #pragma unroll
-          for (int i = 0; i < H; ++i) fp4_far_squares(held[i], ss);
+          for (int i = 0; i < H; ++i) fp4_far(a, warp * span + i * 256 + lane * 8, held[i], ss, down);
         } else {
           for (int first = warp * span; first < end; first += step) {
             fp4_load8<NORM>(a, row, first + lane * 8, held[0]);  // (h is not stored yet)
-            fp4_far_squares(held[0], ss);
+            fp4_far(a, first + lane * 8, held[0], ss, down);
           }
         }
         warp_sum(ss[1]);
         warp_sum(ss[2]);
+        down = __reduce_max_sync(0xFFFFFFFFu, down);
         if (a.G > 1) {
           if (lane == 0) {
             red_s[1][local * a.G + warp] = ss[1];
             red_s[2][local * a.G + warp] = ss[2];
+            red_m[local * a.G + warp] = down;  // (the first ones have been read)
           }
           __syncthreads();
           ss[1] = ss[2] = 0.0f;
           for (int j = 0; j < a.G; ++j) {
             ss[1] += red_s[1][local * a.G + j];
             ss[2] += red_s[2][local * a.G + j];
+            down = max(down, red_m[local * a.G + j]);
           }
         }
+        over = amax == 0x7F800000u && ss[1] < INFINITY;
+        if (over) amax = down;
       }
       // (each thread has read the elements that it writes)
       if constexpr (V > 0) {
 #pragma unroll
         for (int i = 0; i < H; ++i)
           if (mine) fp4_store_h<NORM>(a, row, warp * span + i * 256 + lane * 8, held[i]);
+        if (over) {
+          float unused = 0.0f;
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            fp4_down(held[i]);
+            top[i] = fp4_top<NORM>(a, warp * span + i * 256 + lane * 8, held[i], unused);
+          }
+        }
       }
     }
     float scale = MX ? 1.0f : fp4_row_scale(amax, s, inverse);
-    if (NORM && amax != 0) scale = fp4_normed_scale(scale, ss, a.K, a.eps);
+    if (NORM && amax != 0) scale = fp4_normed_scale(scale, ss, a.K, a.eps, over);
     if (mine && warp == 0 && lane == 0) a.row_scales[row] = scale;
   }
   uint8_t* codes = a.codes + row * (a.K / 2);
@@ -313,6 +350,8 @@ __global__ void __launch_bounds__(512) fp4_quant_kernel(const Fp4QuantArgs a) {
       float sum = 0.0f;
       fp4_load8<NORM>(a, row, first + lane * 8, held[0]);
       fp4_store_h<NORM>(a, row, first + lane * 8, held[0]);
+      if constexpr (NORM)
+        if (over) fp4_down(held[0]);
       fp4_store256<MX, NORM>(a, codes, scales, first, lane, held[0], fp4_top<NORM>(a, first + lane * 8, held[0], sum), s,
                              inverse);
     }
