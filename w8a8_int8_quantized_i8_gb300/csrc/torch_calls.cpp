@@ -9,7 +9,8 @@
 // from the launch before.
 //
 // Nothing leaves a function here by a C++ exception: Refusal (an argument that is
-// refused) and whatever torch throws become Python errors.
+// refused) becomes its Python error, and what torch throws the one that torch's own
+// functions raise (torch.OutOfMemoryError where there is no room for an output).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -17,6 +18,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -439,16 +441,14 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", ARGS, n);
     return nullptr;
   }
+  HANDLE_TH_ERRORS
   try {
     return CALL(args);
   } catch (const Refusal& r) {
     if (r.type) PyErr_SetString(r.type, r.what.c_str());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    return nullptr;
   }
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 template <PyObject* (*CALL)(PyObject* const*), int ARGS>
