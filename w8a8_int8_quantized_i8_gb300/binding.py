@@ -85,7 +85,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         if _lib is not None and path is None:
             return _lib
         if path is None:
-            path = _build.build()
+            path = _build.build(calls=False)
         if not os.path.exists(path):
             raise OSError(f"libi8 not found at {path}")
         lib = ctypes.CDLL(path)
@@ -162,12 +162,14 @@ _calls = None
 
 def load_calls():
     """The extension _calls.so (csrc/torch_calls.cpp), built first if it is stale.
-    Raises on failure; there is no other path."""
+    Raises on failure; there is no other path for the calls that go through it (the
+    4-bit route and the heads' rotation)."""
     global _calls
     if _calls is None:
         load()
         with _lock:
             if _calls is None:
+                _build.build()
                 from .fp4 import FP4Rows
                 loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_LIB)
                 module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))

@@ -2,7 +2,8 @@
 and beside it libi8probe.so, a measurement helper for the benchmark (the
 legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path), and _calls.so,
 the CPython extension that hands torch tensors to libi8 where a small call's time
-is the host's (csrc/torch_calls.cpp).
+is the host's (csrc/torch_calls.cpp).  Only the calls that go through the extension
+need it, and g++ and torch's headers with it.
 
 libi8.so is three translation units (the linear layer, the serving operators,
 the 4-bit route), the probe and the extension one each; one ``-gencode`` target
@@ -15,6 +16,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -61,8 +63,9 @@ def _calls_sources():
     return [CALLS_SRC, os.path.join(ROOT, "include", "i8.h")]
 
 
-def stale() -> bool:
-    return _stale(LIB, _sources()) or _stale(PROBE_LIB, [PROBE_SRC]) or _stale(CALLS_LIB, _calls_sources())
+def stale(calls: bool = True) -> bool:
+    return (_stale(LIB, _sources()) or _stale(PROBE_LIB, [PROBE_SRC])
+            or (calls and _stale(CALLS_LIB, _calls_sources())))
 
 
 def _calls_compile(obj: str) -> list[str]:
@@ -83,8 +86,9 @@ def _calls_link(out: str, obj: str) -> list[str]:
             "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libi8.so, libi8probe.so and _calls.so if missing or older than their sources."""
+def build(force: bool = False, verbose: bool = False, calls: bool = True) -> str:
+    """Compile libi8.so, libi8probe.so and, with ``calls``, _calls.so if missing or older
+    than their sources.  An extension that does not compile leaves the libraries built."""
     targets = []
     if force or _stale(LIB, _sources()):
         targets.append((LIB, UNITS))
@@ -101,10 +105,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objects = [f"{lib}.{os.path.basename(u)}.tmp{os.getpid()}.o" for u in units]
         jobs.append((lib, objects, [start([nvcc(), *NVCC_FLAGS, "-c", "-o", o, u])
                                     for o, u in zip(objects, units)]))
-    calls = None
-    if force or _stale(CALLS_LIB, _calls_sources()):
+    obj = proc = None
+    if calls and (force or _stale(CALLS_LIB, _calls_sources())):
         obj = f"{CALLS_LIB}.tmp{os.getpid()}.o"
-        calls = (obj, start(_calls_compile(obj)))
+        try:
+            proc = start(_calls_compile(obj))
+        except OSError as e:    # no compiler
+            print(e, file=sys.stderr)
     failed = []
     for lib, objects, procs in jobs:
         ok = all([p.wait() == 0 for p in procs])
@@ -116,10 +123,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for o in objects:
             if os.path.exists(o):
                 os.remove(o)
-    if calls:
-        obj, proc = calls
+    if obj:
         tmp = f"{CALLS_LIB}.tmp{os.getpid()}"
-        if proc.wait() == 0 and not failed and start(_calls_link(tmp, obj)).wait() == 0:
+        if proc and proc.wait() == 0 and not failed and start(_calls_link(tmp, obj)).wait() == 0:
             os.replace(tmp, CALLS_LIB)
         else:
             failed.append(os.path.basename(CALLS_LIB))
