@@ -36,6 +36,24 @@ def test_the_int8_routes_load_without_the_extension(compiler, tmp_path):
 def test_both_are_loaded_where_they_build():
     _python("""
         import w8a8_int8_quantized_i8_gb300 as i8
-        assert i8.load() and not i8.build.stale()
-        assert i8.binding.load_calls() is i8.binding.load_calls()
+        assert i8.load() and i8.binding.load_calls() is i8.binding.load_calls()
+        assert not i8.build.stale()
     """)
+
+
+def test_an_extension_of_another_torch_or_python_is_not_taken():
+    """After an upgrade the old binary lies there still, newer than its sources."""
+    import importlib
+    import sysconfig
+
+    import torch
+
+    from w8a8_int8_quantized_i8_gb300 import build
+    names = {build.CALLS_LIB}
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1+other")
+        names.add(importlib.reload(build).CALLS_LIB)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name, _f=sysconfig.get_config_var: "cpython-00-other" if name == "SOABI" else _f(name))
+        names.add(importlib.reload(build).CALLS_LIB)
+    assert len(names) == 3 and importlib.reload(build).CALLS_LIB in names

@@ -161,7 +161,7 @@ _calls = None
 
 
 def load_calls():
-    """The extension _calls.so (csrc/torch_calls.cpp), built first if it is stale.
+    """The extension _calls (csrc/torch_calls.cpp), built first if it is stale.
     Raises on failure; there is no other path for the calls that go through it (the
     4-bit route and the heads' rotation)."""
     global _calls

@@ -1,6 +1,6 @@
 """Builds libi8.so (the CUDA library behind include/i8.h) in-tree with nvcc,
 and beside it libi8probe.so, a measurement helper for the benchmark (the
-legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path), and _calls.so,
+legacy warp MMA's int8 and fp16 rates; not part of the W8A8 path), and _calls.*.so,
 the CPython extension that hands torch tensors to libi8 where a small call's time
 is the host's (csrc/torch_calls.cpp).  Only the calls that go through the extension
 need it, and g++ and torch's headers with it.
@@ -19,13 +19,16 @@ import subprocess
 import sys
 import sysconfig
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libi8.so")
 UNITS = [os.path.join(CSRC, name) for name in ("i8_api.cu", "serving_api.cu", "fp4_api.cu")]
-CALLS_LIB = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+# (its name has what its binary interface depends on: another Python or torch builds its own)
+CALLS_LIB = os.path.join(PKG, f"_calls.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 PROBE_LIB = os.path.join(PKG, "libi8probe.so")
 PROBE_SRC = os.path.join(CSRC, "engine_probe.cu")
 
@@ -70,7 +73,6 @@ def stale(calls: bool = True) -> bool:
 
 def _calls_compile(obj: str) -> list[str]:
     """Compiles the extension against this torch and this Python."""
-    import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -80,14 +82,13 @@ def _calls_compile(obj: str) -> list[str]:
 
 
 def _calls_link(out: str, obj: str) -> list[str]:
-    import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-shared", "-o", out, obj, "-L", PKG, "-l:libi8.so", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, calls: bool = True) -> str:
-    """Compile libi8.so, libi8probe.so and, with ``calls``, _calls.so if missing or older
+    """Compile libi8.so, libi8probe.so and, with ``calls``, the extension if missing or older
     than their sources.  An extension that does not compile leaves the libraries built."""
     targets = []
     if force or _stale(LIB, _sources()):
