@@ -465,7 +465,8 @@ i8_status i8_add_rmsnorm_quant_fp4(const void* x_bf16, int64_t M, int64_t K, int
  *   a [M, K] tokens, w [N, K] weights of the same format; N % 8 == 0
  *   bias [N] bf16 or NULL, 16-byte aligned; y [M,N] bf16 (ldy >= N, % 8 == 0),
  *   which shares no memory with the operands
- * The order of the sum is fixed for a shape: repeated calls give the same bits. */
+ * The order of the sum is fixed for a shape (and FORCE_SPLITS and CTA_PAIR, below):
+ * repeated calls give the same bits.                                        */
 i8_status i8_gemm_fp4_bias_bf16(const i8_fp4_rows* a, const i8_fp4_rows* w, const void* bias_bf16, void* y,
                                 int64_t ldy, i8_stream_t stream);
 
@@ -551,24 +552,27 @@ i8_status i8_gemm_dequant_bias_bf16_w16(const int8_t* aq, const float* s_a,
  *                       kernel; the 4-bit route's few-token kernel, at most
  *                       8, or 4 gated, where they leave no split without
  *                       work); 0 = the plan's own choice.
- *   I8_OPT_MAX_CTAS     cap on the persistent grid (0 = one CTA per SM).
- *   I8_OPT_TILE_N       GEMM tile width, 128 or 256 (0 = the table).
+ *   I8_OPT_MAX_CTAS     cap on the persistent grid (0 = one CTA per SM), the
+ *                       4-bit route's CTA pairs among them (a pair at least).
+ *   I8_OPT_TILE_N       GEMM tile width, 128 or 256 (0 = the table; the 4-bit
+ *                       route's tiles are its own).
  *   I8_OPT_CTA_PAIR     GEMM on CTA pairs (256 x 256 tiles per cluster of 2):
  *                       0 = the table (default: pairs for int8 weights when
- *                       the 256 x 256 tiles fill every pair of SMs), 1 = never,
+ *                       the 256 x 256 tiles fill every pair of SMs; 4-bit
+ *                       codes: a model of both kernels' time), 1 = never,
  *                       2 = whenever M, N >= 256.
  *   I8_OPT_SKINNY_MAX_M token counts M up to this value (0..16, default 16)
  *                       use the weight-streaming kernel for few tokens
  *                       (measured faster than the tiled kernels at every
- *                       M <= 16 of the DiT shapes).
- *   I8_OPT_QUANT_VPL    quantizer: most 16-byte vectors one lane holds
+ *                       M <= 16 of the DiT shapes).  The 4-bit route has its own.
+ *   I8_OPT_QUANT_VPL    8-bit quantizer: most 16-byte vectors one lane holds
  *                       (1..16, default 6); more warps share a row above.
  *   I8_OPT_PDL          1 (default): launch the kernels with programmatic
  *                       stream serialization, so a kernel is scheduled while
  *                       the previous one drains (each waits for the previous
  *                       kernel's memory before touching global memory);
  *                       0: plain stream-ordered launches.
- *   I8_OPT_QUANT_ROWS   quantizer rows per CTA, 1..8 (0 = chosen by shape).
+ *   I8_OPT_QUANT_ROWS   8-bit quantizer's rows per CTA, 1..8 (0 = chosen by shape).
  *   I8_OPT_STREAM_K     stream-K schedule for the CTA-pair kernel (equal
  *                       (tile, K-block) shares per pair, tiles cut between
  *                       pairs finished from exact int32 partials; it needs
@@ -587,8 +591,8 @@ i8_status i8_gemm_dequant_bias_bf16_w16(const int8_t* aq, const float* s_a,
  *                       whenever CHUNK_K is a multiple of 128, else 64.
  *   I8_OPT_RASTER       order of the output tiles in the tiled kernels: 1 M
  *                       blocks fastest, 2 N blocks fastest, 0 (default) N
- *                       fastest when M > N, else M fastest.  Results do not
- *                       depend on it.
+ *                       fastest when M > N, else M fastest (always so on the
+ *                       4-bit route).  Results do not depend on it.
  * Changing FORCE_SPLITS changes the *_workspace_bytes() results.
  *
  * The environment variable I8_OPTIONS, read once when the library is

@@ -254,7 +254,8 @@ i8_status launch_pair(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows* c
   }
   if (!GATED) b[1] = b[0], bs[1] = bs[0];
   const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + Cfg::TILE_N - 1) / Cfg::TILE_N);
-  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters[2])));
+  const int pairs = g_opt.max_ctas > 0 ? std::max(1, std::min(clusters[2], g_opt.max_ctas / 2)) : clusters[2];
+  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
   return cuda_status(launch_pdl(kern, grid, dim3(Cfg::THREADS), Cfg::SMEM, st, a, b[0], b[1], as, bs[0], bs[1], p));
 }
 
@@ -324,7 +325,9 @@ i8_status launch_product(Fp4GemmArgs& p, const i8_fp4_rows& t, const i8_fp4_rows
   if (p.M <= 16) return launch_stream<MX, 16, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 32) return launch_stream<MX, 32, ACT>(p, t, w, dev, sms, st);
   if (p.M <= 64) return launch_stream<MX, 64, ACT>(p, t, w, dev, sms, st);
-  if (p.M > 128 && pair_is_faster(p.M, p.N, p.deep, GATED, sms)) return launch_pair<MX, ACT>(p, t, w, dev, sms, st);
+  const bool pairs = g_opt.cta_pair == 0 ? p.M > 128 && pair_is_faster(p.M, p.N, p.deep, GATED, sms)
+                                         : g_opt.cta_pair == 2 && p.M >= 256 && p.N >= 256;
+  if (pairs) return launch_pair<MX, ACT>(p, t, w, dev, sms, st);
   return launch_stream<MX, 128, ACT>(p, t, w, dev, sms, st);
 }
 
