@@ -111,10 +111,11 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t to, uint4 v) {
 // What a product's epilogue does: nothing more, or act(g) * u.
 enum Fp4Epilogue : int { kFp4Plain = 0, kFp4Silu = 1, kFp4Gelu = 2 };
 
-// act(g) * u in fp32.  silu(g) = g / (1 + exp(-g)): exp(-g) = infinity gives 0.
+// act(g) * u in fp32.  silu(g) = g / (1 + exp(-g)): exp(-g) = infinity gives 0.  (Both
+// sides of the quotient in quarters: the reciprocal of a divisor above 2^126 is 0.)
 template <int ACT>
 __device__ __forceinline__ float fp4_gate(float g, float u) {
-  if constexpr (ACT == kFp4Silu) return __fdividef(g, 1.0f + __expf(-g)) * u;
+  if constexpr (ACT == kFp4Silu) return 0.25f * g * rcp_approx(fmaf(0.25f, __expf(-g), 0.25f)) * u;
   else return gelu_erf(g) * u;
 }
 
