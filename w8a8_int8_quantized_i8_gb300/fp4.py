@@ -68,13 +68,6 @@ def _activation(activation) -> int:
     return code
 
 
-def _activation(activation) -> int:
-    code = ACTIVATIONS.get(activation) if isinstance(activation, str) else None
-    if code is None:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    return code
-
-
 _calls = None
 
 
