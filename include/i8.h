@@ -462,7 +462,8 @@ i8_status i8_add_rmsnorm_quant_fp4(const void* x_bf16, int64_t M, int64_t K, int
 
 /* y[m,n] = bf16(acc * s_a[m] * s_w[n] + bias[n]), acc the fp32 sum over k of the
  * products of code * block scale, s_a and s_w the rows' scales; fp32 steps.
- *   a [M, K] tokens, w [N, K] weights of the same format; N % 8 == 0
+ *   a [M, K] tokens, w [N, K] weights of the same format; N % 8 == 0; M <= 128 *
+ *   65535 (I8_ERR_UNSUPPORTED above, here and in the calls below)
  *   bias [N] bf16 or NULL, 16-byte aligned; y [M,N] bf16 (ldy >= N, % 8 == 0),
  *   which shares no memory with the operands
  * The order of the sum is fixed for a shape (and FORCE_SPLITS and CTA_PAIR, below):

@@ -21,7 +21,9 @@
 // Gated: CTA 0 loads the gate's rows and CTA 1 the up projection's, so the two
 // values of an output are 128 columns apart in the same lane.
 //
-// Persistent: tiles go round the pairs, the larger operand's blocks slowest.
+// Persistent: tiles go round the pairs, the larger operand's blocks slowest.  (The
+// products take 64 elements each: the instruction's form for 96 does not divide a
+// stage, or a tile of block scales, of 256.)
 //
 // 8192 x 8192 x 4096: 87 us MX32 (6.3 PFLOP/s), 90 us NV16; gated, 4096 tokens by two
 // weights of 12288 x 4096, 141 and 146 us.  The products' own time at the clock that

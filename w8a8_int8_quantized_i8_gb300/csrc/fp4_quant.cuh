@@ -13,10 +13,12 @@
 // Rows that the registers cannot hold (V = 0) are read twice, the second time
 // mostly from L2.
 //
-// The row's barrier sets the pace where there is one: the fewer warps meet, the
-// better (8192 x 8192 NV16: V = 2 51 us, 4 40, 8 38, 4.6 TB/s; MX32, which has no
-// barrier, 28 us, 6.1 TB/s; with the residual and the norm, V = 4, 78 us, 5.6 TB/s,
-// and V = 8 83).  A few rows are latency: 2 us for one to 64 rows of 4096.
+// The fewer warps a row, the better (8192 x 8192 NV16: V = 2 51 us, 4 40, 8 37, 4.7
+// TB/s; MX32 28 us, 6.1 TB/s; with the residual and the norm, V = 4, 79 us, 5.6 TB/s,
+// MX32 75, 5.8).  NV16 alone is the farthest from HBM's rate: it may write nothing
+// before the row's maximum is known, a CTA has one row in flight, and a third of the
+// warps that an SM holds are there; with the norm the same wait is shared by nearly
+// three times the bytes.  A few rows are latency: 2 us for one to 64 rows of 4096.
 #pragma once
 #include <cuda_bf16.h>
 

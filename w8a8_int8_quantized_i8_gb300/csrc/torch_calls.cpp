@@ -4,7 +4,7 @@
 // give their defaults.
 //
 // A CPython extension and not ctypes, because a small call is the host's time: one
-// token through a layer is 7 us of the GPU's, and 21 us of the host's by ctypes, most
+// token through a layer is 5 us of the GPU's, and 21 us of the host's by ctypes, most
 // of it in the interpreter and in torch.empty's argument parser with the caches cold
 // from the launch before.
 //
